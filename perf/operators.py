@@ -288,7 +288,7 @@ def _table(s):
     need = torch.where(fits, all_ - held, 0)
     upto = used + need.cumsum(0)
     served = fits & ((need == 0) | (upto <= free.numel()))
-    first = torch.where(served, upto - need, -1)
+    first = torch.where(served, (upto - need).clamp(max=free.numel()), -1)
     lens = torch.where(served, cached + new, cached)
     used_out = used + torch.where(served, need, 0).sum()
     starts = torch.cat([torch.zeros_like(used), ends]).clamp(max=tokens)
