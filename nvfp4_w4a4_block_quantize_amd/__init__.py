@@ -15,11 +15,18 @@ Functions carry the C names:
   nvfp4_gemm(a_codes, a_scales, a_gscale,
              w_codes, w_scales, w_gscale,
              out_dtype)                      -> c
+
+The paged FP8 KV cache (include/nvfp4_kv.h) is bound in kv.py and is part of
+this namespace: nvfp4_kv_block_table, nvfp4_rope, nvfp4_kv_cache_write,
+nvfp4_paged_attention, nvfp4_paged_attention_workspace.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+
+from .kv import (KV_SIGNATURES, nvfp4_kv_block_table, nvfp4_kv_cache_write, nvfp4_paged_attention,
+                 nvfp4_paged_attention_workspace, nvfp4_rope)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libnvfp4.so")
@@ -65,7 +72,9 @@ def load_library(path: str | None = None):
     if not os.path.exists(p):
         raise RuntimeError(f"{p} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
     lib = ctypes.CDLL(p)
-    for name, (res, args) in SIGNATURES.items():
+    # another build, named by its path, may hold the linear layer's C ABI alone
+    kv = KV_SIGNATURES if path is None or hasattr(lib, "nvfp4_kv_block_table") else {}
+    for name, (res, args) in {**SIGNATURES, **kv}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

@@ -24,7 +24,8 @@ CONFORMANCE_PATH = os.path.join(ROOT, "tests", "conformance_cvt")
 PROBES_SRC = os.path.join(ROOT, "bench_probes.hip")
 PROBES_PATH = os.path.join(ROOT, "libnvfp4_probes.so")
 
-SOURCES = ["nvfp4_abi.cpp", "quantize.hip", "fuse_rescale.hip", "gemm.hip", "gemm_fast.hip", "gemm_decode.hip", "gemm_stream.hip", "kv_quantize.hip"]
+SOURCES = ["nvfp4_abi.cpp", "quantize.hip", "fuse_rescale.hip", "gemm.hip", "gemm_fast.hip", "gemm_decode.hip", "gemm_stream.hip", "kv_quantize.hip",
+           "nvfp4_kv_abi.cpp", "kv_table.hip", "rope.hip", "kv_cache_write.hip", "paged_attention.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,185 @@
+// Block tables and slot maps from request lengths (nvfp4_kv_block_table).
+//
+// With c cached and n new tokens of a request and pages of P tokens:
+//   held = ceil(c/P), all = ceil((c+n)/P), need = all - held fresh pages;
+//   upto_r = used + sum_{i<=r} need_i picks them from the free list in order;
+//   slot(t) = page(pos / P) * P + pos % P for the new token at position pos.
+//
+// One workgroup scans the requests, 1024 at a time, with running sums of tokens
+// and pages (64-bit: neither sum is bounded by 32 bits before the limits are
+// applied).  The tokens are then spread over threads, four consecutive ones
+// each: a thread finds its request by bisection in the starts and walks on from
+// there.  The thread whose token opens a page also enters it in the block table,
+// so fresh pages cost no pass of their own and nobody reads an entry that this
+// call writes.
+#include <algorithm>
+
+#include "kv_internal.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kScanThreads = 1024;
+constexpr int kScanWaves = kScanThreads / 64;
+constexpr int kSpreadThreads = 256;
+constexpr int kPerThread = 4;       // tokens, one 16-byte store
+constexpr int kStartsInLds = 4096;  // requests whose starts a workgroup keeps in LDS
+// Up to this many slots the scan's own workgroup spreads the tokens too, which saves the second launch.
+constexpr int kOneLaunchTokens = 8192;
+
+// inclusive prefix sum over the workgroup; `total` is the sum of all
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* wave_sums, int64_t& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  __syncthreads();  // the previous scan's sums have been read
+  if (lane == 63) wave_sums[wave] = v;
+  __syncthreads();
+  int64_t sums = wave_sums[lane & (kScanWaves - 1)];
+#pragma unroll
+  for (int d = 1; d < kScanWaves; d <<= 1) {
+    const int64_t o = __shfl_up(sums, d, kScanWaves);
+    if ((lane & (kScanWaves - 1)) >= d) sums += o;
+  }
+  total = __shfl(sums, kScanWaves - 1);
+  const int64_t before = __shfl(sums, max(wave - 1, 0));
+  return v + (wave > 0 ? before : 0);
+}
+
+// slots of tokens t0 .. t0+3; starts: token_starts, in LDS or global memory
+__device__ __forceinline__ void spread4(const BlockTableArgs& a, FastDiv by_page, const int32_t* starts, int t0) {
+  int32_t slot[kPerThread];
+  // the last request that begins at or before t0; n_seqs: behind the last token
+  int lo = 0, hi = a.n_seqs + 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (starts[mid] <= t0) lo = mid + 1;
+    else hi = mid;
+  }
+  int r = lo - 1, loaded = -1, first = 0, cached = 0, held = 0, begin = 0;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int t = t0 + i;
+    while (r < a.n_seqs && starts[r + 1] <= t) ++r;
+    slot[i] = -1;
+    if (r >= a.n_seqs || t >= a.max_tokens) continue;
+    if (r != loaded) {
+      loaded = r;
+      first = a.first_pages[r];
+      // a served request's seq_lens already counts its new tokens
+      cached = a.seq_lens[r] - a.new_lens[r];
+      begin = starts[r];
+      held = first < 0 ? 0 : (int)by_page.div((uint32_t)(cached + a.page_size - 1));
+    }
+    if (first < 0) continue;
+    const int pos = cached + (t - begin);
+    const int col = (int)by_page.div((uint32_t)pos), off = pos - col * a.page_size;
+    int page;
+    if (col < held) {
+      page = a.block_table[(int64_t)r * a.ld_table + col];
+    } else {
+      page = a.free_pages[first + (col - held)];
+      if (off == 0) a.block_table[(int64_t)r * a.ld_table + col] = page;
+    }
+    const int64_t s = (int64_t)page * a.page_size + off;
+    if (page >= 0 && s <= INT32_MAX) slot[i] = (int32_t)s;
+  }
+  int32_t* out = a.slot_map + t0;
+  if (t0 + kPerThread <= a.max_tokens && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+    *reinterpret_cast<int4*>(out) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i)
+      if (t0 + i < a.max_tokens) out[i] = slot[i];
+  }
+}
+
+template <bool SPREAD>
+__global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, FastDiv by_page) {
+  __shared__ int64_t sums[kScanWaves];
+  __shared__ int32_t lds_starts[SPREAD ? kStartsInLds + 1 : 1];
+  __shared__ unsigned long long taken;
+  if (threadIdx.x == 0) taken = 0;
+  const int64_t used = max(0, *a.free_used);
+  int64_t tokens = 0, pages = 0;
+  for (int base = 0; base < a.n_seqs; base += kScanThreads) {
+    const int r = base + threadIdx.x;
+    const bool in = r < a.n_seqs;
+    const int64_t c = in ? a.cached_lens[r] : 0, n = in ? a.new_lens[r] : 0;
+    int64_t sum;
+    const int64_t end = tokens + block_scan(n > 0 ? n : 0, sums, sum);
+    tokens += sum;
+    const int64_t limit = (int64_t)a.max_pages * a.page_size;
+    const bool fits = in && c >= 0 && n >= 0 && c + n <= limit && end <= a.max_tokens;
+    int64_t need = 0;
+    if (fits) {
+      const uint32_t up = (uint32_t)a.page_size - 1;
+      need = (int64_t)by_page.div((uint32_t)(c + n) + up) - by_page.div((uint32_t)c + up);
+    }
+    const int64_t upto = used + pages + block_scan(need, sums, sum);
+    pages += sum;
+    const bool served = fits && (need == 0 || upto <= a.n_free);
+    if (in) {
+      const int64_t start = min(end - (n > 0 ? n : 0), (int64_t)a.max_tokens);
+      a.token_starts[r] = (int32_t)start;
+      if constexpr (SPREAD) {
+        if (a.n_seqs <= kStartsInLds) lds_starts[r] = (int32_t)start;
+      }
+      a.seq_lens[r] = (int32_t)(served ? c + n : c);
+      a.first_pages[r] = served ? (int32_t)min(upto - need, (int64_t)a.n_free) : -1;
+    }
+    // whoever gets pages comes before whoever does not: the last of them says how many are gone
+    const uint64_t got = __ballot(served && need > 0);
+    if (got && (int)(threadIdx.x & 63) == 63 - __builtin_clzll(got))
+      atomicMax(&taken, (unsigned long long)(upto - used));
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int32_t last = (int32_t)min(tokens, (int64_t)a.max_tokens);
+    a.token_starts[a.n_seqs] = last;
+    if constexpr (SPREAD) {
+      if (a.n_seqs <= kStartsInLds) lds_starts[a.n_seqs] = last;
+    }
+    *a.free_used_out = (int32_t)(used + (int64_t)taken);
+  }
+  if constexpr (SPREAD) {
+    __syncthreads();  // the workgroup's own global writes too are visible to it from here
+    const int32_t* starts = a.n_seqs <= kStartsInLds ? lds_starts : a.token_starts;
+    for (int64_t t0 = (int64_t)threadIdx.x * kPerThread; t0 < a.max_tokens; t0 += (int64_t)kScanThreads * kPerThread)
+      spread4(a, by_page, starts, (int)t0);
+  }
+}
+
+__global__ __launch_bounds__(kSpreadThreads) void kv_table_spread(BlockTableArgs a, FastDiv by_page) {
+  __shared__ int32_t lds_starts[kStartsInLds + 1];
+  const int32_t* starts = a.token_starts;
+  if (a.n_seqs <= kStartsInLds) {
+    for (int i = threadIdx.x; i <= a.n_seqs; i += kSpreadThreads) lds_starts[i] = a.token_starts[i];
+    __syncthreads();
+    starts = lds_starts;
+  }
+  const int64_t t0 = ((int64_t)blockIdx.x * kSpreadThreads + threadIdx.x) * kPerThread;
+  if (t0 < a.max_tokens) spread4(a, by_page, starts, (int)t0);
+}
+
+}  // namespace
+
+hipError_t launch_kv_block_table(const BlockTableArgs& a, hipStream_t stream) {
+  const FastDiv by_page((uint32_t)a.page_size);
+  if (a.max_tokens <= kOneLaunchTokens) {
+    kv_table_scan<true><<<1, kScanThreads, 0, stream>>>(a, by_page);
+    return hipGetLastError();
+  }
+  kv_table_scan<false><<<1, kScanThreads, 0, stream>>>(a, by_page);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t per_block = (int64_t)kSpreadThreads * kPerThread;
+  const int64_t blocks = ((int64_t)a.max_tokens + per_block - 1) / per_block;
+  kv_table_spread<<<(unsigned)blocks, kSpreadThreads, 0, stream>>>(a, by_page);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

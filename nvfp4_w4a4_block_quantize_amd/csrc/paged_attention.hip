@@ -1,0 +1,663 @@
+// Attention of one new token per sequence over a paged FP8 cache
+// (nvfp4_paged_attention):
+//   s_j = scale * q . k_j / k_scale,  out = sum_j softmax(s)_j v_j / v_scale.
+//
+// Every cache byte is read once and serves the G = q_heads / kv_heads queries of
+// its head: 4 G operations for each pair of K and V bytes, far below what the
+// matrix units do in the time that HBM takes to deliver them.  The kernel is
+// built to keep loads in flight and little else.
+//
+// Work.  Each (sequence, KV head) is an item of ceil(tokens / 128) units.  The
+// units of all items lie on one axis and the grid's workers take equal
+// consecutive runs of it, whatever the lengths: a run covers the end of one
+// item, whole items, and the beginning of another.  Whole items are finished in
+// place.  Of the others each worker leaves a partial result (maximum, sum,
+// unnormalised output; at most two of them), and a second, small kernel joins
+// those.  Lengths are read on the device, so a captured graph follows them.
+//
+// A unit is one tile of 32 tokens for each of the workgroup's four waves, which
+// run on their own (maxima, sums and outputs of their own) until the item ends.
+// Nothing passes through LDS or between lanes on the way of the data:
+//  * S^T = K Q^T with v_mfma_16x16x32.  Lane (i = lane % 16, g = lane / 16) of
+//    the K operand loads 16 consecutive bytes of one token's row, for two steps
+//    of the product; Q is held in registers in the same order of d.  Row i of
+//    the tile's product T (0, 1) is token 8 (i / 4) + 4 T + i % 4, so that the
+//    lane's eight results are the tokens 8 g .. 8 g + 7 of query i,
+//  * which is just what O^T = V^T P^T wants of it as P^T operand.  For V^T the
+//    lane loads D/16 bytes of those eight tokens' rows; after the exact
+//    conversion to fp16 one v_perm for two values turns token pairs together.
+//    Row i of the product for byte n is d = i D/16 + n.
+//  * A lane's eight tokens lie in one page (page sizes are multiples of 8), so a
+//    lane needs two table entries per tile, fetched one tile ahead of the rows
+//    that they lead to.
+//
+// Softmax.  One pass with a running maximum m, a whole number of powers of two
+// that moves only when some score passes it by kSlack: p = 2^(s' + kShift - m),
+// s' = s log2(e).  m cancels in the end and being whole, its changes scale by
+// exact powers of two.  kShift puts p below 2^15, in fp16's upper range: p keeps
+// its eleven bits down to 2^-26 of the largest.
+#include <type_traits>
+
+#include <algorithm>
+
+#include "nvfp4_device.h"
+#include "kv_internal.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kTile = 32;                  // tokens of a wave's tile
+constexpr int kUnitTokens = kTile * kWaves;
+constexpr int kMaxWorkersPerCu = 4;
+constexpr float kNoMax = -3.0e38f;         // a maximum before any score; finite, so differences are numbers
+constexpr float kShift = 12.0f, kSlack = 3.0f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+// rows of a worker's partial results, and where they lie in the workspace
+struct Partials {
+  int4* tail;    // [workers] {sequence or -1, item of the sequence, last worker of the item, 0}
+  float2* ml;    // [2 workers][rows] maximum and sum
+  float* o;      // [2 workers][rows][D]
+};
+
+struct Params {
+  PagedAttentionArgs a;
+  FastDiv by_page;
+  int group;      // query heads of a KV head
+  int parts;      // items that a KV head's queries are split into
+  int rows;       // query heads of an item
+  int items;      // of a sequence: kv_heads * parts
+  int64_t page_bytes;
+  Partials ws;
+};
+
+// query heads of an item: what the registers hold (float32 queries take three times the room)
+inline int rows_of_item(int group, bool f32) { return std::min(group, f32 ? 16 : 32); }
+
+template <int DT>
+struct OutType;
+template <>
+struct OutType<0> { typedef float type; };
+template <>
+struct OutType<1> { typedef __bf16 type; };
+template <>
+struct OutType<2> { typedef _Float16 type; };
+
+// four outputs of one row
+template <int DT>
+__device__ __forceinline__ void store4(const PagedAttentionArgs& a, int seq, int head, int d, float4 v) {
+  typedef typename OutType<DT>::type T;
+  T* p = static_cast<T*>(a.out.p) + seq * a.out.token + head * a.out.head + d;
+  struct alignas(4 * sizeof(T)) Four { T v[4]; };
+  *reinterpret_cast<Four*>(p) = Four{{(T)v.x, (T)v.y, (T)v.z, (T)v.w}};
+}
+
+__device__ __forceinline__ int4 seq_span(const PagedAttentionArgs& a, int seq) {
+  const int64_t most = (int64_t)a.max_pages * a.page_size;
+  const int len = (int)min((int64_t)max(a.seq_lens[seq], 0), most);
+  const int start = a.window > 0 && a.window < len ? len - (int)a.window : 0;
+  const int origin = start & ~7;  // where tiles begin: groups of eight tokens share a page
+  return make_int4(len, start, origin, (len - origin + kUnitTokens - 1) / kUnitTokens);
+}
+
+#if defined(__HIP_DEVICE_COMPILE__)
+
+// eight matrix operands of a lane: E4M3 bytes as bf16 or fp16 (exact in both)
+template <int DT>
+__device__ __forceinline__ auto k_operand(uint32_t lo, uint32_t hi) {
+  if constexpr (DT == 2) {
+    half8_t r;
+    const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+    const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+    const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
+    r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
+    return r;
+  } else {
+    bf16x8_t r;
+    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+    const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+    const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
+    r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
+    return r;
+  }
+}
+
+__device__ __forceinline__ float4_t mfma(bf16x8_t a, bf16x8_t b, float4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ float4_t mfma(half8_t a, half8_t b, float4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// a lane's query elements, the K operand's partners: one part in the 16-bit
+// types; a float32 query is the exact sum of three bf16 parts (8 + 8 + 8 bits)
+template <int DT>
+struct Query;
+template <>
+struct Query<0> {
+  static constexpr int parts = 3;
+  bf16x8_t v[3];
+  __device__ __forceinline__ void load(const void* q, int64_t e) {
+    const float* p = static_cast<const float*>(q) + e;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float x = p[i];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        v[k][i] = (__bf16)x;
+        x -= (float)v[k][i];
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() { v[0] = v[1] = v[2] = bf16x8_t{}; }
+};
+template <>
+struct Query<1> {
+  static constexpr int parts = 1;
+  bf16x8_t v[1];
+  __device__ __forceinline__ void load(const void* q, int64_t e) {
+    v[0] = *reinterpret_cast<const bf16x8_t*>(static_cast<const __bf16*>(q) + e);
+  }
+  __device__ __forceinline__ void zero() { v[0] = bf16x8_t{}; }
+};
+template <>
+struct Query<2> {
+  static constexpr int parts = 1;
+  half8_t v[1];
+  __device__ __forceinline__ void load(const void* q, int64_t e) {
+    v[0] = *reinterpret_cast<const half8_t*>(static_cast<const _Float16*>(q) + e);
+  }
+  __device__ __forceinline__ void zero() { v[0] = half8_t{}; }
+};
+
+template <int D>
+struct Rows {  // a wave's tile of K and V as loaded
+  u32x4_t k[2][D / 64];
+  uint32_t v[8][D / 64];
+};
+
+template <int D>
+__device__ __forceinline__ void load_k(Rows<D>& r, const uint8_t* p) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int s = 0; s < D / 64; ++s) r.k[t][s] = *reinterpret_cast<const u32x4_t*>(p + t * 4 * D + s * 64);
+}
+
+template <int D>
+__device__ __forceinline__ void load_v(Rows<D>& r, const uint8_t* p) {
+  constexpr int W = D / 64;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p + j * D);
+    if constexpr (W == 1) {
+      r.v[j][0] = src[0];
+    } else if constexpr (W == 2) {
+      const u32x2_t x = *reinterpret_cast<const u32x2_t*>(src);
+      r.v[j][0] = x[0]; r.v[j][1] = x[1];
+    } else if constexpr (W == 3) {
+      r.v[j][0] = src[0]; r.v[j][1] = src[1]; r.v[j][2] = src[2];
+    } else {
+      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(src);
+      r.v[j][0] = x[0]; r.v[j][1] = x[1]; r.v[j][2] = x[2]; r.v[j][3] = x[3];
+    }
+  }
+}
+
+// where a lane's rows of one tile lie
+struct Place {
+  int entry_k, entry_v;  // table entries
+  int off_k, off_v;      // tokens into the page
+};
+
+#endif
+
+// NQ: 16-column tiles of queries (an item has at most 16 NQ query heads)
+template <int DT, int D, int NQ>
+__global__ __launch_bounds__(kThreads, (DT == 0 || NQ == 2) ? 1 : 2) void paged_attention_kernel(Params p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int KS = D / 64, ND = D / 16, VB = D / 16, VW = D / 64;
+  constexpr int PP = DT == 1 ? 1 : 2;  // parts of a probability: what the output type can tell
+  const PagedAttentionArgs& a = p.a;
+  __shared__ __attribute__((aligned(16))) float lds_o[kWaves][16][D + 4];
+  __shared__ float lds_m[kWaves][16], lds_l[kWaves][16];
+  __shared__ int64_t lds_sum[kWaves + 1];
+  __shared__ int64_t lds_first[2];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, grp = lane >> 4;
+  const int worker = blockIdx.x, n = a.n_seqs;
+
+  // This worker's run of units: a prefix sum over the sequences' units, each
+  // thread summing a few neighbours.
+  const int per = (n + kThreads - 1) / kThreads;
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int s = tid * per + i;
+    if (s < n) mine += (int64_t)seq_span(a, s).w * p.items;
+  }
+  int64_t upto = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t o = __shfl_up(upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 63) lds_sum[wave] = upto;
+  __syncthreads();
+  int64_t before = 0, units = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) before += lds_sum[w];
+    units += lds_sum[w];
+  }
+  upto += before;
+  const int64_t workers = min((int64_t)gridDim.x, units);
+
+  // rows that see no token belong to no item
+  for (int s = worker; s < n; s += gridDim.x) {
+    if (seq_span(a, s).w > 0) continue;
+    for (int i = tid; i < a.q_heads * (D / 4); i += kThreads) {
+      const int h = i / (D / 4);
+      store4<DT>(a, s, h, (i - h * (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+    if (a.lse)
+      for (int h = tid; h < a.q_heads; h += kThreads) a.lse[(int64_t)s * a.q_heads + h] = -INFINITY;
+  }
+
+  int4 tail = make_int4(-1, 0, 0, 0);
+  if (worker >= workers) {
+    if (tid == 0) p.ws.tail[worker] = tail;
+    return;
+  }
+  int64_t u = worker * units / workers;
+  const int64_t u_end = (worker + 1) * units / workers;
+  if (mine > 0 && upto - mine <= u && u < upto) {
+    int64_t at = upto - mine;
+    int s = tid * per;
+    for (int64_t c; at + (c = (int64_t)seq_span(a, s).w * p.items) <= u; at += c) ++s;
+    lds_first[0] = s;
+    lds_first[1] = u - at;
+  }
+  __syncthreads();
+  int seq = __builtin_amdgcn_readfirstlane((int)lds_first[0]);
+  int64_t inside = lds_first[1];  // units of this sequence that lie before the run
+
+  const float ks = *a.k_scale, inv_vs = 1.0f / *a.v_scale;
+  const double c64 = (double)a.softmax_scale * 1.44269504088896340736 / (double)ks;
+  const float c_hi = (float)c64, c_lo = DT == 0 ? (float)(c64 - (double)c_hi) : 0.0f;
+
+  while (u < u_end) {
+    const int4 span = seq_span(a, seq);
+    const int len = span.x, start = span.y, origin = span.z, per_item = span.w;
+    if (per_item == 0) {
+      ++seq;
+      continue;
+    }
+    const int item = (int)(inside / per_item);
+    const int unit0 = (int)(inside - (int64_t)item * per_item);
+    const int unit1 = (int)min((int64_t)per_item, unit0 + (u_end - u));
+    const int head = item / p.parts, q0 = (item - head * p.parts) * p.rows;
+    const int rows = min(p.rows, p.group - q0);
+
+    Query<DT> q[NQ][2 * KS];
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) {
+      const int row = t * 16 + col;
+      const int64_t e = seq * a.q.token + (int64_t)(head * p.group + q0 + min(row, rows - 1)) * a.q.head;
+#pragma unroll
+      for (int s = 0; s < 2 * KS; ++s) {
+        q[t][s].load(a.q.p, e + (s >> 1) * 64 + grp * 16 + (s & 1) * 8);
+        if (row >= rows) q[t][s].zero();
+      }
+    }
+
+    float m[NQ], l[NQ];
+    float4_t o[NQ][ND];
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) {
+      m[t] = kNoMax;
+      l[t] = 0.f;
+#pragma unroll
+      for (int i = 0; i < ND; ++i) o[t][i] = float4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
+    const int32_t* table = a.block_table + seq * a.ld_table;
+    const int group_k = col >> 2;
+    auto find = [&](int tile) {
+      Place w;
+      const uint32_t tk = origin + tile * kTile + 8 * group_k, tv = origin + tile * kTile + 8 * grp;
+      const uint32_t ck = p.by_page.div(tk), cv = p.by_page.div(tv);
+      w.off_k = tk - ck * a.page_size;
+      w.off_v = tv - cv * a.page_size;
+      // past the last token a tile may reach past the table's last column
+      w.entry_k = table[min(ck, (uint32_t)a.max_pages - 1)];
+      w.entry_v = table[min(cv, (uint32_t)a.max_pages - 1)];
+      return w;
+    };
+    auto row = [&](const uint8_t* cache, int entry, int off) {
+      const int64_t page = (uint32_t)entry < (uint32_t)a.num_pages ? entry : 0;
+      return cache + page * p.page_bytes + ((int64_t)head * a.page_size + off) * D;
+    };
+    const int tiles = (len - origin + kTile - 1) / kTile;
+    const int tile_end = min(unit1 * kWaves, tiles);
+    int tile = unit0 * kWaves + wave;
+    if (tile < tile_end) {
+      Rows<D> r;
+      Place now = find(tile), next = find(tile + kWaves);
+      load_k(r, row(a.k_cache, now.entry_k, now.off_k + (col & 3)) + grp * 16);
+      load_v(r, row(a.v_cache, now.entry_v, now.off_v) + col * VB);
+      while (true) {
+        const int token = origin + tile * kTile + 8 * grp;  // the first of this lane's eight
+        const bool here = (uint32_t)now.entry_v < (uint32_t)a.num_pages;
+        const bool more = tile + kWaves < tile_end;
+
+        float4_t s[NQ][2];
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) s[t][0] = s[t][1] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const auto k = k_operand<DT>(r.k[h][i >> 1][2 * (i & 1)], r.k[h][i >> 1][2 * (i & 1) + 1]);
+#pragma unroll
+            for (int t = 0; t < NQ; ++t)
+#pragma unroll
+              for (int part = Query<DT>::parts - 1; part >= 0; --part) s[t][h] = mfma(k, q[t][i].v[part], s[t][h]);
+          }
+        if (more) {
+          load_k(r, row(a.k_cache, next.entry_k, next.off_k + (col & 3)) + grp * 16);
+        }
+
+        const bool whole = origin + tile * kTile >= start && origin + (tile + 1) * kTile <= len;
+        uint32_t seen = 0xFF;  // of this lane's tokens
+        if (!whole || !__all(here)) {
+          seen = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (here && token + j >= start && token + j < len) seen |= 1u << j;
+#pragma unroll
+          for (int t = 0; t < NQ; ++t)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (!(seen >> j & 1)) s[t][j >> 2][j & 3] = -INFINITY;
+          // rows behind the last token hold anything, NaN among it
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int w = 0; w < VW; ++w) r.v[j][w] = seen >> j & 1 ? r.v[j][w] : 0u;
+        }
+
+        half8_t pr[NQ][PP];
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) {
+          float top = fmaxf(fmaxf(fmaxf(s[t][0][0], s[t][0][1]), fmaxf(s[t][0][2], s[t][0][3])),
+                            fmaxf(fmaxf(s[t][1][0], s[t][1][1]), fmaxf(s[t][1][2], s[t][1][3]))) * c_hi;
+          if (__any(top > m[t] + kSlack)) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float to = fmaxf(m[t], ceilf(top));
+            const float f = __builtin_amdgcn_exp2f(m[t] - to);
+            m[t] = to;
+            l[t] *= f;
+#pragma unroll
+            for (int i = 0; i < ND; ++i) o[t][i] *= f;
+          }
+          const float base = kShift - m[t];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float sj = s[t][j >> 2][j & 3];
+            float e;
+            if constexpr (DT == 0)
+              e = __builtin_amdgcn_exp2f(fmaf(sj, c_hi, seen >> j & 1 ? fmaf(sj, c_lo, base) : base));
+            else
+              e = __builtin_amdgcn_exp2f(fmaf(sj, c_hi, base));
+            l[t] += e;
+            pr[t][0][j] = (_Float16)e;
+            if constexpr (PP == 2) pr[t][1][j] = (_Float16)(e - (float)pr[t][0][j]);
+          }
+        }
+
+#pragma unroll
+        for (int w = 0; w < VW; ++w)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[8], even[4], odd[4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              x[j] = __builtin_bit_cast(uint32_t, h ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.v[j][w], 1.0f, true)
+                                                    : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.v[j][w], 1.0f, false));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              even[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x05040100u);
+              odd[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x07060302u);
+            }
+            const half8_t ve = __builtin_bit_cast(half8_t, u32x4_t{even[0], even[1], even[2], even[3]});
+            const half8_t vo = __builtin_bit_cast(half8_t, u32x4_t{odd[0], odd[1], odd[2], odd[3]});
+#pragma unroll
+            for (int t = 0; t < NQ; ++t)
+#pragma unroll
+              for (int part = PP - 1; part >= 0; --part) {
+                o[t][4 * w + 2 * h] = mfma(ve, pr[t][part], o[t][4 * w + 2 * h]);
+                o[t][4 * w + 2 * h + 1] = mfma(vo, pr[t][part], o[t][4 * w + 2 * h + 1]);
+              }
+          }
+        if (!more) break;
+        load_v(r, row(a.v_cache, next.entry_v, next.off_v) + col * VB);
+        tile += kWaves;
+        now = next;
+        next = find(tile + kWaves);
+      }
+    }
+
+    // The four waves' results into one, 16 query heads at a time.
+    const bool ends = unit0 == 0 && unit1 == per_item;  // the whole item
+    const int slot = 2 * worker + (unit0 == 0 ? 1 : 0);
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) {
+      if (t * 16 >= rows) break;
+      float sum = l[t];
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      __syncthreads();  // the last results have been read
+      if (grp == 0) {
+        lds_m[wave][col] = m[t];
+        lds_l[wave][col] = sum;
+      }
+      __syncthreads();
+      float top = lds_m[0][col];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, lds_m[w][col]);
+      const float f = __builtin_amdgcn_exp2f(m[t] - top);
+      if (t * 16 + col < rows) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int i = 0; i < VB; i += 4)
+            *reinterpret_cast<float4_t*>(&lds_o[wave][col][(4 * grp + r) * VB + i]) =
+                float4_t{o[t][i][r], o[t][i + 1][r], o[t][i + 2][r], o[t][i + 3][r]} * f;
+      }
+      __syncthreads();
+      const int here = min(16, rows - t * 16);
+      for (int i = tid; i < here * (D / 4); i += kThreads) {
+        const int row_ = i / (D / 4), d = (i - row_ * (D / 4)) * 4;
+        float high = lds_m[0][row_], total = 0.f;
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) high = fmaxf(high, lds_m[w][row_]);
+        float4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          total += lds_l[w][row_] * __builtin_amdgcn_exp2f(lds_m[w][row_] - high);
+          v += *reinterpret_cast<const float4_t*>(&lds_o[w][row_][d]);
+        }
+        const int in_item = t * 16 + row_;
+        if (ends) {
+          const int h = head * p.group + q0 + in_item;
+          const float by = total > 0.f ? inv_vs / total : 0.f;
+          store4<DT>(a, seq, h, d, make_float4(v[0] * by, v[1] * by, v[2] * by, v[3] * by));
+          if (a.lse && d == 0)
+            a.lse[(int64_t)seq * a.q_heads + h] = total > 0.f ? (high - kShift + log2f(total)) * kLn2 : -INFINITY;
+        } else {
+          const int64_t at = (int64_t)slot * p.rows + in_item;
+          *reinterpret_cast<float4_t*>(p.ws.o + at * D + d) = v;
+          if (d == 0) p.ws.ml[at] = make_float2(high, total);
+        }
+      }
+    }
+    if (unit0 == 0 && !ends) {
+      // the item's last unit is that of the first worker whose run ends behind it
+      const int64_t behind = u + per_item;
+      tail = make_int4(seq, item, (int)((behind * workers + units - 1) / units) - 1, 0);
+    }
+    u += unit1 - unit0;
+    inside += unit1 - unit0;
+    if (inside == (int64_t)per_item * p.items) {
+      inside = 0;
+      ++seq;
+    }
+  }
+  if (tid == 0) p.ws.tail[worker] = tail;
+#endif
+}
+
+// Joins the partial results of one query head of the item that begins in worker
+// blockIdx.x and does not end there: the worker's second one and the first ones
+// of the workers up to the item's last.
+template <int DT, int D>
+__global__ __launch_bounds__(kThreads) void paged_attention_join(Params p, int max_workers) {
+  const PagedAttentionArgs& a = p.a;
+  extern __shared__ float weights[];  // [max_workers]
+  __shared__ float4 lds_o[kThreads];
+  __shared__ float lds_r[2][kWaves];
+  const int worker = blockIdx.x, row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int4 tail = p.ws.tail[worker];
+  if (tail.x < 0) return;
+  const int seq = tail.x, head = tail.y / p.parts, q0 = (tail.y - head * p.parts) * p.rows;
+  if (q0 + row >= p.group) return;
+  const int count = tail.z - worker + 1;
+  auto at = [&](int i) { return (int64_t)(i == 0 ? 2 * worker + 1 : 2 * (worker + i)) * p.rows + row; };
+
+  float top = kNoMax;
+  for (int i = tid; i < count; i += kThreads) top = fmaxf(top, p.ws.ml[at(i)].x);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if (lane == 0) lds_r[0][wave] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_r[0][w]);
+  float total = 0.f;
+  for (int i = tid; i < count; i += kThreads) {
+    const float2 ml = p.ws.ml[at(i)];
+    const float f = exp2f(ml.x - top);
+    weights[i] = f;
+    total += ml.y * f;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) total += __shfl_xor(total, d);
+  if (lane == 0) lds_r[1][wave] = total;
+  __syncthreads();
+  total = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) total += lds_r[1][w];
+
+  constexpr int kLanes = D / 4, kSets = kThreads / kLanes;  // lanes of one partial result, and how many at a time
+  const int set = tid / kLanes, d = (tid - set * kLanes) * 4;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (set < kSets) {
+#pragma unroll 4
+    for (int i = set; i < count; i += kSets) {
+      const float4 x = *reinterpret_cast<const float4*>(p.ws.o + at(i) * D + d);
+      const float f = weights[i];
+      v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
+    }
+  }
+  lds_o[tid] = v;
+  __syncthreads();
+  if (set == 0) {
+#pragma unroll
+    for (int s = 1; s < kSets; ++s) {
+      const float4 x = lds_o[s * kLanes + tid];
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    const float by = total > 0.f ? 1.0f / *a.v_scale / total : 0.f;
+    const int h = head * p.group + q0 + row;
+    store4<DT>(a, seq, h, d, make_float4(v.x * by, v.y * by, v.z * by, v.w * by));
+    if (a.lse && tid == 0)
+      a.lse[(int64_t)seq * a.q_heads + h] = total > 0.f ? (top - kShift + log2f(total)) * kLn2 : -INFINITY;
+  }
+}
+
+template <int DT, int D, int NQ>
+hipError_t launch(const Params& p, hipStream_t stream) {
+  const PagedAttentionArgs& a = p.a;
+  const int workers_per_cu = (DT == 0 || NQ == 2) ? 1 : 2;
+  const int64_t item_units = ((int64_t)a.max_pages * a.page_size + kUnitTokens - 1) / kUnitTokens;
+  const int64_t most = (int64_t)a.n_seqs * p.items * item_units;
+  const int workers = (int)std::min<int64_t>((int64_t)device_cu_count() * workers_per_cu, most);
+  paged_attention_kernel<DT, D, NQ><<<workers, kThreads, 0, stream>>>(p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || item_units == 1) return e;  // items of one unit are never split
+  paged_attention_join<DT, D><<<dim3(workers, p.rows), kThreads, workers * sizeof(float), stream>>>(p, workers);
+  return hipGetLastError();
+}
+
+template <int DT, int D>
+hipError_t launch_rows(const Params& p, hipStream_t stream) {
+  if constexpr (DT != 0) {
+    if (p.rows > 16) return launch<DT, D, 2>(p, stream);
+  }
+  return launch<DT, D, 1>(p, stream);
+}
+
+template <int DT>
+hipError_t launch_dim(const Params& p, hipStream_t stream) {
+  switch (p.a.head_dim) {
+    case 64: return launch_rows<DT, 64>(p, stream);
+    case 128: return launch_rows<DT, 128>(p, stream);
+    case 192: return launch_rows<DT, 192>(p, stream);
+    default: return launch_rows<DT, 256>(p, stream);
+  }
+}
+
+}  // namespace
+
+int64_t paged_attention_workspace(int q_heads, int kv_heads, int head_dim) {
+  const int64_t workers = (int64_t)device_cu_count() * kMaxWorkersPerCu;
+  const int64_t rows = rows_of_item(q_heads / kv_heads, false);
+  return workers * (16 + 2 * rows * (8 + 4 * (int64_t)head_dim));
+}
+
+hipError_t launch_paged_attention(const PagedAttentionArgs& a, hipStream_t stream) {
+  Params p;
+  p.a = a;
+  p.by_page = FastDiv((uint32_t)a.page_size);
+  p.group = a.q_heads / a.kv_heads;
+  p.rows = rows_of_item(p.group, a.dtype == 0);
+  p.parts = (p.group + p.rows - 1) / p.rows;
+  p.items = a.kv_heads * p.parts;
+  p.page_bytes = (int64_t)a.kv_heads * a.page_size * a.head_dim;
+  const int64_t workers = (int64_t)device_cu_count() * kMaxWorkersPerCu;
+  char* w = static_cast<char*>(a.workspace);
+  p.ws.o = reinterpret_cast<float*>(w);  // 16-byte aligned pieces first
+  w += workers * 2 * p.rows * 4 * (int64_t)a.head_dim;
+  p.ws.tail = reinterpret_cast<int4*>(w);
+  w += workers * 16;
+  p.ws.ml = reinterpret_cast<float2*>(w);
+  switch (a.dtype) {
+    case 0: return launch_dim<0>(p, stream);
+    case 1: return launch_dim<1>(p, stream);
+    default: return launch_dim<2>(p, stream);
+  }
+}
+
+}  // namespace nvfp4
