@@ -191,7 +191,7 @@ __device__ __forceinline__ void load_k(Rows<D>& r, const uint8_t* p) {
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int s = 0; s < D / 64; ++s) r.k[t][s] = *reinterpret_cast<const u32x4_t*>(p + t * 4 * D + s * 64);
+    for (int s = 0; s < D / 64; ++s) r.k[t][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p + t * 4 * D + s * 64));
 }
 
 template <int D>
@@ -201,14 +201,16 @@ __device__ __forceinline__ void load_v(Rows<D>& r, const uint8_t* p) {
   for (int j = 0; j < 8; ++j) {
     const uint32_t* src = reinterpret_cast<const uint32_t*>(p + j * D);
     if constexpr (W == 1) {
-      r.v[j][0] = src[0];
+      r.v[j][0] = __builtin_nontemporal_load(src);
     } else if constexpr (W == 2) {
-      const u32x2_t x = *reinterpret_cast<const u32x2_t*>(src);
+      const u32x2_t x = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(src));
       r.v[j][0] = x[0]; r.v[j][1] = x[1];
     } else if constexpr (W == 3) {
-      r.v[j][0] = src[0]; r.v[j][1] = src[1]; r.v[j][2] = src[2];
+      r.v[j][0] = __builtin_nontemporal_load(src);
+      r.v[j][1] = __builtin_nontemporal_load(src + 1);
+      r.v[j][2] = __builtin_nontemporal_load(src + 2);
     } else {
-      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(src);
+      const u32x4_t x = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(src));
       r.v[j][0] = x[0]; r.v[j][1] = x[1]; r.v[j][2] = x[2]; r.v[j][3] = x[3];
     }
   }

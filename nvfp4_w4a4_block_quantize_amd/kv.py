@@ -17,7 +17,6 @@ given, and there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 _P = ctypes.c_void_p
@@ -37,71 +36,103 @@ KV_SIGNATURES = {
 }
 
 
-def _base():
+_nv = _torch = None  # the package and torch, once something is called
+_fns = {}
+
+
+def _load():
+    global _nv, _torch
     import nvfp4_w4a4_block_quantize_amd as nv
 
-    return nv
+    _nv, _torch = nv, nv._torch()
 
 
-def _call(name, like, stream, *args):
+def _call(name, like, stream, args):
     """One C call on `like`'s device: on `stream`, else on torch's current stream there."""
-    nv = _base()
-    torch = nv._torch()
-    if not like.is_cuda:
-        raise ValueError(f"{name} needs GPU tensors")
-    fn = getattr(nv.load_library(), name)
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(_nv.load_library(), name)
     index = like.get_device()
-    with contextlib.nullcontext() if index == torch.cuda.current_device() else torch.cuda.device(index):
-        nv._check(name, fn(*args, nv._stream_ptr(stream, like)))
+    if index < 0:
+        raise ValueError(f"{name} needs GPU tensors")
+    if index == _torch.cuda.current_device():
+        status = fn(*args, _nv._stream_ptr(stream, like))
+    else:
+        with _torch.cuda.device(index):
+            status = fn(*args, _nv._stream_ptr(stream, like))
+    if status:
+        _nv._check(name, status)
 
 
 def _ints(t, shape, name, like):
-    """A dense int32 tensor on the device of `like`."""
-    if t.dtype != _base()._torch().int32:
+    """The address of a dense int32 tensor on the device of `like`."""
+    if t.dtype is not _torch.int32:
         raise ValueError(f"{name} must be int32, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    _base()._same_device(t, like, name)
+    if t.get_device() != like.get_device():
+        _nv._same_device(t, like, name)
     return t.data_ptr()
 
 
-def _new(shape, dtype, like):
-    return _base()._torch().empty(shape, dtype=dtype, device=like.device)
+def _scale(t, name, like):
+    """The address of a one-element float32 tensor on the device of `like`."""
+    if t.dtype is not _torch.float32 or t.numel() != 1 or t.get_device() != like.get_device():
+        _nv._scalar_f32(t, name, like)
+    return t.data_ptr()
+
+
+def _new(shape, dtype, like, stream):
+    """A tensor to fill on `stream`: the allocator knows it by the stream that it is used on."""
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=like.device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _table(t, rows, like):
-    """A block table: int32 rows, unit column stride."""
-    if t.dtype != _base()._torch().int32 or t.dim() != 2 or t.shape[0] != rows:
-        raise ValueError(f"block_table must be int32 [{rows}, pages], got {t.dtype} {tuple(t.shape)}")
-    if t.stride(1) != 1 and t.shape[1] != 1:
+    """A block table, int32 with unit column stride: (address, columns, row stride)."""
+    shape = t.shape
+    if t.dtype is not _torch.int32 or len(shape) != 2 or shape[0] != rows:
+        raise ValueError(f"block_table must be int32 [{rows}, pages], got {t.dtype} {tuple(shape)}")
+    ld, unit = t.stride()
+    if unit != 1 and shape[1] != 1:
         raise ValueError("block_table must have unit column stride")
-    _base()._same_device(t, like, "block_table")
-    return t.data_ptr(), t.shape[1], t.stride(0) if rows > 1 else t.shape[1]
+    if t.get_device() != like.get_device():
+        _nv._same_device(t, like, "block_table")
+    return t.data_ptr(), shape[1], ld if rows > 1 else shape[1]
 
 
 def _heads(t, name, like=None):
     """[tokens, heads, head_dim] with any strides between heads and tokens:
-    (pointer, token stride, head stride).  The stride of an axis of one is free."""
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
-        raise ValueError(f"{name} must be [tokens, heads, head_dim] with unit stride along head_dim")
+    (address, token stride, head stride).  The stride of an axis of one is free."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(shape)}")
     if like is not None:
-        if t.dtype != like.dtype or tuple(t.shape) != tuple(like.shape):
-            raise ValueError(f"{name} must be {like.dtype} of shape {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
-        _base()._same_device(t, like, name)
-    tokens, heads, dim = t.shape
-    head = t.stride(1) if heads > 1 else dim
-    return t.data_ptr(), t.stride(0) if tokens > 1 else heads * head, head
+        if t.dtype is not like.dtype or shape != like.shape:
+            raise ValueError(f"{name} must be {like.dtype} of shape {tuple(like.shape)}, got {t.dtype} {tuple(shape)}")
+        if t.get_device() != like.get_device():
+            _nv._same_device(t, like, name)
+    tokens, heads, dim = shape
+    token, head, unit = t.stride()
+    if unit != 1 and dim != 1:
+        raise ValueError(f"{name} must have unit stride along head_dim")
+    if heads == 1:
+        head = dim
+    return t.data_ptr(), token if tokens > 1 else heads * head, head
 
 
 def _cache(k_cache, v_cache, like):
-    """Two [num_pages, kv_heads, page_size, head_dim] byte tensors."""
+    """The addresses of two [num_pages, kv_heads, page_size, head_dim] byte tensors."""
     if k_cache.dim() != 4:
         raise ValueError(f"k_cache must be [num_pages, kv_heads, page_size, head_dim], got {tuple(k_cache.shape)}")
-    nv = _base()
-    nv._bytes_arg(k_cache, k_cache.shape, "k_cache", like)
-    nv._bytes_arg(v_cache, k_cache.shape, "v_cache", like)
+    u8, index = _torch.uint8, like.get_device()
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype is not u8 or t.shape != k_cache.shape or not t.is_contiguous() or t.get_device() != index:
+            _nv._bytes_arg(t, k_cache.shape, name, like)
     return k_cache.data_ptr(), v_cache.data_ptr()
 
 
@@ -115,25 +146,29 @@ def nvfp4_kv_block_table(cached_lens, new_lens, page_size: int, free_pages, free
     seq_lens may be cached_lens and free_used_out may be free_used (updated in
     place).  Returns (seq_lens, token_starts, first_pages, free_used_out).
     """
-    nv = _base()
-    i32 = nv._torch().int32
+    if _nv is None:
+        _load()
+    i32 = _torch.int32
     n = cached_lens.shape[0] if cached_lens.dim() == 1 else -1
     if n < 0 or free_pages.dim() != 1 or slot_map.dim() != 1:
         raise ValueError("cached_lens, free_pages and slot_map must be 1-D")
-    seq_lens = _new((n,), i32, cached_lens) if seq_lens is None else seq_lens
-    token_starts = _new((n + 1,), i32, cached_lens) if token_starts is None else token_starts
-    first_pages = _new((n,), i32, cached_lens) if first_pages is None else first_pages
-    free_used_out = _new((1,), i32, cached_lens) if free_used_out is None else free_used_out
+    if seq_lens is None:
+        seq_lens = _new((n,), i32, cached_lens, stream)
+    if token_starts is None:
+        token_starts = _new((n + 1,), i32, cached_lens, stream)
+    if first_pages is None:
+        first_pages = _new((n,), i32, cached_lens, stream)
+    if free_used_out is None:
+        free_used_out = _new((1,), i32, cached_lens, stream)
     table, max_pages, ld = _table(block_table, n, cached_lens)
     n_free, tokens = free_pages.shape[0], slot_map.shape[0]
-    _call("nvfp4_kv_block_table", cached_lens, stream, n, _ints(cached_lens, (n,), "cached_lens", cached_lens),
-          _ints(new_lens, (n,), "new_lens", cached_lens), page_size,
-          _ints(free_pages, (n_free,), "free_pages", cached_lens), n_free,
-          _ints(free_used, (1,), "free_used", cached_lens), table, max_pages, ld,
-          _ints(slot_map, (tokens,), "slot_map", cached_lens), tokens, _ints(seq_lens, (n,), "seq_lens", cached_lens),
-          _ints(token_starts, (n + 1,), "token_starts", cached_lens),
-          _ints(first_pages, (n,), "first_pages", cached_lens),
-          _ints(free_used_out, (1,), "free_used_out", cached_lens))
+    like = cached_lens
+    _call("nvfp4_kv_block_table", like, stream,
+          (n, _ints(cached_lens, (n,), "cached_lens", like), _ints(new_lens, (n,), "new_lens", like), page_size,
+           _ints(free_pages, (n_free,), "free_pages", like), n_free, _ints(free_used, (1,), "free_used", like), table,
+           max_pages, ld, _ints(slot_map, (tokens,), "slot_map", like), tokens,
+           _ints(seq_lens, (n,), "seq_lens", like), _ints(token_starts, (n + 1,), "token_starts", like),
+           _ints(first_pages, (n,), "first_pages", like), _ints(free_used_out, (1,), "free_used_out", like)))
     return seq_lens, token_starts, first_pages, free_used_out
 
 
@@ -146,34 +181,42 @@ def nvfp4_rope(q, k, positions, inv_freq, axes, adjacent: bool = False, q_out=No
     i + rot_dim / 2.  Pass q (k) itself as q_out (k_out) to turn in place.
     Returns (q_out, k_out).
     """
-    nv = _base()
-    torch = nv._torch()
-    q_out = _new(q.shape, q.dtype, q) if q_out is None else q_out
+    if _nv is None:
+        _load()
+    if q_out is None:
+        q_out = _new(q.shape, q.dtype, q, stream)
     pq, q_token, q_head = _heads(q, "q")
     po, o_token, o_head = _heads(q_out, "q_out", q)
     tokens, q_heads, dim = q.shape
-    if positions.dim() != 2 or positions.dtype != torch.int32 or positions.shape[1] != tokens or \
-            (positions.stride(1) != 1 and tokens != 1):
-        raise ValueError(f"positions must be int32 [axes, {tokens}] with unit stride along tokens")
-    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
+    pos_shape, index = positions.shape, q.get_device()
+    if len(pos_shape) != 2 or positions.dtype is not _torch.int32 or pos_shape[1] != tokens:
+        raise ValueError(f"positions must be int32 [axes, {tokens}], got {positions.dtype} {tuple(pos_shape)}")
+    ld_pos, unit = positions.stride()
+    if unit != 1 and tokens != 1:
+        raise ValueError("positions must have unit stride along tokens")
+    if inv_freq.dim() != 1 or inv_freq.dtype is not _torch.float32 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be float32 [rot_dim / 2], contiguous")
-    nv._same_device(positions, q, "positions")
-    nv._same_device(inv_freq, q, "inv_freq")
-    pairs, n_axes = inv_freq.shape[0], positions.shape[0]
-    keys = [None, None, 0, 0, 0, 0, 0]
+    if positions.get_device() != index or inv_freq.get_device() != index:
+        _nv._same_device(positions, q, "positions")
+        _nv._same_device(inv_freq, q, "inv_freq")
+    pairs, n_axes = inv_freq.shape[0], pos_shape[0]
+    keys = (None, None, 0, 0, 0, 0, 0)
     if k is not None:
-        if k.dim() != 3 or k.dtype != q.dtype or k.shape[0] != tokens or k.shape[2] != dim:
-            raise ValueError(f"k must be {q.dtype} [{tokens}, heads, {dim}], got {k.dtype} {tuple(k.shape)}")
-        nv._same_device(k, q, "k")
-        k_out = _new(k.shape, k.dtype, k) if k_out is None else k_out
         pk, k_token, k_head = _heads(k, "k")
+        if k.dtype is not q.dtype or k.shape[0] != tokens or k.shape[2] != dim:
+            raise ValueError(f"k must be {q.dtype} [{tokens}, heads, {dim}], got {k.dtype} {tuple(k.shape)}")
+        if k.get_device() != index:
+            _nv._same_device(k, q, "k")
+        if k_out is None:
+            k_out = _new(k.shape, k.dtype, k, stream)
         pko, ko_token, ko_head = _heads(k_out, "k_out", k)
-        keys = [pk, pko, k.shape[1], k_token, k_head, ko_token, ko_head]
+        keys = (pk, pko, k.shape[1], k_token, k_head, ko_token, ko_head)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _call("nvfp4_rope", q, stream, tokens, dim, 2 * pairs, nv._dtype_code(q.dtype), int(adjacent),
-          positions.data_ptr(), n_axes, positions.stride(0) if n_axes > 1 else tokens, inv_freq.data_ptr(),
-          _ints(axes, (pairs,), "axes", q), pq, po, q_heads, q_token, q_head, o_token, o_head, *keys)
+    _call("nvfp4_rope", q, stream,
+          (tokens, dim, 2 * pairs, _nv._dtype_code(q.dtype), int(adjacent), positions.data_ptr(), n_axes,
+           ld_pos if n_axes > 1 else tokens, inv_freq.data_ptr(), _ints(axes, (pairs,), "axes", q), pq, po, q_heads,
+           q_token, q_head, o_token, o_head, *keys))
     return q_out, k_out
 
 
@@ -182,27 +225,29 @@ def nvfp4_kv_cache_write(k, v, k_scale, v_scale, slot_map, k_cache, v_cache, str
     their static scales, into the cache at their slots (int32 [tokens]; a slot
     outside the cache leaves its token out).  Caches: uint8 [num_pages, kv_heads,
     page_size, head_dim].  Returns (k_cache, v_cache)."""
-    nv = _base()
+    if _nv is None:
+        _load()
     pk, k_token, k_head = _heads(k, "k")
     pv, v_token, v_head = _heads(v, "v", k)
     tokens, heads, dim = k.shape
     ck, cv = _cache(k_cache, v_cache, k)
-    if k_cache.shape[1] != heads or k_cache.shape[3] != dim:
+    pages, kv_heads, page_size, d = k_cache.shape
+    if kv_heads != heads or d != dim:
         raise ValueError(f"k_cache must be [pages, {heads}, page_size, {dim}], got {tuple(k_cache.shape)}")
-    nv._scalar_f32(k_scale, "k_scale", k)
-    nv._scalar_f32(v_scale, "v_scale", k)
-    _call("nvfp4_kv_cache_write", k, stream, tokens, heads, dim, nv._dtype_code(k.dtype), pk, k_token, k_head, pv,
-          v_token, v_head, k_scale.data_ptr(), v_scale.data_ptr(), _ints(slot_map, (tokens,), "slot_map", k), ck, cv,
-          k_cache.shape[0], k_cache.shape[2])
+    _call("nvfp4_kv_cache_write", k, stream,
+          (tokens, heads, dim, _nv._dtype_code(k.dtype), pk, k_token, k_head, pv, v_token, v_head,
+           _scale(k_scale, "k_scale", k), _scale(v_scale, "v_scale", k), _ints(slot_map, (tokens,), "slot_map", k),
+           ck, cv, pages, page_size))
     return k_cache, v_cache
 
 
 def nvfp4_paged_attention_workspace(q_heads: int, kv_heads: int, head_dim: int) -> int:
     """Bytes of workspace that nvfp4_paged_attention wants for these heads on the current device."""
-    nv = _base()
+    if _nv is None:
+        _load()
     out = ctypes.c_int64(0)
-    nv._check("nvfp4_paged_attention_workspace",
-              nv.load_library().nvfp4_paged_attention_workspace(q_heads, kv_heads, head_dim, ctypes.addressof(out)))
+    _nv._check("nvfp4_paged_attention_workspace",
+               _nv.load_library().nvfp4_paged_attention_workspace(q_heads, kv_heads, head_dim, ctypes.addressof(out)))
     return out.value
 
 
@@ -216,9 +261,10 @@ def nvfp4_paged_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, se
     nvfp4_paged_attention_workspace() bytes that no other running call uses;
     by default one comes from torch's allocator for this call.  Returns out.
     """
-    nv = _base()
-    torch = nv._torch()
-    out = _new(q.shape, q.dtype, q) if out is None else out
+    if _nv is None:
+        _load()
+    if out is None:
+        out = _new(q.shape, q.dtype, q, stream)
     pq, q_token, q_head = _heads(q, "q")
     po, o_token, o_head = _heads(out, "out", q)
     n, heads, dim = q.shape
@@ -226,24 +272,24 @@ def nvfp4_paged_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, se
     pages, kv_heads, page_size, d = k_cache.shape
     if d != dim:
         raise ValueError(f"k_cache has head_dim {d}, q has {dim}")
-    nv._scalar_f32(k_scale, "k_scale", q)
-    nv._scalar_f32(v_scale, "v_scale", q)
     table, max_pages, ld = _table(block_table, n, q)
     if lse is not None:
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (n, heads) or not lse.is_contiguous():
+        if lse.dtype is not _torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous():
             raise ValueError(f"lse must be float32 [{n}, {heads}], contiguous")
-        nv._same_device(lse, q, "lse")
+        _nv._same_device(lse, q, "lse")
     if workspace is None:
         if not q.is_cuda:
             raise ValueError("nvfp4_paged_attention needs GPU tensors")
-        with torch.cuda.device(q.device), torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        with _torch.cuda.device(q.device):
             size = nvfp4_paged_attention_workspace(heads, kv_heads, dim)
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        workspace = _new((size,), _torch.uint8, q, stream)
+    elif workspace.dtype is not _torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
-    nv._same_device(workspace, q, "workspace")
-    _call("nvfp4_paged_attention", q, stream, n, heads, kv_heads, dim, nv._dtype_code(q.dtype), pq, q_token, q_head,
-          ck, cv, pages, page_size, k_scale.data_ptr(), v_scale.data_ptr(), table, max_pages, ld,
-          _ints(seq_lens, (n,), "seq_lens", q), dim ** -0.5 if softmax_scale is None else softmax_scale, window, po,
-          o_token, o_head, None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
+    elif workspace.get_device() != q.get_device():
+        _nv._same_device(workspace, q, "workspace")
+    _call("nvfp4_paged_attention", q, stream,
+          (n, heads, kv_heads, dim, _nv._dtype_code(q.dtype), pq, q_token, q_head, ck, cv, pages, page_size,
+           _scale(k_scale, "k_scale", q), _scale(v_scale, "v_scale", q), table, max_pages, ld,
+           _ints(seq_lens, (n,), "seq_lens", q), dim ** -0.5 if softmax_scale is None else softmax_scale, window, po,
+           o_token, o_head, None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel()))
     return out
