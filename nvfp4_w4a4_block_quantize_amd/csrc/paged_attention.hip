@@ -7,22 +7,30 @@
 // matrix units do in the time that HBM takes to deliver them.  The kernel is
 // built to keep loads in flight and little else.
 //
-// Work.  Each (sequence, KV head) is an item of ceil(tokens / 128) units.  The
-// units of all items lie on one axis and the grid's workers take equal
-// consecutive runs of it, whatever the lengths: a run covers the end of one
-// item, whole items, and the beginning of another.  Whole items are finished in
-// place.  Of the others each worker leaves a partial result (maximum, sum,
+// Work.  Each (sequence, KV head) is an item of ceil(tokens / 128) units, and one
+// more for what beginning and ending it costs.  The units of all items lie on
+// one axis and the grid's workers take equal consecutive runs of it, whatever
+// the lengths: a run covers the end of one item, whole items, and the beginning
+// of another.  Whole items are finished in place.  Of the others each worker leaves a partial result (maximum, sum,
 // unnormalised output; at most two of them), and a second, small kernel joins
 // those.  Lengths are read on the device, so a captured graph follows them.
 //
-// A unit is one tile of 32 tokens for each of the workgroup's four waves, which
+// In a unit the workgroup's four waves take tiles of 32 tokens in turn and
 // run on their own (maxima, sums and outputs of their own) until the item ends.
 // Nothing passes through LDS or between lanes on the way of the data:
 //  * S^T = K Q^T with v_mfma_16x16x32.  Lane (i = lane % 16, g = lane / 16) of
 //    the K operand loads 16 consecutive bytes of one token's row, for two steps
-//    of the product; Q is held in registers in the same order of d.  Row i of
-//    the tile's product T (0, 1) is token 8 (i / 4) + 4 T + i % 4, so that the
-//    lane's eight results are the tokens 8 g .. 8 g + 7 of query i,
+//    of the product; Q is held in registers in the same order of d.  A load
+//    should cover whole 128-byte lines of the rows that it touches, but the
+//    operand's rows are 16 with 64 bytes each.  So lanes 2 i and 2 i + 1 take the
+//    two halves of one token's line, the operand meets the queries' first halves
+//    in one product and the second halves in another, and a token's score is the
+//    sum of the first one's even row and the second one's odd row (half of what
+//    the matrix unit does is thrown away; it has the time).  Four products j = 0
+//    .. 3 make a tile; row i of product j is token 8 (i / 4) + 2 j + i / 2 % 2.
+//    Where 64 bytes of a row remain (head_dim 64, 192), row i of the products j =
+//    0, 1 is token 8 (i / 4) + 4 j + i % 4.  Either way a lane's eight scores are
+//    the tokens 8 g .. 8 g + 7 of query i,
 //  * which is just what O^T = V^T P^T wants of it as P^T operand.  For V^T the
 //    lane loads D/16 bytes of those eight tokens' rows; after the exact
 //    conversion to fp16 one v_perm for two values turns token pairs together.
@@ -49,7 +57,8 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 32;                  // tokens of a wave's tile
-constexpr int kUnitTokens = kTile * kWaves;
+constexpr int kUnitTokens = kTile * kWaves;  // the smallest unit
+constexpr int kItemCost = 1;  // what beginning and ending an item costs, in units
 constexpr int kMaxWorkersPerCu = 4;
 constexpr float kNoMax = -3.0e38f;         // a maximum before any score; finite, so differences are numbers
 constexpr float kShift = 12.0f, kSlack = 3.0f;
@@ -61,7 +70,8 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 // rows of a worker's partial results, and where they lie in the workspace
 struct Partials {
-  int4* tail;    // [workers] {sequence or -1, item of the sequence, last worker of the item, 0}
+  int4* split;   // items that several workers share: {sequence or -1, item of it, first worker, last worker},
+                 // one entry for each item (by_item) or for each worker (the item that it leaves unfinished)
   float2* ml;    // [2 workers][rows] maximum and sum
   float* o;      // [2 workers][rows][D]
 };
@@ -73,6 +83,8 @@ struct Params {
   int parts;      // items that a KV head's queries are split into
   int rows;       // query heads of an item
   int items;      // of a sequence: kv_heads * parts
+  bool by_item;   // how `split` is indexed: by item where there are no more of them than workers
+  bool whole;     // items are not split, and count the same on the axis of work
   int64_t page_bytes;
   Partials ws;
 };
@@ -98,15 +110,30 @@ __device__ __forceinline__ void store4(const PagedAttentionArgs& a, int seq, int
   *reinterpret_cast<Four*>(p) = Four{{(T)v.x, (T)v.y, (T)v.z, (T)v.w}};
 }
 
-__device__ __forceinline__ int4 seq_span(const PagedAttentionArgs& a, int seq) {
+// {tokens, first seen token, where tiles begin, units} of a sequence
+__device__ __forceinline__ int4 seq_span(const Params& p, int seq) {
+  const PagedAttentionArgs& a = p.a;
   const int64_t most = (int64_t)a.max_pages * a.page_size;
   const int len = (int)min((int64_t)max(a.seq_lens[seq], 0), most);
   const int start = a.window > 0 && a.window < len ? len - (int)a.window : 0;
-  const int origin = start & ~7;  // where tiles begin: groups of eight tokens share a page
+  const int origin = start & ~7;  // groups of eight tokens share a page
   return make_int4(len, start, origin, (len - origin + kUnitTokens - 1) / kUnitTokens);
 }
 
+// a sequence's length on the axis of work
+__device__ __forceinline__ int64_t cost(const Params& p, int seq) {
+  const int units = seq_span(p, seq).w;
+  return units > 0 ? (int64_t)(p.whole ? 1 : units + kItemCost) * p.items : 0;
+}
+
 #if defined(__HIP_DEVICE_COMPILE__)
+
+// a value that all lanes hold, known as such to the compiler (it came through LDS or a vector load)
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = uniform((int)(uint32_t)v), hi = uniform((int)(uint32_t)((uint64_t)v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
 
 // eight matrix operands of a lane: E4M3 bytes as bf16 or fp16 (exact in both)
 template <int DT>
@@ -159,7 +186,6 @@ struct Query<0> {
       }
     }
   }
-  __device__ __forceinline__ void zero() { v[0] = v[1] = v[2] = bf16x8_t{}; }
 };
 template <>
 struct Query<1> {
@@ -168,7 +194,6 @@ struct Query<1> {
   __device__ __forceinline__ void load(const void* q, int64_t e) {
     v[0] = *reinterpret_cast<const bf16x8_t*>(static_cast<const __bf16*>(q) + e);
   }
-  __device__ __forceinline__ void zero() { v[0] = bf16x8_t{}; }
 };
 template <>
 struct Query<2> {
@@ -177,21 +202,30 @@ struct Query<2> {
   __device__ __forceinline__ void load(const void* q, int64_t e) {
     v[0] = *reinterpret_cast<const half8_t*>(static_cast<const _Float16*>(q) + e);
   }
-  __device__ __forceinline__ void zero() { v[0] = half8_t{}; }
 };
 
 template <int D>
 struct Rows {  // a wave's tile of K and V as loaded
-  u32x4_t k[2][D / 64];
+  static constexpr int kLines = D / 128, kRest = D % 128 / 64;  // of a row: whole lines, and whether half a one remains
+  u32x4_t k[4][kLines > 0 ? kLines : 1], k_rest[2];
   uint32_t v[8][D / 64];
 };
 
+// p: the first of the eight tokens that this lane's row of the products counts
 template <int D>
-__device__ __forceinline__ void load_k(Rows<D>& r, const uint8_t* p) {
+__device__ __forceinline__ void load_k(Rows<D>& r, const uint8_t* p, int col, int grp) {
+  const uint8_t* line = p + (col >> 1 & 1) * D + (col & 1) * 64 + grp * 16;
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int s = 0; s < D / 64; ++s) r.k[t][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p + t * 4 * D + s * 64));
+    for (int s = 0; s < Rows<D>::kLines; ++s)
+      r.k[j][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(line + 2 * j * D + s * 128));
+  if constexpr (Rows<D>::kRest) {
+    const uint8_t* rest = p + (col & 3) * D + (D - 64) + grp * 16;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      r.k_rest[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(rest + 4 * j * D));
+  }
 }
 
 template <int D>
@@ -224,9 +258,17 @@ struct Place {
 
 #endif
 
+// Workgroups that a CU holds (waves per SIMD), by what the registers and the LDS hold.
+template <int DT, int D, int NQ>
+constexpr int workers_per_cu() {
+  if (NQ == 2) return D == 64 ? 2 : 1;
+  if (DT == 0) return D == 64 ? 3 : D == 128 ? 2 : 1;
+  return D == 64 ? 4 : 2;
+}
+
 // NQ: 16-column tiles of queries (an item has at most 16 NQ query heads)
 template <int DT, int D, int NQ>
-__global__ __launch_bounds__(kThreads, (DT == 0 || NQ == 2) ? 1 : 2) void paged_attention_kernel(Params p) {
+__global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged_attention_kernel(Params p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int KS = D / 64, ND = D / 16, VB = D / 16, VW = D / 64;
   constexpr int PP = DT == 1 ? 1 : 2;  // parts of a probability: what the output type can tell
@@ -237,7 +279,7 @@ __global__ __launch_bounds__(kThreads, (DT == 0 || NQ == 2) ? 1 : 2) void paged_
   __shared__ int64_t lds_first[2];
 
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = uniform(tid >> 6);
   const int col = lane & 15, grp = lane >> 4;
   const int worker = blockIdx.x, n = a.n_seqs;
 
@@ -247,7 +289,7 @@ __global__ __launch_bounds__(kThreads, (DT == 0 || NQ == 2) ? 1 : 2) void paged_
   int64_t mine = 0;
   for (int i = 0; i < per; ++i) {
     const int s = tid * per + i;
-    if (s < n) mine += (int64_t)seq_span(a, s).w * p.items;
+    if (s < n) mine += cost(p, s);
   }
   int64_t upto = mine;
 #pragma unroll
@@ -264,22 +306,27 @@ __global__ __launch_bounds__(kThreads, (DT == 0 || NQ == 2) ? 1 : 2) void paged_
     units += lds_sum[w];
   }
   upto += before;
+  units = uniform(units);
   const int64_t workers = min((int64_t)gridDim.x, units);
 
   // rows that see no token belong to no item
-  for (int s = worker; s < n; s += gridDim.x) {
-    if (seq_span(a, s).w > 0) continue;
-    for (int i = tid; i < a.q_heads * (D / 4); i += kThreads) {
-      const int h = i / (D / 4);
-      store4<DT>(a, s, h, (i - h * (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+  auto clear = [&] {
+    for (int s = worker; s < n; s += gridDim.x) {
+      if (seq_span(p, s).w > 0) continue;
+      for (int i = tid; i < a.q_heads * (D / 4); i += kThreads) {
+        const int h = i / (D / 4);
+        store4<DT>(a, s, h, (i - h * (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+      }
+      if (a.lse)
+        for (int h = tid; h < a.q_heads; h += kThreads) a.lse[(int64_t)s * a.q_heads + h] = -INFINITY;
+      if (p.by_item)
+        for (int i = tid; i < p.items; i += kThreads) p.ws.split[s * p.items + i] = make_int4(-1, 0, 0, 0);
     }
-    if (a.lse)
-      for (int h = tid; h < a.q_heads; h += kThreads) a.lse[(int64_t)s * a.q_heads + h] = -INFINITY;
-  }
-
-  int4 tail = make_int4(-1, 0, 0, 0);
+  };
+  int4 split = make_int4(-1, 0, 0, 0);
   if (worker >= workers) {
-    if (tid == 0) p.ws.tail[worker] = tail;
+    if (!p.by_item && tid == 0) p.ws.split[worker] = split;
+    clear();
     return;
   }
   int64_t u = worker * units / workers;
@@ -287,55 +334,44 @@ __global__ __launch_bounds__(kThreads, (DT == 0 || NQ == 2) ? 1 : 2) void paged_
   if (mine > 0 && upto - mine <= u && u < upto) {
     int64_t at = upto - mine;
     int s = tid * per;
-    for (int64_t c; at + (c = (int64_t)seq_span(a, s).w * p.items) <= u; at += c) ++s;
+    for (int64_t c; at + (c = cost(p, s)) <= u; at += c) ++s;
     lds_first[0] = s;
     lds_first[1] = u - at;
   }
   __syncthreads();
-  int seq = __builtin_amdgcn_readfirstlane((int)lds_first[0]);
-  int64_t inside = lds_first[1];  // units of this sequence that lie before the run
+  int seq = uniform((int)lds_first[0]);
+  int64_t inside = uniform(lds_first[1]);  // how far into this sequence the run begins
 
   const float ks = *a.k_scale, inv_vs = 1.0f / *a.v_scale;
   const double c64 = (double)a.softmax_scale * 1.44269504088896340736 / (double)ks;
   const float c_hi = (float)c64, c_lo = DT == 0 ? (float)(c64 - (double)c_hi) : 0.0f;
 
+  const int group_k = col >> 2;
   while (u < u_end) {
-    const int4 span = seq_span(a, seq);
-    const int len = span.x, start = span.y, origin = span.z, per_item = span.w;
+    const int4 span = seq_span(p, seq);
+    const int len = uniform(span.x), start = uniform(span.y), origin = uniform(span.z), per_item = uniform(span.w);
     if (per_item == 0) {
       ++seq;
       continue;
     }
-    const int item = (int)(inside / per_item);
-    const int unit0 = (int)(inside - (int64_t)item * per_item);
-    const int unit1 = (int)min((int64_t)per_item, unit0 + (u_end - u));
+    // the run's part in this item
+    const int length = p.whole ? 1 : per_item + kItemCost;
+    const int item = (int)((uint32_t)inside / (uint32_t)length), from = (int)inside - item * length;
+    const int take = (int)min((int64_t)(length - from), u_end - u);
+    const int unit0 = max(from - kItemCost, 0), unit1 = p.whole ? per_item : from + take - kItemCost;
+    const int64_t begin = u - from;
+    u += take;
+    inside += take;
+    const int in = seq;
+    if (inside == (int64_t)length * p.items) {
+      inside = 0;
+      ++seq;
+    }
+    if (unit1 <= unit0) continue;
     const int head = item / p.parts, q0 = (item - head * p.parts) * p.rows;
     const int rows = min(p.rows, p.group - q0);
 
-    Query<DT> q[NQ][2 * KS];
-#pragma unroll
-    for (int t = 0; t < NQ; ++t) {
-      const int row = t * 16 + col;
-      const int64_t e = seq * a.q.token + (int64_t)(head * p.group + q0 + min(row, rows - 1)) * a.q.head;
-#pragma unroll
-      for (int s = 0; s < 2 * KS; ++s) {
-        q[t][s].load(a.q.p, e + (s >> 1) * 64 + grp * 16 + (s & 1) * 8);
-        if (row >= rows) q[t][s].zero();
-      }
-    }
-
-    float m[NQ], l[NQ];
-    float4_t o[NQ][ND];
-#pragma unroll
-    for (int t = 0; t < NQ; ++t) {
-      m[t] = kNoMax;
-      l[t] = 0.f;
-#pragma unroll
-      for (int i = 0; i < ND; ++i) o[t][i] = float4_t{0.f, 0.f, 0.f, 0.f};
-    }
-
-    const int32_t* table = a.block_table + seq * a.ld_table;
-    const int group_k = col >> 2;
+    const int32_t* table = a.block_table + in * a.ld_table;
     auto find = [&](int tile) {
       Place w;
       const uint32_t tk = origin + tile * kTile + 8 * group_k, tv = origin + tile * kTile + 8 * grp;
@@ -354,32 +390,77 @@ __global__ __launch_bounds__(kThreads, (DT == 0 || NQ == 2) ? 1 : 2) void paged_
     const int tiles = (len - origin + kTile - 1) / kTile;
     const int tile_end = min(unit1 * kWaves, tiles);
     int tile = unit0 * kWaves + wave;
+    Place now = find(tile), next = find(tile + kWaves);
+
+    Query<DT> q[NQ][2 * KS];
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) {
+      const int64_t e = in * a.q.token + (int64_t)(head * p.group + q0 + min(t * 16 + col, rows - 1)) * a.q.head;
+#pragma unroll
+      for (int s = 0; s < 2 * KS; ++s) q[t][s].load(a.q.p, e + (s >> 1) * 64 + grp * 16 + (s & 1) * 8);
+    }
+    float m[NQ], l[NQ];
+    float4_t o[NQ][ND];
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) {
+      m[t] = kNoMax;
+      l[t] = 0.f;
+#pragma unroll
+      for (int i = 0; i < ND; ++i) o[t][i] = float4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
     if (tile < tile_end) {
+      // the next tile's rows are under way before the present ones' results are used
       Rows<D> r;
-      Place now = find(tile), next = find(tile + kWaves);
-      load_k(r, row(a.k_cache, now.entry_k, now.off_k + (col & 3)) + grp * 16);
+      load_k(r, row(a.k_cache, now.entry_k, now.off_k), col, grp);
       load_v(r, row(a.v_cache, now.entry_v, now.off_v) + col * VB);
       while (true) {
         const int token = origin + tile * kTile + 8 * grp;  // the first of this lane's eight
         const bool here = (uint32_t)now.entry_v < (uint32_t)a.num_pages;
         const bool more = tile + kWaves < tile_end;
 
-        float4_t s[NQ][2];
+        float s[NQ][8];  // of this lane's eight tokens
 #pragma unroll
-        for (int t = 0; t < NQ; ++t) s[t][0] = s[t][1] = float4_t{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < 4; ++j) {
+          float4_t lo[NQ] = {}, hi[NQ] = {};
 #pragma unroll
-        for (int i = 0; i < 2 * KS; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const auto k = k_operand<DT>(r.k[h][i >> 1][2 * (i & 1)], r.k[h][i >> 1][2 * (i & 1) + 1]);
+          for (int i = 0; i < 2 * Rows<D>::kLines; ++i) {
+            const auto k = k_operand<DT>(r.k[j][i >> 1][2 * (i & 1)], r.k[j][i >> 1][2 * (i & 1) + 1]);
+            const int at = 4 * (i >> 1) + (i & 1);  // of the row's 16-byte pieces: this lane's in its half of the line
 #pragma unroll
             for (int t = 0; t < NQ; ++t)
 #pragma unroll
-              for (int part = Query<DT>::parts - 1; part >= 0; --part) s[t][h] = mfma(k, q[t][i].v[part], s[t][h]);
+              for (int part = Query<DT>::parts - 1; part >= 0; --part) {
+                lo[t] = mfma(k, q[t][at].v[part], lo[t]);
+                hi[t] = mfma(k, q[t][at + 2].v[part], hi[t]);
+              }
           }
-        if (more) {
-          load_k(r, row(a.k_cache, next.entry_k, next.off_k + (col & 3)) + grp * 16);
+#pragma unroll
+          for (int t = 0; t < NQ; ++t) {
+            s[t][2 * j] = lo[t][0] + hi[t][1];
+            s[t][2 * j + 1] = lo[t][2] + hi[t][3];
+          }
         }
+        if constexpr (Rows<D>::kRest) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float4_t sum[NQ] = {};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const auto k = k_operand<DT>(r.k_rest[j][2 * i], r.k_rest[j][2 * i + 1]);
+#pragma unroll
+              for (int t = 0; t < NQ; ++t)
+#pragma unroll
+                for (int part = Query<DT>::parts - 1; part >= 0; --part)
+                  sum[t] = mfma(k, q[t][2 * KS - 2 + i].v[part], sum[t]);
+            }
+#pragma unroll
+            for (int t = 0; t < NQ; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[t][4 * j + i] += sum[t][i];
+          }
+        }
+        if (more) load_k(r, row(a.k_cache, next.entry_k, next.off_k), col, grp);
 
         const bool whole = origin + tile * kTile >= start && origin + (tile + 1) * kTile <= len;
         uint32_t seen = 0xFF;  // of this lane's tokens
@@ -392,7 +473,7 @@ __global__ __launch_bounds__(kThreads, (DT == 0 || NQ == 2) ? 1 : 2) void paged_
           for (int t = 0; t < NQ; ++t)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              if (!(seen >> j & 1)) s[t][j >> 2][j & 3] = -INFINITY;
+              if (!(seen >> j & 1)) s[t][j] = -INFINITY;
           // rows behind the last token hold anything, NaN among it
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -403,8 +484,10 @@ __global__ __launch_bounds__(kThreads, (DT == 0 || NQ == 2) ? 1 : 2) void paged_
         half8_t pr[NQ][PP];
 #pragma unroll
         for (int t = 0; t < NQ; ++t) {
-          float top = fmaxf(fmaxf(fmaxf(s[t][0][0], s[t][0][1]), fmaxf(s[t][0][2], s[t][0][3])),
-                            fmaxf(fmaxf(s[t][1][0], s[t][1][1]), fmaxf(s[t][1][2], s[t][1][3]))) * c_hi;
+          float top = s[t][0];
+#pragma unroll
+          for (int j = 1; j < 8; ++j) top = fmaxf(top, s[t][j]);
+          top *= c_hi;
           if (__any(top > m[t] + kSlack)) {
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
@@ -418,7 +501,7 @@ __global__ __launch_bounds__(kThreads, (DT == 0 || NQ == 2) ? 1 : 2) void paged_
           const float base = kShift - m[t];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float sj = s[t][j >> 2][j & 3];
+            const float sj = s[t][j];
             float e;
             if constexpr (DT == 0)
               e = __builtin_amdgcn_exp2f(fmaf(sj, c_hi, seen >> j & 1 ? fmaf(sj, c_lo, base) : base));
@@ -506,9 +589,9 @@ __global__ __launch_bounds__(kThreads, (DT == 0 || NQ == 2) ? 1 : 2) void paged_
         if (ends) {
           const int h = head * p.group + q0 + in_item;
           const float by = total > 0.f ? inv_vs / total : 0.f;
-          store4<DT>(a, seq, h, d, make_float4(v[0] * by, v[1] * by, v[2] * by, v[3] * by));
+          store4<DT>(a, in, h, d, make_float4(v[0] * by, v[1] * by, v[2] * by, v[3] * by));
           if (a.lse && d == 0)
-            a.lse[(int64_t)seq * a.q_heads + h] = total > 0.f ? (high - kShift + log2f(total)) * kLn2 : -INFINITY;
+            a.lse[(int64_t)in * a.q_heads + h] = total > 0.f ? (high - kShift + log2f(total)) * kLn2 : -INFINITY;
         } else {
           const int64_t at = (int64_t)slot * p.rows + in_item;
           *reinterpret_cast<float4_t*>(p.ws.o + at * D + d) = v;
@@ -516,100 +599,117 @@ __global__ __launch_bounds__(kThreads, (DT == 0 || NQ == 2) ? 1 : 2) void paged_
         }
       }
     }
-    if (unit0 == 0 && !ends) {
+    if (unit0 == 0) {
       // the item's last unit is that of the first worker whose run ends behind it
-      const int64_t behind = u + per_item;
-      tail = make_int4(seq, item, (int)((behind * workers + units - 1) / units) - 1, 0);
-    }
-    u += unit1 - unit0;
-    inside += unit1 - unit0;
-    if (inside == (int64_t)per_item * p.items) {
-      inside = 0;
-      ++seq;
+      if (!ends) split = make_int4(in, item, worker, (int)(((begin + length) * workers + units - 1) / units) - 1);
+      if (p.by_item && tid == 0) p.ws.split[in * p.items + item] = split;
     }
   }
-  if (tid == 0) p.ws.tail[worker] = tail;
+  if (!p.by_item && tid == 0) p.ws.split[worker] = split;
+  clear();
 #endif
 }
 
-// Joins the partial results of one query head of the item that begins in worker
-// blockIdx.x and does not end there: the worker's second one and the first ones
-// of the workers up to the item's last.
+// Joins the partial results of a shared item: its first worker's second one and
+// the first ones of the workers up to its last.  blockIdx.x is the entry of
+// `split`, blockIdx.y a query head of the item and a slice of its outputs:
+// `lanes` lanes, four outputs each.
+constexpr int kJoinThreads = 256, kJoinWaves = kJoinThreads / 64;
+
 template <int DT, int D>
-__global__ __launch_bounds__(kThreads) void paged_attention_join(Params p, int max_workers) {
+__global__ __launch_bounds__(kJoinThreads) void paged_attention_join(Params p, int lanes) {
   const PagedAttentionArgs& a = p.a;
-  extern __shared__ float weights[];  // [max_workers]
-  __shared__ float4 lds_o[kThreads];
-  __shared__ float lds_r[2][kWaves];
-  const int worker = blockIdx.x, row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int4 tail = p.ws.tail[worker];
-  if (tail.x < 0) return;
-  const int seq = tail.x, head = tail.y / p.parts, q0 = (tail.y - head * p.parts) * p.rows;
+  extern __shared__ float weights[];  // [workers]
+  __shared__ float4 lds_o[kJoinThreads];
+  __shared__ float lds_r[2][kJoinWaves];
+  const int4 split = p.ws.split[blockIdx.x];
+  if (split.x < 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int slices = D / 4 / lanes, row = blockIdx.y / slices, slice = blockIdx.y - row * slices;
+  const int seq = split.x, head = split.y / p.parts, q0 = (split.y - head * p.parts) * p.rows, worker = split.z;
   if (q0 + row >= p.group) return;
-  const int count = tail.z - worker + 1;
+  const int count = split.w - worker + 1;
   auto at = [&](int i) { return (int64_t)(i == 0 ? 2 * worker + 1 : 2 * (worker + i)) * p.rows + row; };
 
-  float top = kNoMax;
-  for (int i = tid; i < count; i += kThreads) top = fmaxf(top, p.ws.ml[at(i)].x);
+  constexpr int kDeep = 16;  // loads of a lane in flight
+  const int sets = kJoinThreads / lanes;  // partial results that are read side by side
+  const int set = tid / lanes, in_set = tid - set * lanes, d = (slice * lanes + in_set) * 4;
+  float4 x[kDeep];
+  auto fetch = [&](int i) {
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    for (int u = 0; u < kDeep; ++u)
+      if (i + u * sets < count) x[u] = *reinterpret_cast<const float4*>(p.ws.o + at(i + u * sets) * D + d);
+  };
+  if (set < sets) fetch(set);  // needs no weights yet
+
+  float top = kNoMax;
+  for (int i = tid; i < count; i += kJoinThreads) top = fmaxf(top, p.ws.ml[at(i)].x);
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
   if (lane == 0) lds_r[0][wave] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_r[0][w]);
+  for (int w = 0; w < kJoinWaves; ++w) top = fmaxf(top, lds_r[0][w]);
   float total = 0.f;
-  for (int i = tid; i < count; i += kThreads) {
+  for (int i = tid; i < count; i += kJoinThreads) {
     const float2 ml = p.ws.ml[at(i)];
     const float f = exp2f(ml.x - top);
     weights[i] = f;
     total += ml.y * f;
   }
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) total += __shfl_xor(total, d);
+  for (int s = 32; s > 0; s >>= 1) total += __shfl_xor(total, s);
   if (lane == 0) lds_r[1][wave] = total;
   __syncthreads();
   total = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) total += lds_r[1][w];
+  for (int w = 0; w < kJoinWaves; ++w) total += lds_r[1][w];
 
-  constexpr int kLanes = D / 4, kSets = kThreads / kLanes;  // lanes of one partial result, and how many at a time
-  const int set = tid / kLanes, d = (tid - set * kLanes) * 4;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (set < kSets) {
-#pragma unroll 4
-    for (int i = set; i < count; i += kSets) {
-      const float4 x = *reinterpret_cast<const float4*>(p.ws.o + at(i) * D + d);
-      const float f = weights[i];
-      v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
+  if (set < sets) {
+    for (int i = set; i < count; i += sets * kDeep) {
+      if (i != set) fetch(i);
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) {
+        if (i + u * sets >= count) break;
+        const float f = weights[i + u * sets];
+        v.x += x[u].x * f; v.y += x[u].y * f; v.z += x[u].z * f; v.w += x[u].w * f;
+      }
     }
   }
   lds_o[tid] = v;
   __syncthreads();
   if (set == 0) {
-#pragma unroll
-    for (int s = 1; s < kSets; ++s) {
-      const float4 x = lds_o[s * kLanes + tid];
-      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    for (int s = 1; s < min(sets, count); ++s) {
+      const float4 y = lds_o[s * lanes + tid];
+      v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
     }
     const float by = total > 0.f ? 1.0f / *a.v_scale / total : 0.f;
     const int h = head * p.group + q0 + row;
     store4<DT>(a, seq, h, d, make_float4(v.x * by, v.y * by, v.z * by, v.w * by));
-    if (a.lse && tid == 0)
+    if (a.lse && slice == 0 && tid == 0)
       a.lse[(int64_t)seq * a.q_heads + h] = total > 0.f ? (top - kShift + log2f(total)) * kLn2 : -INFINITY;
   }
 }
 
 template <int DT, int D, int NQ>
-hipError_t launch(const Params& p, hipStream_t stream) {
+hipError_t launch(Params p, hipStream_t stream) {
   const PagedAttentionArgs& a = p.a;
-  const int workers_per_cu = (DT == 0 || NQ == 2) ? 1 : 2;
-  const int64_t item_units = ((int64_t)a.max_pages * a.page_size + kUnitTokens - 1) / kUnitTokens;
-  const int64_t most = (int64_t)a.n_seqs * p.items * item_units;
-  const int workers = (int)std::min<int64_t>((int64_t)device_cu_count() * workers_per_cu, most);
+  const int64_t units = ((int64_t)a.max_pages * a.page_size + kUnitTokens - 1) / kUnitTokens;  // of a full table row
+  const int64_t items = (int64_t)a.n_seqs * p.items;
+  // Up to 512 tokens in a table's row the longest item takes a workgroup less time than the second kernel would
+  // (64 sequences of up to 300 tokens, 8 heads of 128: 11.3 against 17.4 us; of up to 1000: 27.3 against 26.4).
+  p.whole = units <= 4;
+  const int workers = (int)std::min<int64_t>((int64_t)device_cu_count() * workers_per_cu<DT, D, NQ>(),
+                                             items * (p.whole ? 1 : units + kItemCost));
+  p.by_item = items <= workers;
   paged_attention_kernel<DT, D, NQ><<<workers, kThreads, 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || item_units == 1) return e;  // items of one unit are never split
-  paged_attention_join<DT, D><<<dim3(workers, p.rows), kThreads, workers * sizeof(float), stream>>>(p, workers);
+  if (e != hipSuccess || p.whole) return e;
+  // Few items are shared by many workers each: then slices of 64 outputs, to have more readers.
+  const int entries = p.by_item ? (int)items : workers, slices = entries * p.rows <= 64 ? D / 64 : 1;
+  paged_attention_join<DT, D><<<dim3(entries, p.rows * slices), kJoinThreads, workers * sizeof(float), stream>>>(
+      p, D / 4 / slices);
   return hipGetLastError();
 }
 
@@ -652,7 +752,7 @@ hipError_t launch_paged_attention(const PagedAttentionArgs& a, hipStream_t strea
   char* w = static_cast<char*>(a.workspace);
   p.ws.o = reinterpret_cast<float*>(w);  // 16-byte aligned pieces first
   w += workers * 2 * p.rows * 4 * (int64_t)a.head_dim;
-  p.ws.tail = reinterpret_cast<int4*>(w);
+  p.ws.split = reinterpret_cast<int4*>(w);
   w += workers * 16;
   p.ws.ml = reinterpret_cast<float2*>(w);
   switch (a.dtype) {
