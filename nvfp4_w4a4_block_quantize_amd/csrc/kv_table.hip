@@ -24,6 +24,7 @@ constexpr int kScanWaves = kScanThreads / 64;
 constexpr int kSpreadThreads = 256;
 constexpr int kPerThread = 4;       // tokens, one 16-byte store
 constexpr int kStartsInLds = 4096;  // requests whose starts a workgroup keeps in LDS
+constexpr int kOwn = 8;             // tokens of a request, at most one fresh page among them
 // Up to this many slots the scan's own workgroup spreads the tokens too, which saves the second launch.
 constexpr int kOneLaunchTokens = 8192;
 
@@ -102,34 +103,55 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
   __shared__ int64_t sums[kScanWaves];
   __shared__ int32_t lds_starts[SPREAD ? kStartsInLds + 1 : 1];
   __shared__ unsigned long long taken;
-  if (threadIdx.x == 0) taken = 0;
+  __shared__ int lds_many;  // whether some request brings more than kOwn tokens
+  if (threadIdx.x == 0) {
+    taken = 0;
+    lds_many = 0;
+  }
   const int64_t used = max(0, *a.free_used);
   int64_t tokens = 0, pages = 0;
   for (int base = 0; base < a.n_seqs; base += kScanThreads) {
     const int r = base + threadIdx.x;
     const bool in = r < a.n_seqs;
     const int64_t c = in ? a.cached_lens[r] : 0, n = in ? a.new_lens[r] : 0;
+    const int64_t limit = (int64_t)a.max_pages * a.page_size;
+    const bool valid = in && c >= 0 && n >= 0 && c + n <= limit;
+    const uint32_t up = (uint32_t)a.page_size - 1;
+    const uint32_t held = valid ? by_page.div((uint32_t)c + up) : 0;
+    int32_t* row = a.block_table + (int64_t)r * a.ld_table;
+    int page = -1;  // that the first new token continues
+    if constexpr (SPREAD) {
+      if (valid && n > 0 && held > 0) page = row[held - 1];
+    }
     int64_t sum;
     const int64_t end = tokens + block_scan(n > 0 ? n : 0, sums, sum);
     tokens += sum;
-    const int64_t limit = (int64_t)a.max_pages * a.page_size;
-    const bool fits = in && c >= 0 && n >= 0 && c + n <= limit && end <= a.max_tokens;
-    int64_t need = 0;
-    if (fits) {
-      const uint32_t up = (uint32_t)a.page_size - 1;
-      need = (int64_t)by_page.div((uint32_t)(c + n) + up) - by_page.div((uint32_t)c + up);
-    }
+    const bool fits = valid && end <= a.max_tokens;
+    const int64_t need = fits ? (int64_t)by_page.div((uint32_t)(c + n) + up) - held : 0;
     const int64_t upto = used + pages + block_scan(need, sums, sum);
     pages += sum;
     const bool served = fits && (need == 0 || upto <= a.n_free);
     if (in) {
       const int64_t start = min(end - (n > 0 ? n : 0), (int64_t)a.max_tokens);
       a.token_starts[r] = (int32_t)start;
-      if constexpr (SPREAD) {
-        if (a.n_seqs <= kStartsInLds) lds_starts[r] = (int32_t)start;
-      }
       a.seq_lens[r] = (int32_t)(served ? c + n : c);
       a.first_pages[r] = served ? (int32_t)min(upto - need, (int64_t)a.n_free) : -1;
+      if constexpr (SPREAD) {
+        if (a.n_seqs <= kStartsInLds) lds_starts[r] = (int32_t)start;
+        if (n > kOwn) {
+          lds_many = 1;
+        } else if (n > 0) {
+          int fresh = -1;
+          if (served && need > 0) row[held] = fresh = a.free_pages[upto - need];
+          const int64_t own = (int64_t)held * a.page_size;  // positions that held pages have
+          for (int i = 0; i < n && start + i < a.max_tokens; ++i) {
+            const int64_t pos = c + i, off = pos - (pos < own ? own - a.page_size : own);
+            const int p = pos < own ? page : fresh;
+            const int64_t slot = (int64_t)p * a.page_size + off;
+            a.slot_map[start + i] = served && p >= 0 && slot <= INT32_MAX ? (int32_t)slot : -1;
+          }
+        }
+      }
     }
     // whoever gets pages comes before whoever does not: the last of them says how many are gone
     const uint64_t got = __ballot(served && need > 0);
@@ -137,8 +159,8 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
       atomicMax(&taken, (unsigned long long)(upto - used));
   }
   __syncthreads();
+  const int last = (int)min(tokens, (int64_t)a.max_tokens);
   if (threadIdx.x == 0) {
-    const int32_t last = (int32_t)min(tokens, (int64_t)a.max_tokens);
     a.token_starts[a.n_seqs] = last;
     if constexpr (SPREAD) {
       if (a.n_seqs <= kStartsInLds) lds_starts[a.n_seqs] = last;
@@ -146,6 +168,10 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
     *a.free_used_out = (int32_t)(used + (int64_t)taken);
   }
   if constexpr (SPREAD) {
+    if (!lds_many) {
+      for (int64_t t = (int64_t)last + threadIdx.x; t < a.max_tokens; t += kScanThreads) a.slot_map[t] = -1;
+      return;
+    }
     __syncthreads();  // the workgroup's own global writes too are visible to it from here
     const int32_t* starts = a.n_seqs <= kStartsInLds ? lds_starts : a.token_starts;
     for (int64_t t0 = (int64_t)threadIdx.x * kPerThread; t0 < a.max_tokens; t0 += (int64_t)kScanThreads * kPerThread)

@@ -8,14 +8,17 @@
 // a pair, not to a head, so a workgroup computes the angles of its tokens once,
 // into LDS, and all heads of q and k use them.
 //
-// Bandwidth kernel: every element is read once and written once.  A workgroup
-// owns a run of consecutive items of the flat list (token, head, item of the
-// head), each thread four of them with all loads in flight before the first is
-// used (one, where few heads share an angle and four items' angles would fill
-// the LDS).  An item is two vectors of a head that turn together, or one vector
-// past rot_dim that is copied; a vector is the widest of 16, 8, 4 or 2 bytes that
-// pointers, strides and the two parts of a head allow.
+// Bandwidth kernel: every element is read once and written once.  The loads are
+// issued before the angles are computed, which hides them.  A workgroup owns a
+// run of consecutive items of the flat list (token; turning or copied; head; item
+// of the head), so that a wave's lanes do the same.  An item is two vectors of a
+// head that turn together, or one vector past rot_dim that is copied, each as
+// wide as 16 bytes and the part of the head allow, at any alignment: a part's
+// last vector ends where the part ends and shares elements with the one before
+// (both store the same values).  In place, where nothing may be turned twice, a
+// vector's width divides the part.
 #include <algorithm>
+#include <type_traits>
 
 #include "nvfp4_device.h"
 #include "kv_internal.h"
@@ -24,15 +27,16 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMore = 2;  // items of a thread, where that leaves no CU idle
 constexpr size_t kLdsMost = 32 * 1024;  // of angles in a workgroup, so that four fit a CU
 
 struct Plan {
-  int pairs;          // rot_dim / 2
-  int turn_items;     // items of a head that turn
-  int head_items;     // and with those that are copied
+  int pairs;           // rot_dim / 2
+  int turn_last, copy_last;  // where the last vector of a head's turning and copied part begins
+  uint32_t turning;    // items of a token that turn; those that are copied follow them
   uint32_t token_items;
   int64_t items;
-  FastDiv by_token, by_head;
+  FastDiv by_token, by_turn, by_copy, by_pair;  // items of a token, and of a head that turn and that are copied
 };
 
 template <int DT>
@@ -56,16 +60,28 @@ struct Elem<2> {
   static __device__ __forceinline__ _Float16 put(float v) { return (_Float16)v; }
 };
 
-// VEC elements, moved as one access; ALIGNED false: at element alignment, in as many accesses as it takes
+// VEC elements, moved as one access; ALIGNED false: at element alignment
 template <typename T, int VEC, bool ALIGNED>
 struct alignas(ALIGNED ? sizeof(T) * VEC : sizeof(T)) Pack {
   T v[VEC];
 };
 
-template <int DT, int VEC, bool ADJACENT, bool ALIGNED, int kUnroll>
+// Stores past the caches where they are as wide as that takes: the outputs of a prompt do not fit there, and
+// leave the other halves of the lines being read in place (8192 tokens, 28 heads of 256: 70 -> 47 us).
+template <typename V>
+__device__ __forceinline__ void store(void* p, const V& v) {
+  if constexpr (sizeof(V) == 16)
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, v), reinterpret_cast<u32x4_t*>(p));
+  else
+    *reinterpret_cast<V*>(p) = v;
+}
+
+// VEC, COPY: elements of a turning and of a copied vector
+template <int DT, int VEC, int COPY, bool ADJACENT, bool ALIGNED, int kUnroll>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Plan p) {
   typedef typename Elem<DT>::type T;
   typedef Pack<T, VEC, ALIGNED> V;
+  typedef Pack<T, COPY, ALIGNED> C;
   constexpr int kItems = kThreads * kUnroll;
   extern __shared__ float2 turns[];  // [token of this workgroup][pair] cosine and sine
 
@@ -75,18 +91,8 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Plan p) {
   const int count = (int)min((int64_t)kItems, p.items - item0);
   const int tokens = (int)(p.by_token.div(skip + count - 1)) + 1;
 
-  constexpr double kPerTurn = 0.15915494309189533576888;  // 1 / (2 pi)
-  for (int i = threadIdx.x; i < tokens * p.pairs; i += kThreads) {
-    const int t = i / p.pairs, pair = i - t * p.pairs;
-    const int axis = min(max(a.axes[pair], 0), a.n_axes - 1);
-    const double turn = (double)a.positions[axis * a.ld_pos + token0 + t] * ((double)a.inv_freq[pair] * kPerTurn);
-    float s, c;
-    sincospif((float)((turn - rint(turn)) * 2.0), &s, &c);
-    turns[i] = make_float2(c, s);
-  }
-  __syncthreads();
-
   V x[kUnroll], y[kUnroll];
+  C z[kUnroll];
   T* out[kUnroll];
   int kind[kUnroll];  // 0 nothing, 1 turn, 2 copy
   int angle[kUnroll];
@@ -98,32 +104,44 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Plan p) {
     if (n >= count) continue;
     const uint32_t at = skip + n;
     const uint32_t t = p.by_token.div(at), in_token = at - t * p.token_items;
-    uint32_t head = p.by_head.div(in_token);
-    const int item = (int)(in_token - head * p.head_items);
+    const bool turn = in_token < p.turning;
+    const uint32_t i = turn ? in_token : in_token - p.turning;
+    const FastDiv& by = turn ? p.by_turn : p.by_copy;
+    uint32_t head = by.div(i);
+    const int item = (int)(i - head * by.d);
     const bool key = head >= (uint32_t)a.q_heads;
     if (key) head -= a.q_heads;
     const HeadsIn& hi = key ? a.k : a.q;
     const HeadsOut& ho = key ? a.k_out : a.q_out;
     const int64_t token = token0 + t;
-    const T* in = static_cast<const T*>(hi.p) + token * hi.token + head * hi.head;
-    out[u] = static_cast<T*>(ho.p) + token * ho.token + head * ho.head;
-    if (item < p.turn_items) {
-      const int e = item * VEC;
-      kind[u] = 1;
-      angle[u] = (int)t * p.pairs + (ADJACENT ? e / 2 : e);
-      out[u] += e;
-      x[u] = *reinterpret_cast<const V*>(in + e);
-      if constexpr (kTwo) y[u] = *reinterpret_cast<const V*>(in + e + p.pairs);
+    const int e = turn ? min(item * VEC, p.turn_last) : min(a.rot_dim + item * COPY, p.copy_last);
+    const T* in = static_cast<const T*>(hi.p) + token * hi.token + head * hi.head + e;
+    out[u] = static_cast<T*>(ho.p) + token * ho.token + head * ho.head + e;
+    kind[u] = turn ? 1 : 2;
+    angle[u] = (int)t * p.pairs + (ADJACENT ? e / 2 : e);
+    if constexpr (COPY == VEC) {  // one load for both: a branch around it would wait for it
+      x[u] = *reinterpret_cast<const V*>(in);
     } else {
-      const int e = a.rot_dim + (item - p.turn_items) * VEC;
-      kind[u] = 2;
-      out[u] += e;
-      x[u] = *reinterpret_cast<const V*>(in + e);
+      if (turn) x[u] = *reinterpret_cast<const V*>(in);
+      else z[u] = *reinterpret_cast<const C*>(in);
+    }
+    if constexpr (kTwo) {
+      if (turn) y[u] = *reinterpret_cast<const V*>(in + p.pairs);
     }
   }
+  constexpr double kPerTurn = 0.15915494309189533576888;  // 1 / (2 pi)
+  for (int i = threadIdx.x; i < tokens * p.pairs; i += kThreads) {
+    const int t = (int)p.by_pair.div((uint32_t)i), pair = i - t * p.pairs;
+    const int axis = min(max(a.axes[pair], 0), a.n_axes - 1);
+    const double turn = (double)a.positions[axis * a.ld_pos + token0 + t] * ((double)a.inv_freq[pair] * kPerTurn);
+    float s, c;
+    sincospif((float)((turn - rint(turn)) * 2.0), &s, &c);
+    turns[i] = make_float2(c, s);
+  }
+  __syncthreads();
+
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    if (kind[u] == 0) continue;
     if (kind[u] == 1) {
       if constexpr (kTwo) {
 #pragma unroll
@@ -133,7 +151,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Plan p) {
           x[u].v[i] = Elem<DT>::put(p0 * cs.x - p1 * cs.y);
           y[u].v[i] = Elem<DT>::put(p1 * cs.x + p0 * cs.y);
         }
-        *reinterpret_cast<V*>(out[u] + p.pairs) = y[u];
+        store<V>(out[u] + p.pairs, y[u]);
       } else {
 #pragma unroll
         for (int i = 0; i < VEC / 2; ++i) {
@@ -143,73 +161,87 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Plan p) {
           x[u].v[2 * i + 1] = Elem<DT>::put(p1 * cs.x + p0 * cs.y);
         }
       }
+      store<V>(out[u], x[u]);
+    } else if (kind[u] == 2) {
+      if constexpr (COPY == VEC) store<V>(out[u], x[u]);
+      else store<C>(out[u], z[u]);
     }
-    *reinterpret_cast<V*>(out[u]) = x[u];
   }
 }
 
-template <int DT, int VEC, bool ADJACENT, bool ALIGNED = true>
+bool in_place(const RopeArgs& a) { return a.q_out.p == a.q.p && (a.k_heads == 0 || a.k_out.p == a.k.p); }
+
+template <int DT, int VEC, int COPY, bool ADJACENT, bool ALIGNED>
 hipError_t launch_vec(const RopeArgs& a, hipStream_t stream) {
-  const bool in_place = a.q_out.p == a.q.p && (a.k_heads == 0 || a.k_out.p == a.k.p);
   Plan p;
   p.pairs = a.rot_dim / 2;
-  p.turn_items = (ADJACENT ? a.rot_dim : p.pairs) / VEC;
-  p.head_items = p.turn_items + (in_place ? 0 : (a.head_dim - a.rot_dim) / VEC);
-  p.token_items = (uint32_t)(a.q_heads + a.k_heads) * (uint32_t)p.head_items;
+  const uint32_t heads = (uint32_t)(a.q_heads + a.k_heads);
+  const int turn = ADJACENT ? a.rot_dim : p.pairs, copy = in_place(a) ? 0 : a.head_dim - a.rot_dim;
+  p.turn_last = turn - VEC;
+  p.copy_last = a.head_dim - COPY;
+  p.by_turn = FastDiv((uint32_t)(turn + VEC - 1) / VEC);
+  p.by_copy = FastDiv((uint32_t)(copy + COPY - 1) / COPY);
+  p.turning = heads * p.by_turn.d;
+  p.token_items = p.turning + heads * p.by_copy.d;
   p.items = a.tokens * (int64_t)p.token_items;
   p.by_token = FastDiv(p.token_items);
-  p.by_head = FastDiv((uint32_t)p.head_items);
+  p.by_pair = FastDiv((uint32_t)p.pairs);
   // a run of n items that begins and ends inside a token touches at most this many tokens
   auto lds = [&](int64_t n) {
     return (size_t)std::min<int64_t>(a.tokens, (n - 2) / p.token_items + 2) * p.pairs * sizeof(float2);
   };
-  const bool four = lds(4 * kThreads) <= kLdsMost;
-  const int64_t n = four ? 4 * kThreads : kThreads, blocks = (p.items + n - 1) / n;
+  const bool more = lds(kMore * kThreads) <= kLdsMost && p.items >= (int64_t)device_cu_count() * kMore * kThreads;
+  const int64_t n = more ? kMore * kThreads : kThreads, blocks = (p.items + n - 1) / n;
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  if (four)
-    rope_kernel<DT, VEC, ADJACENT, ALIGNED, 4><<<(unsigned)blocks, kThreads, lds(n), stream>>>(a, p);
+  if (more)
+    rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, kMore><<<(unsigned)blocks, kThreads, lds(n), stream>>>(a, p);
   else
-    rope_kernel<DT, VEC, ADJACENT, ALIGNED, 1><<<(unsigned)blocks, kThreads, lds(n), stream>>>(a, p);
+    rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, 1><<<(unsigned)blocks, kThreads, lds(n), stream>>>(a, p);
   return hipGetLastError();
 }
 
-// the lowest set bit of everything that a vector has to divide, in elements
-uint64_t spacing(const RopeArgs& a, int es) {
-  uint64_t m = (uint64_t)a.rot_dim | (uint64_t)a.head_dim | 16u;
-  if (!a.adjacent) m |= (uint64_t)a.rot_dim / 2;
-  m |= (uint64_t)a.q.token | (uint64_t)a.q.head | (uint64_t)a.q_out.token | (uint64_t)a.q_out.head;
-  m |= (reinterpret_cast<uintptr_t>(a.q.p) | reinterpret_cast<uintptr_t>(a.q_out.p)) / es;
-  if (a.k_heads) {
-    m |= (uint64_t)a.k.token | (uint64_t)a.k.head | (uint64_t)a.k_out.token | (uint64_t)a.k_out.head;
-    m |= (reinterpret_cast<uintptr_t>(a.k.p) | reinterpret_cast<uintptr_t>(a.k_out.p)) / es;
-  }
-  return m & (~m + 1);
-}
-
-template <int DT, int ES, bool ADJACENT>
+template <int DT, bool ADJACENT>
 hipError_t launch_widest(const RopeArgs& a, hipStream_t stream) {
-  const uint64_t by = spacing(a, ES);
-  if constexpr (ES == 2) {
-    if (by >= 8) return launch_vec<DT, 8, ADJACENT>(a, stream);
+  constexpr int ES = DT == 0 ? 4 : 2, kFull = 16 / ES;
+  const int turn = ADJACENT ? a.rot_dim : a.rot_dim / 2, copy = in_place(a) ? 0 : a.head_dim - a.rot_dim;
+  int vec = kFull;
+  while (in_place(a) ? turn % vec != 0 : vec > turn) vec /= 2;
+  const bool wide = copy == 0 || copy >= kFull;
+  uint64_t at = (uint64_t)(turn | copy) * ES;  // its lowest set bit is that of all vectors' addresses
+  for (int64_t s : {a.q.token, a.q.head, a.q_out.token, a.q_out.head}) at |= (uint64_t)s * ES;
+  at |= reinterpret_cast<uintptr_t>(a.q.p) | reinterpret_cast<uintptr_t>(a.q_out.p);
+  if (a.k_heads) {
+    for (int64_t s : {a.k.token, a.k.head, a.k_out.token, a.k_out.head}) at |= (uint64_t)s * ES;
+    at |= reinterpret_cast<uintptr_t>(a.k.p) | reinterpret_cast<uintptr_t>(a.k_out.p);
   }
-  if (by >= 4) return launch_vec<DT, 4, ADJACENT>(a, stream);
-  if (by >= 2) return launch_vec<DT, 2, ADJACENT>(a, stream);
-  // neighbours turn together even where nothing lets them move together (head_dim and rot_dim are even)
-  return launch_vec<DT, ADJACENT ? 2 : 1, ADJACENT, !ADJACENT>(a, stream);
+  if (vec == kFull && wide && at % 16 == 0) return launch_vec<DT, kFull, kFull, ADJACENT, true>(a, stream);
+  auto launch = [&](auto v) {
+    constexpr int VEC = decltype(v)::value;
+    return wide ? launch_vec<DT, VEC, kFull, ADJACENT, false>(a, stream)
+                : launch_vec<DT, VEC, 1, ADJACENT, false>(a, stream);
+  };
+  if constexpr (ES == 2) {
+    if (vec == 8) return launch(std::integral_constant<int, 8>());
+  }
+  if (vec == 4) return launch(std::integral_constant<int, 4>());
+  if constexpr (!ADJACENT) {
+    if (vec == 1) return launch(std::integral_constant<int, 1>());
+  }
+  return launch(std::integral_constant<int, 2>());  // neighbours always go together: rot_dim is even
 }
 
-template <int DT, int ES>
+template <int DT>
 hipError_t launch_typed(const RopeArgs& a, hipStream_t stream) {
-  return a.adjacent ? launch_widest<DT, ES, true>(a, stream) : launch_widest<DT, ES, false>(a, stream);
+  return a.adjacent ? launch_widest<DT, true>(a, stream) : launch_widest<DT, false>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream) {
   switch (a.dtype) {
-    case 0: return launch_typed<0, 4>(a, stream);
-    case 1: return launch_typed<1, 2>(a, stream);
-    default: return launch_typed<2, 2>(a, stream);
+    case 0: return launch_typed<0>(a, stream);
+    case 1: return launch_typed<1>(a, stream);
+    default: return launch_typed<2>(a, stream);
   }
 }
 
