@@ -8,13 +8,16 @@
 //
 // Bandwidth kernel: 2 B read and 1 B written per bf16 element.  One thread takes 16
 // consecutive elements (8 where head_dim is no multiple of 16) and stores 16
-// bytes at once, past the caches, which the rows do not fit.  More pieces a
-// thread were no faster on long prompts and slower on short calls (32 tokens, 4
-// heads of 256: 2.3 us, 3.2 with four pieces; 5003 tokens, 8 heads of 128, f16:
-// 7.0 and 8.6 us).  Rows that are too many to be in the caches are read past them
-// too (32768 tokens, 8 heads of 128, bf16: 37.5 us, 41.5 through the caches; the
-// 5003 tokens: 8.6 and 7.0) but for float32, where a lane's four loads share
-// their lines (83 us, 63 through the caches).
+// bytes at once.  More pieces a thread were no faster on long prompts and slower
+// on short calls (32 tokens, 4 heads of 256: 2.3 us, 3.2 with four pieces).
+// What goes past the caches, in us a call:           32768 x 8 x 128   5003 x 8 x
+//                                                    bf16       f32    128, f16
+//   loads (rows too many to be there)                37.5       83     8.6
+//   stores                                           41.5       62     6.6
+//   both                                             40.1       81     8.0
+//   neither                                          42.3       65     6.8
+// (a lane's four float32 loads share their lines).  So many rows of a 16-bit type
+// are loaded past them, and all others are stored past them.
 #include "nvfp4_device.h"
 #include "kv_internal.h"
 
@@ -26,7 +29,7 @@ constexpr int64_t kManyElements = 1 << 24;  // of K: 64 MiB with V, a quarter of
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
-// E elements from 16-byte loads, PAST: past the caches
+// E elements from 16-byte loads (PAST: past the caches)
 template <int DT, int E, bool PAST>
 struct Raw {
   static constexpr int kLoads = E * (DT == 0 ? 4 : 2) / 16;
@@ -63,27 +66,31 @@ __global__ __launch_bounds__(kThreads) void kv_cache_write_kernel(CacheWriteArgs
   const HeadsIn in = value ? a.v : a.k;
   const float s = value ? *a.v_scale : *a.k_scale;
   const int64_t first = (int64_t)blockIdx.x * kThreads;
-  if (first + threadIdx.x >= chunks) return;
   const int64_t token0 = first / by_row.d;  // one division for the workgroup; the rest fits 32 bits
   const uint32_t at = (uint32_t)(first - token0 * by_row.d) + threadIdx.x;
   const uint32_t t = by_row.div(at), in_row = at - t * by_row.d;
   const uint32_t head = by_head.div(in_row), chunk = in_row - head * by_head.d;
-  const int64_t token = token0 + t;
+  // no branch before the store, which would wait for what it asks (39.4 us for 37.2, 32768 tokens of 8 x 128)
+  const bool inside = first + threadIdx.x < chunks;
+  const int64_t token = inside ? token0 + t : 0;
+  const int slot = a.slot_map[token];  // asked for before the elements: loads return in order
   Raw<DT, E, PAST> raw;
   raw.load(in.p, token * in.token + head * in.head + chunk * E);
-  const int slot = a.slot_map[token];
-  if (slot < 0 || slot >= a.num_pages * a.page_size) return;
-  const uint32_t page = by_page.div((uint32_t)slot), off = (uint32_t)slot - page * by_page.d;
+  const bool there = slot >= 0 && slot < a.num_pages * a.page_size;
+  const uint32_t page = by_page.div((uint32_t)slot & 0x7FFFFFFFu), off = (uint32_t)slot - page * by_page.d;
   uint8_t* out = (value ? a.v_cache : a.k_cache) +
                  (((int64_t)page * a.kv_heads + head) * a.page_size + off) * a.head_dim + chunk * E;
   uint32_t w[E / 4];
 #pragma unroll
   for (int i = 0; i < E / 4; ++i)
     w[i] = e4m3x4(raw.get(4 * i) * s, raw.get(4 * i + 1) * s, raw.get(4 * i + 2) * s, raw.get(4 * i + 3) * s);
-  if constexpr (E == 16)
-    __builtin_nontemporal_store(u32x4_t{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4_t*>(out));
+  if (!there || !inside) return;
+  if constexpr (E == 8)
+    *reinterpret_cast<u32x2_t*>(out) = u32x2_t{w[0], w[1]};
+  else if constexpr (PAST)
+    *reinterpret_cast<u32x4_t*>(out) = u32x4_t{w[0], w[1], w[2], w[3]};
   else
-    __builtin_nontemporal_store(u32x2_t{w[0], w[1]}, reinterpret_cast<u32x2_t*>(out));
+    __builtin_nontemporal_store(u32x4_t{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4_t*>(out));
 }
 
 template <int DT, int E, bool PAST>

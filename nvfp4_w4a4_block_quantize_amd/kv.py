@@ -36,15 +36,22 @@ KV_SIGNATURES = {
 }
 
 
-_nv = _torch = None  # the package and torch, once something is called
+_nv = _torch = _int32 = None  # the package and torch, once something is called
+_device = _raw_stream = None  # torch's current device, and its current stream on one
 _fns = {}
 
 
 def _load():
-    global _nv, _torch
+    global _nv, _torch, _int32, _device, _raw_stream
     import nvfp4_w4a4_block_quantize_amd as nv
 
-    _nv, _torch = nv, nv._torch()
+    _torch = nv._torch()
+    _int32 = _torch.int32
+    # the accessors below torch's own skip its per-call initialisation check: a GPU tensor is at hand
+    _device = getattr(_torch._C, "_cuda_getDevice", _torch.cuda.current_device)
+    _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: _torch.cuda.current_stream(index).cuda_stream)
+    _nv = nv
 
 
 def _call(name, like, stream, args):
@@ -55,26 +62,28 @@ def _call(name, like, stream, args):
     index = like.get_device()
     if index < 0:
         raise ValueError(f"{name} needs GPU tensors")
-    if index == _torch.cuda.current_device():
-        status = fn(*args, _nv._stream_ptr(stream, like))
+    queue = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == _device():
+        status = fn(*args, queue)
     else:
         with _torch.cuda.device(index):
-            status = fn(*args, _nv._stream_ptr(stream, like))
+            status = fn(*args, queue)
     if status:
         _nv._check(name, status)
 
 
-def _ints(t, shape, name, like):
-    """The address of a dense int32 tensor on the device of `like`."""
-    if t.dtype is not _torch.int32:
+def _ints(t, n, name, like):
+    """The address of a dense int32 tensor [n] on the device of `like`."""
+    if t.dtype is _int32 and t.numel() == n and t.dim() == 1 and t.is_contiguous() and \
+            t.get_device() == like.get_device():
+        return t.data_ptr()
+    if t.dtype is not _int32:
         raise ValueError(f"{name} must be int32, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if tuple(t.shape) != (n,):
+        raise ValueError(f"{name} must have shape {(n,)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != like.get_device():
-        _nv._same_device(t, like, name)
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, expected {like.device}")
 
 
 def _scale(t, name, like):
@@ -95,7 +104,7 @@ def _new(shape, dtype, like, stream):
 def _table(t, rows, like):
     """A block table, int32 with unit column stride: (address, columns, row stride)."""
     shape = t.shape
-    if t.dtype is not _torch.int32 or len(shape) != 2 or shape[0] != rows:
+    if t.dtype is not _int32 or len(shape) != 2 or shape[0] != rows:
         raise ValueError(f"block_table must be int32 [{rows}, pages], got {t.dtype} {tuple(shape)}")
     ld, unit = t.stride()
     if unit != 1 and shape[1] != 1:
@@ -148,27 +157,26 @@ def nvfp4_kv_block_table(cached_lens, new_lens, page_size: int, free_pages, free
     """
     if _nv is None:
         _load()
-    i32 = _torch.int32
     n = cached_lens.shape[0] if cached_lens.dim() == 1 else -1
     if n < 0 or free_pages.dim() != 1 or slot_map.dim() != 1:
         raise ValueError("cached_lens, free_pages and slot_map must be 1-D")
     if seq_lens is None:
-        seq_lens = _new((n,), i32, cached_lens, stream)
+        seq_lens = _new((n,), _int32, cached_lens, stream)
     if token_starts is None:
-        token_starts = _new((n + 1,), i32, cached_lens, stream)
+        token_starts = _new((n + 1,), _int32, cached_lens, stream)
     if first_pages is None:
-        first_pages = _new((n,), i32, cached_lens, stream)
+        first_pages = _new((n,), _int32, cached_lens, stream)
     if free_used_out is None:
-        free_used_out = _new((1,), i32, cached_lens, stream)
+        free_used_out = _new((1,), _int32, cached_lens, stream)
     table, max_pages, ld = _table(block_table, n, cached_lens)
     n_free, tokens = free_pages.shape[0], slot_map.shape[0]
     like = cached_lens
     _call("nvfp4_kv_block_table", like, stream,
-          (n, _ints(cached_lens, (n,), "cached_lens", like), _ints(new_lens, (n,), "new_lens", like), page_size,
-           _ints(free_pages, (n_free,), "free_pages", like), n_free, _ints(free_used, (1,), "free_used", like), table,
-           max_pages, ld, _ints(slot_map, (tokens,), "slot_map", like), tokens,
-           _ints(seq_lens, (n,), "seq_lens", like), _ints(token_starts, (n + 1,), "token_starts", like),
-           _ints(first_pages, (n,), "first_pages", like), _ints(free_used_out, (1,), "free_used_out", like)))
+          (n, _ints(cached_lens, n, "cached_lens", like), _ints(new_lens, n, "new_lens", like), page_size,
+           _ints(free_pages, n_free, "free_pages", like), n_free, _ints(free_used, 1, "free_used", like), table,
+           max_pages, ld, _ints(slot_map, tokens, "slot_map", like), tokens,
+           _ints(seq_lens, n, "seq_lens", like), _ints(token_starts, n + 1, "token_starts", like),
+           _ints(first_pages, n, "first_pages", like), _ints(free_used_out, 1, "free_used_out", like)))
     return seq_lens, token_starts, first_pages, free_used_out
 
 
@@ -189,7 +197,7 @@ def nvfp4_rope(q, k, positions, inv_freq, axes, adjacent: bool = False, q_out=No
     po, o_token, o_head = _heads(q_out, "q_out", q)
     tokens, q_heads, dim = q.shape
     pos_shape, index = positions.shape, q.get_device()
-    if len(pos_shape) != 2 or positions.dtype is not _torch.int32 or pos_shape[1] != tokens:
+    if len(pos_shape) != 2 or positions.dtype is not _int32 or pos_shape[1] != tokens:
         raise ValueError(f"positions must be int32 [axes, {tokens}], got {positions.dtype} {tuple(pos_shape)}")
     ld_pos, unit = positions.stride()
     if unit != 1 and tokens != 1:
@@ -215,7 +223,7 @@ def nvfp4_rope(q, k, positions, inv_freq, axes, adjacent: bool = False, q_out=No
         raise ValueError("k_out without k")
     _call("nvfp4_rope", q, stream,
           (tokens, dim, 2 * pairs, _nv._dtype_code(q.dtype), int(adjacent), positions.data_ptr(), n_axes,
-           ld_pos if n_axes > 1 else tokens, inv_freq.data_ptr(), _ints(axes, (pairs,), "axes", q), pq, po, q_heads,
+           ld_pos if n_axes > 1 else tokens, inv_freq.data_ptr(), _ints(axes, pairs, "axes", q), pq, po, q_heads,
            q_token, q_head, o_token, o_head, *keys))
     return q_out, k_out
 
@@ -236,7 +244,7 @@ def nvfp4_kv_cache_write(k, v, k_scale, v_scale, slot_map, k_cache, v_cache, str
         raise ValueError(f"k_cache must be [pages, {heads}, page_size, {dim}], got {tuple(k_cache.shape)}")
     _call("nvfp4_kv_cache_write", k, stream,
           (tokens, heads, dim, _nv._dtype_code(k.dtype), pk, k_token, k_head, pv, v_token, v_head,
-           _scale(k_scale, "k_scale", k), _scale(v_scale, "v_scale", k), _ints(slot_map, (tokens,), "slot_map", k),
+           _scale(k_scale, "k_scale", k), _scale(v_scale, "v_scale", k), _ints(slot_map, tokens, "slot_map", k),
            ck, cv, pages, page_size))
     return k_cache, v_cache
 
@@ -290,6 +298,6 @@ def nvfp4_paged_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, se
     _call("nvfp4_paged_attention", q, stream,
           (n, heads, kv_heads, dim, _nv._dtype_code(q.dtype), pq, q_token, q_head, ck, cv, pages, page_size,
            _scale(k_scale, "k_scale", q), _scale(v_scale, "v_scale", q), table, max_pages, ld,
-           _ints(seq_lens, (n,), "seq_lens", q), dim ** -0.5 if softmax_scale is None else softmax_scale, window, po,
+           _ints(seq_lens, n, "seq_lens", q), dim ** -0.5 if softmax_scale is None else softmax_scale, window, po,
            o_token, o_head, None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel()))
     return out
