@@ -21,32 +21,32 @@
 //  * S^T = K Q^T with v_mfma_16x16x32.  Lane (i = lane % 16, g = lane / 16) of
 //    the K operand loads 16 consecutive bytes of one token's row, for two steps
 //    of the product; Q is held in registers in the same order of d.  A load
-//    should cover whole 128-byte lines of the rows that it touches, but the
-//    operand's rows are 16 with 64 bytes each.  So lanes 2 i and 2 i + 1 take the
-//    two halves of one token's line, the operand meets the queries' first halves
-//    in one product and the second halves in another, and a token's score is the
-//    sum of the first one's even row and the second one's odd row (half of what
-//    the matrix unit does is thrown away; it has the time).  Four products j = 0
-//    .. 3 make a tile; row i of product j is token 8 (i / 4) + 2 j + i / 2 % 2.
-//    Where 64 bytes of a row remain (head_dim 64, 192), row i of the products j =
-//    0, 1 is token 8 (i / 4) + 4 j + i % 4.  Either way a lane's eight scores are
-//    the tokens 8 g .. 8 g + 7 of query i,
+//    should cover whole 128-byte lines, and neighbouring rows (a wave's loads are
+//    then spread over the L2's channels), but the operand's rows are 16 with 64
+//    bytes each.  So lanes i = 2 r and 2 r + 1 take the two halves of one token's
+//    line, the operand meets the queries' first halves in one product and the
+//    second halves in another, and a token's score is the sum of the first one's
+//    even row and the second one's odd row (half of what the matrix unit does is
+//    thrown away; it has the time).  Four products j = 0 .. 3 make a tile, of 8
+//    neighbouring tokens each: row i is token 8 j + 4 (r % 2) + r / 2.  Where 64
+//    bytes of a row remain (head_dim 64, 192), row i of the products j = 0, 1 is
+//    token 16 j + 4 (i % 4) + i / 4.  Either way a lane's eight scores are those of
+//    query i with the tokens g, 4 + g, .. 28 + g,
 //  * which is just what O^T = V^T P^T wants of it as P^T operand.  For V^T the
-//    lane loads D/16 bytes of those eight tokens' rows; after the exact
-//    conversion to fp16 one v_perm for two values turns token pairs together.
-//    Row i of the product for byte n is d = i D/16 + n.
-//  * A lane's eight tokens lie in one page (page sizes are multiples of 8), so a
-//    lane needs two table entries per tile, fetched one tile ahead of the rows
-//    that they lead to.
+//    lane loads D/16 bytes of those eight tokens' rows (four neighbouring rows a
+//    load); after the exact conversion to fp16 one v_perm for two values turns
+//    token pairs together.  Row i of the product for byte n is d = i D/16 + n.
+//  * Eight neighbouring tokens lie in one page (page sizes are multiples of 8), so
+//    a tile has four addresses, the same for all lanes: they are made from scalar
+//    loads of the table, one tile ahead of the rows that they lead to.
 //
 // Softmax.  One pass with a running maximum m, a whole number of powers of two
 // that moves only when some score passes it by kSlack: p = 2^(s' + kShift - m),
 // s' = s log2(e).  m cancels in the end and being whole, its changes scale by
 // exact powers of two.  kShift puts p below 2^15, in fp16's upper range: p keeps
 // its eleven bits down to 2^-26 of the largest.
-#include <type_traits>
-
 #include <algorithm>
+#include <type_traits>
 
 #include "nvfp4_device.h"
 #include "kv_internal.h"
@@ -213,29 +213,39 @@ struct Rows {  // a wave's tile of K and V as loaded
   uint32_t v[8][D / 64];
 };
 
-// p: the first of the eight tokens that this lane's row of the products counts
+// Where a tile's four groups of eight tokens lie, the same for all lanes.
+struct Place {
+  int entry[4];  // of the table
+  int off[4];    // tokens into the page
+};
+
+// at: byte offsets of the four groups in the cache, of this head
 template <int D>
-__device__ __forceinline__ void load_k(Rows<D>& r, const uint8_t* p, int col, int grp) {
-  const uint8_t* line = p + (col >> 1 & 1) * D + (col & 1) * 64 + grp * 16;
+__device__ __forceinline__ void load_k(Rows<D>& r, const uint8_t* cache, const int64_t (&at)[4], int col, int grp) {
+  const uint32_t line = ((col >> 1 & 1) * 4 + (col >> 2)) * D + (col & 1) * 64 + grp * 16;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int s = 0; s < Rows<D>::kLines; ++s)
-      r.k[j][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(line + 2 * j * D + s * 128));
+      r.k[j][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(cache + at[j] + (line + s * 128)));
   if constexpr (Rows<D>::kRest) {
-    const uint8_t* rest = p + (col & 3) * D + (D - 64) + grp * 16;
+    const uint32_t rest = ((col & 1) * 4 + (col >> 2)) * D + (D - 64) + grp * 16;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      r.k_rest[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(rest + 4 * j * D));
+    for (int j = 0; j < 2; ++j) {
+      const int64_t second = at[2 * j + 1] - at[2 * j];  // rows 8 to 15 of the product lie in the next group
+      r.k_rest[j] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4_t*>(cache + at[2 * j] + (col & 2 ? second : 0) + rest));
+    }
   }
 }
 
 template <int D>
-__device__ __forceinline__ void load_v(Rows<D>& r, const uint8_t* p) {
+__device__ __forceinline__ void load_v(Rows<D>& r, const uint8_t* cache, const int64_t (&at)[4], int col, int grp) {
   constexpr int W = D / 64;
+  const uint32_t row = grp * D + col * (D / 16);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(p + j * D);
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(cache + at[j >> 1] + (row + (j & 1) * 4 * D));
     if constexpr (W == 1) {
       r.v[j][0] = __builtin_nontemporal_load(src);
     } else if constexpr (W == 2) {
@@ -251,12 +261,6 @@ __device__ __forceinline__ void load_v(Rows<D>& r, const uint8_t* p) {
     }
   }
 }
-
-// where a lane's rows of one tile lie
-struct Place {
-  int entry_k, entry_v;  // table entries
-  int off_k, off_v;      // tokens into the page
-};
 
 #endif
 
@@ -348,7 +352,6 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
   const double c64 = (double)a.softmax_scale * 1.44269504088896340736 / (double)ks;
   const float c_hi = (float)c64, c_lo = DT == 0 ? (float)(c64 - (double)c_hi) : 0.0f;
 
-  const int group_k = col >> 2;
   while (u < u_end) {
     const int4 span = seq_span(p, seq);
     const int len = uniform(span.x), start = uniform(span.y), origin = uniform(span.z), per_item = uniform(span.w);
@@ -373,21 +376,29 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
     const int head = item / p.parts, q0 = (item - head * p.parts) * p.rows;
     const int rows = min(p.rows, p.group - q0);
 
-    const int32_t* table = a.block_table + in * a.ld_table;
+    // scalar loads: nothing in this kernel writes to the table
+    typedef const __attribute__((address_space(4))) int32_t* ConstInts;
+    const ConstInts table = (ConstInts)(a.block_table + in * a.ld_table);
     auto find = [&](int tile) {
       Place w;
-      const uint32_t tk = origin + tile * kTile + 8 * group_k, tv = origin + tile * kTile + 8 * grp;
-      const uint32_t ck = p.by_page.div(tk), cv = p.by_page.div(tv);
-      w.off_k = tk - ck * a.page_size;
-      w.off_v = tv - cv * a.page_size;
-      // past the last token a tile may reach past the table's last column
-      w.entry_k = table[min(ck, (uint32_t)a.max_pages - 1)];
-      w.entry_v = table[min(cv, (uint32_t)a.max_pages - 1)];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t token = origin + tile * kTile + 8 * j, column = p.by_page.div(token);
+        w.off[j] = token - column * a.page_size;
+        // past the last token a tile may reach past the table's last column
+        w.entry[j] = table[min(column, (uint32_t)a.max_pages - 1)];
+      }
       return w;
     };
-    auto row = [&](const uint8_t* cache, int entry, int off) {
-      const int64_t page = (uint32_t)entry < (uint32_t)a.num_pages ? entry : 0;
-      return cache + page * p.page_bytes + ((int64_t)head * a.page_size + off) * D;
+    auto place = [&](const Place& w, int64_t (&at)[4]) {  // and whether all its pages are the cache's
+      bool good = true;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool ok = (uint32_t)w.entry[j] < (uint32_t)a.num_pages;
+        good = good && ok;
+        at[j] = (ok ? w.entry[j] : 0) * p.page_bytes + ((int64_t)head * a.page_size + w.off[j]) * D;
+      }
+      return good;
     };
     const int tiles = (len - origin + kTile - 1) / kTile;
     const int tile_end = min(unit1 * kWaves, tiles);
@@ -414,11 +425,11 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
     if (tile < tile_end) {
       // the next tile's rows are under way before the present ones' results are used
       Rows<D> r;
-      load_k(r, row(a.k_cache, now.entry_k, now.off_k), col, grp);
-      load_v(r, row(a.v_cache, now.entry_v, now.off_v) + col * VB);
+      int64_t at[4];
+      bool good = place(now, at);
+      load_k(r, a.k_cache, at, col, grp);
+      load_v(r, a.v_cache, at, col, grp);
       while (true) {
-        const int token = origin + tile * kTile + 8 * grp;  // the first of this lane's eight
-        const bool here = (uint32_t)now.entry_v < (uint32_t)a.num_pages;
         const bool more = tile + kWaves < tile_end;
 
         float s[NQ][8];  // of this lane's eight tokens
@@ -428,13 +439,13 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
 #pragma unroll
           for (int i = 0; i < 2 * Rows<D>::kLines; ++i) {
             const auto k = k_operand<DT>(r.k[j][i >> 1][2 * (i & 1)], r.k[j][i >> 1][2 * (i & 1) + 1]);
-            const int at = 4 * (i >> 1) + (i & 1);  // of the row's 16-byte pieces: this lane's in its half of the line
+            const int piece = 4 * (i >> 1) + (i & 1);  // of the row's 16-byte pieces: this lane's in its half of the line
 #pragma unroll
             for (int t = 0; t < NQ; ++t)
 #pragma unroll
               for (int part = Query<DT>::parts - 1; part >= 0; --part) {
-                lo[t] = mfma(k, q[t][at].v[part], lo[t]);
-                hi[t] = mfma(k, q[t][at + 2].v[part], hi[t]);
+                lo[t] = mfma(k, q[t][piece].v[part], lo[t]);
+                hi[t] = mfma(k, q[t][piece + 2].v[part], hi[t]);
               }
           }
 #pragma unroll
@@ -462,15 +473,21 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
               for (int i = 0; i < 4; ++i) s[t][4 * j + i] += sum[t][i];
           }
         }
-        if (more) load_k(r, row(a.k_cache, next.entry_k, next.off_k), col, grp);
+        const bool good_now = good;
+        if (more) {
+          good = place(next, at);
+          load_k(r, a.k_cache, at, col, grp);
+        }
 
         const bool whole = origin + tile * kTile >= start && origin + (tile + 1) * kTile <= len;
         uint32_t seen = 0xFF;  // of this lane's tokens
-        if (!whole || !__all(here)) {
+        if (!whole || !good_now) {
+          const int token = origin + tile * kTile + grp;  // the first of this lane's eight
           seen = 0;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (here && token + j >= start && token + j < len) seen |= 1u << j;
+            if ((uint32_t)now.entry[j >> 1] < (uint32_t)a.num_pages && token + 4 * j >= start && token + 4 * j < len)
+              seen |= 1u << j;
 #pragma unroll
           for (int t = 0; t < NQ; ++t)
 #pragma unroll
@@ -540,7 +557,7 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
               }
           }
         if (!more) break;
-        load_v(r, row(a.v_cache, next.entry_v, next.off_v) + col * VB);
+        load_v(r, a.v_cache, at, col, grp);
         tile += kWaves;
         now = next;
         next = find(tile + kWaves);
