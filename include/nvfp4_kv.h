@@ -196,7 +196,8 @@ nvfp4_status nvfp4_kv_cache_write(int64_t tokens, int64_t kv_heads, int64_t head
  * on the lengths and the device's CU count, and is the same in every call.
  *
  * Errors: NULL pointers -> ERR_NULL; sizes <= 0, head_dim not one of the four,
- * q_heads % kv_heads != 0, window < 0, page_size and max_pages as above,
+ * q_heads % kv_heads != 0, n_seqs * q_heads >= 2^31, max_pages * page_size *
+ * q_heads > 2^37, window < 0, page_size and max_pages as above,
  * num_pages * page_size >= 2^31, ld_table < max_pages, overlapping strides,
  * workspace_bytes too small -> ERR_SHAPE; alignment -> ERR_ALIGN; dtype ->
  * ERR_DTYPE; softmax_scale not finite or <= 0 -> ERR_RANGE.

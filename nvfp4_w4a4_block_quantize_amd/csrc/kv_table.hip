@@ -5,13 +5,26 @@
 //   upto_r = used + sum_{i<=r} need_i picks them from the free list in order;
 //   slot(t) = page(pos / P) * P + pos % P for the new token at position pos.
 //
-// One workgroup scans the requests, 1024 at a time, with running sums of tokens
-// and pages (64-bit: neither sum is bounded by 32 bits before the limits are
-// applied).  The tokens are then spread over threads, four consecutive ones
+// A workgroup of 1024 threads scans the requests, 1024 at a time, with running sums
+// of tokens and pages (64-bit: neither sum is bounded by 32 bits before the limits
+// are applied).  The tokens are then spread over threads, four consecutive ones
 // each: a thread finds its request by bisection in the starts and walks on from
 // there.  The thread whose token opens a page also enters it in the block table,
 // so fresh pages cost no pass of their own and nobody reads an entry that this
 // call writes.
+//
+// Latency decides, so there is one launch where that is less: up to kInLds
+// requests, every workgroup makes the sums for itself, keeps what it needs of them
+// in LDS and spreads its tokens; the first one writes them down (1000 requests,
+// 150 thousand tokens: 9.0 us, 11.2 with a second kernel that spreads them; 96
+// requests, 1.6 million: 14.6 and 11.0).  In place (seq_lens is cached_lens, or
+// free_used_out is free_used) that holds for a single workgroup only, since the
+// others could find lengths that the first one has moved on already.
+//
+// A decode step's requests bring one token each: while no request brings more than
+// kOwn, the single workgroup's threads place their requests' tokens themselves,
+// with the page that a token continues already loaded while the sums are made
+// (256 requests: 5.1 us, 8.2 by bisection).
 #include <algorithm>
 
 #include "kv_internal.h"
@@ -23,10 +36,25 @@ constexpr int kScanThreads = 1024;
 constexpr int kScanWaves = kScanThreads / 64;
 constexpr int kSpreadThreads = 256;
 constexpr int kPerThread = 4;       // tokens, one 16-byte store
-constexpr int kStartsInLds = 4096;  // requests whose starts a workgroup keeps in LDS
+constexpr int kInLds = 4096;        // requests whose sums a workgroup keeps in LDS
 constexpr int kOwn = 8;             // tokens of a request, at most one fresh page among them
-// Up to this many slots the scan's own workgroup spreads the tokens too, which saves the second launch.
-constexpr int kOneLaunchTokens = 8192;
+constexpr int kOneWorkgroup = 8192; // slots that a single workgroup fills in less time than a second launch takes
+constexpr int kOneLaunch = 1 << 19; // slots up to which making the sums again in every workgroup takes less
+
+// What spreading the tokens needs of the requests' sums: in LDS, or as they were written down.
+struct LdsSums {
+  const int32_t *starts, *first, *cached;
+  __device__ __forceinline__ int start(int r) const { return starts[r]; }
+  __device__ __forceinline__ int first_page(int r) const { return first[r]; }
+  __device__ __forceinline__ int cached_len(int r) const { return cached[r]; }
+};
+struct WrittenSums {
+  const int32_t *starts, *first, *seq_lens, *new_lens;
+  __device__ __forceinline__ int start(int r) const { return starts[r]; }
+  __device__ __forceinline__ int first_page(int r) const { return first[r]; }
+  // of a served request, whose seq_lens counts its new tokens already
+  __device__ __forceinline__ int cached_len(int r) const { return seq_lens[r] - new_lens[r]; }
+};
 
 // inclusive prefix sum over the workgroup; `total` is the sum of all
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* wave_sums, int64_t& total) {
@@ -50,30 +78,32 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* wave_sums, int
   return v + (wave > 0 ? before : 0);
 }
 
-// slots of tokens t0 .. t0+3; starts: token_starts, in LDS or global memory
-__device__ __forceinline__ void spread4(const BlockTableArgs& a, FastDiv by_page, const int32_t* starts, int t0) {
+// slots of tokens t0 .. t0+3
+template <typename Sums>
+__device__ __forceinline__ void spread4(const BlockTableArgs& a, FastDiv by_page, const Sums& sums, int t0) {
   int32_t slot[kPerThread];
   // the last request that begins at or before t0; n_seqs: behind the last token
   int lo = 0, hi = a.n_seqs + 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (starts[mid] <= t0) lo = mid + 1;
+    if (sums.start(mid) <= t0) lo = mid + 1;
     else hi = mid;
   }
   int r = lo - 1, loaded = -1, first = 0, cached = 0, held = 0, begin = 0;
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     const int t = t0 + i;
-    while (r < a.n_seqs && starts[r + 1] <= t) ++r;
+    while (r < a.n_seqs && sums.start(r + 1) <= t) ++r;
     slot[i] = -1;
     if (r >= a.n_seqs || t >= a.max_tokens) continue;
     if (r != loaded) {
       loaded = r;
-      first = a.first_pages[r];
-      // a served request's seq_lens already counts its new tokens
-      cached = a.seq_lens[r] - a.new_lens[r];
-      begin = starts[r];
-      held = first < 0 ? 0 : (int)by_page.div((uint32_t)(cached + a.page_size - 1));
+      first = sums.first_page(r);
+      begin = sums.start(r);
+      if (first >= 0) {
+        cached = sums.cached_len(r);
+        held = (int)by_page.div((uint32_t)(cached + a.page_size - 1));
+      }
     }
     if (first < 0) continue;
     const int pos = cached + (t - begin);
@@ -98,15 +128,17 @@ __device__ __forceinline__ void spread4(const BlockTableArgs& a, FastDiv by_page
   }
 }
 
-template <bool SPREAD>
+// ONE: the only launch, of one or more workgroups
+template <bool ONE>
 __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, FastDiv by_page) {
   __shared__ int64_t sums[kScanWaves];
-  __shared__ int32_t lds_starts[SPREAD ? kStartsInLds + 1 : 1];
+  __shared__ int32_t lds_starts[ONE ? kInLds + 1 : 1], lds_first[ONE ? kInLds : 1], lds_cached[ONE ? kInLds : 1];
   __shared__ unsigned long long taken;
-  __shared__ int lds_many;  // whether some request brings more than kOwn tokens
+  __shared__ int lds_many;  // whether some request brings more than kOwn tokens, or there are more workgroups
+  const bool writes = !ONE || blockIdx.x == 0, alone = gridDim.x == 1;
   if (threadIdx.x == 0) {
     taken = 0;
-    lds_many = 0;
+    lds_many = !alone;
   }
   const int64_t used = max(0, *a.free_used);
   int64_t tokens = 0, pages = 0;
@@ -120,8 +152,8 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
     const uint32_t held = valid ? by_page.div((uint32_t)c + up) : 0;
     int32_t* row = a.block_table + (int64_t)r * a.ld_table;
     int page = -1;  // that the first new token continues
-    if constexpr (SPREAD) {
-      if (valid && n > 0 && held > 0) page = row[held - 1];
+    if constexpr (ONE) {
+      if (alone && valid && n > 0 && held > 0) page = row[held - 1];
     }
     int64_t sum;
     const int64_t end = tokens + block_scan(n > 0 ? n : 0, sums, sum);
@@ -132,15 +164,20 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
     pages += sum;
     const bool served = fits && (need == 0 || upto <= a.n_free);
     if (in) {
-      const int64_t start = min(end - (n > 0 ? n : 0), (int64_t)a.max_tokens);
-      a.token_starts[r] = (int32_t)start;
-      a.seq_lens[r] = (int32_t)(served ? c + n : c);
-      a.first_pages[r] = served ? (int32_t)min(upto - need, (int64_t)a.n_free) : -1;
-      if constexpr (SPREAD) {
-        if (a.n_seqs <= kStartsInLds) lds_starts[r] = (int32_t)start;
+      const int32_t start = (int32_t)min(end - (n > 0 ? n : 0), (int64_t)a.max_tokens);
+      const int32_t first = served ? (int32_t)min(upto - need, (int64_t)a.n_free) : -1;
+      if (writes) {
+        a.token_starts[r] = start;
+        a.seq_lens[r] = (int32_t)(served ? c + n : c);
+        a.first_pages[r] = first;
+      }
+      if constexpr (ONE) {
+        lds_starts[r] = start;
+        lds_first[r] = first;
+        lds_cached[r] = (int32_t)c;
         if (n > kOwn) {
           lds_many = 1;
-        } else if (n > 0) {
+        } else if (alone && n > 0) {
           int fresh = -1;
           if (served && need > 0) row[held] = fresh = a.free_pages[upto - need];
           const int64_t own = (int64_t)held * a.page_size;  // positions that held pages have
@@ -160,43 +197,39 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
   }
   __syncthreads();
   const int last = (int)min(tokens, (int64_t)a.max_tokens);
-  if (threadIdx.x == 0) {
+  if (writes && threadIdx.x == 0) {
     a.token_starts[a.n_seqs] = last;
-    if constexpr (SPREAD) {
-      if (a.n_seqs <= kStartsInLds) lds_starts[a.n_seqs] = last;
-    }
     *a.free_used_out = (int32_t)(used + (int64_t)taken);
   }
-  if constexpr (SPREAD) {
+  if constexpr (ONE) {
     if (!lds_many) {
       for (int64_t t = (int64_t)last + threadIdx.x; t < a.max_tokens; t += kScanThreads) a.slot_map[t] = -1;
       return;
     }
-    __syncthreads();  // the workgroup's own global writes too are visible to it from here
-    const int32_t* starts = a.n_seqs <= kStartsInLds ? lds_starts : a.token_starts;
-    for (int64_t t0 = (int64_t)threadIdx.x * kPerThread; t0 < a.max_tokens; t0 += (int64_t)kScanThreads * kPerThread)
-      spread4(a, by_page, starts, (int)t0);
+    if (threadIdx.x == 0) lds_starts[a.n_seqs] = last;
+    __syncthreads();
+    const LdsSums all{lds_starts, lds_first, lds_cached};
+    for (int64_t t0 = ((int64_t)blockIdx.x * kScanThreads + threadIdx.x) * kPerThread; t0 < a.max_tokens;
+         t0 += (int64_t)gridDim.x * kScanThreads * kPerThread)
+      spread4(a, by_page, all, (int)t0);
   }
 }
 
 __global__ __launch_bounds__(kSpreadThreads) void kv_table_spread(BlockTableArgs a, FastDiv by_page) {
-  __shared__ int32_t lds_starts[kStartsInLds + 1];
-  const int32_t* starts = a.token_starts;
-  if (a.n_seqs <= kStartsInLds) {
-    for (int i = threadIdx.x; i <= a.n_seqs; i += kSpreadThreads) lds_starts[i] = a.token_starts[i];
-    __syncthreads();
-    starts = lds_starts;
-  }
+  const WrittenSums all{a.token_starts, a.first_pages, a.seq_lens, a.new_lens};
   const int64_t t0 = ((int64_t)blockIdx.x * kSpreadThreads + threadIdx.x) * kPerThread;
-  if (t0 < a.max_tokens) spread4(a, by_page, starts, (int)t0);
+  if (t0 < a.max_tokens) spread4(a, by_page, all, (int)t0);
 }
 
 }  // namespace
 
 hipError_t launch_kv_block_table(const BlockTableArgs& a, hipStream_t stream) {
   const FastDiv by_page((uint32_t)a.page_size);
-  if (a.max_tokens <= kOneLaunchTokens) {
-    kv_table_scan<true><<<1, kScanThreads, 0, stream>>>(a, by_page);
+  const bool in_place = a.seq_lens == a.cached_lens || a.free_used_out == a.free_used;
+  if (a.n_seqs <= kInLds && a.max_tokens <= (in_place ? kOneWorkgroup : kOneLaunch)) {
+    const int per_block = kScanThreads * kPerThread;
+    const int blocks = a.max_tokens <= kOneWorkgroup ? 1 : (a.max_tokens + per_block - 1) / per_block;
+    kv_table_scan<true><<<blocks, kScanThreads, 0, stream>>>(a, by_page);
     return hipGetLastError();
   }
   kv_table_scan<false><<<1, kScanThreads, 0, stream>>>(a, by_page);

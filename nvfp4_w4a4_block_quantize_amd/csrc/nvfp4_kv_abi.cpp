@@ -25,6 +25,8 @@ constexpr int64_t kMaxDim = (int64_t)1 << 31;     // sizes are below 2^31
 constexpr int64_t kMaxStride = (int64_t)1 << 40;  // strides too large for a byte offset are refused
 constexpr int64_t kMaxRow = (int64_t)1 << 26;     // elements of one token's heads
 
+constexpr int64_t kMaxReach = (int64_t)1 << 37;   // tokens of a full table row times query heads
+
 inline bool size_ok(int64_t n) { return n > 0 && n < kMaxDim; }
 
 // heads * head_dim elements of a token; both factors are checked before they are multiplied
@@ -200,8 +202,9 @@ nvfp4_status nvfp4_paged_attention(int64_t n_seqs, int64_t q_heads, int64_t kv_h
   const int es = dtype_size(dtype);
   if (es == 0) return NVFP4_ERR_DTYPE;
   if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.0f)) return NVFP4_ERR_RANGE;
-  if (!size_ok(n_seqs) || !attention_heads_ok(q_heads, kv_heads, head_dim) || window < 0 ||
-      !cache_ok(num_pages, page_size) || !table_ok(max_pages, page_size, ld_table) ||
+  if (!size_ok(n_seqs) || !attention_heads_ok(q_heads, kv_heads, head_dim) || n_seqs * q_heads >= kMaxDim ||
+      window < 0 || !cache_ok(num_pages, page_size) || !table_ok(max_pages, page_size, ld_table) ||
+      max_pages * page_size * q_heads > kMaxReach ||
       !strides_ok(q_heads, head_dim, q_token, q_head) || !strides_ok(q_heads, head_dim, out_token, out_head))
     return NVFP4_ERR_SHAPE;
   if (!aligned(q, 16) || !by16(q_token, es) || !by16(q_head, es) || !aligned(out, 16) || !by16(out_token, es) ||

@@ -72,10 +72,9 @@ def _call(name, like, stream, args):
         _nv._check(name, status)
 
 
-def _ints(t, n, name, like):
-    """The address of a dense int32 tensor [n] on the device of `like`."""
-    if t.dtype is _int32 and t.numel() == n and t.dim() == 1 and t.is_contiguous() and \
-            t.get_device() == like.get_device():
+def _ints(t, n, name, index):
+    """The address of a dense int32 tensor [n] on device `index`."""
+    if t.dtype is _int32 and t.numel() == n and t.dim() == 1 and t.is_contiguous() and t.get_device() == index:
         return t.data_ptr()
     if t.dtype is not _int32:
         raise ValueError(f"{name} must be int32, got {t.dtype}")
@@ -83,13 +82,19 @@ def _ints(t, n, name, like):
         raise ValueError(f"{name} must have shape {(n,)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    raise _elsewhere(t, name, index)
 
 
-def _scale(t, name, like):
-    """The address of a one-element float32 tensor on the device of `like`."""
-    if t.dtype is not _torch.float32 or t.numel() != 1 or t.get_device() != like.get_device():
-        _nv._scalar_f32(t, name, like)
+def _elsewhere(t, name, index):
+    return ValueError(f"{name} is on {t.device}, expected {'cpu' if index < 0 else f'cuda:{index}'}")
+
+
+def _scale(t, name, index):
+    """The address of a one-element float32 tensor on device `index`."""
+    if t.dtype is not _torch.float32 or t.numel() != 1:
+        _nv._scalar_f32(t, name)
+    if t.get_device() != index:
+        raise _elsewhere(t, name, index)
     return t.data_ptr()
 
 
@@ -101,7 +106,7 @@ def _new(shape, dtype, like, stream):
         return _torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _table(t, rows, like):
+def _table(t, rows, index):
     """A block table, int32 with unit column stride: (address, columns, row stride)."""
     shape = t.shape
     if t.dtype is not _int32 or len(shape) != 2 or shape[0] != rows:
@@ -109,40 +114,41 @@ def _table(t, rows, like):
     ld, unit = t.stride()
     if unit != 1 and shape[1] != 1:
         raise ValueError("block_table must have unit column stride")
-    if t.get_device() != like.get_device():
-        _nv._same_device(t, like, "block_table")
+    if t.get_device() != index:
+        raise _elsewhere(t, "block_table", index)
     return t.data_ptr(), shape[1], ld if rows > 1 else shape[1]
 
 
-def _heads(t, name, like=None):
-    """[tokens, heads, head_dim] with any strides between heads and tokens:
-    (address, token stride, head stride).  The stride of an axis of one is free."""
-    shape = t.shape
+def _heads(t, name, shape, dtype, index):
+    """[tokens, heads, head_dim] of `shape` and `dtype` on device `index`, with any
+    strides between heads and tokens: (address, token stride, head stride).  The
+    stride of an axis of one is free."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(shape)}")
-    if like is not None:
-        if t.dtype is not like.dtype or shape != like.shape:
-            raise ValueError(f"{name} must be {like.dtype} of shape {tuple(like.shape)}, got {t.dtype} {tuple(shape)}")
-        if t.get_device() != like.get_device():
-            _nv._same_device(t, like, name)
-    tokens, heads, dim = shape
+    if t.get_device() != index:
+        raise _elsewhere(t, name, index)
     token, head, unit = t.stride()
-    if unit != 1 and dim != 1:
+    if unit != 1 and shape[2] != 1:
         raise ValueError(f"{name} must have unit stride along head_dim")
-    if heads == 1:
-        head = dim
-    return t.data_ptr(), token if tokens > 1 else heads * head, head
+    if shape[1] == 1:
+        head = shape[2]
+    return t.data_ptr(), token if shape[0] > 1 else shape[1] * head, head
 
 
-def _cache(k_cache, v_cache, like):
-    """The addresses of two [num_pages, kv_heads, page_size, head_dim] byte tensors."""
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache must be [num_pages, kv_heads, page_size, head_dim], got {tuple(k_cache.shape)}")
-    u8, index = _torch.uint8, like.get_device()
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype is not u8 or t.shape != k_cache.shape or not t.is_contiguous() or t.get_device() != index:
-            _nv._bytes_arg(t, k_cache.shape, name, like)
-    return k_cache.data_ptr(), v_cache.data_ptr()
+def _cache(k_cache, v_cache, index):
+    """Two [num_pages, kv_heads, page_size, head_dim] byte tensors: (addresses, shape)."""
+    shape, u8 = k_cache.shape, _torch.uint8
+    if len(shape) != 4:
+        raise ValueError(f"k_cache must be [num_pages, kv_heads, page_size, head_dim], got {tuple(shape)}")
+    if k_cache.dtype is not u8 or not k_cache.is_contiguous():
+        _nv._bytes_arg(k_cache, shape, "k_cache")
+    if v_cache.dtype is not u8 or v_cache.shape != shape or not v_cache.is_contiguous():
+        _nv._bytes_arg(v_cache, shape, "v_cache")
+    if k_cache.get_device() != index or v_cache.get_device() != index:
+        raise _elsewhere(k_cache if k_cache.get_device() != index else v_cache, "k_cache or v_cache", index)
+    return k_cache.data_ptr(), v_cache.data_ptr(), shape
 
 
 def nvfp4_kv_block_table(cached_lens, new_lens, page_size: int, free_pages, free_used, block_table, slot_map,
@@ -157,7 +163,7 @@ def nvfp4_kv_block_table(cached_lens, new_lens, page_size: int, free_pages, free
     """
     if _nv is None:
         _load()
-    n = cached_lens.shape[0] if cached_lens.dim() == 1 else -1
+    n = cached_lens.numel() if cached_lens.dim() == 1 else -1
     if n < 0 or free_pages.dim() != 1 or slot_map.dim() != 1:
         raise ValueError("cached_lens, free_pages and slot_map must be 1-D")
     if seq_lens is None:
@@ -168,15 +174,15 @@ def nvfp4_kv_block_table(cached_lens, new_lens, page_size: int, free_pages, free
         first_pages = _new((n,), _int32, cached_lens, stream)
     if free_used_out is None:
         free_used_out = _new((1,), _int32, cached_lens, stream)
-    table, max_pages, ld = _table(block_table, n, cached_lens)
-    n_free, tokens = free_pages.shape[0], slot_map.shape[0]
-    like = cached_lens
-    _call("nvfp4_kv_block_table", like, stream,
-          (n, _ints(cached_lens, n, "cached_lens", like), _ints(new_lens, n, "new_lens", like), page_size,
-           _ints(free_pages, n_free, "free_pages", like), n_free, _ints(free_used, 1, "free_used", like), table,
-           max_pages, ld, _ints(slot_map, tokens, "slot_map", like), tokens,
-           _ints(seq_lens, n, "seq_lens", like), _ints(token_starts, n + 1, "token_starts", like),
-           _ints(first_pages, n, "first_pages", like), _ints(free_used_out, 1, "free_used_out", like)))
+    index = cached_lens.get_device()
+    table, max_pages, ld = _table(block_table, n, index)
+    n_free, tokens = free_pages.numel(), slot_map.numel()
+    _call("nvfp4_kv_block_table", cached_lens, stream,
+          (n, _ints(cached_lens, n, "cached_lens", index), _ints(new_lens, n, "new_lens", index), page_size,
+           _ints(free_pages, n_free, "free_pages", index), n_free, _ints(free_used, 1, "free_used", index), table,
+           max_pages, ld, _ints(slot_map, tokens, "slot_map", index), tokens,
+           _ints(seq_lens, n, "seq_lens", index), _ints(token_starts, n + 1, "token_starts", index),
+           _ints(first_pages, n, "first_pages", index), _ints(free_used_out, 1, "free_used_out", index)))
     return seq_lens, token_starts, first_pages, free_used_out
 
 
@@ -193,10 +199,11 @@ def nvfp4_rope(q, k, positions, inv_freq, axes, adjacent: bool = False, q_out=No
         _load()
     if q_out is None:
         q_out = _new(q.shape, q.dtype, q, stream)
-    pq, q_token, q_head = _heads(q, "q")
-    po, o_token, o_head = _heads(q_out, "q_out", q)
-    tokens, q_heads, dim = q.shape
-    pos_shape, index = positions.shape, q.get_device()
+    shape, dtype, index = q.shape, q.dtype, q.get_device()
+    pq, q_token, q_head = _heads(q, "q", shape, dtype, index)
+    po, o_token, o_head = _heads(q_out, "q_out", shape, dtype, index)
+    tokens, q_heads, dim = shape
+    pos_shape = positions.shape
     if len(pos_shape) != 2 or positions.dtype is not _int32 or pos_shape[1] != tokens:
         raise ValueError(f"positions must be int32 [axes, {tokens}], got {positions.dtype} {tuple(pos_shape)}")
     ld_pos, unit = positions.stride()
@@ -204,26 +211,25 @@ def nvfp4_rope(q, k, positions, inv_freq, axes, adjacent: bool = False, q_out=No
         raise ValueError("positions must have unit stride along tokens")
     if inv_freq.dim() != 1 or inv_freq.dtype is not _torch.float32 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be float32 [rot_dim / 2], contiguous")
-    if positions.get_device() != index or inv_freq.get_device() != index:
-        _nv._same_device(positions, q, "positions")
-        _nv._same_device(inv_freq, q, "inv_freq")
+    for t, name in ((positions, "positions"), (inv_freq, "inv_freq")):
+        if t.get_device() != index:
+            raise _elsewhere(t, name, index)
     pairs, n_axes = inv_freq.shape[0], pos_shape[0]
     keys = (None, None, 0, 0, 0, 0, 0)
     if k is not None:
-        pk, k_token, k_head = _heads(k, "k")
-        if k.dtype is not q.dtype or k.shape[0] != tokens or k.shape[2] != dim:
-            raise ValueError(f"k must be {q.dtype} [{tokens}, heads, {dim}], got {k.dtype} {tuple(k.shape)}")
-        if k.get_device() != index:
-            _nv._same_device(k, q, "k")
+        k_shape = k.shape
+        if k.dtype is not dtype or len(k_shape) != 3 or k_shape[0] != tokens or k_shape[2] != dim:
+            raise ValueError(f"k must be {dtype} [{tokens}, heads, {dim}], got {k.dtype} {tuple(k_shape)}")
         if k_out is None:
-            k_out = _new(k.shape, k.dtype, k, stream)
-        pko, ko_token, ko_head = _heads(k_out, "k_out", k)
-        keys = (pk, pko, k.shape[1], k_token, k_head, ko_token, ko_head)
+            k_out = _new(k_shape, dtype, k, stream)
+        pk, k_token, k_head = _heads(k, "k", k_shape, dtype, index)
+        pko, ko_token, ko_head = _heads(k_out, "k_out", k_shape, dtype, index)
+        keys = (pk, pko, k_shape[1], k_token, k_head, ko_token, ko_head)
     elif k_out is not None:
         raise ValueError("k_out without k")
     _call("nvfp4_rope", q, stream,
-          (tokens, dim, 2 * pairs, _nv._dtype_code(q.dtype), int(adjacent), positions.data_ptr(), n_axes,
-           ld_pos if n_axes > 1 else tokens, inv_freq.data_ptr(), _ints(axes, pairs, "axes", q), pq, po, q_heads,
+          (tokens, dim, 2 * pairs, _nv._dtype_code(dtype), int(adjacent), positions.data_ptr(), n_axes,
+           ld_pos if n_axes > 1 else tokens, inv_freq.data_ptr(), _ints(axes, pairs, "axes", index), pq, po, q_heads,
            q_token, q_head, o_token, o_head, *keys))
     return q_out, k_out
 
@@ -235,16 +241,17 @@ def nvfp4_kv_cache_write(k, v, k_scale, v_scale, slot_map, k_cache, v_cache, str
     page_size, head_dim].  Returns (k_cache, v_cache)."""
     if _nv is None:
         _load()
-    pk, k_token, k_head = _heads(k, "k")
-    pv, v_token, v_head = _heads(v, "v", k)
-    tokens, heads, dim = k.shape
-    ck, cv = _cache(k_cache, v_cache, k)
-    pages, kv_heads, page_size, d = k_cache.shape
+    shape, dtype, index = k.shape, k.dtype, k.get_device()
+    pk, k_token, k_head = _heads(k, "k", shape, dtype, index)
+    pv, v_token, v_head = _heads(v, "v", shape, dtype, index)
+    tokens, heads, dim = shape
+    ck, cv, (pages, kv_heads, page_size, d) = _cache(k_cache, v_cache, index)
     if kv_heads != heads or d != dim:
         raise ValueError(f"k_cache must be [pages, {heads}, page_size, {dim}], got {tuple(k_cache.shape)}")
     _call("nvfp4_kv_cache_write", k, stream,
-          (tokens, heads, dim, _nv._dtype_code(k.dtype), pk, k_token, k_head, pv, v_token, v_head,
-           _scale(k_scale, "k_scale", k), _scale(v_scale, "v_scale", k), _ints(slot_map, tokens, "slot_map", k),
+          (tokens, heads, dim, _nv._dtype_code(dtype), pk, k_token, k_head, pv, v_token, v_head,
+           _scale(k_scale, "k_scale", index), _scale(v_scale, "v_scale", index),
+           _ints(slot_map, tokens, "slot_map", index),
            ck, cv, pages, page_size))
     return k_cache, v_cache
 
@@ -273,31 +280,32 @@ def nvfp4_paged_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, se
         _load()
     if out is None:
         out = _new(q.shape, q.dtype, q, stream)
-    pq, q_token, q_head = _heads(q, "q")
-    po, o_token, o_head = _heads(out, "out", q)
-    n, heads, dim = q.shape
-    ck, cv = _cache(k_cache, v_cache, q)
-    pages, kv_heads, page_size, d = k_cache.shape
+    shape, dtype, index = q.shape, q.dtype, q.get_device()
+    pq, q_token, q_head = _heads(q, "q", shape, dtype, index)
+    po, o_token, o_head = _heads(out, "out", shape, dtype, index)
+    n, heads, dim = shape
+    ck, cv, (pages, kv_heads, page_size, d) = _cache(k_cache, v_cache, index)
     if d != dim:
         raise ValueError(f"k_cache has head_dim {d}, q has {dim}")
-    table, max_pages, ld = _table(block_table, n, q)
+    table, max_pages, ld = _table(block_table, n, index)
     if lse is not None:
         if lse.dtype is not _torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous():
             raise ValueError(f"lse must be float32 [{n}, {heads}], contiguous")
-        _nv._same_device(lse, q, "lse")
+        if lse.get_device() != index:
+            raise _elsewhere(lse, "lse", index)
     if workspace is None:
-        if not q.is_cuda:
+        if index < 0:
             raise ValueError("nvfp4_paged_attention needs GPU tensors")
         with _torch.cuda.device(q.device):
             size = nvfp4_paged_attention_workspace(heads, kv_heads, dim)
         workspace = _new((size,), _torch.uint8, q, stream)
     elif workspace.dtype is not _torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
-    elif workspace.get_device() != q.get_device():
-        _nv._same_device(workspace, q, "workspace")
+    elif workspace.get_device() != index:
+        raise _elsewhere(workspace, "workspace", index)
     _call("nvfp4_paged_attention", q, stream,
-          (n, heads, kv_heads, dim, _nv._dtype_code(q.dtype), pq, q_token, q_head, ck, cv, pages, page_size,
-           _scale(k_scale, "k_scale", q), _scale(v_scale, "v_scale", q), table, max_pages, ld,
-           _ints(seq_lens, n, "seq_lens", q), dim ** -0.5 if softmax_scale is None else softmax_scale, window, po,
+          (n, heads, kv_heads, dim, _nv._dtype_code(dtype), pq, q_token, q_head, ck, cv, pages, page_size,
+           _scale(k_scale, "k_scale", index), _scale(v_scale, "v_scale", index), table, max_pages, ld,
+           _ints(seq_lens, n, "seq_lens", index), dim ** -0.5 if softmax_scale is None else softmax_scale, window, po,
            o_token, o_head, None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel()))
     return out

@@ -123,6 +123,10 @@ def test_pages_of_a_long_table_and_cache(lib):
     assert c["table"](max_pages=1 << 28, ld=1 << 28, page=1024) == SHAPE
     assert c["attend"](max_pages=1 << 28, ld=1 << 28, page=16) == SHAPE
     assert c["attend"](hq=1 << 33, hk=1) == SHAPE
+    assert c["attend"](n=1 << 28) == SHAPE  # 8 query heads each
+    long = dict(max_pages=1 << 24, ld=1 << 24, page=16)  # 2^28 tokens
+    assert c["attend"](hq=1024, qt=1 << 16, ot=1 << 16, **long) == SHAPE
+    assert c["attend"](hq=512, qt=1 << 15, ot=1 << 15, n=1 << 22, **long) == SHAPE
     assert c["write"](heads=1 << 25, dim=1 << 25) == SHAPE
 
 
