@@ -119,12 +119,12 @@ __device__ __forceinline__ void spread4(const BlockTableArgs& a, FastDiv by_page
     if (page >= 0 && s <= INT32_MAX) slot[i] = (int32_t)s;
   }
   int32_t* out = a.slot_map + t0;
-  if (t0 + kPerThread <= a.max_tokens && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+  if (a.max_tokens - t0 >= kPerThread && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
     *reinterpret_cast<int4*>(out) = make_int4(slot[0], slot[1], slot[2], slot[3]);
   } else {
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i)
-      if (t0 + i < a.max_tokens) out[i] = slot[i];
+      if (i < a.max_tokens - t0) out[i] = slot[i];
   }
 }
 

@@ -293,9 +293,10 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
   // thread summing a few neighbours.
   const int per = (n + kThreads - 1) / kThreads;
   int64_t mine = 0;
+#pragma unroll 4
   for (int i = 0; i < per; ++i) {
     const int s = tid * per + i;
-    if (s < n) mine += cost(p, s);
+    mine += s < n ? cost(p, min(s, n - 1)) : 0;
   }
   int64_t upto = mine;
 #pragma unroll
@@ -315,18 +316,23 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
   units = uniform(units);
   const int64_t workers = min((int64_t)gridDim.x, units);
 
-  // rows that see no token belong to no item
+  // rows that see no token belong to no item: the grid's waves look for them, 64 sequences at a time
   auto clear = [&] {
-    for (int s = worker; s < n; s += gridDim.x) {
-      if (seq_span(p, s).w > 0) continue;
-      for (int i = tid; i < a.q_heads * (D / 4); i += kThreads) {
-        const int h = i / (D / 4);
-        store4<DT>(a, s, h, (i - h * (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+    const int64_t waves = (int64_t)gridDim.x * kWaves;
+    for (int64_t base = worker * kWaves + wave; base < n; base += 64 * waves) {
+      const int64_t mine_ = base + lane * waves;
+      uint64_t empty = __ballot(mine_ < n && seq_span(p, (int)min(mine_, (int64_t)n - 1)).w == 0);
+      for (; empty; empty &= empty - 1) {
+        const int s = (int)(base + __builtin_ctzll(empty) * waves);
+        for (int i = lane; i < a.q_heads * (D / 4); i += 64) {
+          const int h = i / (D / 4);
+          store4<DT>(a, s, h, (i - h * (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+        }
+        if (a.lse)
+          for (int h = lane; h < a.q_heads; h += 64) a.lse[(int64_t)s * a.q_heads + h] = -INFINITY;
+        if (p.by_item)
+          for (int i = lane; i < p.items; i += 64) p.ws.split[s * p.items + i] = make_int4(-1, 0, 0, 0);
       }
-      if (a.lse)
-        for (int h = tid; h < a.q_heads; h += kThreads) a.lse[(int64_t)s * a.q_heads + h] = -INFINITY;
-      if (p.by_item)
-        for (int i = tid; i < p.items; i += kThreads) p.ws.split[s * p.items + i] = make_int4(-1, 0, 0, 0);
     }
   };
   int4 split = make_int4(-1, 0, 0, 0);
@@ -352,11 +358,16 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
   const double c64 = (double)a.softmax_scale * 1.44269504088896340736 / (double)ks;
   const float c_hi = (float)c64, c_lo = DT == 0 ? (float)(c64 - (double)c_hi) : 0.0f;
 
-  while (u < u_end) {
+  while (u < u_end && seq < n) {
     const int4 span = seq_span(p, seq);
     const int len = uniform(span.x), start = uniform(span.y), origin = uniform(span.z), per_item = uniform(span.w);
-    if (per_item == 0) {
-      ++seq;
+    if (per_item == 0) {  // the next one with units, of which there are some ahead
+      uint64_t some = 0;
+      for (++seq; seq < n; seq += 64) {
+        some = __ballot(seq + lane < n && seq_span(p, min(seq + lane, n - 1)).w > 0);
+        if (some) break;
+      }
+      seq += some ? __builtin_ctzll(some) : 0;
       continue;
     }
     // the run's part in this item

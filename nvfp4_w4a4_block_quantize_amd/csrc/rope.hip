@@ -169,14 +169,16 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Plan p) {
   }
 }
 
-bool in_place(const RopeArgs& a) { return a.q_out.p == a.q.p && (a.k_heads == 0 || a.k_out.p == a.k.p); }
+// whether all heads are turned in place, and whether some are
+bool all_in_place(const RopeArgs& a) { return a.q_out.p == a.q.p && (a.k_heads == 0 || a.k_out.p == a.k.p); }
+bool some_in_place(const RopeArgs& a) { return a.q_out.p == a.q.p || (a.k_heads > 0 && a.k_out.p == a.k.p); }
 
 template <int DT, int VEC, int COPY, bool ADJACENT, bool ALIGNED>
 hipError_t launch_vec(const RopeArgs& a, hipStream_t stream) {
   Plan p;
   p.pairs = a.rot_dim / 2;
   const uint32_t heads = (uint32_t)(a.q_heads + a.k_heads);
-  const int turn = ADJACENT ? a.rot_dim : p.pairs, copy = in_place(a) ? 0 : a.head_dim - a.rot_dim;
+  const int turn = ADJACENT ? a.rot_dim : p.pairs, copy = all_in_place(a) ? 0 : a.head_dim - a.rot_dim;
   p.turn_last = turn - VEC;
   p.copy_last = a.head_dim - COPY;
   p.by_turn = FastDiv((uint32_t)(turn + VEC - 1) / VEC);
@@ -203,9 +205,9 @@ hipError_t launch_vec(const RopeArgs& a, hipStream_t stream) {
 template <int DT, bool ADJACENT>
 hipError_t launch_widest(const RopeArgs& a, hipStream_t stream) {
   constexpr int ES = DT == 0 ? 4 : 2, kFull = 16 / ES;
-  const int turn = ADJACENT ? a.rot_dim : a.rot_dim / 2, copy = in_place(a) ? 0 : a.head_dim - a.rot_dim;
+  const int turn = ADJACENT ? a.rot_dim : a.rot_dim / 2, copy = all_in_place(a) ? 0 : a.head_dim - a.rot_dim;
   int vec = kFull;
-  while (in_place(a) ? turn % vec != 0 : vec > turn) vec /= 2;
+  while (some_in_place(a) ? turn % vec != 0 : vec > turn) vec /= 2;
   const bool wide = copy == 0 || copy >= kFull;
   uint64_t at = (uint64_t)(turn | copy) * ES;  // its lowest set bit is that of all vectors' addresses
   for (int64_t s : {a.q.token, a.q.head, a.q_out.token, a.q_out.head}) at |= (uint64_t)s * ES;

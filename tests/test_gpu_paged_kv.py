@@ -150,6 +150,23 @@ def test_rope(gpu_lib, dtype, adjacent, tokens, q_heads, k_heads, dim, rot):
 
 
 @pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_rope_one_tensor_in_place(gpu_lib, adjacent, which):
+    """Only q, or only k, turned in place, with parts that 16 bytes do not divide."""
+    rng = np.random.default_rng(31)
+    tokens, dim, rot = 67, 96, 54
+    positions, axes = rng.integers(0, 4000, (1, tokens)), np.zeros(rot // 2, int)
+    inv_freq = (1e4 ** (-np.arange(rot // 2) / (rot // 2))).astype(np.float32)
+    q, k = (dev(rng.standard_normal((tokens, h, dim)), torch.bfloat16) for h in (6, 2))
+    before = q.clone(), k.clone()
+    q_out, k_out = turn(gpu_lib, q, k, positions, inv_freq, axes, adjacent, **({"q_out": q} if which == "q" else {"k_out": k}))
+    check_rope(q_out, before[0], positions, inv_freq, axes, adjacent, "bf16")
+    check_rope(k_out, before[1], positions, inv_freq, axes, adjacent, "bf16")
+    assert (q_out is q) == (which == "q") and (k_out is k) == (which == "k")
+    assert torch.equal((k, q)[which == "k"], before[which == "q"])  # the other one's input stays
+
+
+@pytest.mark.parametrize("adjacent", [False, True])
 @pytest.mark.parametrize("shift", [0, 1, 2, 4])
 def test_rope_in_the_rows_of_a_projection(gpu_lib, adjacent, shift):
     """Heads with their gates between them, at every alignment; what lies between stays as it was."""
@@ -277,6 +294,18 @@ def test_attention_split_over_workers(gpu_lib, dtype, dim, lens):
     log("attention split", dtype, dim, lens[:4])
     q, k, v, table = attention_case(rng, lens, 6, 2, dim, 16, dtype)
     check_attention(gpu_lib, q, k, v, table, lens, dtype=dtype)
+
+
+@pytest.mark.parametrize("n,live", [(70, [0, 69]), (300, [5, 6, 250]), (1100, [0, 1, 600, 1099]), (2500, [2499]), (900, range(900)), (400, [])])
+def test_attention_batches_with_few_live_rows(gpu_lib, n, live):
+    """Long batches, most of whose rows are empty; and one of very many short sequences."""
+    rng = np.random.default_rng(n)
+    lens = np.zeros(n, int)
+    lens[list(live)] = rng.integers(1, 900 if len(live) < 10 else 60, len(live))
+    lens[::7] = np.where(lens[::7] == 0, -3, lens[::7])
+    log("attention live rows", n, len(live))
+    q, k, v, table = attention_case(rng, lens, 4, 2, 64, 16, "bf16")
+    check_attention(gpu_lib, q, k, v, table, lens)
 
 
 @pytest.mark.parametrize("window", [1, 5, 8, 100, 128, 1000, 2 ** 40])
