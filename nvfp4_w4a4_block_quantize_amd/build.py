@@ -27,7 +27,13 @@ PROBES_PATH = os.path.join(ROOT, "libnvfp4_probes.so")
 SOURCES = ["nvfp4_abi.cpp", "quantize.hip", "fuse_rescale.hip", "gemm.hip", "gemm_fast.hip", "gemm_decode.hip", "gemm_stream.hip", "kv_quantize.hip",
            "nvfp4_kv_abi.cpp", "kv_table.hip", "rope.hip", "kv_cache_write.hip", "paged_attention.hip"]
 
+# the native side of the paged KV cache's Python binding: an extension module
+# beside the library, built against torch's headers
+BIND_SRC = "kv_bind.cpp"
+BIND_PATH = os.path.join(HERE, "_kv_bind.so")
+
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 
 COMMON_FLAGS = [
     "--offload-arch=gfx950",
@@ -53,17 +59,48 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_bind() -> str:
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    obj = os.path.join(BUILD_DIR, "kv_bind.o")
+    includes = [INCLUDE, sysconfig.get_paths()["include"], *include_paths()]
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(f"-I{p}" for p in includes), "-c", os.path.join(CSRC, BIND_SRC), "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for {BIND_SRC}:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    return obj
+
+
+def _link_bind(obj: str):
+    import torch
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [CXX, "-shared", "-o", BIND_PATH + ".tmp", obj, "-L" + HERE, "-lnvfp4", "-Wl,-rpath,$ORIGIN", "-L" + libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    os.replace(BIND_PATH + ".tmp", BIND_PATH)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libnvfp4.so; returns the library path."""
+    """Compile every source and link libnvfp4.so and the binding's module; returns the library path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(SOURCES), 8)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=8) as ex:
+        bind = ex.submit(_compile_bind)
         objs = list(ex.map(_compile, SOURCES))
+        bind_obj = bind.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_bind(bind_obj)
     # conformance check of the conversion instructions the kernels rely on
     # (a standalone program, run by the GPU tests)
     cmd = [HIPCC, *COMMON_FLAGS, CONFORMANCE_SRC, "-o", CONFORMANCE_PATH + ".tmp"]
@@ -78,7 +115,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc failed for bench_probes.hip:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(PROBES_PATH + ".tmp", PROBES_PATH)
     if verbose:
-        print(f"built {LIB_PATH}, {CONFORMANCE_PATH} and {PROBES_PATH}")
+        print(f"built {LIB_PATH}, {BIND_PATH}, {CONFORMANCE_PATH} and {PROBES_PATH}")
     return LIB_PATH
 
 
