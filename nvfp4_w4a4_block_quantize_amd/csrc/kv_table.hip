@@ -56,26 +56,38 @@ struct WrittenSums {
   __device__ __forceinline__ int cached_len(int r) const { return seq_lens[r] - new_lens[r]; }
 };
 
-// inclusive prefix sum over the workgroup; `total` is the sum of all
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* wave_sums, int64_t& total) {
+struct Sums {
+  int64_t tokens, pages;
+};
+
+__device__ __forceinline__ Sums operator+(Sums x, Sums y) { return {x.tokens + y.tokens, x.pages + y.pages}; }
+
+__device__ __forceinline__ Sums shifted(Sums x, int d, int width) {
+  return {__shfl_up(x.tokens, d, width), __shfl_up(x.pages, d, width)};
+}
+
+// inclusive prefix sums over the workgroup; `total` is the sum of all
+__device__ __forceinline__ Sums block_scan(Sums v, Sums* wave_sums, Sums& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int64_t o = __shfl_up(v, d);
-    if (lane >= d) v += o;
+    const Sums o = shifted(v, d, 64);
+    if (lane >= d) v = v + o;
   }
   __syncthreads();  // the previous scan's sums have been read
   if (lane == 63) wave_sums[wave] = v;
   __syncthreads();
-  int64_t sums = wave_sums[lane & (kScanWaves - 1)];
+  const int in_row = lane & (kScanWaves - 1);
+  Sums sums = wave_sums[in_row];
 #pragma unroll
   for (int d = 1; d < kScanWaves; d <<= 1) {
-    const int64_t o = __shfl_up(sums, d, kScanWaves);
-    if ((lane & (kScanWaves - 1)) >= d) sums += o;
+    const Sums o = shifted(sums, d, kScanWaves);
+    if (in_row >= d) sums = sums + o;
   }
-  total = __shfl(sums, kScanWaves - 1);
-  const int64_t before = __shfl(sums, max(wave - 1, 0));
-  return v + (wave > 0 ? before : 0);
+  total = {__shfl(sums.tokens, kScanWaves - 1), __shfl(sums.pages, kScanWaves - 1)};
+  const int before = max(wave - 1, 0);
+  const Sums b = {__shfl(sums.tokens, before), __shfl(sums.pages, before)};
+  return wave > 0 ? v + b : v;
 }
 
 // slots of tokens t0 .. t0+3
@@ -131,7 +143,7 @@ __device__ __forceinline__ void spread4(const BlockTableArgs& a, FastDiv by_page
 // ONE: the only launch, of one or more workgroups
 template <bool ONE>
 __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, FastDiv by_page) {
-  __shared__ int64_t sums[kScanWaves];
+  __shared__ Sums sums[kScanWaves];
   __shared__ int32_t lds_starts[ONE ? kInLds + 1 : 1], lds_first[ONE ? kInLds : 1], lds_cached[ONE ? kInLds : 1];
   __shared__ unsigned long long taken;
   __shared__ int lds_many;  // whether some request brings more than kOwn tokens, or there are more workgroups
@@ -141,7 +153,7 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
     lds_many = !alone;
   }
   const int64_t used = max(0, *a.free_used);
-  int64_t tokens = 0, pages = 0;
+  Sums done = {0, 0};
   for (int base = 0; base < a.n_seqs; base += kScanThreads) {
     const int r = base + threadIdx.x;
     const bool in = r < a.n_seqs;
@@ -155,13 +167,14 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
     if constexpr (ONE) {
       if (alone && valid && n > 0 && held > 0) page = row[held - 1];
     }
-    int64_t sum;
-    const int64_t end = tokens + block_scan(n > 0 ? n : 0, sums, sum);
-    tokens += sum;
+    // A request past the slot map's end is followed by such only, so that its pages, which are counted here though it
+    // cannot have them, change nothing for those that fit.
+    const int64_t need = valid ? (int64_t)by_page.div((uint32_t)(c + n) + up) - held : 0;
+    Sums sum;
+    const Sums to = done + block_scan(Sums{n > 0 ? n : 0, need}, sums, sum);
+    done = done + sum;
+    const int64_t end = to.tokens, upto = used + to.pages;
     const bool fits = valid && end <= a.max_tokens;
-    const int64_t need = fits ? (int64_t)by_page.div((uint32_t)(c + n) + up) - held : 0;
-    const int64_t upto = used + pages + block_scan(need, sums, sum);
-    pages += sum;
     const bool served = fits && (need == 0 || upto <= a.n_free);
     if (in) {
       const int32_t start = (int32_t)min(end - (n > 0 ? n : 0), (int64_t)a.max_tokens);
@@ -196,7 +209,7 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
       atomicMax(&taken, (unsigned long long)(upto - used));
   }
   __syncthreads();
-  const int last = (int)min(tokens, (int64_t)a.max_tokens);
+  const int last = (int)min(done.tokens, (int64_t)a.max_tokens);
   if (writes && threadIdx.x == 0) {
     a.token_starts[a.n_seqs] = last;
     *a.free_used_out = (int32_t)(used + (int64_t)taken);

@@ -84,7 +84,7 @@ struct Params {
   int rows;       // query heads of an item
   int items;      // of a sequence: kv_heads * parts
   bool by_item;   // how `split` is indexed: by item where there are no more of them than workers
-  bool whole;     // items are not split, and count the same on the axis of work
+  bool whole;     // items are not split: each has a workgroup of its own
   int64_t page_bytes;
   Partials ws;
 };
@@ -125,7 +125,7 @@ __device__ __forceinline__ int4 seq_span(const Params& p, int seq) {
 // a sequence's length on the axis of work
 __device__ __forceinline__ int64_t cost(const Params& p, int seq) {
   const int units = seq_span(p, seq).w;
-  return units > 0 ? (int64_t)(p.whole ? 1 : units + kItemCost) * p.items : 0;
+  return units > 0 ? (int64_t)(units + kItemCost) * p.items : 0;
 }
 
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -289,70 +289,86 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
   const int col = lane & 15, grp = lane >> 4;
   const int worker = blockIdx.x, n = a.n_seqs;
 
-  // This worker's run of units: a prefix sum over the sequences' units, each
-  // thread summing a few neighbours.
-  const int per = (n + kThreads - 1) / kThreads;
-  int64_t mine = 0;
-#pragma unroll 4
-  for (int i = 0; i < per; ++i) {
-    const int s = tid * per + i;
-    mine += s < n ? cost(p, min(s, n - 1)) : 0;
-  }
-  int64_t upto = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t o = __shfl_up(upto, d);
-    if (lane >= d) upto += o;
-  }
-  if (lane == 63) lds_sum[wave] = upto;
-  __syncthreads();
-  int64_t before = 0, units = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += lds_sum[w];
-    units += lds_sum[w];
-  }
-  upto += before;
-  units = uniform(units);
-  const int64_t workers = min((int64_t)gridDim.x, units);
+  int seq = 0;                        // where this worker's run begins:
+  int64_t inside = 0, u = 0, u_end = 1;  // how far into the sequence, and where on the axis of work it begins and ends
+  int64_t units = 1, workers = 1;
+  int4 split = make_int4(-1, 0, 0, 0);
 
-  // rows that see no token belong to no item: the grid's waves look for them, 64 sequences at a time
-  auto clear = [&] {
+  // no token seen: zeros for the query heads h0 .. h1 - 1 of a sequence, by `count` threads of which this is the i-th
+  auto clear = [&](int s, int h0, int h1, int i, int count) {
+    for (int j = i; j < (h1 - h0) * (D / 4); j += count) {
+      const int h = j / (D / 4);
+      store4<DT>(a, s, h0 + h, (j - h * (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+    if (a.lse)
+      for (int h = h0 + i; h < h1; h += count) a.lse[(int64_t)s * a.q_heads + h] = -INFINITY;
+  };
+  // the same for all empty sequences: the grid's waves look for them, 64 at a time
+  auto clear_empty = [&] {
     const int64_t waves = (int64_t)gridDim.x * kWaves;
     for (int64_t base = worker * kWaves + wave; base < n; base += 64 * waves) {
-      const int64_t mine_ = base + lane * waves;
-      uint64_t empty = __ballot(mine_ < n && seq_span(p, (int)min(mine_, (int64_t)n - 1)).w == 0);
+      const int64_t s = base + lane * waves;
+      uint64_t empty = __ballot(s < n && seq_span(p, (int)min(s, (int64_t)n - 1)).w == 0);
       for (; empty; empty &= empty - 1) {
-        const int s = (int)(base + __builtin_ctzll(empty) * waves);
-        for (int i = lane; i < a.q_heads * (D / 4); i += 64) {
-          const int h = i / (D / 4);
-          store4<DT>(a, s, h, (i - h * (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
-        }
-        if (a.lse)
-          for (int h = lane; h < a.q_heads; h += 64) a.lse[(int64_t)s * a.q_heads + h] = -INFINITY;
+        const int e = (int)(base + __builtin_ctzll(empty) * waves);
+        clear(e, 0, a.q_heads, lane, 64);
         if (p.by_item)
-          for (int i = lane; i < p.items; i += 64) p.ws.split[s * p.items + i] = make_int4(-1, 0, 0, 0);
+          for (int i = lane; i < p.items; i += 64) p.ws.split[e * p.items + i] = make_int4(-1, 0, 0, 0);
       }
     }
   };
-  int4 split = make_int4(-1, 0, 0, 0);
-  if (worker >= workers) {
-    if (!p.by_item && tid == 0) p.ws.split[worker] = split;
-    clear();
-    return;
+
+  if (p.whole) {  // one item
+    seq = worker / p.items;
+    inside = worker - seq * p.items;
+    if (uniform(seq_span(p, seq).w) == 0) {
+      const int head = (int)inside / p.parts, first = head * p.group + ((int)inside - head * p.parts) * p.rows;
+      clear(seq, first, min(first + p.rows, (head + 1) * p.group), tid, kThreads);
+      return;
+    }
+  } else {
+    // A prefix sum over the sequences' lengths on the axis, each thread summing a few neighbours.
+    const int per = (n + kThreads - 1) / kThreads;
+    int64_t mine = 0;
+#pragma unroll 4
+    for (int i = 0; i < per; ++i) {
+      const int s = tid * per + i;
+      mine += s < n ? cost(p, min(s, n - 1)) : 0;
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t o = __shfl_up(upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 63) lds_sum[wave] = upto;
+    __syncthreads();
+    units = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w == wave) upto += units;
+      units += lds_sum[w];
+    }
+    units = uniform(units);
+    workers = min((int64_t)gridDim.x, units);
+    if (worker >= workers) {
+      if (!p.by_item && tid == 0) p.ws.split[worker] = split;
+      clear_empty();
+      return;
+    }
+    u = worker * units / workers;
+    u_end = (worker + 1) * units / workers;
+    if (mine > 0 && upto - mine <= u && u < upto) {
+      int64_t at = upto - mine;
+      int s = tid * per;
+      for (int64_t c; at + (c = cost(p, s)) <= u; at += c) ++s;
+      lds_first[0] = s;
+      lds_first[1] = u - at;
+    }
+    __syncthreads();
+    seq = uniform((int)lds_first[0]);
+    inside = uniform(lds_first[1]);
   }
-  int64_t u = worker * units / workers;
-  const int64_t u_end = (worker + 1) * units / workers;
-  if (mine > 0 && upto - mine <= u && u < upto) {
-    int64_t at = upto - mine;
-    int s = tid * per;
-    for (int64_t c; at + (c = cost(p, s)) <= u; at += c) ++s;
-    lds_first[0] = s;
-    lds_first[1] = u - at;
-  }
-  __syncthreads();
-  int seq = uniform((int)lds_first[0]);
-  int64_t inside = uniform(lds_first[1]);  // how far into this sequence the run begins
 
   const float ks = *a.k_scale, inv_vs = 1.0f / *a.v_scale;
   const double c64 = (double)a.softmax_scale * 1.44269504088896340736 / (double)ks;
@@ -629,14 +645,15 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
         }
       }
     }
-    if (unit0 == 0) {
+    if (unit0 == 0 && !p.whole) {
       // the item's last unit is that of the first worker whose run ends behind it
       if (!ends) split = make_int4(in, item, worker, (int)(((begin + length) * workers + units - 1) / units) - 1);
       if (p.by_item && tid == 0) p.ws.split[in * p.items + item] = split;
     }
   }
+  if (p.whole) return;
   if (!p.by_item && tid == 0) p.ws.split[worker] = split;
-  clear();
+  clear_empty();
 #endif
 }
 
@@ -728,11 +745,11 @@ hipError_t launch(Params p, hipStream_t stream) {
   const int64_t units = ((int64_t)a.max_pages * a.page_size + kUnitTokens - 1) / kUnitTokens;  // of a full table row
   const int64_t items = (int64_t)a.n_seqs * p.items;
   // Up to 512 tokens in a table's row the longest item takes a workgroup less time than the second kernel would
-  // (64 sequences of up to 300 tokens, 8 heads of 128: 11.3 against 17.4 us; of up to 1000: 27.3 against 26.4).
+  // (64 sequences of up to 300 tokens, 8 heads of 128: 10.6 against 17.4 us; of up to 1000: 27.3 against 26.4).
   p.whole = units <= 4;
-  const int workers = (int)std::min<int64_t>((int64_t)device_cu_count() * workers_per_cu<DT, D, NQ>(),
-                                             items * (p.whole ? 1 : units + kItemCost));
-  p.by_item = items <= workers;
+  const int64_t resident = (int64_t)device_cu_count() * workers_per_cu<DT, D, NQ>();
+  const int workers = (int)(p.whole ? items : std::min<int64_t>(resident, items * (units + kItemCost)));
+  p.by_item = !p.whole && items <= workers;
   paged_attention_kernel<DT, D, NQ><<<workers, kThreads, 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.whole) return e;
