@@ -742,12 +742,16 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join(Params p, i
 template <int DT, int D, int NQ>
 hipError_t launch(Params p, hipStream_t stream) {
   const PagedAttentionArgs& a = p.a;
-  const int64_t units = ((int64_t)a.max_pages * a.page_size + kUnitTokens - 1) / kUnitTokens;  // of a full table row
-  const int64_t items = (int64_t)a.n_seqs * p.items;
-  // Up to 512 tokens in a table's row the longest item takes a workgroup less time than the second kernel would
-  // (64 sequences of up to 300 tokens, 8 heads of 128: 10.6 against 17.4 us; of up to 1000: 27.3 against 26.4).
-  p.whole = units <= 4;
+  int64_t tokens = (int64_t)a.max_pages * a.page_size;  // of the longest item
+  if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + kUnitTokens);
+  const int64_t units = (tokens + kUnitTokens - 1) / kUnitTokens, items = (int64_t)a.n_seqs * p.items;
   const int64_t resident = (int64_t)device_cu_count() * workers_per_cu<DT, D, NQ>();
+  // Unsplit, a call lasts as long as its longest item; split, as all tokens take on the resident workers, and some 8 us
+  // more, for the scan of the lengths, the partial results and the second kernel.  Unsplit against split, in us:
+  //   units of an item     5           9            9            9             13            17            17           63
+  //   items  64 of 512    256 of 512   512 of 512   128 of 512    128 of 512    512 of 512    512 of 1024  512 of 512
+  //         9.7 / 11.0  21.2 / 27.1  19.1 / 26.2  15.3 / 14.7   25.7 / 21.1   32.4 / 36.6   23.4 / 22.9  113 / 105
+  p.whole = units <= 6 || (units <= 20 && units * resident <= 20 * items);
   const int workers = (int)(p.whole ? items : std::min<int64_t>(resident, items * (units + kItemCost)));
   p.by_item = !p.whole && items <= workers;
   paged_attention_kernel<DT, D, NQ><<<workers, kThreads, 0, stream>>>(p);
