@@ -5,9 +5,10 @@
 //   upto_r = used + sum_{i<=r} need_i picks them from the free list in order;
 //   slot(t) = page(pos / P) * P + pos % P for the new token at position pos.
 //
-// A workgroup of 1024 threads scans the requests, 1024 at a time, with running sums
-// of tokens and pages (64-bit: neither sum is bounded by 32 bits before the limits
-// are applied).  The tokens are then spread over threads, four consecutive ones
+// A workgroup of 1024 threads scans the requests, one to a thread or, where there are
+// more of them, four neighbours (4000 requests of 200 tokens: 12.6 us, 16.4 in four
+// rounds of one), with running sums of tokens and pages (64-bit: neither sum is
+// bounded by 32 bits before the limits are applied).  The tokens are then spread over threads, four consecutive ones
 // each: a thread finds its request by bisection in the starts and walks on from
 // there.  The thread whose token opens a page also enters it in the block table,
 // so fresh pages cost no pass of their own and nobody reads an entry that this
@@ -16,15 +17,18 @@
 // Latency decides, so there is one launch where that is less: up to kInLds
 // requests, every workgroup makes the sums for itself, keeps what it needs of them
 // in LDS and spreads its tokens; the first one writes them down (1000 requests,
-// 150 thousand tokens: 9.0 us, 11.2 with a second kernel that spreads them; 96
-// requests, 1.6 million: 14.6 and 11.0).  In place (seq_lens is cached_lens, or
+// 150 thousand tokens: 8.5 us, 11.5 with a second kernel that spreads them; 96
+// requests, 1.6 million: 13.6 and 11.1).  In place (seq_lens is cached_lens, or
 // free_used_out is free_used) that holds for a single workgroup only, since the
 // others could find lengths that the first one has moved on already.
 //
 // A decode step's requests bring one token each: while no request brings more than
-// kOwn, the single workgroup's threads place their requests' tokens themselves,
-// with the page that a token continues already loaded while the sums are made
-// (256 requests: 5.1 us, 8.2 by bisection).
+// kOwn, threads place their requests' tokens themselves, with the page that a token
+// continues already loaded while the sums are made (256 requests: 4.4 us, 7.7 by
+// bisection).  Every request has a line of the block table to itself, so four
+// requests to a thread are placed by four workgroups (4096 requests: 10.0 us, 11.7
+// by one).  What is left is latency: a launch, the lengths, the sums, a page and
+// the stores, one after another.
 #include <algorithm>
 
 #include "kv_internal.h"
@@ -37,8 +41,9 @@ constexpr int kScanWaves = kScanThreads / 64;
 constexpr int kSpreadThreads = 256;
 constexpr int kPerThread = 4;       // tokens, one 16-byte store
 constexpr int kInLds = 4096;        // requests whose sums a workgroup keeps in LDS
+constexpr int kMany = kInLds / kScanThreads;  // neighbouring requests of a thread, where there are more than threads
 constexpr int kOwn = 8;             // tokens of a request, at most one fresh page among them
-constexpr int kOneWorkgroup = 8192; // slots that a single workgroup fills in less time than a second launch takes
+constexpr int kOneWorkgroup = 8192; // slots that workgroups which place tokens themselves fill in less time than more of them
 constexpr int kOneLaunch = 1 << 19; // slots up to which making the sums again in every workgroup takes less
 
 // What spreading the tokens needs of the requests' sums: in LDS, or as they were written down.
@@ -97,7 +102,7 @@ __device__ __forceinline__ void spread4(const BlockTableArgs& a, FastDiv by_page
   // the last request that begins at or before t0; n_seqs: behind the last token
   int lo = 0, hi = a.n_seqs + 1;
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
+    const int mid = (int)(((uint32_t)lo + (uint32_t)hi) >> 1);
     if (sums.start(mid) <= t0) lo = mid + 1;
     else hi = mid;
   }
@@ -140,73 +145,105 @@ __device__ __forceinline__ void spread4(const BlockTableArgs& a, FastDiv by_page
   }
 }
 
-// ONE: the only launch, of one or more workgroups
-template <bool ONE>
+// ONE: the only launch, of one or more workgroups.  PER: neighbouring requests of a thread in a round
+template <bool ONE, int PER>
 __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, FastDiv by_page) {
   __shared__ Sums sums[kScanWaves];
   __shared__ int32_t lds_starts[ONE ? kInLds + 1 : 1], lds_first[ONE ? kInLds : 1], lds_cached[ONE ? kInLds : 1];
   __shared__ unsigned long long taken;
-  __shared__ int lds_many;  // whether some request brings more than kOwn tokens, or there are more workgroups
-  const bool writes = !ONE || blockIdx.x == 0, alone = gridDim.x == 1;
+  __shared__ int lds_many;  // whether some request brings more than kOwn tokens, or nothing is placed here
+  const bool writes = !ONE || blockIdx.x == 0;
+  // whether requests' tokens may be placed right here, and this workgroup's requests of each thread then
+  const bool places = ONE && a.max_tokens <= kOneWorkgroup;
+  auto own = [&](int k) { return places && (gridDim.x == 1 || k == (int)blockIdx.x); };
   if (threadIdx.x == 0) {
     taken = 0;
-    lds_many = !alone;
+    lds_many = !places;
   }
   const int64_t used = max(0, *a.free_used);
+  const uint32_t up = (uint32_t)a.page_size - 1;
   Sums done = {0, 0};
-  for (int base = 0; base < a.n_seqs; base += kScanThreads) {
-    const int r = base + threadIdx.x;
-    const bool in = r < a.n_seqs;
-    const int64_t c = in ? a.cached_lens[r] : 0, n = in ? a.new_lens[r] : 0;
-    const int64_t limit = (int64_t)a.max_pages * a.page_size;
-    const bool valid = in && c >= 0 && n >= 0 && c + n <= limit;
-    const uint32_t up = (uint32_t)a.page_size - 1;
-    const uint32_t held = valid ? by_page.div((uint32_t)c + up) : 0;
-    int32_t* row = a.block_table + (int64_t)r * a.ld_table;
-    int page = -1;  // that the first new token continues
-    if constexpr (ONE) {
-      if (alone && valid && n > 0 && held > 0) page = row[held - 1];
+  for (int64_t base = 0; base < a.n_seqs; base += kScanThreads * PER) {
+    const int64_t r0 = base + threadIdx.x * PER;
+    int cached[PER], news[PER], pages[PER];  // pages: the one that the first new token continues
+    Sums mine = {0, 0};
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const bool in = r0 + k < a.n_seqs;
+      cached[k] = in ? a.cached_lens[r0 + k] : 0;
+      news[k] = in ? a.new_lens[r0 + k] : 0;
     }
+    const int64_t limit = (int64_t)a.max_pages * a.page_size;
+    auto valid = [&](int k) {
+      return r0 + k < a.n_seqs && cached[k] >= 0 && news[k] >= 0 && (int64_t)cached[k] + news[k] <= limit;
+    };
+    auto pages_held = [&](int k) { return valid(k) ? by_page.div((uint32_t)cached[k] + up) : 0u; };
     // A request past the slot map's end is followed by such only, so that its pages, which are counted here though it
     // cannot have them, change nothing for those that fit.
-    const int64_t need = valid ? (int64_t)by_page.div((uint32_t)(c + n) + up) - held : 0;
+    auto pages_needed = [&](int k) -> int64_t {
+      return valid(k) ? by_page.div((uint32_t)cached[k] + (uint32_t)news[k] + up) - pages_held(k) : 0;
+    };
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const uint32_t held = pages_held(k);
+      pages[k] = -1;
+      if constexpr (ONE) {
+        if (own(k) && news[k] > 0 && held > 0) pages[k] = a.block_table[(r0 + k) * a.ld_table + held - 1];
+      }
+      mine = mine + Sums{max(news[k], 0), pages_needed(k)};
+    }
     Sums sum;
-    const Sums to = done + block_scan(Sums{n > 0 ? n : 0, need}, sums, sum);
+    const Sums upto_mine = block_scan(mine, sums, sum);
+    Sums to = {done.tokens + upto_mine.tokens - mine.tokens, done.pages + upto_mine.pages - mine.pages};
     done = done + sum;
-    const int64_t end = to.tokens, upto = used + to.pages;
-    const bool fits = valid && end <= a.max_tokens;
-    const bool served = fits && (need == 0 || upto <= a.n_free);
-    if (in) {
-      const int32_t start = (int32_t)min(end - (n > 0 ? n : 0), (int64_t)a.max_tokens);
-      const int32_t first = served ? (int32_t)min(upto - need, (int64_t)a.n_free) : -1;
+    int64_t got = -1;  // pages gone with this thread's last request that gets any
+    int32_t start[PER], first[PER], fresh[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int64_t need = pages_needed(k), start_all = to.tokens, first_all = used + to.pages;
+      to = to + Sums{max(news[k], 0), need};
+      const bool served = valid(k) && to.tokens <= a.max_tokens && (need == 0 || used + to.pages <= a.n_free);
+      start[k] = (int32_t)min(start_all, (int64_t)a.max_tokens);
+      first[k] = served ? (int32_t)min(first_all, (int64_t)a.n_free) : -1;
+      fresh[k] = -1;
+      if (served && need > 0) {
+        got = to.pages;
+        if constexpr (ONE) {
+          if (own(k) && news[k] <= kOwn) fresh[k] = a.free_pages[first[k]];
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int64_t r = r0 + k;
+      if (r >= a.n_seqs) break;
       if (writes) {
-        a.token_starts[r] = start;
-        a.seq_lens[r] = (int32_t)(served ? c + n : c);
-        a.first_pages[r] = first;
+        a.token_starts[r] = start[k];
+        a.seq_lens[r] = first[k] >= 0 ? cached[k] + news[k] : cached[k];
+        a.first_pages[r] = first[k];
       }
       if constexpr (ONE) {
-        lds_starts[r] = start;
-        lds_first[r] = first;
-        lds_cached[r] = (int32_t)c;
-        if (n > kOwn) {
+        lds_starts[r] = start[k];
+        lds_first[r] = first[k];
+        lds_cached[r] = cached[k];
+        if (news[k] > kOwn) {
           lds_many = 1;
-        } else if (alone && n > 0) {
-          int fresh = -1;
-          if (served && need > 0) row[held] = fresh = a.free_pages[upto - need];
-          const int64_t own = (int64_t)held * a.page_size;  // positions that held pages have
-          for (int i = 0; i < n && start + i < a.max_tokens; ++i) {
-            const int64_t pos = c + i, off = pos - (pos < own ? own - a.page_size : own);
-            const int p = pos < own ? page : fresh;
+        } else if (own(k) && news[k] > 0) {
+          const int64_t held = pages_held(k), own = held * a.page_size;  // positions that held pages have
+          if (first[k] >= 0 && pages_needed(k) > 0) a.block_table[r * a.ld_table + held] = fresh[k];
+          for (int i = 0; i < news[k] && start[k] + i < a.max_tokens; ++i) {
+            const int64_t pos = (int64_t)cached[k] + i, off = pos - (pos < own ? own - a.page_size : own);
+            const int p = pos < own ? pages[k] : fresh[k];
             const int64_t slot = (int64_t)p * a.page_size + off;
-            a.slot_map[start + i] = served && p >= 0 && slot <= INT32_MAX ? (int32_t)slot : -1;
+            a.slot_map[start[k] + i] = first[k] >= 0 && p >= 0 && slot <= INT32_MAX ? (int32_t)slot : -1;
           }
         }
       }
     }
     // whoever gets pages comes before whoever does not: the last of them says how many are gone
-    const uint64_t got = __ballot(served && need > 0);
-    if (got && (int)(threadIdx.x & 63) == 63 - __builtin_clzll(got))
-      atomicMax(&taken, (unsigned long long)(upto - used));
+    const uint64_t some = __ballot(got >= 0);
+    if (some && (int)(threadIdx.x & 63) == 63 - __builtin_clzll(some))
+      atomicMax(&taken, (unsigned long long)got);
   }
   __syncthreads();
   const int last = (int)min(done.tokens, (int64_t)a.max_tokens);
@@ -216,7 +253,8 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
   }
   if constexpr (ONE) {
     if (!lds_many) {
-      for (int64_t t = (int64_t)last + threadIdx.x; t < a.max_tokens; t += kScanThreads) a.slot_map[t] = -1;
+      if (writes)
+        for (int64_t t = (int64_t)last + threadIdx.x; t < a.max_tokens; t += kScanThreads) a.slot_map[t] = -1;
       return;
     }
     if (threadIdx.x == 0) lds_starts[a.n_seqs] = last;
@@ -241,11 +279,14 @@ hipError_t launch_kv_block_table(const BlockTableArgs& a, hipStream_t stream) {
   const bool in_place = a.seq_lens == a.cached_lens || a.free_used_out == a.free_used;
   if (a.n_seqs <= kInLds && a.max_tokens <= (in_place ? kOneWorkgroup : kOneLaunch)) {
     const int per_block = kScanThreads * kPerThread;
-    const int blocks = a.max_tokens <= kOneWorkgroup ? 1 : (a.max_tokens + per_block - 1) / per_block;
-    kv_table_scan<true><<<blocks, kScanThreads, 0, stream>>>(a, by_page);
+    const int blocks = a.max_tokens > kOneWorkgroup ? (a.max_tokens + per_block - 1) / per_block
+                       : a.n_seqs <= kScanThreads || in_place ? 1 : kMany;
+    if (a.n_seqs <= kScanThreads) kv_table_scan<true, 1><<<blocks, kScanThreads, 0, stream>>>(a, by_page);
+    else kv_table_scan<true, kMany><<<blocks, kScanThreads, 0, stream>>>(a, by_page);
     return hipGetLastError();
   }
-  kv_table_scan<false><<<1, kScanThreads, 0, stream>>>(a, by_page);
+  if (a.n_seqs <= kScanThreads) kv_table_scan<false, 1><<<1, kScanThreads, 0, stream>>>(a, by_page);
+  else kv_table_scan<false, kMany><<<1, kScanThreads, 0, stream>>>(a, by_page);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t per_block = (int64_t)kSpreadThreads * kPerThread;

@@ -91,6 +91,25 @@ def test_block_table_serves_what_fits(gpu_lib, n, page, in_place):
                 check_table(gpu_lib, c, w, page, short, used, table, tokens, in_place)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("long", [0, 9, 500])
+def test_block_table_of_many_short_requests(gpu_lib, in_place, long):
+    """More requests than a workgroup has threads, each with a few tokens, or one of them with more."""
+    rng = np.random.default_rng([7, long])
+    n, page = 2501, 8
+    c, w, table, free = table_case(rng, n, page, 80, 50, 3, 70)
+    w[rng.random(n) < 0.3] = 0
+    if long:
+        w[1700] = long
+    w[40], c[2222] = -1, 2 ** 31 - 1
+    total = int(np.clip(w, 0, 1000).sum())
+    for share in (0.5, 1.0):
+        short = free[:int(len(free) * share)]
+        for tokens in (total // 2, total, total + 100):
+            log("block table, many", in_place, long, len(short), tokens)
+            check_table(gpu_lib, c, w, page, short, 3, table, tokens, in_place)
+
+
 def test_block_table_slots_past_31_bits(gpu_lib):
     page = 1024
     free = np.array([2 ** 21 - 1, 2 ** 21, 2 ** 31 - 1, -5])
