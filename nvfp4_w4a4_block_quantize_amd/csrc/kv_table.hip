@@ -17,8 +17,8 @@
 // Latency decides, so there is one launch where that is less: up to kInLds
 // requests, every workgroup makes the sums for itself, keeps what it needs of them
 // in LDS and spreads its tokens; the first one writes them down (1000 requests,
-// 150 thousand tokens: 8.5 us, 11.5 with a second kernel that spreads them; 96
-// requests, 1.6 million: 13.6 and 11.1).  In place (seq_lens is cached_lens, or
+// 150 thousand tokens: 8.5 us, 11.4 with a second kernel that spreads them; 96
+// requests, 1.6 million: 13.6 and 10.5).  In place (seq_lens is cached_lens, or
 // free_used_out is free_used) that holds for a single workgroup only, since the
 // others could find lengths that the first one has moved on already.
 //
@@ -39,11 +39,12 @@ namespace {
 constexpr int kScanThreads = 1024;
 constexpr int kScanWaves = kScanThreads / 64;
 constexpr int kSpreadThreads = 256;
+constexpr int kSpreadLds = 1024;    // requests that a workgroup of the second launch keeps in LDS
 constexpr int kPerThread = 4;       // tokens, one 16-byte store
 constexpr int kInLds = 4096;        // requests whose sums a workgroup keeps in LDS
 constexpr int kMany = kInLds / kScanThreads;  // neighbouring requests of a thread, where there are more than threads
 constexpr int kOwn = 8;             // tokens of a request, at most one fresh page among them
-constexpr int kOneWorkgroup = 8192; // slots that workgroups which place tokens themselves fill in less time than more of them
+constexpr int kOneWorkgroup = 8192; // slots up to which requests' own threads may place them, and a single workgroup does it in place
 constexpr int kOneLaunch = 1 << 19; // slots up to which making the sums again in every workgroup takes less
 
 // What spreading the tokens needs of the requests' sums: in LDS, or as they were written down.
@@ -266,10 +267,25 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
   }
 }
 
+// LDS: what is needed of the requests is loaded at once, not one dependent load after another
+template <bool LDS>
 __global__ __launch_bounds__(kSpreadThreads) void kv_table_spread(BlockTableArgs a, FastDiv by_page) {
   const WrittenSums all{a.token_starts, a.first_pages, a.seq_lens, a.new_lens};
   const int64_t t0 = ((int64_t)blockIdx.x * kSpreadThreads + threadIdx.x) * kPerThread;
-  if (t0 < a.max_tokens) spread4(a, by_page, all, (int)t0);
+  if constexpr (LDS) {
+    __shared__ int32_t starts[kSpreadLds + 1], first[kSpreadLds], cached[kSpreadLds];
+    for (int r = threadIdx.x; r <= a.n_seqs; r += kSpreadThreads) {
+      starts[r] = all.start(r);
+      if (r < a.n_seqs) {
+        first[r] = all.first_page(r);
+        cached[r] = all.cached_len(r);
+      }
+    }
+    __syncthreads();
+    if (t0 < a.max_tokens) spread4(a, by_page, LdsSums{starts, first, cached}, (int)t0);
+  } else {
+    if (t0 < a.max_tokens) spread4(a, by_page, all, (int)t0);
+  }
 }
 
 }  // namespace
@@ -279,8 +295,8 @@ hipError_t launch_kv_block_table(const BlockTableArgs& a, hipStream_t stream) {
   const bool in_place = a.seq_lens == a.cached_lens || a.free_used_out == a.free_used;
   if (a.n_seqs <= kInLds && a.max_tokens <= (in_place ? kOneWorkgroup : kOneLaunch)) {
     const int per_block = kScanThreads * kPerThread;
-    const int blocks = a.max_tokens > kOneWorkgroup ? (a.max_tokens + per_block - 1) / per_block
-                       : a.n_seqs <= kScanThreads || in_place ? 1 : kMany;
+    const int spread = (a.max_tokens + per_block - 1) / per_block;  // at most
+    const int blocks = in_place ? 1 : a.n_seqs <= kScanThreads ? spread : std::max(spread, kMany);
     if (a.n_seqs <= kScanThreads) kv_table_scan<true, 1><<<blocks, kScanThreads, 0, stream>>>(a, by_page);
     else kv_table_scan<true, kMany><<<blocks, kScanThreads, 0, stream>>>(a, by_page);
     return hipGetLastError();
@@ -291,7 +307,8 @@ hipError_t launch_kv_block_table(const BlockTableArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   const int64_t per_block = (int64_t)kSpreadThreads * kPerThread;
   const int64_t blocks = ((int64_t)a.max_tokens + per_block - 1) / per_block;
-  kv_table_spread<<<(unsigned)blocks, kSpreadThreads, 0, stream>>>(a, by_page);
+  if (a.n_seqs <= kSpreadLds) kv_table_spread<true><<<(unsigned)blocks, kSpreadThreads, 0, stream>>>(a, by_page);
+  else kv_table_spread<false><<<(unsigned)blocks, kSpreadThreads, 0, stream>>>(a, by_page);
   return hipGetLastError();
 }
 
