@@ -6,7 +6,8 @@
 //   cache[page][head][offset][:], slot = page * page_size + offset,
 // head_dim consecutive bytes.
 //
-// Bandwidth kernel: 2 B read and 1 B written per bf16 element.  One thread takes 16
+// Bandwidth kernel: 2 B read and 1 B written per bf16 element (32768 tokens, 4
+// heads of 256 in rows of 14336: 38 us, 5.3 TB/s).  One thread takes 16
 // consecutive elements (8 where head_dim is no multiple of 16) and stores 16
 // bytes at once.  More pieces a thread were no faster on long prompts and slower
 // on short calls (32 tokens, 4 heads of 256: 2.3 us, 3.2 with four pieces).
@@ -18,6 +19,11 @@
 //   neither                                          42.3       65     6.8
 // (a lane's four float32 loads share their lines).  So many rows of a 16-bit type
 // are loaded past them, and all others are stored past them.
+//
+// Where that many rows are strided, K's and V's of a token lie in one projection's
+// row, and workgroups take them in turns of kRun: 38 us with 64 or 256, 41 with 1024,
+// 45 with all of K first (the same 32768 tokens in rows of 14336).  Dense rows gain
+// nothing (36.3 and 35.9 us for 32768 tokens of 8 x 128) and take K first.
 #include "nvfp4_device.h"
 #include "kv_internal.h"
 
@@ -25,6 +31,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr uint32_t kRun = 256;
 constexpr int64_t kManyElements = 1 << 24;  // of K: 64 MiB with V, a quarter of the Infinity Cache
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
@@ -61,11 +68,13 @@ __device__ __forceinline__ uint32_t e4m3x4(float y0, float y1, float y2, float y
 
 template <int DT, int E, bool PAST>
 __global__ __launch_bounds__(kThreads) void kv_cache_write_kernel(CacheWriteArgs a, FastDiv by_row, FastDiv by_head,
-                                                                  FastDiv by_page, int64_t chunks) {
-  const bool value = blockIdx.y != 0;  // K, then V
+                                                                  FastDiv by_page, FastDiv by_run, int64_t chunks) {
+  const uint32_t turn = PAST ? by_run.div(blockIdx.x) : blockIdx.y;
+  const uint32_t block = PAST ? (turn >> 1) * by_run.d + blockIdx.x - turn * by_run.d : blockIdx.x;
+  const bool value = turn & 1;  // K, then V
   const HeadsIn in = value ? a.v : a.k;
   const float s = value ? *a.v_scale : *a.k_scale;
-  const int64_t first = (int64_t)blockIdx.x * kThreads;
+  const int64_t first = (int64_t)block * kThreads;
   const int64_t token0 = first / by_row.d;  // one division for the workgroup; the rest fits 32 bits
   const uint32_t at = (uint32_t)(first - token0 * by_row.d) + threadIdx.x;
   const uint32_t t = by_row.div(at), in_row = at - t * by_row.d;
@@ -97,9 +106,12 @@ template <int DT, int E, bool PAST>
 hipError_t launch_chunks(const CacheWriteArgs& a, hipStream_t stream) {
   const uint32_t of_head = (uint32_t)(a.head_dim / E), of_row = (uint32_t)a.kv_heads * of_head;
   const int64_t chunks = a.tokens * of_row, blocks = (chunks + kThreads - 1) / kThreads;
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  kv_cache_write_kernel<DT, E, PAST><<<dim3((unsigned)blocks, 2), kThreads, 0, stream>>>(
-      a, FastDiv(of_row), FastDiv(of_head), FastDiv((uint32_t)a.page_size), chunks);
+  if (blocks > INT32_MAX / 4) return hipErrorInvalidValue;
+  const bool strided = a.k.token != (int64_t)a.kv_heads * a.head_dim;
+  const uint32_t all = (uint32_t)blocks, run = PAST && strided && all > kRun ? kRun : all;
+  const dim3 grid = PAST ? dim3((all + run - 1) / run * run * 2) : dim3(all, 2);
+  kv_cache_write_kernel<DT, E, PAST><<<grid, kThreads, 0, stream>>>(
+      a, FastDiv(of_row), FastDiv(of_head), FastDiv((uint32_t)a.page_size), FastDiv(run), chunks);
   return hipGetLastError();
 }
 

@@ -247,6 +247,31 @@ def test_cache_write(gpu_lib, dtype, tokens, heads, dim, page, gap):
         assert np.array_equal(host(got), want)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("tokens,heads,dim,page", [(17001, 8, 128, 48), (4099, 16, 256, 8), (120011, 3, 48, 256)])
+@pytest.mark.parametrize("strided", [False, True])
+def test_cache_write_of_long_prompts(gpu_lib, dtype, tokens, heads, dim, page, strided):
+    """Rows that do not fit the caches, alone or inside wider rows, against torch's cast of the same products."""
+    g = torch.Generator("cuda").manual_seed(tokens)
+    wide = torch.randn(tokens, heads * (3 if strided else 1), dim, generator=g, device="cuda").mul_(60).to(DTYPES[dtype])
+    k, v = (wide[:, heads:2 * heads], wide[:, 2 * heads:]) if strided else (wide, wide.flip(0).contiguous())
+    pages = tokens // page + 3
+    slots = torch.randperm(pages * page, generator=g, device="cuda")[:tokens].to(torch.int32)
+    slots[::97] = -1
+    scales = dev([2.3, 9.7], torch.float32)
+    ck, cv = (torch.full((pages, heads, page, dim), 0x55, dtype=torch.uint8, device="cuda") for _ in range(2))
+    log("cache write, long", dtype, tokens, heads, dim, page, strided)
+    gpu_lib.nvfp4_kv_cache_write(k, v, scales[:1], scales[1:], slots, ck, cv)
+    torch.cuda.synchronize()
+    kept = slots >= 0
+    at = slots[kept].long()
+    for got, x, scale in ((ck, k, scales[0]), (cv, v, scales[1])):
+        want = torch.full_like(got, 0x55)
+        code = (x[kept].float() * scale).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        want[at // page, :, at % page] = code
+        assert torch.equal(got, want)
+
+
 # --------------------------------------------------------------------- attention
 
 def attention_case(rng, lens, heads, kv_heads, dim, page, dtype, sharpen=2.0, columns=None):
