@@ -103,16 +103,24 @@ __global__ __launch_bounds__(kThreads) void kv_cache_write_kernel(CacheWriteArgs
 }
 
 template <int DT, int E, bool PAST>
-hipError_t launch_chunks(const CacheWriteArgs& a, hipStream_t stream) {
+hipError_t launch_chunks(CacheWriteArgs a, hipStream_t stream) {
   const uint32_t of_head = (uint32_t)(a.head_dim / E), of_row = (uint32_t)a.kv_heads * of_head;
-  const int64_t chunks = a.tokens * of_row, blocks = (chunks + kThreads - 1) / kThreads;
-  if (blocks > INT32_MAX / 4) return hipErrorInvalidValue;
   const bool strided = a.k.token != (int64_t)a.kv_heads * a.head_dim;
-  const uint32_t all = (uint32_t)blocks, run = PAST && strided && all > kRun ? kRun : all;
-  const dim3 grid = PAST ? dim3((all + run - 1) / run * run * 2) : dim3(all, 2);
-  kv_cache_write_kernel<DT, E, PAST><<<grid, kThreads, 0, stream>>>(
-      a, FastDiv(of_row), FastDiv(of_head), FastDiv((uint32_t)a.page_size), FastDiv(run), chunks);
-  return hipGetLastError();
+  for (int64_t left = a.tokens;;) {
+    a.tokens = std::min(left, std::max<int64_t>(kMostWorkgroups * kThreads / of_row, 1));
+    const int64_t chunks = a.tokens * of_row;
+    const uint32_t all = (uint32_t)((chunks + kThreads - 1) / kThreads), run = PAST && strided && all > kRun ? kRun : all;
+    const dim3 grid = PAST ? dim3((all + run - 1) / run * run * 2) : dim3(all, 2);
+    kv_cache_write_kernel<DT, E, PAST><<<grid, kThreads, 0, stream>>>(
+        a, FastDiv(of_row), FastDiv(of_head), FastDiv((uint32_t)a.page_size), FastDiv(run), chunks);
+    const hipError_t e = hipGetLastError();
+    left -= a.tokens;
+    if (e != hipSuccess || left == 0) return e;
+    auto behind = [&](HeadsIn x) { return static_cast<const char*>(x.p) + a.tokens * x.token * (DT == 0 ? 4 : 2); };
+    a.k.p = behind(a.k);
+    a.v.p = behind(a.v);
+    a.slot_map += a.tokens;
+  }
 }
 
 template <int DT>

@@ -24,6 +24,9 @@ struct FastDiv {
 #endif
 };
 
+// of a launch: the grid's threads are counted in 32 bits, and larger calls go in pieces
+constexpr int64_t kMostWorkgroups = 1 << 20;
+
 struct BlockTableArgs {
   int n_seqs;
   const int32_t *cached_lens, *new_lens;

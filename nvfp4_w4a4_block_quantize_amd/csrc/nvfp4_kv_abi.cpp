@@ -203,7 +203,7 @@ nvfp4_status nvfp4_paged_attention(int64_t n_seqs, int64_t q_heads, int64_t kv_h
   if (es == 0) return NVFP4_ERR_DTYPE;
   if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.0f)) return NVFP4_ERR_RANGE;
   if (!size_ok(n_seqs) || !attention_heads_ok(q_heads, kv_heads, head_dim) || n_seqs * q_heads >= kMaxDim ||
-      window < 0 || !cache_ok(num_pages, page_size) || !table_ok(max_pages, page_size, ld_table) ||
+      window < 0 || q == out || !cache_ok(num_pages, page_size) || !table_ok(max_pages, page_size, ld_table) ||
       max_pages * page_size * q_heads > kMaxReach ||
       !strides_ok(q_heads, head_dim, q_token, q_head) || !strides_ok(q_heads, head_dim, out_token, out_head))
     return NVFP4_ERR_SHAPE;

@@ -378,7 +378,8 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
 
   const float ks = *a.k_scale, inv_vs = 1.0f / *a.v_scale;
   const double c64 = (double)a.softmax_scale * 1.44269504088896340736 / (double)ks;
-  const float c_hi = (float)c64, c_lo = DT == 0 ? (float)(c64 - (double)c_hi) : 0.0f;
+  // never 0, so that it leaves the -infinity of tokens that are not seen
+  const float c_hi = fmaxf((float)c64, 0x1p-149f), c_lo = DT == 0 ? (float)(c64 - (double)c_hi) : 0.0f;
 
   while (u < u_end && seq < n) {
     const int4 span = seq_span(p, seq);
@@ -749,7 +750,7 @@ template <int DT, int D, int NQ>
 hipError_t launch(Params p, hipStream_t stream) {
   const PagedAttentionArgs& a = p.a;
   int64_t tokens = (int64_t)a.max_pages * a.page_size;  // of the longest item
-  if (a.window > 0) tokens = std::min<int64_t>(tokens, (int64_t)a.window + kUnitTokens);
+  if (a.window > 0 && a.window < tokens) tokens = std::min(tokens, a.window + kUnitTokens);
   const int64_t units = (tokens + kUnitTokens - 1) / kUnitTokens, items = (int64_t)a.n_seqs * p.items;
   const int64_t resident = (int64_t)device_cu_count() * workers_per_cu<DT, D, NQ>();
   // Unsplit, a call lasts as long as its longest item; split, as all tokens take on the resident workers, and some 8 us
@@ -757,7 +758,8 @@ hipError_t launch(Params p, hipStream_t stream) {
   //   units of an item     5           9            9            9             13            17            17           63
   //   items  64 of 512    256 of 512   512 of 512   128 of 512    128 of 512    512 of 512    512 of 1024  512 of 512
   //         9.7 / 11.0  21.2 / 27.1  19.1 / 26.2  15.3 / 14.7   25.7 / 21.1   32.4 / 36.6   23.4 / 22.9  113 / 105
-  p.whole = units <= 6 || (units <= 20 && units * resident <= 20 * items);
+  const bool launchable = items <= kMostWorkgroups;
+  p.whole = launchable && (units <= 6 || (units <= 20 && units * resident <= 20 * items));
   const int workers = (int)(p.whole ? items : std::min<int64_t>(resident, items * (units + kItemCost)));
   p.by_item = !p.whole && items <= workers;
   paged_attention_kernel<DT, D, NQ><<<workers, kThreads, 0, stream>>>(p);

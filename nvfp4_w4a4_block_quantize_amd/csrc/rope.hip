@@ -176,7 +176,7 @@ bool all_in_place(const RopeArgs& a) { return a.q_out.p == a.q.p && (a.k_heads =
 bool some_in_place(const RopeArgs& a) { return a.q_out.p == a.q.p || (a.k_heads > 0 && a.k_out.p == a.k.p); }
 
 template <int DT, int VEC, int COPY, bool ADJACENT, bool ALIGNED>
-hipError_t launch_vec(const RopeArgs& a, hipStream_t stream) {
+hipError_t launch_vec(RopeArgs a, hipStream_t stream) {
   Plan p;
   p.pairs = a.rot_dim / 2;
   const uint32_t heads = (uint32_t)(a.q_heads + a.k_heads);
@@ -187,21 +187,33 @@ hipError_t launch_vec(const RopeArgs& a, hipStream_t stream) {
   p.by_copy = FastDiv((uint32_t)(copy + COPY - 1) / COPY);
   p.turning = heads * p.by_turn.d;
   p.token_items = p.turning + heads * p.by_copy.d;
-  p.items = a.tokens * (int64_t)p.token_items;
   p.by_token = FastDiv(p.token_items);
   p.by_pair = FastDiv((uint32_t)p.pairs);
-  // a run of n items that begins and ends inside a token touches at most this many tokens
-  auto lds = [&](int64_t n) {
-    return (size_t)std::min<int64_t>(a.tokens, (n - 2) / p.token_items + 2) * p.pairs * sizeof(float2);
-  };
-  const bool more = lds(kMore * kThreads) <= kLdsMost && p.items >= (int64_t)device_cu_count() * kMore * kThreads;
-  const int64_t n = more ? kMore * kThreads : kThreads, blocks = (p.items + n - 1) / n;
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  if (more)
-    rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, kMore><<<(unsigned)blocks, kThreads, lds(n), stream>>>(a, p);
-  else
-    rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, 1><<<(unsigned)blocks, kThreads, lds(n), stream>>>(a, p);
-  return hipGetLastError();
+  for (int64_t left = a.tokens;;) {
+    a.tokens = std::min(left, std::max<int64_t>(kMostWorkgroups * kThreads / p.token_items, 1));
+    p.items = a.tokens * (int64_t)p.token_items;
+    // a run of n items that begins and ends inside a token touches at most this many tokens
+    auto lds = [&](int64_t n) {
+      return (size_t)std::min<int64_t>(a.tokens, (n - 2) / p.token_items + 2) * p.pairs * sizeof(float2);
+    };
+    const bool more = lds(kMore * kThreads) <= kLdsMost && p.items >= (int64_t)device_cu_count() * kMore * kThreads;
+    const int64_t n = more ? kMore * kThreads : kThreads, blocks = (p.items + n - 1) / n;
+    if (more)
+      rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, kMore><<<(unsigned)blocks, kThreads, lds(n), stream>>>(a, p);
+    else
+      rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, 1><<<(unsigned)blocks, kThreads, lds(n), stream>>>(a, p);
+    const hipError_t e = hipGetLastError();
+    left -= a.tokens;
+    if (e != hipSuccess || left == 0) return e;
+    auto skip = [&](auto& x) {
+      if (x.p) x.p = (decltype(x.p))((uintptr_t)x.p + (uintptr_t)(a.tokens * x.token) * sizeof(typename Elem<DT>::type));
+    };
+    skip(a.q);
+    skip(a.q_out);
+    skip(a.k);
+    skip(a.k_out);
+    a.positions += a.tokens;
+  }
 }
 
 template <int DT, bool ADJACENT>

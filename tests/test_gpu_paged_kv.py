@@ -168,6 +168,29 @@ def test_rope(gpu_lib, dtype, adjacent, tokens, q_heads, k_heads, dim, rot):
     assert torch.equal(again, q_out) and (k is None or torch.equal(key, k_out))
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_rope_of_more_than_one_launch(gpu_lib, in_place):
+    tokens, q_heads, k_heads = (1 << 20) + 3, 250, 7
+    g = torch.Generator("cuda").manual_seed(2)
+    wide = torch.randn(tokens, q_heads + k_heads, 2, generator=g, device="cuda", dtype=torch.bfloat16)
+    q, k = wide[:, :q_heads], wide[:, q_heads:]
+    positions = torch.randint(-2 ** 31, 2 ** 31 - 1, (2, tokens), generator=g, device="cuda", dtype=torch.int32)
+    at = torch.cat([torch.arange(a, b) for a, b in ((0, 3), (1044494 - 3, 1044494 + 3), (tokens - 3, tokens))]).cuda()
+    was, out = wide[at], {"q_out": q, "k_out": k} if in_place else {}
+    log("rope, pieces", in_place)
+    q_out, k_out = gpu_lib.nvfp4_rope(q, k, positions, dev([0.37], torch.float32), dev([1]), **out)
+    torch.cuda.synchronize()
+    got = torch.cat([q_out[at], k_out[at]], 1)
+    check_rope(got, was, host(positions[:, at]), np.array([0.37], np.float32), np.array([1]), False, "bf16")
+    if in_place:  # every token turned once: lengths stay, to two roundings
+        size = lambda x: x.double().square().sum()
+        before = torch.Generator("cuda").manual_seed(2)
+        before = size(torch.randn(tokens, q_heads + k_heads, 2, generator=before, device="cuda", dtype=torch.bfloat16))
+        assert abs(size(wide) / before - 1) <= 2.0 ** -7
+    del wide, q, k, q_out, k_out
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("adjacent", [False, True])
 @pytest.mark.parametrize("which", ["q", "k"])
 def test_rope_one_tensor_in_place(gpu_lib, adjacent, which):
@@ -272,6 +295,30 @@ def test_cache_write_of_long_prompts(gpu_lib, dtype, tokens, heads, dim, page, s
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("tokens,heads,dim,strided", [((1 << 18) + 5, 1024, 8, False), ((1 << 19) + 3, 32, 256, True)])
+def test_cache_write_of_more_than_one_launch(gpu_lib, tokens, heads, dim, strided):
+    g = torch.Generator("cuda").manual_seed(tokens)
+    wide = torch.randn(tokens, heads * (2 if strided else 1), dim, generator=g, device="cuda", dtype=torch.bfloat16)
+    k = wide[:, -heads:]
+    at = np.unique(np.concatenate([[0, 1, tokens - 1], (1 << 18) + np.arange(-3, 5), (1 << 19) + np.arange(-2, 3)]))
+    at = at[at < tokens]
+    slots = torch.full((tokens,), -1, dtype=torch.int32, device="cuda")
+    slots[torch.from_numpy(at).cuda()] = torch.arange(len(at), dtype=torch.int32, device="cuda") + 1
+    scales = dev([100.0, 200.0], torch.float32)
+    ck, cv = (torch.full((4, heads, 8, dim), 0x55, dtype=torch.uint8, device="cuda") for _ in range(2))
+    log("cache write, pieces", tokens, heads, dim, strided)
+    gpu_lib.nvfp4_kv_cache_write(k, k, scales[:1], scales[1:], slots, ck, cv)
+    torch.cuda.synchronize()
+    for got, scale in ((ck, 100.0), (cv, 200.0)):
+        want = torch.full_like(got, 0x55)
+        code = (k[torch.from_numpy(at).cuda()].float() * scale).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        slot = torch.arange(len(at), device="cuda") + 1
+        want[slot // 8, :, slot % 8] = code
+        assert torch.equal(got, want)
+    del wide, k
+    torch.cuda.empty_cache()
+
+
 # --------------------------------------------------------------------- attention
 
 def attention_case(rng, lens, heads, kv_heads, dim, page, dtype, sharpen=2.0, columns=None):
@@ -352,7 +399,72 @@ def test_attention_batches_with_few_live_rows(gpu_lib, n, live):
     check_attention(gpu_lib, q, k, v, table, lens)
 
 
-@pytest.mark.parametrize("window", [1, 5, 8, 100, 128, 1000, 2 ** 40])
+@pytest.mark.parametrize("dtype,dim,heads,kv_heads,page", [
+    ("f32", 64, 6, 1, 8), ("bf16", 256, 10, 2, 24), ("f16", 128, 34, 2, 16), ("bf16", 192, 40, 1, 1024), ("f16", 256, 1, 1, 48)])
+@pytest.mark.parametrize("window", [0, 40])
+def test_attention_short_lengths_in_wide_tables(gpu_lib, dtype, dim, heads, kv_heads, page, window):
+    """Tables with room for sequences that would be split."""
+    rng = np.random.default_rng([dim, heads, page, 1])
+    log("attention wide tables", dtype, dim, heads, kv_heads, page, window)
+    q, k, v, table = attention_case(rng, SHORT, heads, kv_heads, dim, page, dtype, columns=20000 // page)
+    check_attention(gpu_lib, q, k, v, table, SHORT, window=window, dtype=dtype)
+
+
+@pytest.mark.parametrize("n,live,by", [(1100, [0, 1, 600, 1099], 1), (2500, [2499], 7), (900, range(900), 3), (400, [], 1)])
+def test_attention_batches_with_few_live_rows_in_wide_tables(gpu_lib, n, live, by):
+    rng = np.random.default_rng([n, 1])
+    lens = np.zeros(n, int)
+    lens[list(live)] = rng.integers(1, 900 if len(live) < 10 else 60, len(live))
+    lens[::by] = np.where(lens[::by] == 0, -3, lens[::by])
+    log("attention live rows, wide tables", n, len(live))
+    q, k, v, table = attention_case(rng, lens, 4, 2, 64, 16, "bf16", columns=600)
+    check_attention(gpu_lib, q, k, v, table, lens)
+
+
+@pytest.mark.parametrize("most,n,kv_heads", [(1200, 130, 8), (2500, 128, 4), (2600, 128, 4), (760, 3, 1), (770, 3, 1)])
+@pytest.mark.parametrize("window", [0, 500])
+def test_attention_of_items_that_may_be_split_or_not(gpu_lib, most, n, kv_heads, window):
+    """Sizes to both sides of where items stop being split; the lengths stop at the table's end."""
+    rng = np.random.default_rng([most, n])
+    lens = rng.integers(0, 200, n)
+    lens[:3] = [most, most - 1, most + 7]
+    log("attention split or not", most, n, kv_heads, window)
+    columns = -(-most // 16)
+    q, k, v, table = attention_case(rng, lens, 2 * kv_heads, kv_heads, 128, 16, "bf16", columns=columns)
+    check_attention(gpu_lib, q, k, v, table, np.minimum(lens, columns * 16), window=window)
+
+
+def test_attention_of_a_million_sequences(gpu_lib):
+    """More (sequence, KV head) items than one launch has workgroups."""
+    n = (1 << 20) + 7
+    g = torch.Generator("cuda").manual_seed(1)
+    q = torch.randn(n, 1, 64, generator=g, device="cuda").to(torch.bfloat16)
+    cache = torch.randint(0, 0x7F, (50, 1, 8, 64), generator=g, device="cuda", dtype=torch.uint8)
+    table = torch.randint(0, 50, (n, 1), generator=g, device="cuda", dtype=torch.int32)
+    lens = torch.randint(0, 2, (n,), generator=g, device="cuda", dtype=torch.int32)
+    s = dev([20.0], torch.float32)
+    log("attention, a million sequences")
+    lse = torch.empty(n, 1, device="cuda")
+    got = gpu_lib.nvfp4_paged_attention(q, cache, cache.clone(), s, s, table, lens, lse=lse)
+    torch.cuda.synchronize()
+    # one token: its value itself, which has 4 bits (a division by 20 and the output's rounding)
+    want = torch.where((lens > 0)[:, None], cache.view(torch.float8_e4m3fn).double()[table[:, 0].long(), 0, 0] / 20, 0.0)
+    assert ((got[:, 0].double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20)).all()
+    assert torch.equal(torch.isneginf(lse[:, 0]), lens == 0)
+
+
+def test_attention_of_scales_next_to_nothing(gpu_lib):
+    """All tokens weigh the same, and those behind the last one still nothing."""
+    rng = np.random.default_rng(17)
+    lens = [1, 45, 300, 0]
+    for dtype in ("bf16", "f32"):
+        q, k, v, table = attention_case(rng, lens, 4, 2, 128, 16, dtype)
+        for scale in (1e-40, 1.5e-45):
+            log("attention scale", dtype, scale)
+            check_attention(gpu_lib, q, k, v, table, lens, scale=scale, dtype=dtype)
+
+
+@pytest.mark.parametrize("window", [1, 5, 8, 100, 128, 1000, 2 ** 40, 2 ** 63 - 1])
 def test_attention_window(gpu_lib, window):
     lens = [1, 3, 99, 100, 101, 900, 3001, 0]
     rng = np.random.default_rng(window)

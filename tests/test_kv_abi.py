@@ -71,7 +71,7 @@ def calls(lib):
                     "n hq hk dim dtype q qt qh ck cv pages page ks vs table max_pages ld lens scale window out ot oh lse ws bytes "
                     "stream",
                     dict(n=4, hq=8, hk=2, dim=64, dtype=1, q=P, qt=512, qh=64, ck=P, cv=2 * P, pages=8, page=16, ks=P, vs=P,
-                         table=P, max_pages=8, ld=8, lens=P, scale=0.125, window=0, out=P, ot=512, oh=64, lse=None, ws=P,
+                         table=P, max_pages=8, ld=8, lens=P, scale=0.125, window=0, out=2 * P, ot=512, oh=64, lse=None, ws=P,
                          bytes=1 << 28, stream=None))
     return {"table": table, "rope": rope, "write": write, "attend": attend}
 
@@ -98,7 +98,7 @@ REFUSED = {
     + [(DTYPE, "dtype", 5), (RANGE, "scale", 0.0), (RANGE, "scale", -1.0), (RANGE, "scale", math.inf), (RANGE, "scale", math.nan),
        (SHAPE, "n", 0), (SHAPE, "hq", 0), (SHAPE, "hq", 7), (SHAPE, "hk", 3), (SHAPE, "dim", 96), (SHAPE, "dim", 32),
        (SHAPE, "window", -1), (SHAPE, "pages", 0), (SHAPE, "pages", BIG // 16), (SHAPE, "page", 4), (SHAPE, "max_pages", 9),
-       (SHAPE, "max_pages", 0), (SHAPE, "qt", 448), (SHAPE, "oh", 32), (SHAPE, "bytes", 1024), (SHAPE, "bytes", -1),
+       (SHAPE, "max_pages", 0), (SHAPE, "out", P), (SHAPE, "qt", 448), (SHAPE, "oh", 32), (SHAPE, "bytes", 1024), (SHAPE, "bytes", -1),
        (ALIGN, "q", P + 8), (ALIGN, "out", P + 4), (ALIGN, "qt", 516), (ALIGN, "ck", P + 8), (ALIGN, "lse", P + 2),
        (ALIGN, "ws", P + 8), (ALIGN, "table", P + 1), (ALIGN, "lens", P + 2), (ALIGN, "vs", P + 1)],
 }
