@@ -19,9 +19,10 @@
 // second, small kernel joins those.  Lengths are read on the device, so a captured
 // graph follows them.  Runs are one to a resident workgroup: with two or four of
 // them the ends are no more even (201 us: 209 and 228).  Where items are short, each
-// has a workgroup to itself instead, and nothing is joined (launch() says where).
+// has a workgroup to itself instead, of more waves where it has the CU to itself, and
+// nothing is joined (launch() says where).
 //
-// In a unit the workgroup's four waves take tiles of 32 tokens in turn and
+// The workgroup's waves (four of them for a unit) take tiles of 32 tokens in turn and
 // run on their own (maxima, sums and outputs of their own) until the item ends.
 // Nothing passes through LDS or between lanes on the way of the data:
 //  * S^T = K Q^T with v_mfma_16x16x32.  Lane (i = lane % 16, g = lane / 16) of
@@ -60,10 +61,9 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 32;                  // tokens of a wave's tile
-constexpr int kUnitTokens = kTile * kWaves;  // the smallest unit
+constexpr int kUnitTiles = 4;
+constexpr int kUnitTokens = kTile * kUnitTiles;  // the smallest unit
 constexpr int kItemCost = 1;  // what beginning and ending an item costs, in units
 constexpr int kMaxWorkersPerCu = 4;
 constexpr float kNoMax = -3.0e38f;         // a maximum before any score; finite, so differences are numbers
@@ -278,10 +278,21 @@ constexpr int workers_per_cu() {
   return D == 64 ? 4 : 2;
 }
 
-// NQ: 16-column tiles of queries (an item has at most 16 NQ query heads)
+// Waves of a workgroup that has a CU to itself: four to each SIMD, or what its registers hold.
 template <int DT, int D, int NQ>
-__global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged_attention_kernel(Params p) {
+constexpr int wide_waves() {
+  const int held = workers_per_cu<DT, D, NQ>();
+  return held >= 4 ? 16 : held >= 2 ? 8 : 4;
+}
+
+// NQ: 16-column tiles of queries (an item has at most 16 NQ query heads).  Workgroups of more than four waves are for
+// items that are not split.
+template <int DT, int D, int NQ, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, (kWaves == 4 ? workers_per_cu<DT, D, NQ>() : kWaves / 4)) void
+paged_attention_kernel(Params p) {
 #if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int kThreads = 64 * kWaves;
+  const bool no_split = kWaves > 4 || p.whole;
   constexpr int KS = D / 64, ND = D / 16, VB = D / 16, VW = D / 64;
   constexpr int PP = DT == 1 ? 1 : 2;  // parts of a probability: what the output type can tell
   const PagedAttentionArgs& a = p.a;
@@ -324,7 +335,7 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
     }
   };
 
-  if (p.whole) {  // one item
+  if (no_split) {  // one item
     seq = worker / p.items;
     inside = worker - seq * p.items;
     if (uniform(seq_span(p, seq).w) == 0) {
@@ -394,10 +405,10 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
       continue;
     }
     // the run's part in this item
-    const int length = p.whole ? 1 : per_item + kItemCost;
+    const int length = no_split ? 1 : per_item + kItemCost;
     const int item = (int)((uint32_t)inside / (uint32_t)length), from = (int)inside - item * length;
     const int take = (int)min((int64_t)(length - from), u_end - u);
-    const int unit0 = max(from - kItemCost, 0), unit1 = p.whole ? per_item : from + take - kItemCost;
+    const int unit0 = max(from - kItemCost, 0), unit1 = no_split ? per_item : from + take - kItemCost;
     const int64_t begin = u - from;
     u += take;
     inside += take;
@@ -435,8 +446,8 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
       return good;
     };
     const int tiles = (len - origin + kTile - 1) / kTile;
-    const int tile_end = min(unit1 * kWaves, tiles);
-    int tile = unit0 * kWaves + wave;
+    const int tile_end = min(unit1 * kUnitTiles, tiles);
+    int tile = unit0 * kUnitTiles + wave;
     Place now = find(tile), next = find(tile + kWaves);
 
     Query<DT> q[NQ][2 * KS];
@@ -652,13 +663,13 @@ __global__ __launch_bounds__(kThreads, (workers_per_cu<DT, D, NQ>())) void paged
         }
       }
     }
-    if (unit0 == 0 && !p.whole) {
+    if (unit0 == 0 && !no_split) {
       // the item's last unit is that of the first worker whose run ends behind it
       if (!ends) split = make_int4(in, item, worker, (int)(((begin + length) * workers + units - 1) / units) - 1);
       if (p.by_item && tid == 0) p.ws.split[in * p.items + item] = split;
     }
   }
-  if (p.whole) return;
+  if (no_split) return;
   if (!p.by_item && tid == 0) p.ws.split[worker] = split;
   clear_empty();
 #endif
@@ -752,17 +763,30 @@ hipError_t launch(Params p, hipStream_t stream) {
   int64_t tokens = (int64_t)a.max_pages * a.page_size;  // of the longest item
   if (a.window > 0 && a.window < tokens) tokens = std::min(tokens, a.window + kUnitTokens);
   const int64_t units = (tokens + kUnitTokens - 1) / kUnitTokens, items = (int64_t)a.n_seqs * p.items;
-  const int64_t resident = (int64_t)device_cu_count() * workers_per_cu<DT, D, NQ>();
+  const int64_t cus = device_cu_count(), resident = cus * workers_per_cu<DT, D, NQ>();
   // Unsplit, a call lasts as long as its longest item; split, as all tokens take on the resident workers, and some 8 us
-  // more, for the scan of the lengths, the partial results and the second kernel.  Unsplit against split, in us:
-  //   units of an item     5           9            9            9             13            17            17           63
-  //   items  64 of 512    256 of 512   512 of 512   128 of 512    128 of 512    512 of 512    512 of 1024  512 of 512
-  //         9.7 / 11.0  21.2 / 27.1  19.1 / 26.2  15.3 / 14.7   25.7 / 21.1   32.4 / 36.6   23.4 / 22.9  113 / 105
-  const bool launchable = items <= kMostWorkgroups;
-  p.whole = launchable && (units <= 6 || (units <= 20 && units * resident <= 20 * items));
+  // more, for the scan of the lengths, the partial results and the second kernel.  With a CU to itself an item has more
+  // waves, and takes 4 us and 0.7 for a unit of heads of 128 (0.5 with 64, 1.5 with 256).  Unsplit against split, in us:
+  //   one to a CU, heads of 128:
+  //     units of an item         3            9           12           17           15           19           32
+  //     items                   16           32           64           64          128          128          256
+  //                         6.2 / 10.3  10.5 / 11.2  13.4 / 14.5  16.2 / 15.0  15.9 / 17.8  19.0 / 18.1  32.8 / 34.9
+  //   (heads of 64, 32 items of 6 and 16 units: 7.8 / 10.0 and 12.8 / 11.0; of 256, 64 of 6 and 128 of 13: 13.8 / 14.7
+  //   and 23.3 / 21.5), and the same items in workgroups of four waves: 32 of 9 units 14.9, 64 of 5 units 9.8 for 7.7
+  //   more than that, or too many registers for it:
+  //     items, of what the CUs hold  512 of 512   1600 of 512   128 of 512   512 of 1024  512 of 512
+  //     units                             9            17            9            17           63
+  //                                  19.1 / 26.2  83.1 / 87.4  15.3 / 14.7  23.4 / 22.9  113 / 105
+  constexpr int kWide = wide_waves<DT, D, NQ>();
+  const bool wide = kWide > 4 && items <= cus;
+  p.whole = items <= kMostWorkgroups && (wide ? units * std::max(D, 104) * cus <= 128 * (9 * cus + 23 * items)
+                                              : units <= 6 || (units <= 20 && units * resident <= 20 * items));
   const int workers = (int)(p.whole ? items : std::min<int64_t>(resident, items * (units + kItemCost)));
   p.by_item = !p.whole && items <= workers;
-  paged_attention_kernel<DT, D, NQ><<<workers, kThreads, 0, stream>>>(p);
+  if (wide && p.whole)
+    paged_attention_kernel<DT, D, NQ, kWide><<<workers, 64 * kWide, 0, stream>>>(p);
+  else
+    paged_attention_kernel<DT, D, NQ, 4><<<workers, 256, 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.whole) return e;
   // Few items are shared by many workers each: then slices of 64 outputs, to have more readers.

@@ -410,6 +410,19 @@ def test_attention_short_lengths_in_wide_tables(gpu_lib, dtype, dim, heads, kv_h
     check_attention(gpu_lib, q, k, v, table, SHORT, window=window, dtype=dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("heads,kv_heads", [(8, 2), (40, 2)])
+def test_attention_of_many_short_sequences(gpu_lib, dtype, dim, heads, kv_heads):
+    """More items than CUs, each short enough for a workgroup of its own."""
+    rng = np.random.default_rng([dim, heads, 3])
+    lens = rng.integers(-5, 140, 140)
+    log("attention many short", dtype, dim, heads)
+    q, k, v, table = attention_case(rng, lens, heads, kv_heads, dim, 16, dtype)
+    check_attention(gpu_lib, q, k, v, table, lens, dtype=dtype)
+    check_attention(gpu_lib, q, k, v, table, lens, window=33, dtype=dtype)
+
+
 @pytest.mark.parametrize("n,live,by", [(1100, [0, 1, 600, 1099], 1), (2500, [2499], 7), (900, range(900), 3), (400, [], 1)])
 def test_attention_batches_with_few_live_rows_in_wide_tables(gpu_lib, n, live, by):
     rng = np.random.default_rng([n, 1])
