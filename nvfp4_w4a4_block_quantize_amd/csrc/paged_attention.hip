@@ -118,15 +118,16 @@ __device__ __forceinline__ void store4(const PagedAttentionArgs& a, int seq, int
   *reinterpret_cast<Four*>(p) = Four{{(T)v.x, (T)v.y, (T)v.z, (T)v.w}};
 }
 
-// {tokens, first seen token, where tiles begin, units} of a sequence
-__device__ __forceinline__ int4 seq_span(const Params& p, int seq) {
+// {tokens, first seen token, where tiles begin, units} of a sequence of length `given`
+__device__ __forceinline__ int4 span_of(const Params& p, int given) {
   const PagedAttentionArgs& a = p.a;
-  const int64_t most = (int64_t)a.max_pages * a.page_size;
-  const int len = (int)min((int64_t)max(a.seq_lens[seq], 0), most);
+  const int len = min(max(given, 0), a.max_pages * a.page_size);
   const int start = a.window > 0 && a.window < len ? len - (int)a.window : 0;
   const int origin = start & ~7;  // groups of eight tokens share a page
   return make_int4(len, start, origin, (len - origin + kUnitTokens - 1) / kUnitTokens);
 }
+
+__device__ __forceinline__ int4 seq_span(const Params& p, int seq) { return span_of(p, p.a.seq_lens[seq]); }
 
 // a sequence's length on the axis of work
 __device__ __forceinline__ int64_t cost(const Params& p, int seq) {
@@ -300,6 +301,7 @@ paged_attention_kernel(Params p) {
   __shared__ float lds_m[kWaves][16], lds_l[kWaves][16];
   __shared__ int64_t lds_sum[kWaves + 1];
   __shared__ int64_t lds_first[2];
+  __shared__ int lds_given;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
@@ -309,6 +311,7 @@ paged_attention_kernel(Params p) {
   int seq = 0;                        // where this worker's run begins:
   int64_t inside = 0, u = 0, u_end = 1;  // how far into the sequence, and where on the axis of work it begins and ends
   int64_t units = 1, workers = 1;
+  int given = 0;  // the length of the run's first sequence
   int4 split = make_int4(-1, 0, 0, 0);
 
   // no token seen: zeros for the query heads h0 .. h1 - 1 of a sequence, by `count` threads of which this is the i-th
@@ -338,7 +341,8 @@ paged_attention_kernel(Params p) {
   if (no_split) {  // one item
     seq = worker / p.items;
     inside = worker - seq * p.items;
-    if (uniform(seq_span(p, seq).w) == 0) {
+    given = uniform(a.seq_lens[seq]);
+    if (span_of(p, given).w == 0) {
       const int head = (int)inside / p.parts, first = head * p.group + ((int)inside - head * p.parts) * p.rows;
       clear(seq, first, min(first + p.rows, (head + 1) * p.group), tid, kThreads);
       return;
@@ -381,19 +385,18 @@ paged_attention_kernel(Params p) {
       for (int64_t c; at + (c = cost(p, s)) <= u; at += c) ++s;
       lds_first[0] = s;
       lds_first[1] = u - at;
+      lds_given = a.seq_lens[s];
     }
     __syncthreads();
     seq = uniform((int)lds_first[0]);
     inside = uniform(lds_first[1]);
+    given = uniform(lds_given);
   }
 
-  const float ks = *a.k_scale, inv_vs = 1.0f / *a.v_scale;
-  const double c64 = (double)a.softmax_scale * 1.44269504088896340736 / (double)ks;
-  // never 0, so that it leaves the -infinity of tokens that are not seen
-  const float c_hi = fmaxf((float)c64, 0x1p-149f), c_lo = DT == 0 ? (float)(c64 - (double)c_hi) : 0.0f;
-
+  bool first = true;
   while (u < u_end && seq < n) {
-    const int4 span = seq_span(p, seq);
+    const int4 span = span_of(p, first ? given : a.seq_lens[seq]);
+    first = false;
     const int len = uniform(span.x), start = uniform(span.y), origin = uniform(span.z), per_item = uniform(span.w);
     if (per_item == 0) {  // the next one with units, of which there are some ahead
       uint64_t some = 0;
@@ -474,6 +477,9 @@ paged_attention_kernel(Params p) {
       bool good = place(now, at);
       load_k(r, a.k_cache, at, col, grp);
       load_v(r, a.v_cache, at, col, grp);
+      const double c64 = (double)a.softmax_scale * 1.44269504088896340736 / (double)*a.k_scale;
+      // never 0, so that it leaves the -infinity of tokens that are not seen
+      const float c_hi = fmaxf((float)c64, 0x1p-149f), c_lo = DT == 0 ? (float)(c64 - (double)c_hi) : 0.0f;
       while (true) {
         const bool more = tile + kWaves < tile_end;
 
@@ -609,7 +615,8 @@ paged_attention_kernel(Params p) {
       }
     }
 
-    // The four waves' results into one, 16 query heads at a time.
+    // The waves' results into one, 16 query heads at a time.
+    const float inv_vs = 1.0f / *a.v_scale;
     const bool ends = unit0 == 0 && unit1 == per_item;  // the whole item
     const int slot = 2 * worker + (unit0 == 0 ? 1 : 0);
 #pragma unroll
