@@ -68,20 +68,18 @@ __device__ __forceinline__ uint32_t e4m3x4(float y0, float y1, float y2, float y
 
 template <int DT, int E, bool PAST>
 __global__ __launch_bounds__(kThreads) void kv_cache_write_kernel(CacheWriteArgs a, FastDiv by_row, FastDiv by_head,
-                                                                  FastDiv by_page, FastDiv by_run, int64_t chunks) {
+                                                                  FastDiv by_page, FastDiv by_run, uint32_t chunks) {
   const uint32_t turn = PAST ? by_run.div(blockIdx.x) : blockIdx.y;
   const uint32_t block = PAST ? (turn >> 1) * by_run.d + blockIdx.x - turn * by_run.d : blockIdx.x;
   const bool value = turn & 1;  // K, then V
   const HeadsIn in = value ? a.v : a.k;
   const float s = value ? *a.v_scale : *a.k_scale;
-  const int64_t first = (int64_t)block * kThreads;
-  const int64_t token0 = first / by_row.d;  // one division for the workgroup; the rest fits 32 bits
-  const uint32_t at = (uint32_t)(first - token0 * by_row.d) + threadIdx.x;
+  const uint32_t at = block * kThreads + threadIdx.x;  // a launch has at most 2^28 chunks, and a row 2^23
   const uint32_t t = by_row.div(at), in_row = at - t * by_row.d;
   const uint32_t head = by_head.div(in_row), chunk = in_row - head * by_head.d;
   // no branch before the store, which would wait for what it asks (39.4 us for 37.2, 32768 tokens of 8 x 128)
-  const bool inside = first + threadIdx.x < chunks;
-  const int64_t token = inside ? token0 + t : 0;
+  const bool inside = at < chunks;
+  const int64_t token = inside ? t : 0;
   const int slot = a.slot_map[token];  // asked for before the elements: loads return in order
   Raw<DT, E, PAST> raw;
   raw.load(in.p, token * in.token + head * in.head + chunk * E);
@@ -108,8 +106,8 @@ hipError_t launch_chunks(CacheWriteArgs a, hipStream_t stream) {
   const bool strided = a.k.token != (int64_t)a.kv_heads * a.head_dim;
   for (int64_t left = a.tokens;;) {
     a.tokens = std::min(left, std::max<int64_t>(kMostWorkgroups * kThreads / of_row, 1));
-    const int64_t chunks = a.tokens * of_row;
-    const uint32_t all = (uint32_t)((chunks + kThreads - 1) / kThreads), run = PAST && strided && all > kRun ? kRun : all;
+    const uint32_t chunks = (uint32_t)(a.tokens * of_row), all = (chunks + kThreads - 1) / kThreads;
+    const uint32_t run = PAST && strided && all > kRun ? kRun : all;
     const dim3 grid = PAST ? dim3((all + run - 1) / run * run * 2) : dim3(all, 2);
     kv_cache_write_kernel<DT, E, PAST><<<grid, kThreads, 0, stream>>>(
         a, FastDiv(of_row), FastDiv(of_head), FastDiv((uint32_t)a.page_size), FastDiv(run), chunks);

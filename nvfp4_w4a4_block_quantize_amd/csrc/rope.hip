@@ -9,7 +9,7 @@
 // into LDS, and all heads of q and k use them.
 //
 // Bandwidth kernel: every element is read once and written once (8192 tokens, 28
-// heads of 256 in bf16, 64 of them turning: 46 us, 5.1 TB/s, where a copy of that
+// heads of 256 in bf16, 64 of them turning: 41 us, 5.7 TB/s, where a copy of that
 // size reaches 5.5; 4099 tokens, 18 heads of 128 in f32: 13.6 us).  The loads are
 // issued before the angles are computed, which hides them.  A workgroup owns a
 // run of consecutive items of the flat list (token; turning or copied; head; item
@@ -37,7 +37,7 @@ struct Plan {
   int turn_last, copy_last;  // where the last vector of a head's turning and copied part begins
   uint32_t turning;    // items of a token that turn; those that are copied follow them
   uint32_t token_items;
-  int64_t items;
+  uint32_t items;
   FastDiv by_token, by_turn, by_copy, by_pair;  // items of a token, and of a head that turn and that are copied
 };
 
@@ -87,10 +87,9 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Plan p) {
   constexpr int kItems = kThreads * kUnroll;
   extern __shared__ float2 turns[];  // [token of this workgroup][pair] cosine and sine
 
-  const int64_t item0 = (int64_t)blockIdx.x * kItems;
-  const int64_t token0 = item0 / p.token_items;
-  const uint32_t skip = (uint32_t)(item0 - token0 * p.token_items);
-  const int count = (int)min((int64_t)kItems, p.items - item0);
+  const uint32_t item0 = blockIdx.x * kItems;  // a launch has fewer than 2^29 items
+  const uint32_t token0 = p.by_token.div(item0), skip = item0 - token0 * p.token_items;
+  const int count = (int)min((uint32_t)kItems, p.items - item0);
   const int tokens = (int)(p.by_token.div(skip + count - 1)) + 1;
 
   V x[kUnroll], y[kUnroll];
@@ -108,13 +107,14 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Plan p) {
     const uint32_t t = p.by_token.div(at), in_token = at - t * p.token_items;
     const bool turn = in_token < p.turning;
     const uint32_t i = turn ? in_token : in_token - p.turning;
-    const FastDiv& by = turn ? p.by_turn : p.by_copy;
-    uint32_t head = by.div(i);
-    const int item = (int)(i - head * by.d);
+    uint32_t head = turn ? p.by_turn.div(i) : p.by_copy.div(i);
+    const int item = (int)(i - head * (turn ? p.by_turn.d : p.by_copy.d));
     const bool key = head >= (uint32_t)a.q_heads;
     if (key) head -= a.q_heads;
-    const HeadsIn& hi = key ? a.k : a.q;
-    const HeadsOut& ho = key ? a.k_out : a.q_out;
+    // by value: a reference to either would be read from memory by each lane
+    const HeadsIn hi = {key ? a.k.p : a.q.p, key ? a.k.token : a.q.token, key ? a.k.head : a.q.head};
+    const HeadsOut ho = {key ? a.k_out.p : a.q_out.p, key ? a.k_out.token : a.q_out.token,
+                         key ? a.k_out.head : a.q_out.head};
     const int64_t token = token0 + t;
     const int e = turn ? min(item * VEC, p.turn_last) : min(a.rot_dim + item * COPY, p.copy_last);
     const T* in = static_cast<const T*>(hi.p) + token * hi.token + head * hi.head + e;
@@ -189,19 +189,23 @@ hipError_t launch_vec(RopeArgs a, hipStream_t stream) {
   p.token_items = p.turning + heads * p.by_copy.d;
   p.by_token = FastDiv(p.token_items);
   p.by_pair = FastDiv((uint32_t)p.pairs);
+  // Items of one vector are two to a thread, those of halves, which have two already, one: 8192 tokens, 28 heads of 256 of
+  // which 64 elements turn, 41 us (one: 44); 4099 tokens, 18 heads of 128 in f32, neighbours paired, 14.0 (15.7); but
+  // 32768 tokens, 40 heads of 128, halves, 123 (115); 4096, 72 heads of 192 with 64 turning, 41.2 (40.5).
+  const bool single = ADJACENT || 6 * p.by_turn.d <= p.by_copy.d;
   for (int64_t left = a.tokens;;) {
     a.tokens = std::min(left, std::max<int64_t>(kMostWorkgroups * kThreads / p.token_items, 1));
-    p.items = a.tokens * (int64_t)p.token_items;
+    p.items = (uint32_t)(a.tokens * p.token_items);
     // a run of n items that begins and ends inside a token touches at most this many tokens
     auto lds = [&](int64_t n) {
       return (size_t)std::min<int64_t>(a.tokens, (n - 2) / p.token_items + 2) * p.pairs * sizeof(float2);
     };
-    const bool more = lds(kMore * kThreads) <= kLdsMost && p.items >= (int64_t)device_cu_count() * kMore * kThreads;
-    const int64_t n = more ? kMore * kThreads : kThreads, blocks = (p.items + n - 1) / n;
+    const bool more = single && lds(kMore * kThreads) <= kLdsMost && p.items >= (uint32_t)device_cu_count() * kMore * kThreads;
+    const uint32_t n = more ? kMore * kThreads : kThreads, blocks = (p.items + n - 1) / n;
     if (more)
-      rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, kMore><<<(unsigned)blocks, kThreads, lds(n), stream>>>(a, p);
+      rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, kMore><<<blocks, kThreads, lds(n), stream>>>(a, p);
     else
-      rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, 1><<<(unsigned)blocks, kThreads, lds(n), stream>>>(a, p);
+      rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, 1><<<blocks, kThreads, lds(n), stream>>>(a, p);
     const hipError_t e = hipGetLastError();
     left -= a.tokens;
     if (e != hipSuccess || left == 0) return e;
