@@ -8,28 +8,29 @@
 // A workgroup of 1024 threads scans the requests, one to a thread or, where there are
 // more of them, four neighbours (4000 requests of 200 tokens: 12.6 us, 16.4 in four
 // rounds of one), with running sums of tokens and pages (64-bit: neither sum is
-// bounded by 32 bits before the limits are applied).  The tokens are then spread over threads, four consecutive ones
-// each: a thread finds its request by bisection in the starts and walks on from
-// there.  The thread whose token opens a page also enters it in the block table,
-// so fresh pages cost no pass of their own and nobody reads an entry that this
-// call writes.
+// bounded by 32 bits before the limits are applied).  The tokens are then spread
+// over threads, up to four consecutive ones each: a thread finds its request by
+// bisection in the starts and walks on from there.  The thread whose token opens a
+// page also enters it in the block table, so fresh pages cost no pass of their own
+// and nobody reads an entry that this call writes.
 //
 // Latency decides, so there is one launch where that is less: up to kInLds
 // requests, every workgroup makes the sums for itself, keeps what it needs of them
 // in LDS and spreads its tokens; the first one writes them down (1000 requests,
-// 150 thousand tokens: 8.5 us, 11.4 with a second kernel that spreads them; 96
-// requests, 1.6 million: 13.6 and 10.5).  In place (seq_lens is cached_lens, or
+// 150 thousand tokens: 6.7 us, 11.5 with a second kernel that spreads them; 96
+// requests, 1.6 million: 13.6 and 10.6).  In place (seq_lens is cached_lens, or
 // free_used_out is free_used) that holds for a single workgroup only, since the
 // others could find lengths that the first one has moved on already.
 //
-// A decode step's requests bring one token each: while no request brings more than
-// kOwn, threads place their requests' tokens themselves, with the page that a token
-// continues already loaded while the sums are made (256 requests: 4.4 us, 7.7 by
-// bisection).  Every request has a line of the block table to itself, so four
-// requests to a thread are placed by four workgroups (4096 requests: 10.0 us, 11.7
-// by one).  What is left is latency: a launch, the lengths, the sums, a page and
-// the stores, one after another.
+// A decode step's requests bring one token each.  Where the slot map has room for
+// kOwn tokens of each at most, and none brings more, threads place their requests'
+// tokens themselves, with the page that a token continues already loaded while the
+// sums are made (256 requests: 4.4 us, 5.5 by bisection).  More requests than
+// threads are placed faster by many workgroups (4096 requests: 10.2 and 9.9 us).
+// What is left is latency: a launch, the lengths, the sums, a page and the stores,
+// one after another.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_internal.h"
 
@@ -40,11 +41,11 @@ constexpr int kScanThreads = 1024;
 constexpr int kScanWaves = kScanThreads / 64;
 constexpr int kSpreadThreads = 256;
 constexpr int kSpreadLds = 1024;    // requests that a workgroup of the second launch keeps in LDS
-constexpr int kPerThread = 4;       // tokens, one 16-byte store
+constexpr int kPerThread = 4;       // tokens at most, one 16-byte store
 constexpr int kInLds = 4096;        // requests whose sums a workgroup keeps in LDS
 constexpr int kMany = kInLds / kScanThreads;  // neighbouring requests of a thread, where there are more than threads
 constexpr int kOwn = 8;             // tokens of a request, at most one fresh page among them
-constexpr int kOneWorkgroup = 8192; // slots up to which requests' own threads may place them, and a single workgroup does it in place
+constexpr int kOneWorkgroup = 8192; // slots that a single workgroup fills in less time than a second launch takes
 constexpr int kOneLaunch = 1 << 19; // slots up to which making the sums again in every workgroup takes less
 
 // What spreading the tokens needs of the requests' sums: in LDS, or as they were written down.
@@ -96,10 +97,10 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* wave_sums, Sums& total)
   return wave > 0 ? v + b : v;
 }
 
-// slots of tokens t0 .. t0+3
-template <typename Sums>
-__device__ __forceinline__ void spread4(const BlockTableArgs& a, FastDiv by_page, const Sums& sums, int t0) {
-  int32_t slot[kPerThread];
+// slots of P tokens from t0
+template <int P, typename Sums>
+__device__ __forceinline__ void spread(const BlockTableArgs& a, FastDiv by_page, const Sums& sums, int t0) {
+  int32_t slot[P];
   // the last request that begins at or before t0; n_seqs: behind the last token
   int lo = 0, hi = a.n_seqs + 1;
   while (lo < hi) {
@@ -109,7 +110,7 @@ __device__ __forceinline__ void spread4(const BlockTableArgs& a, FastDiv by_page
   }
   int r = lo - 1, loaded = -1, first = 0, cached = 0, held = 0, begin = 0;
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
+  for (int i = 0; i < P; ++i) {
     const int t = t0 + i;
     while (r < a.n_seqs && sums.start(r + 1) <= t) ++r;
     slot[i] = -1;
@@ -137,29 +138,29 @@ __device__ __forceinline__ void spread4(const BlockTableArgs& a, FastDiv by_page
     if (page >= 0 && s <= INT32_MAX) slot[i] = (int32_t)s;
   }
   int32_t* out = a.slot_map + t0;
-  if (a.max_tokens - t0 >= kPerThread && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
-    *reinterpret_cast<int4*>(out) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i)
-      if (i < a.max_tokens - t0) out[i] = slot[i];
+  if constexpr (P == 4) {
+    if (a.max_tokens - t0 >= P && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+      *reinterpret_cast<int4*>(out) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      return;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (i < a.max_tokens - t0) out[i] = slot[i];
 }
 
-// ONE: the only launch, of one or more workgroups.  PER: neighbouring requests of a thread in a round
-template <bool ONE, int PER>
+// ONE: the only launch, of one or more workgroups.  OWN: the first of them places its threads' short requests right away.
+// PER: neighbouring requests of a thread in a round.  P: neighbouring tokens of a thread
+template <bool ONE, bool OWN, int PER, int P>
 __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, FastDiv by_page) {
   __shared__ Sums sums[kScanWaves];
   __shared__ int32_t lds_starts[ONE ? kInLds + 1 : 1], lds_first[ONE ? kInLds : 1], lds_cached[ONE ? kInLds : 1];
   __shared__ unsigned long long taken;
-  __shared__ int lds_many;  // whether some request brings more than kOwn tokens, or nothing is placed here
+  __shared__ int lds_many;  // whether some request brings more than kOwn tokens
   const bool writes = !ONE || blockIdx.x == 0;
-  // whether requests' tokens may be placed right here, and this workgroup's requests of each thread then
-  const bool places = ONE && a.max_tokens <= kOneWorkgroup;
-  auto own = [&](int k) { return places && (gridDim.x == 1 || k == (int)blockIdx.x); };
   if (threadIdx.x == 0) {
     taken = 0;
-    lds_many = !places;
+    lds_many = !OWN;
   }
   const int64_t used = max(0, *a.free_used);
   const uint32_t up = (uint32_t)a.page_size - 1;
@@ -188,8 +189,8 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
     for (int k = 0; k < PER; ++k) {
       const uint32_t held = pages_held(k);
       pages[k] = -1;
-      if constexpr (ONE) {
-        if (own(k) && news[k] > 0 && held > 0) pages[k] = a.block_table[(r0 + k) * a.ld_table + held - 1];
+      if constexpr (OWN) {
+        if (writes && news[k] > 0 && held > 0) pages[k] = a.block_table[(r0 + k) * a.ld_table + held - 1];
       }
       mine = mine + Sums{max(news[k], 0), pages_needed(k)};
     }
@@ -209,8 +210,8 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
       fresh[k] = -1;
       if (served && need > 0) {
         got = to.pages;
-        if constexpr (ONE) {
-          if (own(k) && news[k] <= kOwn) fresh[k] = a.free_pages[first[k]];
+        if constexpr (OWN) {
+          if (writes && news[k] <= kOwn) fresh[k] = a.free_pages[first[k]];
         }
       }
     }
@@ -227,9 +228,11 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
         lds_starts[r] = start[k];
         lds_first[r] = first[k];
         lds_cached[r] = cached[k];
+      }
+      if constexpr (OWN) {
         if (news[k] > kOwn) {
           lds_many = 1;
-        } else if (own(k) && news[k] > 0) {
+        } else if (writes && news[k] > 0) {
           const int64_t held = pages_held(k), own = held * a.page_size;  // positions that held pages have
           if (first[k] >= 0 && pages_needed(k) > 0) a.block_table[r * a.ld_table + held] = fresh[k];
           for (int i = 0; i < news[k] && start[k] + i < a.max_tokens; ++i) {
@@ -253,7 +256,7 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
     *a.free_used_out = (int32_t)(used + (int64_t)taken);
   }
   if constexpr (ONE) {
-    if (!lds_many) {
+    if (OWN && !lds_many) {
       if (writes)
         for (int64_t t = (int64_t)last + threadIdx.x; t < a.max_tokens; t += kScanThreads) a.slot_map[t] = -1;
       return;
@@ -261,9 +264,9 @@ __global__ __launch_bounds__(kScanThreads) void kv_table_scan(BlockTableArgs a, 
     if (threadIdx.x == 0) lds_starts[a.n_seqs] = last;
     __syncthreads();
     const LdsSums all{lds_starts, lds_first, lds_cached};
-    for (int64_t t0 = ((int64_t)blockIdx.x * kScanThreads + threadIdx.x) * kPerThread; t0 < a.max_tokens;
-         t0 += (int64_t)gridDim.x * kScanThreads * kPerThread)
-      spread4(a, by_page, all, (int)t0);
+    for (int64_t t0 = ((int64_t)blockIdx.x * kScanThreads + threadIdx.x) * P; t0 < a.max_tokens;
+         t0 += (int64_t)gridDim.x * kScanThreads * P)
+      spread<P>(a, by_page, all, (int)t0);
   }
 }
 
@@ -282,9 +285,9 @@ __global__ __launch_bounds__(kSpreadThreads) void kv_table_spread(BlockTableArgs
       }
     }
     __syncthreads();
-    if (t0 < a.max_tokens) spread4(a, by_page, LdsSums{starts, first, cached}, (int)t0);
+    if (t0 < a.max_tokens) spread<kPerThread>(a, by_page, LdsSums{starts, first, cached}, (int)t0);
   } else {
-    if (t0 < a.max_tokens) spread4(a, by_page, all, (int)t0);
+    if (t0 < a.max_tokens) spread<kPerThread>(a, by_page, all, (int)t0);
   }
 }
 
@@ -294,15 +297,26 @@ hipError_t launch_kv_block_table(const BlockTableArgs& a, hipStream_t stream) {
   const FastDiv by_page((uint32_t)a.page_size);
   const bool in_place = a.seq_lens == a.cached_lens || a.free_used_out == a.free_used;
   if (a.n_seqs <= kInLds && a.max_tokens <= (in_place ? kOneWorkgroup : kOneLaunch)) {
-    const int per_block = kScanThreads * kPerThread;
-    const int spread = (a.max_tokens + per_block - 1) / per_block;  // at most
-    const int blocks = in_place ? 1 : a.n_seqs <= kScanThreads ? spread : std::max(spread, kMany);
-    if (a.n_seqs <= kScanThreads) kv_table_scan<true, 1><<<blocks, kScanThreads, 0, stream>>>(a, by_page);
-    else kv_table_scan<true, kMany><<<blocks, kScanThreads, 0, stream>>>(a, by_page);
-    return hipGetLastError();
+    // as few tokens to a thread as leave no more workgroups than CUs (1000 requests, 150 thousand tokens: 6.7 us with one
+    // token, 7.3 with two, 8.6 with four; 4000 requests, 400 thousand tokens: 18, 11 and 12)
+    const int most = in_place ? 1 : device_cu_count(), work = (a.max_tokens + kScanThreads - 1) / kScanThreads;
+    auto launch = [&](auto own, auto per, auto p) {
+      constexpr int P = decltype(p)::value;
+      kv_table_scan<true, decltype(own)::value, decltype(per)::value, P>
+          <<<in_place ? 1 : (work + P - 1) / P, kScanThreads, 0, stream>>>(a, by_page);
+      return hipGetLastError();
+    };
+    auto spread_over = [&](auto own, auto per) {
+      if (work <= most) return launch(own, per, std::integral_constant<int, 1>());
+      if (work <= 2 * most) return launch(own, per, std::integral_constant<int, 2>());
+      return launch(own, per, std::integral_constant<int, kPerThread>());
+    };
+    if (a.n_seqs > kScanThreads) return spread_over(std::false_type(), std::integral_constant<int, kMany>());
+    if (a.max_tokens > kOwn * a.n_seqs) return spread_over(std::false_type(), std::integral_constant<int, 1>());
+    return spread_over(std::true_type(), std::integral_constant<int, 1>());
   }
-  if (a.n_seqs <= kScanThreads) kv_table_scan<false, 1><<<1, kScanThreads, 0, stream>>>(a, by_page);
-  else kv_table_scan<false, kMany><<<1, kScanThreads, 0, stream>>>(a, by_page);
+  if (a.n_seqs <= kScanThreads) kv_table_scan<false, false, 1, 1><<<1, kScanThreads, 0, stream>>>(a, by_page);
+  else kv_table_scan<false, false, kMany, 1><<<1, kScanThreads, 0, stream>>>(a, by_page);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t per_block = (int64_t)kSpreadThreads * kPerThread;
