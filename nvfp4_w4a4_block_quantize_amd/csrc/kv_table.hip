@@ -18,7 +18,7 @@
 // requests, every workgroup makes the sums for itself, keeps what it needs of them
 // in LDS and spreads its tokens; the first one writes them down (1000 requests,
 // 150 thousand tokens: 6.7 us, 11.5 with a second kernel that spreads them; 96
-// requests, 1.6 million: 13.6 and 10.6).  In place (seq_lens is cached_lens, or
+// requests, 1.6 million: 13.3 and 10.6).  In place (seq_lens is cached_lens, or
 // free_used_out is free_used) that holds for a single workgroup only, since the
 // others could find lengths that the first one has moved on already.
 //
