@@ -6,7 +6,7 @@
 //   slot(t) = page(pos / P) * P + pos % P for the new token at position pos.
 //
 // A workgroup of 1024 threads scans the requests, one to a thread or, where there are
-// more of them, four neighbours (4000 requests of 200 tokens: 12.6 us, 16.4 in four
+// more of them, four neighbours (4000 requests of 200 tokens: 3.8 us less than in four
 // rounds of one), with running sums of tokens and pages (64-bit: neither sum is
 // bounded by 32 bits before the limits are applied).  The tokens are then spread
 // over threads, up to four consecutive ones each: a thread finds its request by

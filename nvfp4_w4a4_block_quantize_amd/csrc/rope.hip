@@ -10,7 +10,7 @@
 //
 // Bandwidth kernel: every element is read once and written once (8192 tokens, 28
 // heads of 256 in bf16, 64 of them turning: 41 us, 5.7 TB/s, where a copy of that
-// size reaches 5.5; 4099 tokens, 18 heads of 128 in f32: 13.6 us).  The loads are
+// size reaches 5.5; 4099 tokens, 18 heads of 128 in f32: 13.8 us).  The loads are
 // issued before the angles are computed, which hides them.  A workgroup owns a
 // run of consecutive items of the flat list (token; turning or copied; head; item
 // of the head), so that a wave's lanes do the same.  An item is two vectors of a
