@@ -191,10 +191,9 @@ nvfp4_status nvfp4_kv_cache_write(int64_t tokens, int64_t kv_heads, int64_t head
  *
  * q, probabilities and values meet in matrix instructions: cache bytes are
  * exact in their 16-bit types, float32 queries are split into three bf16 parts
- * (nothing is lost), probabilities are rounded to fp16 (for fp16 and float32
- * outputs carried as two fp16 parts), sums, maxima and outputs are held in
- * fp32.  The result depends on the lengths, the window, the table's width and the device's
- * CU count, and is the same in every call.
+ * (nothing is lost), probabilities into two fp16 parts (22 bits), sums, maxima
+ * and outputs are held in fp32.  The result depends on the lengths, the window,
+ * the table's width and the device's CU count, and is the same in every call.
  *
  * Errors: NULL pointers -> ERR_NULL; sizes <= 0, head_dim not one of the four,
  * q_heads % kv_heads != 0, n_seqs * q_heads >= 2^31, max_pages * page_size *
