@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from tests import kv_reference as R
-from tests.test_gpu_paged_kv import DTYPES, dev, host, log
+from tests.test_gpu_paged_kv import DTYPES, dev, host, log, turn
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -63,3 +63,26 @@ def test_attention_of_values_that_cancel(gpu_lib, dtype, dim, heads, kv_heads, l
     assert (off <= b_out).all(), float((off / b_out).max())
     off = np.abs(host(lse) - want_lse)
     assert (off <= b_lse).all(), float((off / b_lse).max())
+
+
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("tokens", [40, 3000])
+def test_rope_near_the_zeros_of_sine_and_cosine(gpu_lib, adjacent, tokens):
+    """Pairs (1, 0) and (0, 1) become the cosine and sine themselves: each to a few steps of its own size."""
+    rng = np.random.default_rng(tokens)
+    pairs = 64
+    positions = rng.integers(-1000000, 1000000, (2, tokens))
+    inv_freq = (1e4 ** (-np.arange(pairs) / pairs)).astype(np.float32)
+    axes = np.arange(pairs) % 2
+    x = np.zeros((tokens, 2, 2 * pairs))
+    first = slice(0, None, 2) if adjacent else slice(0, pairs)
+    second = slice(1, None, 2) if adjacent else slice(pairs, None)
+    x[:, 0, first] = x[:, 1, second] = 1
+    log("rope, zeros", adjacent, tokens)
+    got, _ = turn(gpu_lib, dev(x, torch.float32), None, positions, inv_freq, axes, adjacent)
+    want, _ = R.rope(x, positions, inv_freq, axes, adjacent)
+    # two steps of the 32-bit sine and cosine (2^-23 each) and a rounding where the angle's low part is added; the angle
+    # itself to 2^-51, twice, of at most a million radians
+    bound = 5 * 2.0 ** -24 * np.abs(want) + 2.0 ** -30
+    off = np.abs(host(got) - want)
+    assert (off <= bound).all(), float((off / bound).max())
