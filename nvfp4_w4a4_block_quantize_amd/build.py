@@ -28,7 +28,8 @@ SOURCES = ["nvfp4_abi.cpp", "quantize.hip", "fuse_rescale.hip", "gemm.hip", "gem
            "nvfp4_kv_abi.cpp", "kv_table.hip", "rope.hip", "kv_cache_write.hip", "paged_attention.hip"]
 
 # the native side of the paged KV cache's Python binding: an extension module
-# beside the library, built against torch's headers
+# beside the library, built against torch's headers (without torch: not at all,
+# the C ABI does not need it)
 BIND_SRC = "kv_bind.cpp"
 BIND_PATH = os.path.join(HERE, "_kv_bind.so")
 
@@ -87,20 +88,26 @@ def _link_bind(obj: str):
     os.replace(BIND_PATH + ".tmp", BIND_PATH)
 
 
+def _has_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libnvfp4.so and the binding's module; returns the library path."""
+    """Compile every source and link libnvfp4.so, then the binding's module where torch is; returns the library path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=8) as ex:
-        bind = ex.submit(_compile_bind)
+        bind = ex.submit(_compile_bind) if _has_torch() else None
         objs = list(ex.map(_compile, SOURCES))
-        bind_obj = bind.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
-    _link_bind(bind_obj)
     # conformance check of the conversion instructions the kernels rely on
     # (a standalone program, run by the GPU tests)
     cmd = [HIPCC, *COMMON_FLAGS, CONFORMANCE_SRC, "-o", CONFORMANCE_PATH + ".tmp"]
@@ -115,7 +122,14 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc failed for bench_probes.hip:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(PROBES_PATH + ".tmp", PROBES_PATH)
     if verbose:
-        print(f"built {LIB_PATH}, {BIND_PATH}, {CONFORMANCE_PATH} and {PROBES_PATH}")
+        print(f"built {LIB_PATH}, {CONFORMANCE_PATH} and {PROBES_PATH}")
+    # last, so that nothing else is missing if it fails
+    if bind is not None:
+        _link_bind(bind.result())
+    elif os.path.exists(BIND_PATH):
+        os.remove(BIND_PATH)  # linked to an earlier library
+    if verbose:
+        print(f"built {BIND_PATH}" if bind is not None else f"no PyTorch: {BIND_PATH} is not built")
     return LIB_PATH
 
 

@@ -46,8 +46,11 @@ def _load():
 
     _torch = nv._torch()
     nv.load_library()  # raises if nothing is built
-    from . import _kv_bind
-
+    try:
+        from . import _kv_bind
+    except ModuleNotFoundError:
+        raise RuntimeError("_kv_bind.so is missing: it is built where PyTorch is installed "
+                           "(python -c 'import __graft_entry__ as g; g.build()')") from None
     _nv, _bind = nv, _kv_bind
 
 
