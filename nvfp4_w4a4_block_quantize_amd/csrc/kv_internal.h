@@ -70,6 +70,15 @@ struct RopeArgs {
   HeadsOut k_out;
   int k_heads;
 };
+
+// The heads (queries, then keys) whose elements past rot_dim are copied: those that are not turned in place.
+struct RopeCopied {
+  int first, count;
+};
+inline RopeCopied rope_copied(const RopeArgs& a) {
+  const int q = a.q_out.p == a.q.p ? 0 : a.q_heads, k = a.k_heads == 0 || a.k_out.p == a.k.p ? 0 : a.k_heads;
+  return {a.q_heads - q, q + k};
+}
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 
 struct CacheWriteArgs {

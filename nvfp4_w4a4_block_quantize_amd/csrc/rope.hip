@@ -18,7 +18,8 @@
 // issued before the angles are computed, which hides them.  A workgroup owns a
 // run of consecutive items of the flat list (token; turning or copied; head; item
 // of the head), so that a wave's lanes do the same.  An item is two vectors of a
-// head that turn together, or one vector past rot_dim that is copied, each as
+// head that turn together, or one vector past rot_dim that is copied (of heads that
+// are not turned in place), each as
 // wide as 16 bytes and the part of the head allow, at any alignment: a part's
 // last vector ends where the part ends and shares elements with the one before
 // (both store the same values).  In place, where nothing may be turned twice, a
@@ -40,6 +41,7 @@ struct Plan {
   int pairs;           // rot_dim / 2
   int turn_last, copy_last;  // where the last vector of a head's turning and copied part begins
   uint32_t turning;    // items of a token that turn; those that are copied follow them
+  uint32_t copy_from;  // the first head that is copied
   uint32_t token_items;
   uint32_t items;
   FastDiv by_token, by_turn, by_copy, by_pair;  // items of a token, and of a head that turn and that are copied
@@ -113,6 +115,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Plan p) {
     const uint32_t i = turn ? in_token : in_token - p.turning;
     uint32_t head = turn ? p.by_turn.div(i) : p.by_copy.div(i);
     const int item = (int)(i - head * (turn ? p.by_turn.d : p.by_copy.d));
+    if (!turn) head += p.copy_from;
     const bool key = head >= (uint32_t)a.q_heads;
     if (key) head -= a.q_heads;
     // by value: a reference to either would be read from memory by each lane
@@ -177,22 +180,23 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Plan p) {
   }
 }
 
-// whether all heads are turned in place, and whether some are
-bool all_in_place(const RopeArgs& a) { return a.q_out.p == a.q.p && (a.k_heads == 0 || a.k_out.p == a.k.p); }
-bool some_in_place(const RopeArgs& a) { return a.q_out.p == a.q.p || (a.k_heads > 0 && a.k_out.p == a.k.p); }
+// whether some heads are turned in place, and what each of the others copies
+bool some_in_place(const RopeArgs& a) { return rope_copied(a).count < a.q_heads + a.k_heads; }
+int copied(const RopeArgs& a) { return rope_copied(a).count > 0 ? a.head_dim - a.rot_dim : 0; }
 
 template <int DT, int VEC, int COPY, bool ADJACENT, bool ALIGNED>
 hipError_t launch_vec(RopeArgs a, hipStream_t stream) {
   Plan p;
   p.pairs = a.rot_dim / 2;
   const uint32_t heads = (uint32_t)(a.q_heads + a.k_heads);
-  const int turn = ADJACENT ? a.rot_dim : p.pairs, copy = all_in_place(a) ? 0 : a.head_dim - a.rot_dim;
+  const int turn = ADJACENT ? a.rot_dim : p.pairs, copy = copied(a);
   p.turn_last = turn - VEC;
   p.copy_last = a.head_dim - COPY;
   p.by_turn = FastDiv((uint32_t)(turn + VEC - 1) / VEC);
   p.by_copy = FastDiv((uint32_t)(copy + COPY - 1) / COPY);
   p.turning = heads * p.by_turn.d;
-  p.token_items = p.turning + heads * p.by_copy.d;
+  p.token_items = p.turning + (uint32_t)rope_copied(a).count * p.by_copy.d;
+  p.copy_from = (uint32_t)rope_copied(a).first;
   p.by_token = FastDiv(p.token_items);
   p.by_pair = FastDiv((uint32_t)p.pairs);
   // Items of one vector are two to a thread, those of halves, which have two already, one: 8192 tokens, 28 heads of 256 of
@@ -229,7 +233,7 @@ hipError_t launch_vec(RopeArgs a, hipStream_t stream) {
 template <int DT, bool ADJACENT>
 hipError_t launch_widest(const RopeArgs& a, hipStream_t stream) {
   constexpr int ES = DT == 0 ? 4 : 2, kFull = 16 / ES;
-  const int turn = ADJACENT ? a.rot_dim : a.rot_dim / 2, copy = all_in_place(a) ? 0 : a.head_dim - a.rot_dim;
+  const int turn = ADJACENT ? a.rot_dim : a.rot_dim / 2, copy = copied(a);
   int vec = kFull;
   while (some_in_place(a) ? turn % vec != 0 : vec > turn) vec /= 2;
   const bool wide = copy == 0 || copy >= kFull;

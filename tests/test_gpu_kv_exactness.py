@@ -86,3 +86,30 @@ def test_rope_near_the_zeros_of_sine_and_cosine(gpu_lib, adjacent, tokens):
     bound = 5 * 2.0 ** -24 * np.abs(want) + 2.0 ** -30
     off = np.abs(host(got) - want)
     assert (off <= bound).all(), float((off / bound).max())
+
+
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("adjacent", [False, True])
+def test_rope_leaves_the_rest_of_heads_in_place_alone(gpu_lib, adjacent, which):
+    """One tensor in place and the other not, while another stream writes what lies behind rot_dim in the first."""
+    rng = np.random.default_rng(41)
+    tokens, dim, rot, rounds = 6000, 256, 64, 12
+    positions, axes = dev(rng.integers(0, 4000, (1, tokens))), dev(np.zeros(rot // 2, int))
+    inv_freq = dev(1e4 ** (-np.arange(rot // 2) / (rot // 2)), torch.float32)
+    q, k = (dev(rng.standard_normal((tokens, h, dim)), torch.bfloat16) for h in (8, 8))
+    mine, other = (q, k) if which == "q" else (k, q)
+    out, before, side = torch.empty_like(other), mine.clone(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    log("rope, in place beside a writer", adjacent, which)
+    for i in range(rounds):
+        gpu_lib.nvfp4_rope(q, k, positions, inv_freq, axes, adjacent=adjacent, **{which + "_out": mine, "qk"[which == "q"] + "_out": out})
+        with torch.cuda.stream(side):
+            mine[:, :, rot:].fill_(float(i))
+    torch.cuda.synchronize()
+    assert (mine[:, :, rot:] == rounds - 1).all()
+    assert torch.equal(out[:, :, rot:], other[:, :, rot:])
+    again = before.clone()
+    for _ in range(rounds):
+        gpu_lib.nvfp4_rope(again, None, positions, inv_freq, axes, adjacent=adjacent, q_out=again)
+    torch.cuda.synchronize()
+    assert torch.equal(again[:, :, :rot], mine[:, :, :rot])
