@@ -19,11 +19,10 @@
 // run of consecutive items of the flat list (token; turning or copied; head; item
 // of the head), so that a wave's lanes do the same.  An item is two vectors of a
 // head that turn together, or one vector past rot_dim that is copied (of heads that
-// are not turned in place), each as
-// wide as 16 bytes and the part of the head allow, at any alignment: a part's
-// last vector ends where the part ends and shares elements with the one before
-// (both store the same values).  In place, where nothing may be turned twice, a
-// vector's width divides the part.
+// are not turned in place), each as wide as 16 bytes and the part of the head allow,
+// at any alignment: a part's last vector ends where the part ends and shares elements
+// with the one before (both store the same values).  In place, where nothing may be
+// turned twice, a vector's width divides the part.
 #include <algorithm>
 #include <type_traits>
 
@@ -74,14 +73,22 @@ struct alignas(ALIGNED ? sizeof(T) * VEC : sizeof(T)) Pack {
   T v[VEC];
 };
 
+// sixteen bytes at the alignment of a float32 or 16-bit element (a type's reduced alignment does not pass a template)
+typedef uint32_t u32x4_by4_t __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_by2_t __attribute__((ext_vector_type(4), aligned(2)));
+
 // Stores past the caches where they are as wide as that takes: the outputs of a prompt do not fit there, and
 // leave the other halves of the lines being read in place (8192 tokens, 28 heads of 256: 70 -> 47 us).
 template <typename V>
 __device__ __forceinline__ void store(void* p, const V& v) {
-  if constexpr (sizeof(V) == 16)
-    __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, v), reinterpret_cast<u32x4_t*>(p));
-  else
+  if constexpr (sizeof(V) != 16) {
     *reinterpret_cast<V*>(p) = v;
+  } else {
+    const u32x4_t w = __builtin_bit_cast(u32x4_t, v);
+    if constexpr (alignof(V) == 16) __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(p));
+    else if constexpr (alignof(V) == 4) __builtin_nontemporal_store(w, reinterpret_cast<u32x4_by4_t*>(p));
+    else __builtin_nontemporal_store(w, reinterpret_cast<u32x4_by2_t*>(p));
+  }
 }
 
 // VEC, COPY: elements of a turning and of a copied vector
