@@ -212,9 +212,9 @@ nvfp4_status nvfp4_paged_attention(int64_t n_seqs, int64_t q_heads, int64_t kv_h
                                    int64_t workspace_bytes, void* stream);
 
 /*
- * Bytes of workspace that nvfp4_paged_attention wants for these heads on the
- * current device, whatever the number and length of the sequences.  *bytes is
- * host memory, written before the call returns.
+ * Bytes of workspace that nvfp4_paged_attention wants for these heads, whatever
+ * the number and length of the sequences.  *bytes is host memory, written before
+ * the call returns.
  *
  * Errors: NULL bytes -> ERR_NULL; heads and head_dim as above -> ERR_SHAPE.
  */

@@ -109,6 +109,23 @@ struct PagedAttentionArgs {
   void* workspace;
 };
 hipError_t launch_paged_attention(const PagedAttentionArgs& a, hipStream_t stream);
-int64_t paged_attention_workspace(int q_heads, int kv_heads, int head_dim);
+
+// Workgroups of an attention call that leave partial results: up to four on each of an MI355X's CUs.  A number of its
+// own, so that the workspace's size can be checked without asking HIP.
+constexpr int kMaxCus = 256, kMaxWorkersPerCu = 4, kMostWorkers = kMaxCus * kMaxWorkersPerCu;
+
+// Query heads of an item: two tiles of 16 where the registers hold them, so that more queries meet each row that is
+// read.  They do not for float32 queries, which take three times the room, nor for heads of 256 (32 query heads on
+// one KV head, 32 contexts up to 16000: 61 us with 16 rows, 73 with 32, which spills; heads of 192: 84 and 66).
+inline int attention_rows_of_item(int group, bool f32, int head_dim) {
+  const int most = f32 || head_dim > 192 ? 16 : 32;
+  return group < most ? group : most;
+}
+
+// of the workspace: for each worker an entry of 16 bytes and two partial results of a maximum, a sum and outputs a row
+inline int64_t attention_workspace_bytes(int q_heads, int kv_heads, int head_dim) {
+  const int64_t rows = attention_rows_of_item(q_heads / kv_heads, false, head_dim);
+  return kMostWorkers * (16 + 2 * rows * (8 + 4 * (int64_t)head_dim));
+}
 
 }  // namespace nvfp4

@@ -185,7 +185,7 @@ nvfp4_status nvfp4_kv_cache_write(int64_t tokens, int64_t kv_heads, int64_t head
 nvfp4_status nvfp4_paged_attention_workspace(int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t* bytes) {
   if (!bytes) return NVFP4_ERR_NULL;
   if (!attention_heads_ok(q_heads, kv_heads, head_dim)) return NVFP4_ERR_SHAPE;
-  *bytes = nvfp4::paged_attention_workspace((int)q_heads, (int)kv_heads, (int)head_dim);
+  *bytes = nvfp4::attention_workspace_bytes((int)q_heads, (int)kv_heads, (int)head_dim);
   return NVFP4_OK;
 }
 
@@ -212,7 +212,7 @@ nvfp4_status nvfp4_paged_attention(int64_t n_seqs, int64_t q_heads, int64_t kv_h
       !aligned(v_scale, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) ||
       !aligned(workspace, 16))
     return NVFP4_ERR_ALIGN;
-  if (workspace_bytes < nvfp4::paged_attention_workspace((int)q_heads, (int)kv_heads, (int)head_dim))
+  if (workspace_bytes < nvfp4::attention_workspace_bytes((int)q_heads, (int)kv_heads, (int)head_dim))
     return NVFP4_ERR_SHAPE;
   if (!device_ok()) return NVFP4_ERR_DEVICE;
   nvfp4::PagedAttentionArgs a;

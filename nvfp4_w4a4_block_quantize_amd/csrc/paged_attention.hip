@@ -69,7 +69,6 @@ constexpr int kTile = 32;                  // tokens of a wave's tile
 constexpr int kUnitTiles = 4;
 constexpr int kUnitTokens = kTile * kUnitTiles;  // the smallest unit
 constexpr int kItemCost = 1;  // what beginning and ending an item costs, in units
-constexpr int kMaxWorkersPerCu = 4;
 constexpr float kNoMax = -3.0e38f;         // a maximum before any score; finite, so differences are numbers
 constexpr float kShift = 12.0f, kSlack = 3.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -98,11 +97,6 @@ struct Params {
   int64_t page_bytes;
   Partials ws;
 };
-
-// Query heads of an item: two tiles of 16 where the registers hold them, so that more queries meet each row that is
-// read.  They do not for float32 queries, which take three times the room, nor for heads of 256 (32 query heads on
-// one KV head, 32 contexts up to 16000: 61 us with 16 rows, 73 with 32, which spills; heads of 192: 84 and 66).
-inline int rows_of_item(int group, bool f32, int head_dim) { return std::min(group, f32 || head_dim > 192 ? 16 : 32); }
 
 template <int DT>
 struct OutType;
@@ -774,7 +768,7 @@ hipError_t launch(Params p, hipStream_t stream) {
   int64_t tokens = (int64_t)a.max_pages * a.page_size;  // of the longest item
   if (a.window > 0 && a.window < tokens) tokens = std::min(tokens, a.window + kUnitTokens);
   const int64_t units = (tokens + kUnitTokens - 1) / kUnitTokens, items = (int64_t)a.n_seqs * p.items;
-  const int64_t cus = device_cu_count(), resident = cus * workers_per_cu<DT, D, NQ>();
+  const int64_t cus = std::min(device_cu_count(), kMaxCus), resident = cus * workers_per_cu<DT, D, NQ>();
   // Unsplit, a call lasts as long as its longest item; split, as all tokens take on the resident workers, and some 8 us
   // more, for the scan of the lengths, the partial results and the second kernel.  With a CU to itself an item has more
   // waves, and takes 4 us and 0.7 for a unit of heads of 128 (0.5 with 64, 1.5 with 256).  Unsplit against split, in us:
@@ -827,27 +821,20 @@ hipError_t launch_dim(const Params& p, hipStream_t stream) {
 
 }  // namespace
 
-int64_t paged_attention_workspace(int q_heads, int kv_heads, int head_dim) {
-  const int64_t workers = (int64_t)device_cu_count() * kMaxWorkersPerCu;
-  const int64_t rows = rows_of_item(q_heads / kv_heads, false, head_dim);
-  return workers * (16 + 2 * rows * (8 + 4 * (int64_t)head_dim));
-}
-
 hipError_t launch_paged_attention(const PagedAttentionArgs& a, hipStream_t stream) {
   Params p;
   p.a = a;
   p.by_page = FastDiv((uint32_t)a.page_size);
   p.group = a.q_heads / a.kv_heads;
-  p.rows = rows_of_item(p.group, a.dtype == 0, a.head_dim);
+  p.rows = attention_rows_of_item(p.group, a.dtype == 0, a.head_dim);
   p.parts = (p.group + p.rows - 1) / p.rows;
   p.items = a.kv_heads * p.parts;
   p.page_bytes = (int64_t)a.kv_heads * a.page_size * a.head_dim;
-  const int64_t workers = (int64_t)device_cu_count() * kMaxWorkersPerCu;
   char* w = static_cast<char*>(a.workspace);
   p.ws.o = reinterpret_cast<float*>(w);  // 16-byte aligned pieces first
-  w += workers * 2 * p.rows * 4 * (int64_t)a.head_dim;
+  w += (int64_t)kMostWorkers * 2 * p.rows * 4 * a.head_dim;
   p.ws.split = reinterpret_cast<int4*>(w);
-  w += workers * 16;
+  w += kMostWorkers * 16;
   p.ws.ml = reinterpret_cast<float2*>(w);
   switch (a.dtype) {
     case 0: return launch_dim<0>(p, stream);

@@ -127,7 +127,7 @@ def nvfp4_kv_cache_write(k, v, k_scale, v_scale, slot_map, k_cache, v_cache, str
 
 
 def nvfp4_paged_attention_workspace(q_heads: int, kv_heads: int, head_dim: int) -> int:
-    """Bytes of workspace that nvfp4_paged_attention wants for these heads on the current device."""
+    """Bytes of workspace that nvfp4_paged_attention wants for these heads."""
     if _bind is None:
         _load()
     out = ctypes.c_int64(0)
@@ -155,8 +155,7 @@ def nvfp4_paged_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, se
     if workspace is None:
         if not q.is_cuda:
             raise ValueError("nvfp4_paged_attention needs GPU tensors")
-        with _torch.cuda.device(q.device):
-            size = nvfp4_paged_attention_workspace(q.shape[1], k_cache.shape[1], q.shape[-1])
+        size = nvfp4_paged_attention_workspace(q.shape[1], k_cache.shape[1], q.shape[-1])
         workspace = _new((size,), _torch.uint8, q, stream)
     status = _bind.paged_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, softmax_scale, window,
                                    out, lse, workspace, None if stream is None else stream.cuda_stream)

@@ -27,7 +27,6 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t) {
 }
 hipError_t launch_kv_cache_write(const CacheWriteArgs&, hipStream_t) { return hipSuccess; }
 hipError_t launch_paged_attention(const PagedAttentionArgs&, hipStream_t) { return hipSuccess; }
-int64_t paged_attention_workspace(int, int, int) { return 1024 * (int64_t)device_cu_count(); }
 
 }  // namespace nvfp4
 

@@ -8,7 +8,7 @@ import subprocess
 import pytest
 
 import nvfp4_w4a4_block_quantize_amd as nv
-from tests.test_kv_abi import OK, P, calls
+from tests.test_kv_abi import OK, REFUSED, SHAPE, P, calls
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "nvfp4_w4a4_block_quantize_amd", "csrc")
@@ -48,3 +48,25 @@ def test_rope_copies_no_head_that_is_turned_in_place(host_lib, change, copied):
     first, count = ctypes.c_int32(-1), ctypes.c_int32(-1)
     host_lib.kv_test_rope_copied(ctypes.byref(first), ctypes.byref(count))
     assert (first.value, count.value) == copied
+
+
+@pytest.mark.parametrize("op", sorted(REFUSED))
+def test_refused_calls_ask_hip_nothing(host_lib, op):
+    call, before = calls(host_lib)[op], host_lib.kv_test_hip_calls()
+    for status, name, value in REFUSED[op]:
+        assert call(**{name: value}) == status, (name, value)
+        assert host_lib.kv_test_hip_calls() == before, (name, value)
+    size = ctypes.c_int64(0)
+    for heads in ((24, 4, 256), (7, 2, 64)):
+        host_lib.nvfp4_paged_attention_workspace(*heads, ctypes.addressof(size))
+    assert host_lib.kv_test_hip_calls() == before
+    assert call() == OK and host_lib.kv_test_hip_calls() == before + 1
+
+
+def test_the_workspace_is_wanted_to_the_byte(host_lib):
+    call, size = calls(host_lib)["attend"], ctypes.c_int64(0)
+    for hq, hk, dim in ((8, 2, 64), (24, 4, 256), (64, 1, 192), (32, 32, 128)):
+        assert host_lib.nvfp4_paged_attention_workspace(hq, hk, dim, ctypes.addressof(size)) == OK
+        heads = dict(hq=hq, hk=hk, dim=dim, qt=hq * dim, qh=dim, ot=hq * dim, oh=dim)
+        assert call(**heads, bytes=size.value) == OK
+        assert call(**heads, bytes=size.value - 1) == SHAPE
