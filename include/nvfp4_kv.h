@@ -111,7 +111,8 @@ nvfp4_status nvfp4_kv_block_table(int64_t n_seqs, const int32_t* cached_lens, co
  * the same number on all).  adjacent = 0 pairs element i with i + rot_dim/2,
  * adjacent = 1 pairs 2i with 2i + 1.  Elements from rot_dim on are copied.
  *
- *   positions  int32 [n_axes][ld_pos], ld_pos >= tokens; any value
+ *   positions  int32 [n_axes][ld_pos], ld_pos >= tokens, or 0: one row for all
+ *              axes, as text has it; any value
  *   inv_freq   fp32 [rot_dim/2]
  *   axes       int32 [rot_dim/2], each in 0..n_axes-1 (a value outside counts as
  *              the nearest one inside)

@@ -94,9 +94,10 @@ def nvfp4_rope(q, k, positions, inv_freq, axes, adjacent: bool = False, q_out=No
     """Rotary positions on q [tokens, q_heads, head_dim] and k [tokens, k_heads,
     head_dim] (or None): pair i turns by positions[axes[i], token] * inv_freq[i].
 
-    positions int32 [n_axes, tokens]; inv_freq float32 and axes int32
-    [rot_dim / 2].  adjacent pairs elements 2i and 2i + 1 instead of i and
-    i + rot_dim / 2.  Pass q (k) itself as q_out (k_out) to turn in place.
+    positions int32 [n_axes, tokens], of text one row expanded to all axes;
+    inv_freq float32 and axes int32 [rot_dim / 2].  adjacent pairs elements 2i
+    and 2i + 1 instead of i and i + rot_dim / 2.  Pass q (k) itself as q_out
+    (k_out) to turn in place.
     Returns (q_out, k_out).
     """
     if _bind is None:

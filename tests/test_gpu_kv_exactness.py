@@ -113,3 +113,15 @@ def test_rope_leaves_the_rest_of_heads_in_place_alone(gpu_lib, adjacent, which):
         gpu_lib.nvfp4_rope(again, None, positions, inv_freq, axes, adjacent=adjacent, q_out=again)
     torch.cuda.synchronize()
     assert torch.equal(again[:, :, :rot], mine[:, :, :rot])
+
+
+def test_rope_with_one_row_of_positions(gpu_lib):
+    rng = np.random.default_rng(43)
+    x = dev(rng.standard_normal((50, 3, 64)), torch.bfloat16)
+    row, axes = dev(rng.integers(0, 100000, (1, 50))), dev(np.arange(16) % 3)
+    inv_freq = dev(1e4 ** (-np.arange(16) / 16), torch.float32)
+    log("rope, one row of positions")
+    got, _ = gpu_lib.nvfp4_rope(x, None, row.expand(3, -1), inv_freq, axes)
+    want, _ = gpu_lib.nvfp4_rope(x, None, row.repeat(3, 1), inv_freq, axes)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)

@@ -70,3 +70,10 @@ def test_the_workspace_is_wanted_to_the_byte(host_lib):
         heads = dict(hq=hq, hk=hk, dim=dim, qt=hq * dim, qh=dim, ot=hq * dim, oh=dim)
         assert call(**heads, bytes=size.value) == OK
         assert call(**heads, bytes=size.value - 1) == SHAPE
+
+
+def test_one_row_of_positions_serves_all_axes(host_lib):
+    call = calls(host_lib)["rope"]
+    assert call(ld_pos=0) == OK and call(ld_pos=0, axes_n=1) == OK and call(ld_pos=4) == OK
+    for bad in (-1, 1, 3, -(1 << 40)):
+        assert call(ld_pos=bad) == SHAPE
