@@ -174,7 +174,8 @@ __device__ __forceinline__ float4_t mfma(half8_t a, half8_t b, float4_t c) {
 }
 
 // a lane's query elements, the K operand's partners: one part in the 16-bit
-// types; a float32 query is the exact sum of three bf16 parts (8 + 8 + 8 bits)
+// types; a float32 query is the exact sum of three bf16 parts, its upper, middle and
+// lower eight bits (cut off, not rounded: the largest would become infinite)
 template <int DT>
 struct Query;
 template <>
@@ -188,8 +189,9 @@ struct Query<0> {
       float x = p[i];
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
-        v[k][i] = (__bf16)x;
-        x -= (float)v[k][i];
+        const uint32_t top = __float_as_uint(x) & 0xFFFF0000u;
+        v[k][i] = __builtin_bit_cast(__bf16, (uint16_t)(top >> 16));
+        x -= __uint_as_float(top);
       }
     }
   }

@@ -125,3 +125,26 @@ def test_rope_with_one_row_of_positions(gpu_lib):
     want, _ = gpu_lib.nvfp4_rope(x, None, row.repeat(3, 1), inv_freq, axes)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+def test_attention_of_the_largest_float32_queries(gpu_lib, dim):
+    """Elements up to the type's largest, against keys of zero there; the rest of the row decides."""
+    rng = np.random.default_rng(dim)
+    heads, lens = 4, [1, 7, 40]
+    most = np.finfo(np.float32).max
+    q = np.zeros((3, heads, dim), np.float32)
+    q[..., 0] = rng.uniform(-2, 2, (3, heads))
+    q[..., 1:5] = [most, -most, most * 0.9985, np.float32(3.39e38)]
+    k, v = (rng.integers(0x30, 0x50, (4, 1, 48, dim)).astype(np.uint8) for _ in range(2))
+    k[..., 1:] = 0
+    table, one = np.array([[2], [0], [3]]), torch.ones(1, device="cuda")
+    lse = torch.empty((3, heads), device="cuda")
+    log("attention, largest queries", dim)
+    got = gpu_lib.nvfp4_paged_attention(dev(q, torch.float32), dev(k, torch.uint8), dev(v, torch.uint8), one, one, dev(table), dev(lens),
+                                        softmax_scale=0.5, lse=lse)
+    torch.cuda.synchronize()
+    q[..., 1:5] = 0  # they meet zeros alone
+    ref = R.attention(q, k, v, 1.0, 1.0, table, lens, 0.5, 0, len(k))
+    b_out, b_lse = R.attention_bounds(*ref, lens, "f32")
+    assert (np.abs(host(got) - ref[0]) <= b_out).all() and (np.abs(host(lse) - ref[1]) <= b_lse).all()
