@@ -108,6 +108,7 @@ def test_rope_leaves_the_rest_of_heads_in_place_alone(gpu_lib, adjacent, which):
     torch.cuda.synchronize()
     assert (mine[:, :, rot:] == rounds - 1).all()
     assert torch.equal(out[:, :, rot:], other[:, :, rot:])
+    assert torch.equal(out, gpu_lib.nvfp4_rope(other, None, positions, inv_freq, axes, adjacent=adjacent)[0])
     again = before.clone()
     for _ in range(rounds):
         gpu_lib.nvfp4_rope(again, None, positions, inv_freq, axes, adjacent=adjacent, q_out=again)
@@ -148,3 +149,27 @@ def test_attention_of_the_largest_float32_queries(gpu_lib, dim):
     ref = R.attention(q, k, v, 1.0, 1.0, table, lens, 0.5, 0, len(k))
     b_out, b_lse = R.attention_bounds(*ref, lens, "f32")
     assert (np.abs(host(got) - ref[0]) <= b_out).all() and (np.abs(host(lse) - ref[1]) <= b_lse).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("channel", [0, 37, 63])
+def test_attention_holds_every_bit_of_a_float32_query(gpu_lib, dim, channel):
+    rng = np.random.default_rng([dim, channel])
+    heads, n = 16, 5
+    x = rng.uniform(1, 2, (n, heads)).astype(np.float32)
+    q = np.zeros((n, heads, dim), np.float32)
+    q[..., channel] = x * np.where(rng.random((n, heads)) < 0.5, -1, 1)
+    key = rng.integers(0x70, 0x7F, n).astype(np.uint8)  # 128 to 448
+    k, v = (np.zeros((n, 1, 16, dim), np.uint8) for _ in range(2))
+    k[:, 0, 0, channel] = key
+    s = q[..., channel].astype(np.float64) * R.E4M3[key][:, None] * 4.0
+    one, lse = torch.ones(1, device="cuda"), torch.empty((n, heads), device="cuda")
+    log("attention, every bit", dim, channel)
+    gpu_lib.nvfp4_paged_attention(dev(q, torch.float32), dev(k, torch.uint8), dev(v, torch.uint8), one, one, dev(np.arange(n)[:, None]),
+                                  dev(np.ones(n)), softmax_scale=4.0, lse=lse)
+    torch.cuda.synchronize()
+    # the products of three parts and their sum: 3 roundings; times log2(e): one of the maximum and one of what is left;
+    # back from base 2: 3, all of 2^-24 of the score, and the exponential and logarithm of one term: 2^-19.  Without its
+    # last eight bits a query would be off by up to 2^-16 of itself, fifty times that.
+    off, bound = np.abs(host(lse) - s), 8 * 2.0 ** -24 * np.abs(s) + 2.0 ** -19
+    assert (off <= bound).all(), float((off / bound).max())
