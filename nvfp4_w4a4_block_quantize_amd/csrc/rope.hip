@@ -33,7 +33,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMore = 2;  // items of a thread, where that leaves no CU idle
+constexpr int kMore = 2;  // items of a thread, where that gains
+constexpr int64_t kInfinityCache = 256 << 20;
 constexpr size_t kLdsMost = 32 * 1024;  // of angles in a workgroup, so that four fit a CU
 
 struct Plan {
@@ -206,10 +207,25 @@ hipError_t launch_vec(RopeArgs a, hipStream_t stream) {
   p.copy_from = (uint32_t)rope_copied(a).first;
   p.by_token = FastDiv(p.token_items);
   p.by_pair = FastDiv((uint32_t)p.pairs);
-  // Items of one vector are two to a thread, those of halves, which have two already, one: 8192 tokens, 28 heads of 256 of
-  // which 64 elements turn, 41 us (one: 44); 4099 tokens, 18 heads of 128 in f32, neighbours paired, 14.0 (15.7); but
-  // 32768 tokens, 40 heads of 128, halves, 123 (115); 4096, 72 heads of 192 with 64 turning, 41.2 (40.5).
-  const bool single = ADJACENT || 6 * p.by_turn.d <= p.by_copy.d;
+  // Two items to a thread gain where they leave every CU four workgroups, and while the call (read and written) is within
+  // the Infinity Cache; beyond that they still do where items have one vector and whole 64-byte pieces.  Halves, which
+  // have two vectors already, gain only beside a copied part, if that begins with a 64-byte piece.  One and two items, us
+  // in a graph, operands of three calls in turn:
+  //   tokens x heads x elements, turning         bytes  one / two    tokens x heads x elements, turning         bytes  one / two
+  //   neighbours paired:
+  //   4099 x 18 x 128, 64   bf16                 38 MB   9.3 / 8.2    1024 x 18 x 128, 64   bf16                 9 MB   4.0 / 4.5
+  //   8192 x 28 x 256, 64   bf16                235     44.9 / 41.6   512 x 18 x 64, 64     f32                   5     3.4 / 3.8
+  //   8192 x 28 x 128, 128  f32                 235     45.5 / 41.7   512 x 18 x 128, 48    f32                   9     4.1 / 4.4
+  //   32768 x 28 x 256, 256 bf16                940      166 / 159    32768 x 28 x 256, 48  bf16                940      213 / 239
+  //   4099 x 18 x 256, 48   bf16                 76     17.4 / 16.3
+  //   halves:
+  //   2048 x 28 x 256, 64   bf16                 59     12.4 / 11.5   1024 x 28 x 128, 64   bf16                 15     4.4 / 5.0
+  //   8192 x 28 x 256, 64   bf16                235     43.2 / 42.3   32768 x 40 x 256, 64  bf16               1342      214 / 237
+  //   8192 x 28 x 128, 64   bf16                117     21.9 / 21.3   8192 x 28 x 256, 128  f32                 470     79.1 / 84.4
+  //   4099 x 18 x 256, 48   f32                 151     28.5 / 25.9   2048 x 28 x 128, 128  bf16                 29      7.0 / 7.4
+  //   4099 x 18 x 128, 64   f32                  76     14.7 / 13.6   8192 x 28 x 128, 16   bf16                117     27.5 / 31.3
+  constexpr int64_t ES = sizeof(typename Elem<DT>::type);
+  const bool pieces = ALIGNED && (copy == 0 || a.rot_dim * ES % 64 == 0);
   for (int64_t left = a.tokens;;) {
     a.tokens = std::min(left, std::max<int64_t>(kMostWorkgroups * kThreads / p.token_items, 1));
     p.items = (uint32_t)(a.tokens * p.token_items);
@@ -217,17 +233,20 @@ hipError_t launch_vec(RopeArgs a, hipStream_t stream) {
     auto lds = [&](int64_t n) {
       return (size_t)std::min<int64_t>(a.tokens, (n - 2) / p.token_items + 2) * p.pairs * sizeof(float2);
     };
-    const bool more = single && lds(kMore * kThreads) <= kLdsMost && p.items >= (uint32_t)device_cu_count() * kMore * kThreads;
+    const bool cached = 2 * a.tokens * heads * a.head_dim * ES <= kInfinityCache;
+    const bool gain = ADJACENT ? pieces || cached : copy > 0 && pieces && cached;
+    const bool more = gain && lds(kMore * kThreads) <= kLdsMost &&
+                      p.items >= (int64_t)device_cu_count() * 4 * kMore * kThreads;
     const uint32_t n = more ? kMore * kThreads : kThreads, blocks = (p.items + n - 1) / n;
-    if (more)
-      rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, kMore><<<blocks, kThreads, lds(n), stream>>>(a, p);
-    else
-      rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, 1><<<blocks, kThreads, lds(n), stream>>>(a, p);
+    if constexpr (ADJACENT || ALIGNED) {
+      if (more) rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, kMore><<<blocks, kThreads, lds(n), stream>>>(a, p);
+    }
+    if (!more) rope_kernel<DT, VEC, COPY, ADJACENT, ALIGNED, 1><<<blocks, kThreads, lds(n), stream>>>(a, p);
     const hipError_t e = hipGetLastError();
     left -= a.tokens;
     if (e != hipSuccess || left == 0) return e;
     auto skip = [&](auto& x) {
-      if (x.p) x.p = (decltype(x.p))((uintptr_t)x.p + (uintptr_t)(a.tokens * x.token) * sizeof(typename Elem<DT>::type));
+      if (x.p) x.p = (decltype(x.p))((uintptr_t)x.p + (uintptr_t)(a.tokens * x.token * ES));
     };
     skip(a.q);
     skip(a.q_out);

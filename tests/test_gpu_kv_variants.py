@@ -11,8 +11,8 @@ torch = pytest.importorskip("torch")
 
 
 @pytest.mark.parametrize("dtype,adjacent,tokens,q_heads,k_heads,dim,rot", [
-    ("bf16", False, 701, 5, 2, 256, 64), ("f16", False, 703, 7, 0, 256, 64), ("f32", True, 1001, 3, 2, 128, 128),
-    ("bf16", True, 1003, 11, 5, 72, 40), ("f32", False, 1201, 3, 3, 256, 32), ("bf16", True, 2049, 9, 1, 128, 128)])
+    ("bf16", False, 2803, 5, 2, 256, 64), ("f16", False, 2805, 7, 0, 256, 64), ("f32", True, 4001, 3, 2, 128, 128),
+    ("bf16", True, 4003, 11, 5, 72, 40), ("f32", False, 1601, 3, 3, 256, 32), ("bf16", True, 4099, 9, 1, 128, 128)])
 @pytest.mark.parametrize("shift", [0, 1])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_rope_of_long_prompts(gpu_lib, dtype, adjacent, tokens, q_heads, k_heads, dim, rot, shift, in_place):
