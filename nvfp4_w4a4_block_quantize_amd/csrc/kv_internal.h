@@ -115,8 +115,8 @@ hipError_t launch_paged_attention(const PagedAttentionArgs& a, hipStream_t strea
 constexpr int kMaxCus = 256, kMaxWorkersPerCu = 4, kMostWorkers = kMaxCus * kMaxWorkersPerCu;
 
 // Query heads of an item: two tiles of 16 where the registers hold them, so that more queries meet each row that is
-// read.  They do not for float32 queries, which take three times the room, nor for heads of 256 (32 query heads on
-// one KV head, 32 contexts up to 16000: 61 us with 16 rows, 73 with 32, which spills; heads of 192: 84 and 66).
+// read.  They do not for float32 queries, which take three times the room, nor for heads of 256.  32 contexts up to
+// 16000, 32 bf16 query heads on one KV head, with 16 rows and 32: heads of 192 50 and 42 us, of 256 62 and 63 (spilled).
 inline int attention_rows_of_item(int group, bool f32, int head_dim) {
   const int most = f32 || head_dim > 192 ? 16 : 32;
   return group < most ? group : most;

@@ -2,13 +2,14 @@
 // (nvfp4_paged_attention):
 //   s_j = scale * q . k_j / k_scale,  out = sum_j softmax(s)_j v_j / v_scale.
 //
-// Every cache byte is read once and serves the G = q_heads / kv_heads queries of
-// its head: 4 G operations for each pair of K and V bytes, far below what the
-// matrix units do in the time that HBM takes to deliver them.  The kernel is
-// built to keep loads in flight and little else: without its arithmetic it takes
-// 197 us for 201.  64 contexts up to 16384 tokens, 24 heads of 256 on 4: 192 us for
-// 1.17 GB, 6.1 TB/s (a streaming read reaches 7.1).  One of 131072: 53 us for 268 MB,
-// of which first loads take 4 and the second kernel 5.
+// A cache byte that is read serves all G = q_heads / kv_heads queries of its head, or
+// 16 or 32 of them (attention_rows_of_item), a wider group's bytes being read again
+// for the rest: 4 operations a query for each pair of K and V bytes, far below what
+// the matrix units do in the time that HBM takes to deliver them.  The kernel is built
+// to keep loads in flight and little else: without its arithmetic it took 2% less.
+// 64 contexts up to 16384 tokens, 24 heads of 256 on 4: 192 us for 1.17 GB, 6.1 TB/s (a
+// streaming read reaches 7.1).  One of 131072: 53 us for 268 MB, of which first loads
+// take 4 and the second kernel 5.
 //
 // Work.  Each (sequence, KV head) is an item of ceil(tokens / 128) units, and one
 // more for what beginning and ending it costs.  The units of all items lie on
@@ -18,9 +19,9 @@
 // a partial result (maximum, sum, unnormalised output; at most two of them), and a
 // second, small kernel joins those.  Lengths are read on the device, so a captured
 // graph follows them.  Runs are one to a resident workgroup: with two or four of
-// them the ends are no more even (201 us: 209 and 228).  Where items are short, each
-// has a workgroup to itself instead, of more waves where it has the CU to itself, and
-// nothing is joined (launch() says where).
+// them the ends are no more even (4 and 13% more for the 64 contexts).  Where items
+// are short, each has a workgroup to itself instead, of more waves where it has the
+// CU to itself, and nothing is joined (launch() says where).
 //
 // The workgroup's waves (four of them for a unit) take tiles of 32 tokens in turn and
 // run on their own (maxima, sums and outputs of their own) until the item ends.
