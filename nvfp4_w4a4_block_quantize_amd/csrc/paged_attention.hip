@@ -48,15 +48,17 @@
 //    a tile has four addresses, the same for all lanes: they are made from scalar
 //    loads of the table, one tile ahead of the rows that they lead to.
 //
-// Softmax.  One pass with a running maximum m, a whole number of powers of two
-// that moves only when some score passes it by kSlack: p = 2^(s' + kShift - m),
-// s' = s log2(e).  m cancels in the end and being whole, its changes scale by
-// exact powers of two.  kShift puts p below 2^15, in fp16's upper range.  A
-// probability meets its values as two fp16 parts and so is held to 2^-22 of itself,
-// or to 2^-36 of the largest one where that is more.  With one part, outputs whose
-// values cancel were off by many times their own rounding, bf16 ones too (two
-// tokens, 256 outputs: 10 to 20 times what is allowed); the second part takes 0.4 of
-// 191.7 us (64 contexts up to 16384, 24 heads of 256 on 4) and 0.3 of 53.3 (one of 131072).
+// Softmax.  One pass: p = 2^(s' - m), s' = s log2(e), and m a running whole number that
+// starts kShift below the first maximum and moves only when some score passes it by
+// kShift + kSlack.  m cancels in the end and being whole, its changes scale by exact
+// powers of two.  s' - m is rounded once; past kFar s' is rounded before, as it is for
+// the maximum (else the largest score's p could be anything).  kShift puts p below
+// 2^15, in fp16's upper range.  A probability meets its values as two fp16 parts and so
+// is held to 2^-22 of itself, or to 2^-36 of the largest one where that is more.  With
+// one part, outputs whose values cancel were off by many times their own rounding, bf16
+// ones too (two tokens, 256 outputs: 10 to 20 times what is allowed); the second part
+// takes 0.4 of 191.7 us (64 contexts up to 16384, 24 heads of 256 on 4) and 0.3 of 53.3
+// (one of 131072).
 #include <algorithm>
 #include <type_traits>
 
@@ -70,8 +72,9 @@ constexpr int kTile = 32;                  // tokens of a wave's tile
 constexpr int kUnitTiles = 4;
 constexpr int kUnitTokens = kTile * kUnitTiles;  // the smallest unit
 constexpr int kItemCost = 1;  // what beginning and ending an item costs, in units
-constexpr float kNoMax = -3.0e38f;         // a maximum before any score; finite, so differences are numbers
+constexpr float kNoMax = -3.402823466e38f;  // m before any score; finite, so that differences are numbers
 constexpr float kShift = 12.0f, kSlack = 3.0f;
+constexpr float kFar = 0x1p22f;  // of m, from where on a score's rounding to 32 bits is no small part of a power of two
 constexpr float kLn2 = 0.69314718055994530942f;
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -479,8 +482,12 @@ paged_attention_kernel(Params p) {
       load_k(r, a.k_cache, at, col, grp);
       load_v(r, a.v_cache, at, col, grp);
       const double c64 = (double)a.softmax_scale * 1.44269504088896340736 / (double)*a.k_scale;
-      // never 0, so that it leaves the -infinity of tokens that are not seen
-      const float c_hi = fmaxf((float)c64, 0x1p-149f), c_lo = DT == 0 ? (float)(c64 - (double)c_hi) : 0.0f;
+      // never 0, so that they leave the -infinity of tokens that are not seen (for which c_lo is not negative either)
+      float c_hi = fmaxf((float)c64, 0x1p-149f), c_lo = 0.0f;
+      if constexpr (DT == 0) {
+        if ((double)c_hi > c64) c_hi = fmaxf(__uint_as_float(__float_as_uint(c_hi) - 1), 0x1p-149f);
+        c_lo = fmaxf((float)(c64 - (double)c_hi), 0x1p-149f);
+      }
       while (true) {
         const bool more = tile + kWaves < tile_end;
 
@@ -559,25 +566,33 @@ paged_attention_kernel(Params p) {
 #pragma unroll
           for (int j = 1; j < 8; ++j) top = fmaxf(top, s[t][j]);
           top *= c_hi;
-          if (__any(top > m[t] + kSlack)) {
+          if (__any(top - m[t] > kShift + kSlack)) {
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            const float to = fmaxf(m[t], ceilf(top));
+            const float whole_top = ceilf(top);
+            float to = whole_top - kShift;
+            if (whole_top - to > kShift) to = whole_top;  // past 2^26 steps are wider than that
+            to = fmaxf(m[t], to);
             const float f = __builtin_amdgcn_exp2f(m[t] - to);
             m[t] = to;
             l[t] *= f;
 #pragma unroll
             for (int i = 0; i < ND; ++i) o[t][i] *= f;
           }
-          const float base = kShift - m[t];
+          float y[8];
+          if (__any(fabsf(m[t]) >= kFar && m[t] != kNoMax)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = s[t][j] * c_hi - m[t];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              y[j] = fmaf(s[t][j], c_hi, -m[t]);
+              if constexpr (DT == 0) y[j] = fmaf(s[t][j], c_lo, y[j]);
+            }
+          }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float sj = s[t][j];
-            float e;
-            if constexpr (DT == 0)
-              e = __builtin_amdgcn_exp2f(fmaf(sj, c_hi, seen >> j & 1 ? fmaf(sj, c_lo, base) : base));
-            else
-              e = __builtin_amdgcn_exp2f(fmaf(sj, c_hi, base));
+            const float e = __builtin_amdgcn_exp2f(y[j]);
             l[t] += e;
             pr[t][0][j] = (_Float16)e;
             pr[t][1][j] = (_Float16)(e - (float)pr[t][0][j]);
@@ -663,7 +678,7 @@ paged_attention_kernel(Params p) {
           const float by = total > 0.f ? inv_vs / total : 0.f;
           store4<DT>(a, in, h, d, make_float4(v[0] * by, v[1] * by, v[2] * by, v[3] * by));
           if (a.lse && d == 0)
-            a.lse[(int64_t)in * a.q_heads + h] = total > 0.f ? (high - kShift + log2f(total)) * kLn2 : -INFINITY;
+            a.lse[(int64_t)in * a.q_heads + h] = total > 0.f ? (high + log2f(total)) * kLn2 : -INFINITY;
         } else {
           const int64_t at = (int64_t)slot * p.rows + in_item;
           *reinterpret_cast<float4_t*>(p.ws.o + at * D + d) = v;
@@ -761,7 +776,7 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join(Params p, i
     const int h = head * p.group + q0 + row;
     store4<DT>(a, seq, h, d, make_float4(v.x * by, v.y * by, v.z * by, v.w * by));
     if (a.lse && slice == 0 && tid == 0)
-      a.lse[(int64_t)seq * a.q_heads + h] = total > 0.f ? (top - kShift + log2f(total)) * kLn2 : -INFINITY;
+      a.lse[(int64_t)seq * a.q_heads + h] = total > 0.f ? (top + log2f(total)) * kLn2 : -INFINITY;
   }
 }
 

@@ -173,3 +173,33 @@ def test_attention_holds_every_bit_of_a_float32_query(gpu_lib, dim, channel):
     # last eight bits a query would be off by up to 2^-16 of itself, fifty times that.
     off, bound = np.abs(host(lse) - s), 8 * 2.0 ** -24 * np.abs(s) + 2.0 ** -19
     assert (off <= bound).all(), float((off / bound).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("scale", [1e4, 3e5, 1e6, 7.7e6, 1e8, 1.3e9, 1e12, 1e30])
+@pytest.mark.parametrize("columns", [4, 1200])
+def test_attention_of_very_large_scores(gpu_lib, dtype, scale, columns):
+    """Scores whose neighbours in 32 bits lie more than one apart: the largest takes all, equal ones share."""
+    rng = np.random.default_rng([columns, int(np.log10(scale))])
+    n, heads, dim, page = 12, 6, 64, 16
+    lens = rng.integers(1, 4 * page, n)
+    k, v = (rng.integers(0x20, 0x70, (4 * n, 1, page, dim)).astype(np.uint8) for _ in range(2))
+    k[..., 0] ^= (rng.random(k[..., 0].shape) < 0.5).astype(np.uint8) << 7
+    k[..., 1:] = 0
+    table = np.full((n, columns), -1)
+    table[:, :4] = rng.permutation(4 * n).reshape(n, 4)
+    q = np.zeros((n, heads, dim))
+    q[..., 0] = rng.uniform(0.5, 2, (n, heads)) * np.where(rng.random((n, heads)) < 0.5, -1, 1)
+    q = dev(q, DTYPES[dtype])
+    one, lse = torch.ones(1, device="cuda"), torch.empty((n, heads), device="cuda")
+    log("attention, large scores", dtype, scale, columns)
+    got = gpu_lib.nvfp4_paged_attention(q, dev(k, torch.uint8), dev(v, torch.uint8), one, one, dev(table), dev(lens), softmax_scale=scale,
+                                        lse=lse)
+    torch.cuda.synchronize()
+    scale = float(np.float32(scale))
+    want, want_lse, reach, _ = R.attention(host(q), k, v, 1.0, 1.0, table, lens, scale, 0, len(k))
+    # E4M3 keys and one channel: other tokens are a sixteenth of a score away (e^-625 at least) or equal, so weights are
+    # 0 or 1 over the number of equal ones, a division and the type's own rounding
+    bound = (R.HALF_STEP[dtype] * 1.01 + 2.0 ** -20) * reach
+    assert (np.abs(host(got) - want) <= bound).all()
+    assert (np.abs(host(lse) - want_lse) <= 2.0 ** -20 * np.abs(want_lse)).all()
