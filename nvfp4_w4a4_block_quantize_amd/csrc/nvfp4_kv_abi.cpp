@@ -113,8 +113,8 @@ nvfp4_status nvfp4_rope(int64_t tokens, int64_t head_dim, int64_t rot_dim, int32
   const int es = dtype_size(dtype);
   if (es == 0 || (adjacent != 0 && adjacent != 1)) return NVFP4_ERR_DTYPE;
   if (!size_ok(tokens) || head_dim <= 0 || head_dim > NVFP4_ROPE_MAX_HEAD_DIM || head_dim % 2 != 0 || rot_dim < 2 ||
-      rot_dim % 2 != 0 || rot_dim > head_dim || n_axes < 1 || n_axes > NVFP4_ROPE_MAX_AXES || (ld_pos < tokens && ld_pos != 0) ||
-      ld_pos >= kMaxStride || !row_ok(q_heads, head_dim) || k_heads < 0 ||
+      rot_dim % 2 != 0 || rot_dim > head_dim || n_axes < 1 || n_axes > NVFP4_ROPE_MAX_AXES ||
+      (ld_pos < tokens && ld_pos != 0) || ld_pos >= kMaxStride || !row_ok(q_heads, head_dim) || k_heads < 0 ||
       (k_heads > 0 && !row_ok(k_heads, head_dim)))
     return NVFP4_ERR_SHAPE;
   if (!strides_ok(q_heads, head_dim, q_token, q_head) || !strides_ok(q_heads, head_dim, q_out_token, q_out_head) ||
