@@ -18,13 +18,18 @@ Functions carry the C names:
 
 The paged FP8 KV cache (include/nvfp4_kv.h) is bound in kv.py and is part of
 this namespace: nvfp4_kv_block_table, nvfp4_rope, nvfp4_kv_cache_write,
-nvfp4_paged_attention, nvfp4_paged_attention_workspace.
+nvfp4_paged_attention, nvfp4_paged_attention_workspace.  So is the gated delta
+layer (include/nvfp4_gdn.h), bound in gdn.py: nvfp4_causal_conv,
+nvfp4_causal_conv_step, nvfp4_gated_delta_chunked, nvfp4_gated_delta_step,
+nvfp4_gated_delta_workspace, nvfp4_group_norm.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 
+from .gdn import (GDN_SIGNATURES, nvfp4_causal_conv, nvfp4_causal_conv_step, nvfp4_gated_delta_chunked, nvfp4_gated_delta_step,
+                  nvfp4_gated_delta_workspace, nvfp4_group_norm)
 from .kv import (KV_SIGNATURES, nvfp4_kv_block_table, nvfp4_kv_cache_write, nvfp4_paged_attention,
                  nvfp4_paged_attention_workspace, nvfp4_rope)
 
@@ -73,8 +78,10 @@ def load_library(path: str | None = None):
         raise RuntimeError(f"{p} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
     lib = ctypes.CDLL(p)
     # another build, named by its path, may hold the linear layer's C ABI alone
-    kv = KV_SIGNATURES if path is None or hasattr(lib, "nvfp4_kv_block_table") else {}
-    for name, (res, args) in {**SIGNATURES, **kv}.items():
+    more = {} if path is not None and not hasattr(lib, "nvfp4_kv_block_table") else KV_SIGNATURES
+    if path is None or hasattr(lib, "nvfp4_causal_conv"):
+        more = {**more, **GDN_SIGNATURES}
+    for name, (res, args) in {**SIGNATURES, **more}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

@@ -25,12 +25,13 @@ PROBES_SRC = os.path.join(ROOT, "bench_probes.hip")
 PROBES_PATH = os.path.join(ROOT, "libnvfp4_probes.so")
 
 SOURCES = ["nvfp4_abi.cpp", "quantize.hip", "fuse_rescale.hip", "gemm.hip", "gemm_fast.hip", "gemm_decode.hip", "gemm_stream.hip", "kv_quantize.hip",
-           "nvfp4_kv_abi.cpp", "kv_table.hip", "rope.hip", "kv_cache_write.hip", "paged_attention.hip"]
+           "nvfp4_kv_abi.cpp", "kv_table.hip", "rope.hip", "kv_cache_write.hip", "paged_attention.hip",
+           "nvfp4_gdn_abi.cpp", "causal_conv.hip", "gated_delta_step.hip", "gated_delta_chunked.hip", "group_norm.hip"]
 
-# the native side of the paged KV cache's Python binding: an extension module
-# beside the library, built against torch's headers (without torch: not at all,
+# the native side of the Python binding's short calls (paged KV cache, gated delta
+# layer): an extension module beside the library, built against torch's headers (without torch: not at all,
 # the C ABI does not need it)
-BIND_SRC = "kv_bind.cpp"
+BIND_SRCS = ["kv_bind.cpp", "gdn_bind.cpp"]
 BIND_PATH = os.path.join(HERE, "_kv_bind.so")
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
@@ -60,27 +61,27 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _compile_bind() -> str:
+def _compile_bind(src: str) -> str:
     import sysconfig
 
     import torch
     from torch.utils.cpp_extension import include_paths
 
-    obj = os.path.join(BUILD_DIR, "kv_bind.o")
+    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
     includes = [INCLUDE, sysconfig.get_paths()["include"], *include_paths()]
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-           *(f"-I{p}" for p in includes), "-c", os.path.join(CSRC, BIND_SRC), "-o", obj]
+           *(f"-I{p}" for p in includes), "-c", os.path.join(CSRC, src), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"{CXX} failed for {BIND_SRC}:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+        raise RuntimeError(f"{CXX} failed for {src}:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     return obj
 
 
-def _link_bind(obj: str):
+def _link_bind(objs):
     import torch
 
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
-    cmd = [CXX, "-shared", "-o", BIND_PATH + ".tmp", obj, "-L" + HERE, "-lnvfp4", "-Wl,-rpath,$ORIGIN", "-L" + libs,
+    cmd = [CXX, "-shared", "-o", BIND_PATH + ".tmp", *objs, "-L" + HERE, "-lnvfp4", "-Wl,-rpath,$ORIGIN", "-L" + libs,
            "-ltorch_python", "-ltorch_cpu", "-lc10"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
@@ -100,7 +101,7 @@ def build(verbose: bool = False) -> str:
     """Compile every source and link libnvfp4.so, then the binding's module where torch is; returns the library path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=8) as ex:
-        bind = ex.submit(_compile_bind) if _has_torch() else None
+        bind = [ex.submit(_compile_bind, src) for src in BIND_SRCS] if _has_torch() else None
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB_PATH + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
@@ -125,7 +126,7 @@ def build(verbose: bool = False) -> str:
         print(f"built {LIB_PATH}, {CONFORMANCE_PATH} and {PROBES_PATH}")
     # last, so that nothing else is missing if it fails
     if bind is not None:
-        _link_bind(bind.result())
+        _link_bind([job.result() for job in bind])
     elif os.path.exists(BIND_PATH):
         os.remove(BIND_PATH)  # linked to an earlier library
     if verbose:

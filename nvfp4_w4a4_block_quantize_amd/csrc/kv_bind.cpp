@@ -5,88 +5,13 @@
 //
 // Each function takes its arguments by position, the stream last (None: torch's
 // current one), raises ValueError for a tensor that does not fit, and returns the
-// C status.
-#include <Python.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <cstdarg>
-#include <string>
-
+// C status.  The module also holds the gated delta layer's functions (gdn_bind.cpp).
+#include "bind_common.h"
 #include "nvfp4_kv.h"
 
 namespace {
 
-// torch's accessors, fetched once
-PyObject* get_device = nullptr;       // torch._C._cuda_getDevice
-PyObject* exchange_device = nullptr;  // torch._C._cuda_exchangeDevice
-PyObject* raw_stream = nullptr;       // torch._C._cuda_getCurrentRawStream
-
-struct Refused {};  // a Python exception is set
-
-[[noreturn]] void refuse(const char* format, ...) {
-  va_list args;
-  va_start(args, format);
-  PyErr_FormatV(PyExc_ValueError, format, args);
-  va_end(args);
-  throw Refused();
-}
-
-std::string shape_of(const at::Tensor& t) {
-  std::string s = "(";
-  for (int64_t i = 0; i < t.dim(); ++i) s += (i ? ", " : "") + std::to_string(t.size(i));
-  return s + (t.dim() == 1 ? ",)" : ")");
-}
-
-const at::Tensor& tensor(PyObject* o, const char* name) {
-  if (!THPVariable_Check(o)) {
-    PyErr_Format(PyExc_TypeError, "%s must be a tensor, got %s", name, Py_TYPE(o)->tp_name);
-    throw Refused();
-  }
-  return THPVariable_Unpack(o);
-}
-
-void on_device(const at::Tensor& t, const char* name, const at::Tensor& like) {
-  if (t.device() != like.device())
-    refuse("%s is on %s, expected %s", name, t.device().str().c_str(), like.device().str().c_str());
-}
-
-int64_t integer(PyObject* o) {
-  const int64_t v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) throw Refused();
-  return v;
-}
-
-int32_t dtype_code(const at::Tensor& t) {
-  switch (t.scalar_type()) {
-    case at::kFloat: return NVFP4_F32;
-    case at::kBFloat16: return NVFP4_BF16;
-    case at::kHalf: return NVFP4_F16;
-    default:
-      PyErr_Format(PyExc_TypeError, "unsupported dtype %s", at::toString(t.scalar_type()));
-      throw Refused();
-  }
-}
-
-// a dense int32 tensor [n]
-int32_t* ints(PyObject* o, int64_t n, const char* name, const at::Tensor& like) {
-  const at::Tensor& t = tensor(o, name);
-  if (t.scalar_type() != at::kInt) refuse("%s must be int32, got %s", name, at::toString(t.scalar_type()));
-  if (t.dim() != 1 || t.size(0) != n)
-    refuse("%s must have shape (%lld,), got %s", name, (long long)n, shape_of(t).c_str());
-  if (!t.is_contiguous()) refuse("%s must be contiguous", name);
-  on_device(t, name, like);
-  return static_cast<int32_t*>(t.data_ptr());
-}
-
-// a one-element float32 tensor
-const float* scale(PyObject* o, const char* name, const at::Tensor& like) {
-  const at::Tensor& t = tensor(o, name);
-  if (t.scalar_type() != at::kFloat || t.numel() != 1)
-    refuse("%s must be a float32 tensor with one element, got %s with %lld", name, at::toString(t.scalar_type()),
-           (long long)t.numel());
-  on_device(t, name, like);
-  return static_cast<const float*>(t.data_ptr());
-}
+using namespace nvfp4_bind;
 
 // int32 rows with unit column stride
 struct Table {
@@ -102,28 +27,6 @@ struct Table {
     on_device(t, "block_table", like);
     p = static_cast<int32_t*>(t.data_ptr());
     ld = rows > 1 ? t.stride(0) : columns;
-  }
-};
-
-// [tokens][heads][head_dim] with any strides between heads and tokens; the stride of an axis of one is free
-struct Heads {
-  void* p;
-  int64_t tokens, heads, dim, token, head;
-  Heads() : p(nullptr), tokens(0), heads(0), dim(0), token(0), head(0) {}
-  Heads(PyObject* o, const char* name, const at::Tensor& like, const at::Tensor* same = nullptr) {
-    const at::Tensor& t = tensor(o, name);
-    if (t.scalar_type() != like.scalar_type() || (same && t.sizes() != same->sizes()))
-      refuse("%s must be %s of shape %s, got %s %s", name, at::toString(like.scalar_type()),
-             shape_of(same ? *same : like).c_str(), at::toString(t.scalar_type()), shape_of(t).c_str());
-    if (t.dim() != 3) refuse("%s must be [tokens, heads, head_dim], got %s", name, shape_of(t).c_str());
-    on_device(t, name, like);
-    tokens = t.size(0);
-    heads = t.size(1);
-    dim = t.size(2);
-    if (t.stride(2) != 1 && dim != 1) refuse("%s must have unit stride along head_dim", name);
-    head = heads > 1 ? t.stride(1) : dim;
-    token = tokens > 1 ? t.stride(0) : heads * head;
-    p = t.data_ptr();
   }
 };
 
@@ -151,52 +54,6 @@ struct Caches {
     return static_cast<uint8_t*>(t.data_ptr());
   }
 };
-
-int64_t call1(PyObject* f, int64_t v) {
-  PyObject* arg = PyLong_FromLongLong(v);
-  PyObject* r = arg ? PyObject_CallOneArg(f, arg) : nullptr;
-  Py_XDECREF(arg);
-  if (!r) throw Refused();
-  const int64_t got = PyLong_AsLongLong(r);
-  Py_DECREF(r);
-  if (got == -1 && PyErr_Occurred()) throw Refused();
-  return got;
-}
-
-// `call(stream)` with the tensors' device current
-template <typename F>
-PyObject* launch(const char* name, const at::Tensor& like, PyObject* stream, F call) {
-  if (!like.is_cuda()) refuse("%s needs GPU tensors", name);
-  const int64_t index = like.get_device();
-  PyObject* now = PyObject_CallNoArgs(get_device);
-  if (!now) throw Refused();
-  const int64_t current = PyLong_AsLongLong(now);
-  Py_DECREF(now);
-  void* queue = reinterpret_cast<void*>(stream == Py_None ? call1(raw_stream, index) : integer(stream));
-  if (current != index) call1(exchange_device, index);
-  const int status = call(queue);
-  if (current != index) call1(exchange_device, current);
-  return PyLong_FromLong(status);
-}
-
-void count(Py_ssize_t got, Py_ssize_t want) {
-  if (got != want) {
-    PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, got);
-    throw Refused();
-  }
-}
-
-// no C++ exception leaves a function of the module
-template <typename F>
-PyObject* guarded(F f) {
-  try {
-    return f();
-  } catch (const Refused&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-  }
-  return nullptr;
-}
 
 PyObject* block_table(PyObject*, PyObject* const* o, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
@@ -315,7 +172,8 @@ PyObject* paged_attention(PyObject*, PyObject* const* o, Py_ssize_t n_args) {
 
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(block_table), METHOD(rope), METHOD(cache_write), METHOD(paged_attention),
-                         {nullptr, nullptr, 0, nullptr}};
+                         METHOD(causal_conv), METHOD(causal_conv_step), METHOD(gated_delta_chunked), METHOD(gated_delta_step),
+                         METHOD(group_norm), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kv_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

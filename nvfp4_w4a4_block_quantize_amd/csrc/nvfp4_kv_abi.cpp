@@ -7,38 +7,14 @@
 #include <cmath>
 #include <cstdint>
 
+#include "abi_checks.h"
 #include "kv_internal.h"
 
 namespace {
 
-inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using namespace nvfp4;
 
-inline int dtype_size(int32_t dt) { return dt == NVFP4_F32 ? 4 : (dt == NVFP4_BF16 || dt == NVFP4_F16) ? 2 : 0; }
-
-// true when a GPU is usable from this thread (checked only after validation)
-inline bool device_ok() {
-  int dev = -1;
-  return hipGetDevice(&dev) == hipSuccess && dev >= 0;
-}
-
-constexpr int64_t kMaxDim = (int64_t)1 << 31;     // sizes are below 2^31
-constexpr int64_t kMaxStride = (int64_t)1 << 40;  // strides too large for a byte offset are refused
-constexpr int64_t kMaxRow = (int64_t)1 << 26;     // elements of one token's heads
-
-constexpr int64_t kMaxReach = (int64_t)1 << 37;   // tokens of a full table row times query heads
-
-inline bool size_ok(int64_t n) { return n > 0 && n < kMaxDim; }
-
-// heads * head_dim elements of a token; both factors are checked before they are multiplied
-inline bool row_ok(int64_t heads, int64_t head_dim) {
-  return heads > 0 && head_dim > 0 && heads < kMaxRow && head_dim < kMaxRow && heads * head_dim <= kMaxRow;
-}
-
-// no two elements of a [tokens][heads][head_dim] tensor share a place
-inline bool strides_ok(int64_t heads, int64_t head_dim, int64_t token, int64_t head) {
-  if (token >= kMaxStride || head >= kMaxStride || head < head_dim || token < head_dim) return false;
-  return (heads - 1) * head + head_dim <= token;
-}
+constexpr int64_t kMaxReach = (int64_t)1 << 37;  // tokens of a full table row times query heads
 
 inline bool page_ok(int64_t page_size) {
   return page_size >= 8 && page_size <= NVFP4_KV_MAX_PAGE_SIZE && page_size % 8 == 0;
@@ -57,10 +33,6 @@ inline bool attention_heads_ok(int64_t q_heads, int64_t kv_heads, int64_t head_d
   if (head_dim != 64 && head_dim != 128 && head_dim != 192 && head_dim != 256) return false;
   return row_ok(q_heads, head_dim) && row_ok(kv_heads, head_dim) && q_heads % kv_heads == 0;
 }
-
-inline bool by16(int64_t stride, int es) { return (stride * es) % 16 == 0; }
-
-inline nvfp4_status done(hipError_t e) { return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_DEVICE; }
 
 }  // namespace
 
