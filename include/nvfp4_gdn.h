@@ -137,7 +137,7 @@ nvfp4_status nvfp4_causal_conv_step(int64_t n_seqs, int64_t channels, int64_t wi
  *
  * Errors: NULL pointers -> ERR_NULL; sizes <= 0 or >= 2^31, head counts and
  * sizes other than above, heads * head_dim > 2^26, tokens * v_heads > 2^37,
- * overlapping strides, out = v, workspace_bytes too small -> ERR_SHAPE; alignment
+ * n_seqs * v_heads > 2^28, overlapping strides, out = v, workspace_bytes too small -> ERR_SHAPE; alignment
  * -> ERR_ALIGN; dtype -> ERR_DTYPE; scale not finite or <= 0, eps not finite or
  * < 0 -> ERR_RANGE.
  */

@@ -1,9 +1,28 @@
-// The gated delta rule over ragged prompts (nvfp4_gated_delta_chunked), token by token.
+// The gated delta rule over ragged prompts (nvfp4_gated_delta_chunked).
 //
-//   S' = e^g S;  d = beta (v - S'^T k~);  S_new = S' + k~ d^T;  out = scale S_new^T q~
+//   S <- e^g S;  S <- S + k~ (beta (v - S^T k~))^T;  out = scale S^T q~
 //
-// A workgroup holds 64 columns of one head's state in its threads' registers and walks
-// the sequence's tokens; each token costs a sum over the rows through LDS.
+// In chunks of C = 64 tokens, with G_i the sum of g over the chunk's first i tokens, what
+// the tokens write, V'_i = beta_i (v_i - S_i^T k~_i), solves a unit lower triangular
+// system, and everything else is products:
+//
+//   A_ij = beta_i e^(G_i - G_j) k~_i . k~_j  (j < i),  T = (1 + A)^-1
+//   X    = beta (V - e^G K~ S),  V' = T X
+//   out  = scale (e^G Q~ S + P V'),  P_ij = e^(G_i - G_j) q~_i . k~_j  (j <= i)
+//   S   <- e^(G_C) S + (e^(G_C - G) K~)^T V'
+//
+// Two kernels.  The first has a wave for each chunk and value head, all independent: it
+// normalises keys and queries and leaves T, P and the gates in the workspace.  The second
+// walks the chunks of a sequence with 16 NT columns of the state in a wave's registers:
+// columns never meet, and the matrix unit's results lie as its next operands want them,
+// so S, X and V' pass through neither LDS nor other lanes.
+//
+// Precision.  Operands are fp16 parts, sums fp32.  A row of keys or queries is scaled by a
+// power of two to a length in [16, 32): 16-bit inputs fit one part but for what lies 2^-30
+// below that length; float32 takes two.  |T| and |P| are at most 1 and scaled by 2^14;
+// a column of S, and with it X and V', is scaled by a power of two that follows it and the
+// values: each is cut into two parts, 2^-22 of the element or 2^-31 of the column's largest.
+// Of products of two cut operands the low parts' is dropped (2^-22 again).
 #include <algorithm>
 
 #include "gdn_device.h"
@@ -11,137 +30,721 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kCols = 64;
+constexpr int kC = kDeltaChunk;
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kBlock = 1024;  // an operand of 16 x 32 fp16 elements: 16 bytes a lane
+constexpr int kTies = 6;      // blocks of 16 x 32 that meet the lower triangle of 64 x 64
+constexpr int kPAt = kTies * 2 * kBlock, kGatesAt = 2 * kPAt;
+constexpr float kUp = 16384.0f, kDown = 1.0f / 16384.0f;  // 2^14
+constexpr int kLength = 4;                                // rows of keys and queries have lengths from 2^4 to 2^5
+constexpr float kLong = 1 << kLength;
+
+// per token of a chunk, after T and P
+enum { kBeta, kGainK, kUntil, kGainQ, kWhole, kGates };
+static_assert(kGatesAt + kGates * kC * 4 <= kDeltaTieBytes, "the workspace's entry holds it");
+
+constexpr int tie(int mt, int s) { return mt < 2 ? mt : 2 * mt - 2 + s; }  // of rows 16 mt.., columns 32 s..
+
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ float4_t mfma(half8_t a, half8_t b, float4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// eight floats as fp16 parts, the second what the first leaves
+struct Parts {
+  half8_t hi, lo;
+};
+__device__ __forceinline__ half8_t halves(const float (&x)[8]) {
+  half8_t y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const half2_t p = __builtin_convertvector(float2_t{x[2 * i], x[2 * i + 1]}, half2_t);
+    y[2 * i] = p[0];
+    y[2 * i + 1] = p[1];
+  }
+  return y;
+}
+__device__ __forceinline__ Parts cut(const float (&x)[8]) {
+  Parts p;
+  p.hi = halves(x);
+  float rest[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) rest[i] = x[i] - (float)p.hi[i];
+  p.lo = halves(rest);
+  return p;
+}
+__device__ __forceinline__ Parts cut(float4_t a, float4_t b) {
+  const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return cut(x);
+}
+
+// ---------------------------------------------------------------- a chunk's ties
+
+constexpr int kPitch = 20;  // floats of a row of 16 in LDS: rows that lanes read side by side meet distinct banks
+constexpr int kSquare = 16 * kPitch;
+constexpr int square(int j, int i) { return i * (i + 1) / 2 + j; }  // of block column j, block row i
+
+struct SolveLds {
+  float a[10 * kSquare];  // A^T by blocks: row j, column i; then the inverse's
+  double log_decay[kC];
+  float beta[kC], k_norm[kC], q_norm[kC];
+};
+
+// Rows of q or k as operands: lane (g, m) holds elements 32 s + 8 g.. of row m, a power of two times the input; what that
+// times `norm` is, has length 1.
+template <int DT, int DK>
+struct Row {
+  static constexpr int kSteps = DK / 32, kParts = DT == 0 ? 2 : 1;
+  half8_t part[kParts][kSteps];
+  float norm;
+  __device__ __forceinline__ void load(const HeadsIn& x, int64_t token, int head, int g, bool there, float eps) {
+    Elements<DT, 8> e[kSteps];
+    const int64_t at = token * x.token + head * x.head + 8 * g;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      e[s].load(x.p, at + 32 * s);
+      if (!there) e[s].zero();
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(e[s].get(i)));
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    int up = -__builtin_amdgcn_frexp_expf(top);  // the largest into [1/2, 1), so that squares neither overflow nor vanish
+    float squares = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = __builtin_amdgcn_ldexpf(e[s].get(i), up);
+        squares = __builtin_fmaf(y, y, squares);
+      }
+    squares += __shfl_xor(squares, 16);
+    squares += __shfl_xor(squares, 32);
+    const int more_up = kLength + 1 - ((__builtin_amdgcn_frexp_expf(squares) + 1) >> 1);
+    up += more_up;
+    squares = __builtin_amdgcn_ldexpf(squares, 2 * more_up);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_ldexpf(e[s].get(i), up);
+      if constexpr (kParts == 2) {
+        const Parts p = cut(y);
+        part[0][s] = p.hi;
+        part[1][s] = p.lo;
+      } else {
+        part[0][s] = halves(y);
+      }
+    }
+    // 1 / sqrt(|x|^2 + eps), of x scaled: where eps is then infinite, x is nothing beside it
+    const float more = __builtin_amdgcn_ldexpf(eps, 2 * up), all = squares + more;
+    norm = more > 3e38f ? __builtin_amdgcn_ldexpf(1.0f / sqrtf(eps), -up) : 1.0f / sqrtf(all);
+    if (squares == 0.0f) norm = 0.0f;  // at most 2^-4 then, whatever eps is
+  }
+  __device__ __forceinline__ void store(uint8_t* image, int mt, int lane) const {
+#pragma unroll
+    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        *reinterpret_cast<half8_t*>(image + ((p * 4 + mt) * kSteps + s) * kBlock + lane * 16) = part[p][s];
+  }
+};
+
+// rows of a times rows of b: lane (g, n) has rows 4 g.. of a against row n of b
+template <int DT, int DK>
+__device__ __forceinline__ float4_t dots(const Row<DT, DK>& a, const Row<DT, DK>& b) {
+  float4_t c = {0, 0, 0, 0};
+#pragma unroll
+  for (int s = 0; s < DK / 32; ++s) {
+    c = mfma(a.part[0][s], b.part[0][s], c);
+    if constexpr (DT == 0) {
+      c = mfma(a.part[0][s], b.part[1][s], c);
+      c = mfma(a.part[1][s], b.part[0][s], c);
+    }
+  }
+  return c;
+}
+
+// the chunk of place c: its sequence and rows; false if no sequence has it
+struct Place {
+  int r, slot;
+  int64_t begin, end;
+};
+__device__ __forceinline__ bool find_place(const DeltaArgs& a, int64_t c, Place& p) {
+  int low = 0, high = a.n_seqs;  // the last sequence whose first place is at most c
+  while (high - low > 1) {
+    const int mid = low + (high - low) / 2;
+    if (start_of(a.token_starts, mid, a.tokens) / kC + mid <= c) low = mid; else high = mid;
+  }
+  const int64_t start = start_of(a.token_starts, low, a.tokens);
+  const int64_t at = c - (start / kC + low);
+  p.r = low;
+  p.begin = start + at * kC;
+  p.end = start_of(a.token_starts, low + 1, a.tokens);
+  p.slot = a.slots[low];
+  return at >= 0 && p.begin < p.end && slot_ok(p.slot, a.num_slots);
+}
+
+// c - a b, of 16 x 16 blocks in fp32: a from LDS by rows, b and c as the matrix unit leaves results.  Step r of four takes
+// the products' elements 4 g + r, which are register r of b.
+__device__ __forceinline__ float4_t less_product(const float* a, float4_t b, float4_t c, int g, int n) {
+  const float4_t row = *reinterpret_cast<const float4_t*>(a + n * kPitch + 4 * g);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(-row[r], b[r], c, 0, 0, 0);
+  return c;
+}
+
+__device__ __forceinline__ void store_block(float* to, float4_t x, int g, int n) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) to[(4 * g + r) * kPitch + n] = x[r];
+}
+__device__ __forceinline__ float4_t load_block(const float* from, int g, int n) {
+  float4_t x;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) x[r] = from[(4 * g + r) * kPitch + n];
+  return x;
+}
+
+// rows 16 mt.. of T or P, transposed as the matrix unit leaves them (block j: columns 16 j..), into operands
+__device__ __forceinline__ void store_ties(uint8_t* to, int mt, const float4_t (&block)[4], int lane) {
+  const float4_t none = {0, 0, 0, 0};
+#pragma unroll
+  for (int s = 0; s <= mt / 2; ++s) {
+    const Parts p = cut(block[2 * s] * kUp, 2 * s + 1 <= mt ? block[2 * s + 1] * kUp : none);
+    *reinterpret_cast<half8_t*>(to + (2 * tie(mt, s)) * kBlock + lane * 16) = p.hi;
+    *reinterpret_cast<half8_t*>(to + (2 * tie(mt, s) + 1) * kBlock + lane * 16) = p.lo;
+  }
+}
 
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
 
 template <int DT, int DK>
-__global__ __launch_bounds__(kThreads) void gated_delta_kernel(DeltaArgs a, FastDiv by_group, int64_t first) {
-  constexpr int kLanes = kCols / 4;
-  constexpr int kGroups = kThreads / kLanes;
-  constexpr int kRows = DK / kGroups;
-  constexpr int kWaves = kThreads / 64;
-  __shared__ float lds_k[2][DK], lds_q[2][DK];
-  __shared__ float4_t lds_sum[2][2][kWaves][kLanes];
-  const int slices = a.head_v / kCols;
-  const int64_t item = first + blockIdx.x;
-  const int64_t pair = item / slices;
-  const int column = (int)(item - pair * slices) * kCols;
-  const int64_t r = pair / a.v_heads;
-  const int h = (int)(pair - r * a.v_heads);
-  const int slot = a.slots[r];
-  const int64_t begin = start_of(a.token_starts, (int)r, a.tokens), end = start_of(a.token_starts, (int)r + 1, a.tokens);
-  if (!slot_ok(slot, a.num_slots) || begin >= end) return;
-  const int thread = threadIdx.x, lane = thread & 63, wave = thread >> 6;
-  const int col = thread % kLanes, row = thread / kLanes;
-  const int64_t state = (((int64_t)slot * a.v_heads + h) * DK) * a.head_v + column + 4 * col;
-  const bool carried = !a.cached_lens || a.cached_lens[r] > 0;
-  float4_t s[kRows];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    s[i] = carried ? *reinterpret_cast<const float4_t*>(a.state + state + (int64_t)(row + i * kGroups) * a.head_v)
-                   : float4_t{0, 0, 0, 0};
+__global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a, FastDiv by_group, FastDiv by_blocks,
+                                                                     int64_t first_place) {
+  __shared__ SolveLds all[kWaves];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, n = lane & 15;
+  const uint32_t of_launch = by_blocks.div(blockIdx.x);
+  const int h = (int)(blockIdx.x - of_launch * by_blocks.d) * kWaves + wave;
+  const int64_t place = first_place + of_launch;
+  Place at;
+  if (h >= a.v_heads || !find_place(a, place, at)) return;  // whole waves: the kernel has no barrier
   const int kh = (int)by_group.div((uint32_t)h);
-  const float rate = expf(a.a_log[h]), dt = a.dt_bias[h];
-  constexpr int kOf = DK / 64;
-  for (int64_t t = begin; t < end; ++t) {
-    const int turn = (int)(t & 1);
-    float kv[kOf], qv[kOf], kk = 0.0f, qq = 0.0f, kq = 0.0f;
+  const bool leads = h == kh * (int)by_group.d;  // of its key head
+  const int rows = (int)std::min<int64_t>(kC, at.end - at.begin);
+  SolveLds& lds = all[wave];
+  uint8_t* base = static_cast<uint8_t*>(a.workspace) + place * delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT);
+  uint8_t* keys = base + kh * delta_key_bytes(DK, DT);
+  uint8_t* queries = keys + delta_key_bytes(DK, DT) / 2;
+  uint8_t* ties = base + a.k_heads * delta_key_bytes(DK, DT) + (int64_t)h * kDeltaTieBytes;
+
+  // keys
+  Row<DT, DK> k[4];
 #pragma unroll
-    for (int i = 0; i < kOf; ++i) {
-      kv[i] = element<DT>(a.k.p, t * a.k.token + kh * a.k.head + lane + 64 * i);
-      qv[i] = element<DT>(a.q.p, t * a.q.token + kh * a.q.head + lane + 64 * i);
-      kk = __builtin_fmaf(kv[i], kv[i], kk);
-      qq = __builtin_fmaf(qv[i], qv[i], qq);
-      kq = __builtin_fmaf(kv[i], qv[i], kq);
+  for (int mt = 0; mt < 4; ++mt) {
+    const int row = 16 * mt + n;
+    k[mt].load(a.k, at.begin + std::min(row, rows - 1), kh, g, row < rows, a.eps);
+    if (leads) k[mt].store(keys, mt, lane);
+    if (g == 0) lds.k_norm[row] = k[mt].norm;
+  }
+
+  // gates of token `lane`: the sum of log2 decays in 64 bits, since only differences count
+  const int64_t token = at.begin + std::min(lane, rows - 1);
+  const float decay = -expf(a.a_log[h]) * softplus(element<DT>(a.a, token * a.a_token + h) + a.dt_bias[h]);
+  const float beta = lane < rows ? sigmoid<true>(element<DT>(a.b, token * a.b_token + h)) : 0.0f;
+  double log_decay = lane < rows ? (double)decay * 1.4426950408889634 : 0.0;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const double before = __shfl_up(log_decay, d);
+    if (lane >= d) log_decay += before;
+  }
+  const double whole = __shfl(log_decay, 63);
+  lds.log_decay[lane] = log_decay;
+  lds.beta[lane] = beta;
+  wave_sync();
+
+  // e^(G_i - G_j) of this lane's elements of block (j, i): column i = 16 bi + n, rows j = 16 bj + 4 g + r
+  auto ratio = [&](int bj, int bi) {
+    const double of_i = lds.log_decay[16 * bi + n];
+    float4_t x;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float d = (float)(of_i - lds.log_decay[16 * bj + 4 * g + r]);
+      x[r] = bj < bi || 4 * g + r <= n ? __builtin_amdgcn_exp2f(d) : 0.0f;
     }
+    return x;
+  };
+  auto of_rows = [&](const float* x, int bj) { return *reinterpret_cast<const float4_t*>(x + 16 * bj + 4 * g); };
+
+  // P by rows of blocks, and A^T
 #pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-      kk += __shfl_xor(kk, m);
-      qq += __shfl_xor(qq, m);
-      kq += __shfl_xor(kq, m);
+  for (int bi = 0; bi < 4; ++bi) {
+    Row<DT, DK> q;
+    const int row = 16 * bi + n;
+    q.load(a.q, at.begin + std::min(row, rows - 1), kh, g, row < rows, a.eps);
+    if (leads) q.store(queries, bi, lane);
+    if (g == 0) lds.q_norm[row] = q.norm;
+    const float strength = lds.beta[row] * k[bi].norm;
+    float4_t p[4];
+#pragma unroll
+    for (int bj = 0; bj <= bi; ++bj) {
+      const float4_t e = ratio(bj, bi) * of_rows(lds.k_norm, bj);
+      p[bj] = e * q.norm * dots(k[bj], q);
+      float4_t x = e * strength * dots(k[bj], k[bi]);
+      if (bj == bi) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = 4 * g + r < n ? x[r] : 0.0f;
+      }
+      store_block(lds.a + square(bj, bi) * kSquare, x, g, n);
     }
-    const float kn = 1.0f / sqrtf(kk + a.eps), qn = 1.0f / sqrtf(qq + a.eps);
-    kq *= kn * qn;
-    if (wave == 0) {
+    store_ties(ties + kPAt, bi, p, lane);
+  }
+  wave_sync();
+
+  // T of the diagonal blocks by substitution: lane (b, c) has column c of block b, and takes column j of A once x_j is known
+  {
+    float* block = lds.a + square(g, g) * kSquare;
+    float x[16];
 #pragma unroll
-      for (int i = 0; i < kOf; ++i) {
-        lds_k[turn][lane + 64 * i] = kv[i] * kn;
-        lds_q[turn][lane + 64 * i] = qv[i] * qn;
+    for (int i = 0; i < 16; ++i) x[i] = i == n ? 1.0f : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 15; ++j) {
+#pragma unroll
+      for (int i4 = (j + 1) / 4; i4 < 4; ++i4) {
+        const float4_t col = *reinterpret_cast<const float4_t*>(block + j * kPitch + 4 * i4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * i4 + i > j) x[4 * i4 + i] = __builtin_fmaf(-col[i], x[j], x[4 * i4 + i]);
       }
     }
-    const float alpha = expf(-rate * softplus(element<DT>(a.a, t * a.a_token + h) + dt));
-    const float beta = sigmoid<true>(element<DT>(a.b, t * a.b_token + h));
-    __syncthreads();
-    float4_t u = {0, 0, 0, 0}, w = {0, 0, 0, 0};
+    wave_sync();
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float kr = lds_k[turn][row + i * kGroups], qr = lds_q[turn][row + i * kGroups];
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4_t*>(block + n * kPitch + 4 * i) = float4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+    wave_sync();
+  }
+  // U = T^T by blocks: [U0 U01; 0 U1] has U01 = -U0 A01^T U1, first of 16 x 16, then of 32 x 32
+  const float4_t none = {0, 0, 0, 0};
+  auto of = [&](int j, int i) { return lds.a + square(j, i) * kSquare; };
+  float4_t u[4][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u[j] = __builtin_fmaf(s[i][j], kr, u[j]);
-        w[j] = __builtin_fmaf(s[i][j], qr, w[j]);
-      }
+  for (int b = 0; b < 4; ++b) u[b][b] = load_block(of(b, b), g, n);
+#pragma unroll
+  for (int b = 0; b < 4; b += 2) {
+    const float4_t x = less_product(of(b, b + 1), u[b + 1][b + 1], none, g, n);
+    u[b][b + 1] = -less_product(of(b, b), x, none, g, n);
+  }
+  wave_sync();
+  store_block(of(0, 1), u[0][1], g, n);
+  wave_sync();
+#pragma unroll
+  for (int i = 2; i < 4; ++i) {
+    float4_t x[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      x[j] = less_product(of(j, 2), u[2][i], none, g, n);
+      if (i == 3) x[j] = less_product(of(j, 3), u[3][3], x[j], g, n);
     }
-#pragma unroll
-    for (int m = kLanes; m < 64; m *= 2) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u[j] += __shfl_xor(u[j], m);
-        w[j] += __shfl_xor(w[j], m);
-      }
-    }
-    if (lane < kLanes) {
-      lds_sum[turn][0][wave][lane] = u;
-      lds_sum[turn][1][wave][lane] = w;
-    }
-    __syncthreads();
-    u = lds_sum[turn][0][0][col];
-    w = lds_sum[turn][1][0][col];
-#pragma unroll
-    for (int i = 1; i < kWaves; ++i) {
-      u += lds_sum[turn][0][i][col];
-      w += lds_sum[turn][1][i][col];
-    }
-    float4_t d;
-    const int64_t vo = t * a.v.token + h * a.v.head + column + 4 * col;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d[j] = beta * (element<DT>(a.v.p, vo + j) - alpha * u[j]);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float kr = lds_k[turn][row + i * kGroups];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = __builtin_fmaf(kr, d[j], alpha * s[i][j]);
-    }
-    if (row == 0) {
-      const int64_t o = t * a.out.token + h * a.out.head + column + 4 * col;
-      float y[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = a.scale * __builtin_fmaf(kq, d[j], alpha * w[j]);
-      if constexpr (DT == 0)
-        *reinterpret_cast<float4_t*>(static_cast<float*>(a.out.p) + o) = float4_t{y[0], y[1], y[2], y[3]};
-      else
-        *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out.p) + o) =
-            u32x2_t{pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3])};
-    }
+    u[1][i] = -less_product(of(1, 1), x[1], none, g, n);
+    u[0][i] = -less_product(of(0, 1), x[1], less_product(of(0, 0), x[0], none, g, n), g, n);
   }
 #pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    *reinterpret_cast<float4_t*>(a.state_out + state + (int64_t)(row + i * kGroups) * a.head_v) = s[i];
+  for (int mt = 0; mt < 4; ++mt) {
+    const float4_t rows_of[4] = {u[0][mt], mt >= 1 ? u[1][mt] : none, mt >= 2 ? u[2][mt] : none, mt >= 3 ? u[3][mt] : none};
+    store_ties(ties, mt, rows_of, lane);
+  }
+
+  float* gates = reinterpret_cast<float*>(ties + kGatesAt);
+  const float since = __builtin_amdgcn_exp2f((float)log_decay), k_norm = lds.k_norm[lane];
+  gates[kBeta * kC + lane] = beta;
+  gates[kGainK * kC + lane] = beta * since * k_norm * (1.0f / kLong);
+  gates[kUntil * kC + lane] = __builtin_amdgcn_exp2f((float)(whole - log_decay)) * k_norm * kLong;
+  gates[kGainQ * kC + lane] = since * lds.q_norm[lane] * (kUp / kLong);
+  gates[kWhole * kC + lane] = __builtin_amdgcn_exp2f((float)whole);
+}
+
+// -------------------------------------------------------------- the states' chain
+
+typedef short short4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) short4_t lds_short4_t;
+
+// Four rows of 16 16-bit elements that a group of 16 lanes points at, four elements a lane; lane n gets column n.
+__device__ __forceinline__ short4_t read_columns(const uint8_t* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)p);
+}
+
+template <int DT, int DK, int NT>
+struct Chain {
+  static constexpr int kParts = DT == 0 ? 2 : 1, kSteps = DK / 32, kTiles = DK / 16;
+  static constexpr int kCols = 16 * NT * kWaves;  // of a workgroup
+  static constexpr int kKeys = kParts * 4 * kSteps * kBlock;  // bytes of K; Q follows
+  static constexpr int kValueRow = kCols * element_size(DT);
+  static constexpr int kTiesAt = 2 * kKeys, kValuesAt = kTiesAt + kDeltaTieBytes;
+  static constexpr int kStage = kValuesAt + kC * kValueRow;
+  static constexpr int kStages = 2 * kStage <= (160 << 10) ? 2 : 1;
+  static_assert(kStages * kStage <= (160 << 10), "the stages fit LDS");
+};
+
+#if defined(__HIP_DEVICE_COMPILE__)
+// 16 bytes a lane from memory to LDS byte lds + 16 lane, past the registers.  M0 is set in the same block, one wait state
+// before the load reads it.
+__device__ __forceinline__ void to_lds(uint32_t lds, const void* base, uint32_t offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void to_lds(uint32_t lds, const void* p) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
+}
+#endif
+
+template <int DT, int DK, int NT>
+__global__ __launch_bounds__(kThreads, 1) void gated_delta_chain_kernel(DeltaArgs a, FastDiv by_seq, FastDiv by_key_heads,
+                                                                        uint32_t slices, uint32_t first, uint32_t pairs) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  using L = Chain<DT, DK, NT>;
+  __shared__ __attribute__((aligned(1024))) uint8_t stage[L::kStages * L::kStage];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, n = lane & 15;
+
+  // Workgroups go to the XCDs in turn: those of one sequence and head, which read the same ties, and where there are 8 key
+  // heads (or a multiple) those of one key head lie on one XCD, 8 apart.
+  const uint32_t x = first + blockIdx.x, eight = x >> 3;
+  const uint32_t octet = eight / slices, pair = octet * 8 + (x & 7);
+  if (pair >= pairs) return;
+  const int column = (int)(eight - octet * slices) * L::kCols + wave * 16 * NT;  // of this wave
+  const int group = a.v_heads / a.k_heads;
+  const uint32_t r = by_seq.div(pair), in_seq = pair - r * by_seq.d;
+  const uint32_t of_group = by_key_heads.div(in_seq);
+  const int kh = (int)(in_seq - of_group * by_key_heads.d), h = kh * group + (int)of_group;
+  const int slot = a.slots[r];
+  const int64_t start = start_of(a.token_starts, (int)r, a.tokens), end = start_of(a.token_starts, (int)r + 1, a.tokens);
+  if (!slot_ok(slot, a.num_slots) || start >= end) return;
+  const int64_t chunks = (end - start + kC - 1) / kC;
+  const int64_t chunk_bytes = delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT);
+  const uint8_t* from = static_cast<const uint8_t*>(a.workspace) + (start / kC + r) * chunk_bytes;
+  const int64_t keys_at = kh * delta_key_bytes(DK, DT),
+                ties_at = a.k_heads * delta_key_bytes(DK, DT) + (int64_t)h * kDeltaTieBytes;
+  const int group_column = (int)(eight - octet * slices) * L::kCols;
+  const char* values = static_cast<const char*>(a.v.p) + (h * a.v.head + group_column) * element_size(DT);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)stage;
+
+  auto issue = [&](int64_t c, int to) {
+    const uint32_t lds = lds0 + to * L::kStage;
+    const uint8_t* base = from + c * chunk_bytes;
+#pragma unroll
+    for (int i = 0; i < (2 * L::kKeys / kBlock + kWaves - 1) / kWaves; ++i) {
+      const int p = i * kWaves + wave;
+      if (p < 2 * L::kKeys / kBlock) to_lds(lds + p * kBlock, base + keys_at + p * kBlock, lane * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < (kDeltaTieBytes / kBlock + kWaves - 1) / kWaves; ++i) {
+      const int p = i * kWaves + wave;
+      if (p < kDeltaTieBytes / kBlock) to_lds(lds + L::kTiesAt + p * kBlock, base + ties_at + p * kBlock, lane * 16);
+    }
+    constexpr int kRows = kBlock / L::kValueRow;  // of values a load
+#pragma unroll
+    for (int i = 0; i < kC / kRows / kWaves; ++i) {
+      const int p = i * kWaves + wave;
+      const int64_t token = std::min(start + c * kC + p * kRows + lane * 16 / L::kValueRow, end - 1);
+      to_lds(lds + L::kValuesAt + p * kBlock, values + token * a.v.token * element_size(DT) + lane * 16 % L::kValueRow);
+    }
+  };
+  auto arrived = [&] {  // this wave's loads are there and its LDS reads done, then everyone's
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  issue(0, 0);
+  // The state: tile 2 s + t, register q of lane (g, n) is row 32 s + 8 g + 4 t + q, column n, so that two tiles are the
+  // eight elements of an operand that meet elements 32 s + 8 g.. of a row of K or Q.
+  float4_t s[L::kTiles][NT];
+  int scaled[NT];  // the state is s 2^(scaled - 4), values are taken times 2^-scaled
+  const int64_t state = ((int64_t)slot * a.v_heads + h) * DK * a.head_v + column + n;
+  const bool carried = !a.cached_lens || a.cached_lens[r] > 0;
+#pragma unroll
+  for (int t = 0; t < L::kTiles; ++t)
+#pragma unroll
+    for (int w = 0; w < NT; ++w) {
+      scaled[w] = kLength;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        s[t][w][q] = carried ? a.state[state + (int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * a.head_v + 16 * w] : 0.0f;
+    }
+  arrived();
+
+  for (int64_t c = 0; c < chunks; ++c) {
+    const int now = L::kStages == 2 ? (int)(c & 1) : 0;
+    if (L::kStages == 2 && c + 1 < chunks) issue(c + 1, now ^ 1);
+    const uint8_t* here = stage + now * L::kStage;
+    const uint8_t* ties = here + L::kTiesAt;
+    const float* gates = reinterpret_cast<const float*>(ties + kGatesAt);
+    auto key = [&](int of_q, int part, int mt, int st) {
+      return *reinterpret_cast<const half8_t*>(here + of_q * L::kKeys + ((part * 4 + mt) * L::kSteps + st) * kBlock + lane * 16);
+    };
+    auto tied = [&](int at, int mt, int st, int part) {
+      return *reinterpret_cast<const half8_t*>(ties + at + (2 * tie(mt, st) + part) * kBlock + lane * 16);
+    };
+    auto gate = [&](int which, int mt) { return *reinterpret_cast<const float4_t*>(gates + which * kC + 16 * mt + 4 * g); };
+
+    // values of this wave's columns
+    float4_t x[4][NT];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int w = 0; w < NT; ++w) {
+        const uint8_t* v = here + L::kValuesAt + (wave * 16 * NT + 16 * w) * element_size(DT);
+        if constexpr (DT == 0) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            x[mt][w][q] = *reinterpret_cast<const float*>(v + (16 * mt + 4 * g + q) * L::kValueRow + 4 * n);
+        } else {
+          const short4_t e = read_columns(v + (16 * mt + 4 * g + n / 4) * L::kValueRow + (n % 4) * 8);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (DT == 1)
+              x[mt][w][q] = __uint_as_float((uint32_t)(uint16_t)e[q] << 16);
+            else
+              x[mt][w][q] = (float)__builtin_bit_cast(_Float16, (short)e[q]);
+          }
+        }
+      }
+
+    // What a column's tokens bring, beta v, and its power of two, with M the largest of that and of the state's elements: M
+    // goes to 2^7..2^8 when it has left 2^5..2^9.  The state's length is at most sqrt(128) M and grows by M a token, so that
+    // X and V' stay below 75 M < 2^16; |S| 2^4 is below 2^13; a part's last bit lies 2^31 below M.
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      const float4_t beta = gate(kBeta, mt);
+#pragma unroll
+      for (int w = 0; w < NT; ++w) x[mt][w] *= beta;
+    }
+    {
+      bool off = c == 0;
+      float top[NT], high[NT];
+#pragma unroll
+      for (int w = 0; w < NT; ++w) {
+        top[w] = high[w] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < L::kTiles; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) top[w] = fmaxf(top[w], fabsf(s[t][w][q]));
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) high[w] = fmaxf(high[w], fabsf(x[mt][w][q]));
+        const float both = fmaxf(top[w] * (1.0f / kLong), __builtin_amdgcn_ldexpf(high[w], -scaled[w]));
+        off = off || both > 512.0f || (both < 32.0f && both > 0.0f && scaled[w] > -150);
+      }
+      if (__any(off)) {
+#pragma unroll
+        for (int w = 0; w < NT; ++w) {
+          top[w] = fmaxf(top[w], __shfl_xor(top[w], 16));
+          top[w] = fmaxf(top[w], __shfl_xor(top[w], 32));
+          high[w] = fmaxf(high[w], __shfl_xor(high[w], 16));
+          high[w] = fmaxf(high[w], __shfl_xor(high[w], 32));
+          constexpr int kNone = -100000;
+          const int of_state = top[w] > 0.0f ? __builtin_amdgcn_frexp_expf(top[w]) + scaled[w] - kLength : kNone;
+          const int of_values = high[w] > 0.0f ? __builtin_amdgcn_frexp_expf(high[w]) : kNone;
+          const int most = std::max(of_state, of_values), here_ = most - scaled[w];
+          if (most != kNone && (here_ > 9 || here_ < 6)) {
+            const int next = std::max(most - 8, -150), by = scaled[w] - next;
+            scaled[w] = next;
+#pragma unroll
+            for (int t = 0; t < L::kTiles; ++t)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) s[t][w][q] = __builtin_amdgcn_ldexpf(s[t][w][q], by);
+          }
+        }
+      }
+    }
+
+    // K S and Q S
+    float4_t y[4][NT], o[4][NT];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int w = 0; w < NT; ++w) y[mt][w] = o[mt][w] = float4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int st = 0; st < L::kSteps; ++st) {
+      Parts b[NT];
+#pragma unroll
+      for (int w = 0; w < NT; ++w) b[w] = cut(s[2 * st][w], s[2 * st + 1][w]);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        const half8_t k = key(0, 0, mt, st), q = key(1, 0, mt, st);
+#pragma unroll
+        for (int w = 0; w < NT; ++w) {
+          y[mt][w] = mfma(k, b[w].hi, y[mt][w]);
+          o[mt][w] = mfma(q, b[w].hi, o[mt][w]);
+          y[mt][w] = mfma(k, b[w].lo, y[mt][w]);
+          o[mt][w] = mfma(q, b[w].lo, o[mt][w]);
+        }
+        if constexpr (L::kParts == 2) {
+          const half8_t k2 = key(0, 1, mt, st), q2 = key(1, 1, mt, st);
+#pragma unroll
+          for (int w = 0; w < NT; ++w) {
+            y[mt][w] = mfma(k2, b[w].hi, y[mt][w]);
+            o[mt][w] = mfma(q2, b[w].hi, o[mt][w]);
+          }
+        }
+      }
+    }
+
+    // X, then V' = T X
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      const float4_t gain = gate(kGainK, mt), gain_q = gate(kGainQ, mt);
+#pragma unroll
+      for (int w = 0; w < NT; ++w) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          x[mt][w][q] = __builtin_fmaf(-gain[q], y[mt][w][q], __builtin_amdgcn_ldexpf(x[mt][w][q], -scaled[w]));
+        o[mt][w] *= gain_q;
+        y[mt][w] = float4_t{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      Parts b[NT];
+#pragma unroll
+      for (int w = 0; w < NT; ++w) b[w] = cut(x[2 * st][w], x[2 * st + 1][w]);
+#pragma unroll
+      for (int mt = 2 * st; mt < 4; ++mt) {
+        const half8_t hi = tied(0, mt, st, 0), lo = tied(0, mt, st, 1);
+#pragma unroll
+        for (int w = 0; w < NT; ++w) {
+          y[mt][w] = mfma(hi, b[w].hi, y[mt][w]);
+          y[mt][w] = mfma(hi, b[w].lo, y[mt][w]);
+          y[mt][w] = mfma(lo, b[w].hi, y[mt][w]);
+        }
+      }
+    }
+
+    // P V' onto Q S, and K^T V' onto the decayed state
+    const float whole = gates[kWhole * kC];
+#pragma unroll
+    for (int t = 0; t < L::kTiles; ++t)
+#pragma unroll
+      for (int w = 0; w < NT; ++w) s[t][w] *= whole;
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      Parts b[NT], d[NT];
+      const float4_t until0 = gate(kUntil, 2 * st), until1 = gate(kUntil, 2 * st + 1);
+#pragma unroll
+      for (int w = 0; w < NT; ++w) {
+        const float4_t v0 = y[2 * st][w] * kDown, v1 = y[2 * st + 1][w] * kDown;
+        b[w] = cut(v0, v1);
+        d[w] = cut(v0 * until0, v1 * until1);
+      }
+#pragma unroll
+      for (int mt = 2 * st; mt < 4; ++mt) {
+        const half8_t hi = tied(kPAt, mt, st, 0), lo = tied(kPAt, mt, st, 1);
+#pragma unroll
+        for (int w = 0; w < NT; ++w) {
+          o[mt][w] = mfma(hi, b[w].hi, o[mt][w]);
+          o[mt][w] = mfma(hi, b[w].lo, o[mt][w]);
+          o[mt][w] = mfma(lo, b[w].hi, o[mt][w]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < L::kTiles; ++t) {
+        half8_t k[L::kParts];
+#pragma unroll
+        for (int p = 0; p < L::kParts; ++p) {
+          short4_t e[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)  // tokens 32 st + 16 j + 4 g.., rows of this tile
+            e[j] = read_columns(here + ((p * 4 + 2 * st + j) * L::kSteps + t / 2) * kBlock + ((n % 4) * 16 + 4 * g + n / 4) * 16 +
+                                8 * (t & 1));
+          k[p] = __builtin_bit_cast(half8_t, __builtin_shufflevector(e[0], e[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+#pragma unroll
+        for (int w = 0; w < NT; ++w) {
+          s[t][w] = mfma(k[0], d[w].hi, s[t][w]);
+          s[t][w] = mfma(k[0], d[w].lo, s[t][w]);
+          if constexpr (L::kParts == 2) s[t][w] = mfma(k[1], d[w].hi, s[t][w]);
+        }
+      }
+    }
+
+    // outputs
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t token = start + c * kC + 16 * mt + 4 * g + q;
+        if (token < end) {
+#pragma unroll
+          for (int w = 0; w < NT; ++w) {
+            Elements<DT, 1> e;
+            e.set({__builtin_amdgcn_ldexpf(o[mt][w][q] * a.scale, scaled[w] - 14)});
+            e.store(a.out.p, token * a.out.token + h * a.out.head + column + 16 * w + n);
+          }
+        }
+      }
+
+    arrived();
+    if (L::kStages == 1 && c + 1 < chunks) {
+      issue(c + 1, 0);
+      arrived();
+    }
+  }
+
+#pragma unroll
+  for (int t = 0; t < L::kTiles; ++t)
+#pragma unroll
+    for (int w = 0; w < NT; ++w)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        a.state_out[state + (int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * a.head_v + 16 * w] =
+            __builtin_amdgcn_ldexpf(s[t][w][q], scaled[w] - kLength);
+#endif
 }
 
 template <int DT, int DK>
-hipError_t launch_sized(const DeltaArgs& a, hipStream_t stream) {
-  const int64_t items = (int64_t)a.n_seqs * a.v_heads * (a.head_v / kCols);
-  const FastDiv by_group((uint32_t)(a.v_heads / a.k_heads));
-  for (int64_t first = 0; first < items; first += kMostWorkgroups) {
-    const uint32_t grid = (uint32_t)std::min<int64_t>(kMostWorkgroups, items - first);
-    gated_delta_kernel<DT, DK><<<grid, kThreads, 0, stream>>>(a, by_group, first);
+hipError_t launch_solve(const DeltaArgs& a, hipStream_t stream) {
+  const uint32_t blocks = (uint32_t)((a.v_heads + kWaves - 1) / kWaves);
+  const int64_t places = delta_chunk_places(a.tokens, a.n_seqs), most = std::max<int64_t>(kMostWorkgroups / blocks, 1);
+  const FastDiv by_group((uint32_t)(a.v_heads / a.k_heads)), by_blocks(blocks);
+  for (int64_t first = 0; first < places; first += most) {
+    const uint32_t grid = (uint32_t)std::min(most, places - first) * blocks;
+    gated_delta_solve_kernel<DT, DK><<<grid, kThreads, 0, stream>>>(a, by_group, by_blocks, first);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+template <int DT, int DK, int NT>
+hipError_t launch_chain(const DeltaArgs& a, hipStream_t stream) {
+  const uint32_t slices = (uint32_t)(a.head_v / Chain<DT, DK, NT>::kCols);
+  const FastDiv by_seq((uint32_t)a.v_heads), by_key_heads((uint32_t)a.k_heads);
+  const int64_t pairs = (int64_t)a.n_seqs * a.v_heads, all = (pairs + 7) / 8 * 8 * slices;
+  for (int64_t first = 0; first < all; first += kMostWorkgroups) {
+    const uint32_t grid = (uint32_t)std::min<int64_t>(kMostWorkgroups, all - first);
+    gated_delta_chain_kernel<DT, DK, NT><<<grid, kThreads, 0, stream>>>(a, by_seq, by_key_heads, slices, (uint32_t)first, (uint32_t)pairs);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int DT, int DK>
+hipError_t launch_sized(const DeltaArgs& a, hipStream_t stream) {
+  const hipError_t e = launch_solve<DT, DK>(a, stream);
+  if (e != hipSuccess) return e;
+  if constexpr (DT != 0) {
+    if (a.head_v % 128 == 0 && (int64_t)a.n_seqs * a.v_heads * (a.head_v / 64) > device_cu_count())
+      return launch_chain<DT, DK, 2>(a, stream);
+  }
+  return launch_chain<DT, DK, 1>(a, stream);
 }
 
 template <int DT>

@@ -63,7 +63,20 @@ struct NormArgs {
 };
 hipError_t launch_group_norm(const NormArgs& a, hipStream_t stream);
 
-// of the workspace of nvfp4_gated_delta_chunked
-inline int64_t gated_delta_workspace_bytes(int64_t, int64_t, int, int, int, int, int) { return 16; }
+// The workspace of nvfp4_gated_delta_chunked: for each chunk of 64 tokens of a sequence the normalised keys and queries of
+// every key head, then what ties the chunk's tokens together for every value head.  Chunk i of sequence r has place
+// floor(start_r / 64) + r + i, which no other chunk has.
+constexpr int kDeltaChunk = 64;
+constexpr int kDeltaTieBytes = 26 << 10;
+constexpr int64_t delta_key_bytes(int head_k, int dtype) {
+  return (int64_t)2 * kDeltaChunk * head_k * (dtype == 0 ? 4 : 2);  // float32: two fp16 parts
+}
+constexpr int64_t delta_chunk_bytes(int k_heads, int v_heads, int head_k, int dtype) {
+  return k_heads * delta_key_bytes(head_k, dtype) + (int64_t)v_heads * kDeltaTieBytes;
+}
+inline int64_t delta_chunk_places(int64_t tokens, int64_t n_seqs) { return tokens / kDeltaChunk + n_seqs; }
+inline int64_t gated_delta_workspace_bytes(int64_t tokens, int64_t n_seqs, int k_heads, int v_heads, int head_k, int dtype) {
+  return delta_chunk_places(tokens, n_seqs) * delta_chunk_bytes(k_heads, v_heads, head_k, dtype);
+}
 
 }  // namespace nvfp4

@@ -15,6 +15,7 @@ namespace {
 using namespace nvfp4;
 
 constexpr int64_t kMaxTokenHeads = (int64_t)1 << 37;  // tokens times value heads
+constexpr int64_t kMaxSeqHeads = (int64_t)1 << 28;    // sequences times value heads
 
 inline bool switch_ok(int32_t v) { return v == 0 || v == 1; }
 
@@ -57,7 +58,7 @@ nvfp4_status delta_check(const DeltaArgs& a, const DeltaSizes& n) {
   if (!std::isfinite(a.scale) || !(a.scale > 0.0f) || !std::isfinite(a.eps) || !(a.eps >= 0.0f)) return NVFP4_ERR_RANGE;
   if (!size_ok(n.tokens) || n.n_seqs <= 0 || n.n_seqs >= kMaxDim - 1 || !size_ok(n.num_slots) ||
       !delta_heads_ok(n.k_heads, n.v_heads, n.head_k, n.head_v) || n.tokens * n.v_heads > kMaxTokenHeads ||
-      n.n_seqs * n.v_heads > kMaxTokenHeads || a.out.p == a.v.p ||
+      n.n_seqs * n.v_heads > kMaxSeqHeads || a.out.p == a.v.p ||
       !strides_ok(n.k_heads, n.head_k, a.q.token, a.q.head) || !strides_ok(n.k_heads, n.head_k, a.k.token, a.k.head) ||
       !strides_ok(n.v_heads, n.head_v, a.v.token, a.v.head) ||
       !strides_ok(n.v_heads, n.head_v, a.out.token, a.out.head) || a.a_token < n.v_heads || a.a_token >= kMaxStride ||
@@ -125,9 +126,9 @@ nvfp4_status nvfp4_gated_delta_workspace(int64_t tokens, int64_t n_seqs, int64_t
   if (!bytes) return NVFP4_ERR_NULL;
   if (dtype_size(dtype) == 0) return NVFP4_ERR_DTYPE;
   if (!size_ok(tokens) || n_seqs <= 0 || n_seqs >= kMaxDim - 1 || !delta_heads_ok(k_heads, v_heads, head_k, head_v) ||
-      tokens * v_heads > kMaxTokenHeads || n_seqs * v_heads > kMaxTokenHeads)
+      tokens * v_heads > kMaxTokenHeads || n_seqs * v_heads > kMaxSeqHeads)
     return NVFP4_ERR_SHAPE;
-  *bytes = gated_delta_workspace_bytes(tokens, n_seqs, (int)k_heads, (int)v_heads, (int)head_k, (int)head_v, dtype);
+  *bytes = gated_delta_workspace_bytes(tokens, n_seqs, (int)k_heads, (int)v_heads, (int)head_k, dtype);
   return NVFP4_OK;
 }
 
@@ -148,7 +149,7 @@ nvfp4_status nvfp4_gated_delta_chunked(int64_t tokens, int64_t k_heads, int64_t 
   const nvfp4_status s = delta_check(d, n);
   if (s != NVFP4_OK) return s;
   set_sizes(d, n);
-  if (workspace_bytes < gated_delta_workspace_bytes(tokens, n_seqs, d.k_heads, d.v_heads, d.head_k, d.head_v, dtype))
+  if (workspace_bytes < gated_delta_workspace_bytes(tokens, n_seqs, d.k_heads, d.v_heads, d.head_k, dtype))
     return NVFP4_ERR_SHAPE;
   if (!device_ok()) return NVFP4_ERR_DEVICE;
   return done(launch_gated_delta_chunked(d, static_cast<hipStream_t>(stream)));

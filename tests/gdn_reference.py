@@ -38,31 +38,39 @@ def conv(x, weight, bias, act, state, slots, starts, cached, out):
     return out, sizes, after
 
 
-def delta(q, k, v, a, b, a_log, dt_bias, scale, eps, state, slots, starts, cached, out):
-    """(out, out_slack, state_out, state_slack): slacks grow as a rounding of 1 relative to
+def delta(q, k, v, a, b, a_log, dt_bias, scale, eps, state, slots, starts, cached, out, least=0.0):
+    """(out, out_slack, state_out, state_slack, floors): slacks grow as a rounding of 1 relative to
     what is added would, a token: columns of the state are compared by their length, since
-    each step mixes the rows.  (1 - beta k k^T) e^g shortens every error it meets."""
+    each step mixes the rows.  (1 - beta k k^T) e^g shortens every error it meets.  e^g is off
+    by |g| times g's own roundings.  Beside that, `least` of the largest beta v and state of a
+    column within 64 tokens, which stays in the state behind them; `floors` are the last ones."""
     out, after = np.array(out), np.array(state)
-    out_slack, state_slack = np.zeros_like(out), np.zeros_like(state)
+    out_slack, state_slack, floors = np.zeros_like(out), np.zeros_like(state), np.zeros_like(state[:, :, 0])
     group = v.shape[1] // k.shape[1]
     x = a + dt_bias
-    alpha = np.exp(-np.exp(a_log) * np.logaddexp(0.0, x))
+    decay = np.exp(a_log) * np.logaddexp(0.0, x)
+    alpha = np.exp(-decay)
     beta = 1.0 / (1.0 + np.exp(-b))
     unit = lambda y: np.repeat(y / np.sqrt((y * y).sum(-1, keepdims=True) + eps), group, 1)
     kn, qn = unit(k), unit(q)
     for r, low, high, slot in spans(starts, slots, len(state), len(q)):
         s = np.array(state[slot]) if cached is None or cached[r] > 0 else np.zeros_like(state[slot])
-        off = np.zeros(s.shape[::2])  # [heads, head_v]
+        off = floor = np.zeros(s.shape[::2])  # [heads, head_v]
         for t in range(low, high):
+            if (t - low) % 64 == 0:
+                rows = slice(t, min(t + 64, high))
+                off = off + floor
+                floor = least * np.maximum(np.abs(s).max(1), (beta[rows][..., None] * np.abs(v[rows])).max(0))
             was = np.sqrt((s * s).sum(1))
             s = s * alpha[t][:, None, None]
             d = beta[t][:, None] * (v[t] - np.einsum("hk,hkv->hv", kn[t], s))
             s = s + kn[t][:, :, None] * d[:, None, :]
-            off = off * alpha[t][:, None] + was * alpha[t][:, None] + beta[t][:, None] * np.abs(v[t])
+            off = off * alpha[t][:, None] + was * (alpha[t] * (1.0 + decay[t]))[:, None] + beta[t][:, None] * np.abs(v[t])
             out[t] = scale * np.einsum("hk,hkv->hv", qn[t], s)
-            out_slack[t] = scale * (off + np.sqrt((s * s).sum(1)))
-        after[slot], state_slack[slot] = s, off[:, None, :]
-    return out, out_slack, after, state_slack
+            out_slack[t] = scale * (off + np.sqrt((s * s).sum(1)) + floor)
+        after[slot], state_slack[slot] = s, (off + floor)[:, None, :]
+        floors[slot] = floor
+    return out, out_slack, after, state_slack, floors
 
 
 def norm(x, weight, bias, gate, act, centred, eps):

@@ -121,6 +121,7 @@ def test_products_of_sizes_past_32_bits(lib):
     c = calls(lib)
     assert c["chunked"](tokens=BIG - 1, hv=128, vt=1 << 16, ot=1 << 16, at=128, bt=128) == SHAPE
     assert c["step"](n=BIG - 2, hv=128, vt=1 << 16, ot=1 << 16, at=128, bt=128) == SHAPE
+    assert c["step"](n=(1 << 26) + 1) == SHAPE and c["chunked"](n=(1 << 26) + 1) == SHAPE  # 4 value heads each
     assert c["step"](hk=1 << 25, hv=1 << 25) == SHAPE
 
 

@@ -145,6 +145,9 @@ def test_conv_large_and_small_values(gpu_lib):
 # Each token's 32-bit evaluation makes a handful of roundings of 2^-24 relative to what R.delta adds up, in sums of head_k
 # products (in the matrix units 2^-22 of the operands): 32 of them, 2^-19, hold a token's.
 DELTA_SLACK = 2.0 ** -19
+# Chunks of 64 tokens cut what a column's state and its tokens write at 2^-32 of the largest of them; a token's output and
+# state are made of up to 192 such operands with weights of at most 1: less than 2^-24.
+DELTA_LEAST = 2.0 ** -24 / DELTA_SLACK
 
 
 class Delta:
@@ -163,9 +166,9 @@ class Delta:
         self.scale = head_k ** -0.5
         self.in_place = False
 
-    def want(self, starts, cached, out):
+    def want(self, starts, cached, out, least=0.0):
         return R.delta(*(host(t) for t in (self.q, self.k, self.v, self.a, self.b, self.a_log, self.dt_bias)), self.scale, EPS, host(self.state),
-                       self.slots, starts, cached, out)
+                       self.slots, starts, cached, out, least)
 
     def run(self, nv, starts, cached=None, step=False, state=None, after=None, out=None, **kw):
         state = self.state if state is None else state
@@ -182,7 +185,7 @@ class Delta:
         given = self.state.clone()
         after = given if in_place else torch.full_like(self.state, 3.0)
         was = host(after)
-        want, slack, left, left_slack = self.want(starts, cached, host(out))
+        want, slack, left, left_slack, floors = self.want(starts, cached, host(out), 0.0 if step else DELTA_LEAST)
         touched = [slot for _, _, _, slot in R.spans(starts, self.slots, len(self.state), len(self.q))]
         was[touched] = left[touched]
         got = self.run(nv, starts, cached, step, given, after, out)
@@ -191,11 +194,15 @@ class Delta:
         within(out, want, DELTA_SLACK * slack, self.dtype, "out")
         within(after, was, DELTA_SLACK * left_slack, "f32", "state")
         # Independent roundings of 2^-22 in the operands of the three products that lead to a state, met by a rule that
-        # shortens errors: their length is below 2^-20 of the state's.  A lost part of an operand would leave 2^-12.
+        # shortens errors: their length is below 2^-20 of the state's, where nothing but decay G is left of it 2^-23 |G| more.
+        # A lost part of an operand would leave 2^-12.  The columns' floors come on top.
+        total = np.exp(host(self.a_log)) * np.logaddexp(0, host(self.a) + host(self.dt_bias)).sum(0)
+        share = 2.0 ** -20 + 2.0 ** -23 * np.minimum(total, 64)
         for slot in touched:
             off = np.sqrt(((host(after)[slot] - left[slot]) ** 2).sum((1, 2)))
             length = np.sqrt((left[slot] ** 2).sum((1, 2)))
-            assert (off <= 2.0 ** -20 * length + 1e-37).all(), ("state", slot, float((off / np.maximum(length, 1e-300)).max()))
+            least = DELTA_SLACK * np.sqrt((floors[slot] ** 2).sum(1))
+            assert (off <= share * length + least + 1e-37).all(), ("state", slot, float((off / np.maximum(length, 1e-300)).max()))
         rows = np.ones(len(self.q), bool)
         for _, low, high, _ in R.spans(starts, self.slots, len(self.state), len(self.q)):
             rows[low:high] = False
@@ -308,6 +315,13 @@ def test_small_and_large_keys(gpu_lib):
     d.check(gpu_lib, [0, 140])
     d.k[:, :, 5] *= 300.0  # one element far above the rest
     d.check(gpu_lib, [0, 140])
+
+
+def test_a_long_sequence_stays_exact(gpu_lib):
+    rng = np.random.default_rng(10)
+    log("long")
+    d = Delta(rng, "bf16", 3000, 1, 1, 1, 128, 64, decay=0.05)
+    d.check(gpu_lib, [0, 3000])
 
 
 def test_the_result_is_the_same_in_every_call(gpu_lib):
