@@ -11,9 +11,9 @@
 //   out  = scale (e^G Q~ S + P V'),  P_ij = e^(G_i - G_j) q~_i . k~_j  (j <= i)
 //   S   <- e^(G_C) S + (e^(G_C - G) K~)^T V'
 //
-// Two kernels.  The first has a wave for each chunk and value head, all independent: it
-// normalises keys and queries and leaves T, P and the gates in the workspace.  The second
-// walks the chunks of a sequence with 16 NT columns of the state in a wave's registers:
+// Three kernels.  The first normalises keys and queries.  The second has a wave for each
+// chunk and value head, all independent, and leaves T, P and the gates in the workspace.
+// The third walks the chunks of a sequence with 16 columns of the state in a wave's registers:
 // columns never meet, and the matrix unit's results lie as its next operands want them,
 // so S, X and V' pass through neither LDS nor other lanes.
 //
@@ -71,9 +71,13 @@ __device__ __forceinline__ half8_t halves(const float (&x)[8]) {
 __device__ __forceinline__ Parts cut(const float (&x)[8]) {
   Parts p;
   p.hi = halves(x);
+  // x - hi as one multiply-add that takes the half as it lies (v_fma_mix_f32), which the compiler makes of a factor that
+  // it does not know
+  float less;
+  asm("s_mov_b32 %0, -1.0" : "=s"(less));
   float rest[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) rest[i] = x[i] - (float)p.hi[i];
+  for (int i = 0; i < 8; ++i) rest[i] = __builtin_fmaf((float)p.hi[i], less, x[i]);
   p.lo = halves(rest);
   return p;
 }
@@ -91,7 +95,7 @@ constexpr int square(int j, int i) { return i * (i + 1) / 2 + j; }  // of block 
 struct SolveLds {
   float a[10 * kSquare];  // A^T by blocks: row j, column i; then the inverse's
   double log_decay[kC];
-  float beta[kC], k_norm[kC], q_norm[kC];
+  float beta[kC], k_norm[kC];
 };
 
 // Rows of q or k as operands: lane (g, m) holds elements 32 s + 8 g.. of row m, a power of two times the input; what that
@@ -154,6 +158,13 @@ struct Row {
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
         *reinterpret_cast<half8_t*>(image + ((p * 4 + mt) * kSteps + s) * kBlock + lane * 16) = part[p][s];
+  }
+  __device__ __forceinline__ void read(const uint8_t* image, int mt, int lane) {
+#pragma unroll
+    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        part[p][s] = *reinterpret_cast<const half8_t*>(image + ((p * 4 + mt) * kSteps + s) * kBlock + lane * 16);
   }
 };
 
@@ -225,6 +236,27 @@ __device__ __forceinline__ void store_ties(uint8_t* to, int mt, const float4_t (
 
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
 
+// Keys and queries of a chunk and key head: eight waves take 16 rows each.
+template <int DT, int DK>
+__global__ __launch_bounds__(512) void gated_delta_keys_kernel(DeltaArgs a, FastDiv by_heads, int64_t first_place) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, n = lane & 15;
+  const uint32_t of_launch = by_heads.div(blockIdx.x);
+  const int kh = (int)(blockIdx.x - of_launch * by_heads.d);
+  const int64_t place = first_place + of_launch;
+  Place at;
+  if (!find_place(a, place, at)) return;
+  const int rows = (int)std::min<int64_t>(kC, at.end - at.begin);
+  const bool of_q = wave >= 4;
+  const int mt = wave & 3, row = 16 * mt + n;
+  constexpr int64_t kBytes = delta_key_bytes(DK, DT), kImage = (kBytes - 1024) / 2;
+  uint8_t* keys = static_cast<uint8_t*>(a.workspace) + place * delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT) + kh * kBytes;
+  Row<DT, DK> x;
+  x.load(of_q ? a.q : a.k, at.begin + std::min(row, rows - 1), kh, g, row < rows, a.eps);
+  x.store(keys + (of_q ? kImage : 0), mt, lane);
+  if (g == 0) reinterpret_cast<float*>(keys + 2 * kImage)[(of_q ? kC : 0) + row] = x.norm;
+}
+
 template <int DT, int DK>
 __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a, FastDiv by_group, FastDiv by_blocks,
                                                                      int64_t first_place) {
@@ -237,23 +269,18 @@ __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a
   Place at;
   if (h >= a.v_heads || !find_place(a, place, at)) return;  // whole waves: the kernel has no barrier
   const int kh = (int)by_group.div((uint32_t)h);
-  const bool leads = h == kh * (int)by_group.d;  // of its key head
   const int rows = (int)std::min<int64_t>(kC, at.end - at.begin);
   SolveLds& lds = all[wave];
+  constexpr int64_t kBytes = delta_key_bytes(DK, DT), kImage = (kBytes - 1024) / 2;
   uint8_t* base = static_cast<uint8_t*>(a.workspace) + place * delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT);
-  uint8_t* keys = base + kh * delta_key_bytes(DK, DT);
-  uint8_t* queries = keys + delta_key_bytes(DK, DT) / 2;
-  uint8_t* ties = base + a.k_heads * delta_key_bytes(DK, DT) + (int64_t)h * kDeltaTieBytes;
+  const uint8_t* keys = base + kh * kBytes;
+  const float* norms = reinterpret_cast<const float*>(keys + 2 * kImage);
+  uint8_t* ties = base + a.k_heads * kBytes + (int64_t)h * kDeltaTieBytes;
 
-  // keys
   Row<DT, DK> k[4];
 #pragma unroll
-  for (int mt = 0; mt < 4; ++mt) {
-    const int row = 16 * mt + n;
-    k[mt].load(a.k, at.begin + std::min(row, rows - 1), kh, g, row < rows, a.eps);
-    if (leads) k[mt].store(keys, mt, lane);
-    if (g == 0) lds.k_norm[row] = k[mt].norm;
-  }
+  for (int mt = 0; mt < 4; ++mt) k[mt].read(keys, mt, lane);
+  const float k_norm = norms[lane], q_norm = norms[kC + lane];
 
   // gates of token `lane`: the sum of log2 decays in 64 bits, since only differences count
   const int64_t token = at.begin + std::min(lane, rows - 1);
@@ -267,7 +294,8 @@ __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a
   }
   const double whole = __shfl(log_decay, 63);
   lds.log_decay[lane] = log_decay;
-  lds.beta[lane] = beta;
+  lds.beta[lane] = beta * k_norm;
+  lds.k_norm[lane] = k_norm;
   wave_sync();
 
   // e^(G_i - G_j) of this lane's elements of block (j, i): column i = 16 bi + n, rows j = 16 bj + 4 g + r
@@ -287,16 +315,13 @@ __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a
 #pragma unroll
   for (int bi = 0; bi < 4; ++bi) {
     Row<DT, DK> q;
-    const int row = 16 * bi + n;
-    q.load(a.q, at.begin + std::min(row, rows - 1), kh, g, row < rows, a.eps);
-    if (leads) q.store(queries, bi, lane);
-    if (g == 0) lds.q_norm[row] = q.norm;
-    const float strength = lds.beta[row] * k[bi].norm;
+    q.read(keys + kImage, bi, lane);
+    const float strength = lds.beta[16 * bi + n], of_q = __shfl(q_norm, 16 * bi + n);
     float4_t p[4];
 #pragma unroll
     for (int bj = 0; bj <= bi; ++bj) {
       const float4_t e = ratio(bj, bi) * of_rows(lds.k_norm, bj);
-      p[bj] = e * q.norm * dots(k[bj], q);
+      p[bj] = e * of_q * dots(k[bj], q);
       float4_t x = e * strength * dots(k[bj], k[bi]);
       if (bj == bi) {
 #pragma unroll
@@ -362,11 +387,11 @@ __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a
   }
 
   float* gates = reinterpret_cast<float*>(ties + kGatesAt);
-  const float since = __builtin_amdgcn_exp2f((float)log_decay), k_norm = lds.k_norm[lane];
+  const float since = __builtin_amdgcn_exp2f((float)log_decay);
   gates[kBeta * kC + lane] = beta;
   gates[kGainK * kC + lane] = beta * since * k_norm * (1.0f / kLong);
   gates[kUntil * kC + lane] = __builtin_amdgcn_exp2f((float)(whole - log_decay)) * k_norm * kLong;
-  gates[kGainQ * kC + lane] = since * lds.q_norm[lane] * (kUp / kLong);
+  gates[kGainQ * kC + lane] = since * q_norm * (kUp / kLong);
   gates[kWhole * kC + lane] = __builtin_amdgcn_exp2f((float)whole);
 }
 
@@ -380,48 +405,61 @@ __device__ __forceinline__ short4_t read_columns(const uint8_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)p);
 }
 
-template <int DT, int DK, int NT>
+// WAVES of a workgroup hold columns, LOADERS more move data for them
+template <int DT, int DK, int WAVES, int LOADERS>
 struct Chain {
   static constexpr int kParts = DT == 0 ? 2 : 1, kSteps = DK / 32, kTiles = DK / 16;
-  static constexpr int kCols = 16 * NT * kWaves;  // of a workgroup
+  static constexpr int kCols = 16 * WAVES;                    // of a workgroup
+  static constexpr int kThreads = 64 * (WAVES + LOADERS);
   static constexpr int kKeys = kParts * 4 * kSteps * kBlock;  // bytes of K; Q follows
-  static constexpr int kValueRow = kCols * element_size(DT);
+  static constexpr int kRow = 16 * element_size(DT), kValues = kC * kRow;  // a wave's columns of V, then of the outputs
   static constexpr int kTiesAt = 2 * kKeys, kValuesAt = kTiesAt + kDeltaTieBytes;
-  static constexpr int kStage = kValuesAt + kC * kValueRow;
+  static constexpr int kStage = kValuesAt + WAVES * kValues;
   static constexpr int kStages = 2 * kStage <= (160 << 10) ? 2 : 1;
   static_assert(kStages * kStage <= (160 << 10), "the stages fit LDS");
 };
 
 #if defined(__HIP_DEVICE_COMPILE__)
-// 16 bytes a lane from memory to LDS byte lds + 16 lane, past the registers.  M0 is set in the same block, one wait state
-// before the load reads it.
-__device__ __forceinline__ void to_lds(uint32_t lds, const void* base, uint32_t offset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base) : "memory");
+// From memory to LDS past the registers, 16 bytes a lane to byte lds + 16 lane.  M0 is set in the same block, one wait
+// state before the loads read it; an instruction's offset counts on both sides.
+__device__ __forceinline__ void to_lds4(uint32_t lds, const void* base, uint32_t offset) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2\n\t"
+      "global_load_lds_dwordx4 %1, %2 offset:1024\n\t"
+      "global_load_lds_dwordx4 %1, %2 offset:2048\n\t"
+      "global_load_lds_dwordx4 %1, %2 offset:3072" ::"s"(lds), "v"(offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void to_lds2(uint32_t lds, const void* base, uint32_t offset) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2\n\t"
+      "global_load_lds_dwordx4 %1, %2 offset:1024" ::"s"(lds), "v"(offset), "s"(base) : "memory");
 }
 __device__ __forceinline__ void to_lds(uint32_t lds, const void* p) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
 }
 #endif
 
-template <int DT, int DK, int NT>
-__global__ __launch_bounds__(kThreads, 1) void gated_delta_chain_kernel(DeltaArgs a, FastDiv by_seq, FastDiv by_key_heads,
-                                                                        uint32_t slices, uint32_t first, uint32_t pairs) {
+template <int DT, int DK, int WAVES, int LOADERS>
+__global__ __launch_bounds__(64 * (WAVES + LOADERS), (WAVES + LOADERS + 3) / 4) void gated_delta_chain_kernel(
+    DeltaArgs a, FastDiv by_seq, FastDiv by_key_heads, uint32_t slices, uint32_t first, uint32_t pairs) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using L = Chain<DT, DK, NT>;
+  using L = Chain<DT, DK, WAVES, LOADERS>;
+  constexpr int kSize = element_size(DT);
   __shared__ __attribute__((aligned(1024))) uint8_t stage[L::kStages * L::kStage];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, n = lane & 15;
 
   // Workgroups go to the XCDs in turn: those of one sequence and head, which read the same ties, and where there are 8 key
   // heads (or a multiple) those of one key head lie on one XCD, 8 apart.
-  const uint32_t x = first + blockIdx.x, eight = x >> 3;
-  const uint32_t octet = eight / slices, pair = octet * 8 + (x & 7);
+  const uint32_t at = first + blockIdx.x, eight = at >> 3;
+  const uint32_t octet = eight / slices, pair = octet * 8 + (at & 7);
   if (pair >= pairs) return;
-  const int column = (int)(eight - octet * slices) * L::kCols + wave * 16 * NT;  // of this wave
-  const int group = a.v_heads / a.k_heads;
+  const int group_column = (int)(eight - octet * slices) * L::kCols;
   const uint32_t r = by_seq.div(pair), in_seq = pair - r * by_seq.d;
   const uint32_t of_group = by_key_heads.div(in_seq);
-  const int kh = (int)(in_seq - of_group * by_key_heads.d), h = kh * group + (int)of_group;
+  const int kh = (int)(in_seq - of_group * by_key_heads.d), h = kh * (a.v_heads / a.k_heads) + (int)of_group;
   const int slot = a.slots[r];
   const int64_t start = start_of(a.token_starts, (int)r, a.tokens), end = start_of(a.token_starts, (int)r + 1, a.tokens);
   if (!slot_ok(slot, a.num_slots) || start >= end) return;
@@ -430,61 +468,109 @@ __global__ __launch_bounds__(kThreads, 1) void gated_delta_chain_kernel(DeltaArg
   const uint8_t* from = static_cast<const uint8_t*>(a.workspace) + (start / kC + r) * chunk_bytes;
   const int64_t keys_at = kh * delta_key_bytes(DK, DT),
                 ties_at = a.k_heads * delta_key_bytes(DK, DT) + (int64_t)h * kDeltaTieBytes;
-  const int group_column = (int)(eight - octet * slices) * L::kCols;
-  const char* values = static_cast<const char*>(a.v.p) + (h * a.v.head + group_column) * element_size(DT);
+  const char* values = static_cast<const char*>(a.v.p) + (h * a.v.head + group_column) * kSize;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)stage;
 
+  // Moving data is `of` waves' work, this one's share is `share`: the loaders' where there are any, else each wave's, and
+  // then its columns are its own, so that it may fill them again as soon as it has read them.
+  constexpr int kOf = LOADERS ? LOADERS : WAVES;
+  const int share = LOADERS ? wave - WAVES : wave;
+  constexpr int kLanes = L::kRow / 16, kRows = 64 / kLanes, kMoves = kC / kRows;  // of a row, rows of a move
+  // a chunk on its way into a stage: turns of 4 blocks of keys and queries, then of T and P, the gates, and values
   auto issue = [&](int64_t c, int to) {
     const uint32_t lds = lds0 + to * L::kStage;
     const uint8_t* base = from + c * chunk_bytes;
+    constexpr int kTurns = 2 * L::kKeys / (4 * kBlock), kAll = kTurns + kGatesAt / (4 * kBlock);
 #pragma unroll
-    for (int i = 0; i < (2 * L::kKeys / kBlock + kWaves - 1) / kWaves; ++i) {
-      const int p = i * kWaves + wave;
-      if (p < 2 * L::kKeys / kBlock) to_lds(lds + p * kBlock, base + keys_at + p * kBlock, lane * 16);
+    for (int w = 0; w < WAVES / kOf; ++w) {
+      const int of = share + w * kOf;
+#pragma unroll
+      for (int i = 0; i < kMoves; ++i) {
+        const int64_t token = std::min(start + c * kC + i * kRows + lane / kLanes, end - 1);
+        to_lds(lds + L::kValuesAt + of * L::kValues + i * kBlock,
+               values + token * a.v.token * kSize + of * L::kRow + lane % kLanes * 16);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < (kDeltaTieBytes / kBlock + kWaves - 1) / kWaves; ++i) {
-      const int p = i * kWaves + wave;
-      if (p < kDeltaTieBytes / kBlock) to_lds(lds + L::kTiesAt + p * kBlock, base + ties_at + p * kBlock, lane * 16);
+    for (int i = 0; i < (kAll + kOf - 1) / kOf; ++i) {
+      const int turn = i * kOf + share;
+      if (turn >= kAll) break;
+      const bool tie = turn >= kTurns;
+      to_lds4(lds + turn * 4 * kBlock, base + (tie ? ties_at - L::kTiesAt : keys_at) + turn * 4 * kBlock, lane * 16);
     }
-    constexpr int kRows = kBlock / L::kValueRow;  // of values a load
-#pragma unroll
-    for (int i = 0; i < kC / kRows / kWaves; ++i) {
-      const int p = i * kWaves + wave;
-      const int64_t token = std::min(start + c * kC + p * kRows + lane * 16 / L::kValueRow, end - 1);
-      to_lds(lds + L::kValuesAt + p * kBlock, values + token * a.v.token * element_size(DT) + lane * 16 % L::kValueRow);
-    }
+    if (share == kOf - 1) to_lds2(lds + L::kTiesAt + kGatesAt, base + ties_at + kGatesAt, lane * 16);
   };
-  auto arrived = [&] {  // this wave's loads are there and its LDS reads done, then everyone's
+  // outputs of a chunk from its stage
+  auto put_out = [&](int64_t c, int from_stage) {
+    const int64_t token = start + c * kC + lane / kLanes;
+    char* to = static_cast<char*>(a.out.p) + (token * a.out.token + h * a.out.head + group_column) * kSize + lane % kLanes * 16;
+    u32x4_t held[WAVES / kOf][kMoves];
+#pragma unroll
+    for (int w = 0; w < WAVES / kOf; ++w)
+#pragma unroll
+      for (int i = 0; i < kMoves; ++i)
+        held[w][i] = *reinterpret_cast<const u32x4_t*>(stage + from_stage * L::kStage + L::kValuesAt + (share + w * kOf) * L::kValues +
+                                                       i * kBlock + lane * 16);
+#pragma unroll
+    for (int w = 0; w < WAVES / kOf; ++w)
+#pragma unroll
+      for (int i = 0; i < kMoves; ++i)
+        if (token + i * kRows < end)
+          *reinterpret_cast<u32x4_t*>(to + i * kRows * a.out.token * kSize + (share + w * kOf) * L::kRow) = held[w][i];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read, before it is filled again
+  };
+  auto meet = [&] {  // everyone's loads are there and LDS accesses done
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+  // between two chunks: the last one's outputs leave and the next one's operands come
+  auto move = [&](int64_t c, int now) {
+    if (L::kStages == 1) return;
+    if (c > 0) put_out(c - 1, now ^ 1);
+    if (c + 1 < chunks) issue(c + 1, now ^ 1);
+  };
+  // with one stage: between the chunks, which all wait for
+  auto change = [&](int64_t c) {
+    if (L::kStages == 2 || c + 1 == chunks) return;
+    if (!LOADERS || wave >= WAVES) {
+      put_out(c, 0);
+      issue(c + 1, 0);
+    }
+    meet();
+  };
 
-  issue(0, 0);
+  if (LOADERS && wave >= WAVES) {
+    issue(0, 0);
+    meet();
+    for (int64_t c = 0; c < chunks; ++c) {
+      move(c, (int)(c & 1));
+      meet();
+      change(c);
+    }
+    put_out(chunks - 1, L::kStages == 2 ? (int)((chunks - 1) & 1) : 0);
+    return;
+  }
+  if (!LOADERS) issue(0, 0);
   // The state: tile 2 s + t, register q of lane (g, n) is row 32 s + 8 g + 4 t + q, column n, so that two tiles are the
   // eight elements of an operand that meet elements 32 s + 8 g.. of a row of K or Q.
-  float4_t s[L::kTiles][NT];
-  int scaled[NT];  // the state is s 2^(scaled - 4), values are taken times 2^-scaled
-  const int64_t state = ((int64_t)slot * a.v_heads + h) * DK * a.head_v + column + n;
+  float4_t s[L::kTiles];
+  int scaled = kLength;  // the state is s 2^(scaled - 4), values are taken times 2^-scaled
+  const int64_t state = ((int64_t)slot * a.v_heads + h) * DK * a.head_v + group_column + 16 * wave + n;
   const bool carried = !a.cached_lens || a.cached_lens[r] > 0;
 #pragma unroll
   for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-    for (int w = 0; w < NT; ++w) {
-      scaled[w] = kLength;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        s[t][w][q] = carried ? a.state[state + (int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * a.head_v + 16 * w] : 0.0f;
-    }
-  arrived();
+    for (int q = 0; q < 4; ++q)
+      s[t][q] = carried ? a.state[state + (int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * a.head_v] : 0.0f;
+  meet();
 
   for (int64_t c = 0; c < chunks; ++c) {
     const int now = L::kStages == 2 ? (int)(c & 1) : 0;
-    if (L::kStages == 2 && c + 1 < chunks) issue(c + 1, now ^ 1);
-    const uint8_t* here = stage + now * L::kStage;
+    uint8_t* here = stage + now * L::kStage;
     const uint8_t* ties = here + L::kTiesAt;
     const float* gates = reinterpret_cast<const float*>(ties + kGatesAt);
+    uint8_t* mine = here + L::kValuesAt + wave * L::kValues;
     auto key = [&](int of_q, int part, int mt, int st) {
       return *reinterpret_cast<const half8_t*>(here + of_q * L::kKeys + ((part * 4 + mt) * L::kSteps + st) * kBlock + lane * 16);
     };
@@ -493,169 +579,132 @@ __global__ __launch_bounds__(kThreads, 1) void gated_delta_chain_kernel(DeltaArg
     };
     auto gate = [&](int which, int mt) { return *reinterpret_cast<const float4_t*>(gates + which * kC + 16 * mt + 4 * g); };
 
-    // values of this wave's columns
-    float4_t x[4][NT];
+    float4_t x[4], beta[4];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int mt = 0; mt < 4; ++mt) {
+      beta[mt] = gate(kBeta, mt);
+      if constexpr (DT == 0) {
 #pragma unroll
-      for (int w = 0; w < NT; ++w) {
-        const uint8_t* v = here + L::kValuesAt + (wave * 16 * NT + 16 * w) * element_size(DT);
-        if constexpr (DT == 0) {
+        for (int i = 0; i < 4; ++i) x[mt][i] = *reinterpret_cast<const float*>(mine + (16 * mt + 4 * g + i) * L::kRow + 4 * n);
+      } else {
+        const short4_t e = read_columns(mine + (16 * mt + 4 * g + n / 4) * L::kRow + (n % 4) * 8);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            x[mt][w][q] = *reinterpret_cast<const float*>(v + (16 * mt + 4 * g + q) * L::kValueRow + 4 * n);
-        } else {
-          const short4_t e = read_columns(v + (16 * mt + 4 * g + n / 4) * L::kValueRow + (n % 4) * 8);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if constexpr (DT == 1)
-              x[mt][w][q] = __uint_as_float((uint32_t)(uint16_t)e[q] << 16);
-            else
-              x[mt][w][q] = (float)__builtin_bit_cast(_Float16, (short)e[q]);
-          }
+        for (int q = 0; q < 4; ++q) {
+          if constexpr (DT == 1)
+            x[mt][q] = __uint_as_float((uint32_t)(uint16_t)e[q] << 16);
+          else
+            x[mt][q] = (float)__builtin_bit_cast(_Float16, (short)e[q]);
         }
       }
+    }
+    // Operands are read a step before they are needed: at most two waves a SIMD hide little of what LDS takes.
+    half8_t keys[2][4][L::kParts];
+    auto read_keys = [&](int of_q, int st) {
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int p = 0; p < L::kParts; ++p) keys[st & 1][mt][p] = key(of_q, p, mt, st % L::kSteps);
+    };
+    read_keys(0, 0);
+    if (!LOADERS) move(c, now);
+    __builtin_amdgcn_sched_barrier(0);
 
     // What a column's tokens bring, beta v, and its power of two, with M the largest of that and of the state's elements: M
     // goes to 2^7..2^8 when it has left 2^5..2^9.  The state's length is at most sqrt(128) M and grows by M a token, so that
     // X and V' stay below 75 M < 2^16; |S| 2^4 is below 2^13; a part's last bit lies 2^31 below M.
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      const float4_t beta = gate(kBeta, mt);
-#pragma unroll
-      for (int w = 0; w < NT; ++w) x[mt][w] *= beta;
-    }
     {
-      bool off = c == 0;
-      float top[NT], high[NT];
+      float top = 0.0f, high = 0.0f;
 #pragma unroll
-      for (int w = 0; w < NT; ++w) {
-        top[w] = high[w] = 0.0f;
+      for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-        for (int t = 0; t < L::kTiles; ++t)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) top[w] = fmaxf(top[w], fabsf(s[t][w][q]));
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) high[w] = fmaxf(high[w], fabsf(x[mt][w][q]));
-        const float both = fmaxf(top[w] * (1.0f / kLong), __builtin_amdgcn_ldexpf(high[w], -scaled[w]));
-        off = off || both > 512.0f || (both < 32.0f && both > 0.0f && scaled[w] > -150);
-      }
-      if (__any(off)) {
-#pragma unroll
-        for (int w = 0; w < NT; ++w) {
-          top[w] = fmaxf(top[w], __shfl_xor(top[w], 16));
-          top[w] = fmaxf(top[w], __shfl_xor(top[w], 32));
-          high[w] = fmaxf(high[w], __shfl_xor(high[w], 16));
-          high[w] = fmaxf(high[w], __shfl_xor(high[w], 32));
-          constexpr int kNone = -100000;
-          const int of_state = top[w] > 0.0f ? __builtin_amdgcn_frexp_expf(top[w]) + scaled[w] - kLength : kNone;
-          const int of_values = high[w] > 0.0f ? __builtin_amdgcn_frexp_expf(high[w]) : kNone;
-          const int most = std::max(of_state, of_values), here_ = most - scaled[w];
-          if (most != kNone && (here_ > 9 || here_ < 6)) {
-            const int next = std::max(most - 8, -150), by = scaled[w] - next;
-            scaled[w] = next;
-#pragma unroll
-            for (int t = 0; t < L::kTiles; ++t)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) s[t][w][q] = __builtin_amdgcn_ldexpf(s[t][w][q], by);
-          }
-        }
-      }
-    }
-
-    // K S and Q S
-    float4_t y[4][NT], o[4][NT];
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int w = 0; w < NT; ++w) y[mt][w] = o[mt][w] = float4_t{0, 0, 0, 0};
-#pragma unroll
-    for (int st = 0; st < L::kSteps; ++st) {
-      Parts b[NT];
-#pragma unroll
-      for (int w = 0; w < NT; ++w) b[w] = cut(s[2 * st][w], s[2 * st + 1][w]);
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(s[t][i]));
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
-        const half8_t k = key(0, 0, mt, st), q = key(1, 0, mt, st);
+        x[mt] *= beta[mt];
 #pragma unroll
-        for (int w = 0; w < NT; ++w) {
-          y[mt][w] = mfma(k, b[w].hi, y[mt][w]);
-          o[mt][w] = mfma(q, b[w].hi, o[mt][w]);
-          y[mt][w] = mfma(k, b[w].lo, y[mt][w]);
-          o[mt][w] = mfma(q, b[w].lo, o[mt][w]);
-        }
-        if constexpr (L::kParts == 2) {
-          const half8_t k2 = key(0, 1, mt, st), q2 = key(1, 1, mt, st);
+        for (int i = 0; i < 4; ++i) high = fmaxf(high, fabsf(x[mt][i]));
+      }
+      const float both = fmaxf(top * (1.0f / kLong), __builtin_amdgcn_ldexpf(high, -scaled));
+      if (__any(c == 0 || both > 512.0f || (both < 32.0f && both > 0.0f && scaled > -150))) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        high = fmaxf(high, __shfl_xor(high, 16));
+        high = fmaxf(high, __shfl_xor(high, 32));
+        constexpr int kNone = -100000;
+        const int of_state = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) + scaled - kLength : kNone;
+        const int of_values = high > 0.0f ? __builtin_amdgcn_frexp_expf(high) : kNone;
+        const int most = std::max(of_state, of_values), by_now = most - scaled;
+        if (most != kNone && (by_now > 9 || by_now < 6)) {
+          const int next = std::max(most - 8, -150), by = scaled - next;
+          scaled = next;
 #pragma unroll
-          for (int w = 0; w < NT; ++w) {
-            y[mt][w] = mfma(k2, b[w].hi, y[mt][w]);
-            o[mt][w] = mfma(q2, b[w].hi, o[mt][w]);
-          }
+          for (int t = 0; t < L::kTiles; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[t][i] = __builtin_amdgcn_ldexpf(s[t][i], by);
         }
       }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+
+    // K S
+    const float4_t none = {0, 0, 0, 0};
+    float4_t y[4] = {none, none, none, none}, o[4] = {none, none, none, none};
+    Parts of_s[L::kSteps];
+    float4_t gain[4], gain_q[4];
+    of_s[0] = cut(s[0], s[1]);
+#pragma unroll
+    for (int st = 0; st < L::kSteps; ++st) {
+      if (st + 1 < L::kSteps) {
+        read_keys(0, st + 1);
+      } else {
+        read_keys(1, L::kSteps);
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) gain[mt] = gate(kGainK, mt);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 1 + L::kParts; ++i)
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+          y[mt] = mfma(keys[st & 1][mt][i == 2 ? L::kParts - 1 : 0], i == 1 ? of_s[st].lo : of_s[st].hi, y[mt]);
+      if (st + 1 < L::kSteps) of_s[st + 1] = cut(s[2 * st + 2], s[2 * st + 3]);
     }
 
-    // X, then V' = T X
+    // Q S, which nothing waits for, among the arithmetic of X
+    half8_t turn[kTies][2];
+    auto read_ties = [&](half8_t (&to)[kTies][2], int at, int st) {
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      const float4_t gain = gate(kGainK, mt), gain_q = gate(kGainQ, mt);
+      for (int mt = 2 * st; mt < 4; ++mt)
 #pragma unroll
-      for (int w = 0; w < NT; ++w) {
+        for (int p = 0; p < 2; ++p) to[tie(mt, st)][p] = tied(at, mt, st, p);
+    };
+    Parts b[2], d[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          x[mt][w][q] = __builtin_fmaf(-gain[q], y[mt][w][q], __builtin_amdgcn_ldexpf(x[mt][w][q], -scaled[w]));
-        o[mt][w] *= gain_q;
-        y[mt][w] = float4_t{0, 0, 0, 0};
-      }
+    for (int st = 0; st < L::kSteps; ++st) {
+      if (st + 1 < L::kSteps) read_keys(1, st + 1 + L::kSteps);
+      else read_ties(turn, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 1 + L::kParts; ++i)
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+          o[mt] = mfma(keys[st & 1][mt][i == 2 ? L::kParts - 1 : 0], i == 1 ? of_s[st].lo : of_s[st].hi, o[mt]);
+      // a share of X in each step
+#pragma unroll
+      for (int mt = 4 * st / L::kSteps; mt < 4 * (st + 1) / L::kSteps; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[mt][i] = __builtin_fmaf(-gain[mt][i], y[mt][i], __builtin_amdgcn_ldexpf(x[mt][i], -scaled));
+      if (st == L::kSteps / 2) b[0] = cut(x[0], x[1]);
     }
-#pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      Parts b[NT];
-#pragma unroll
-      for (int w = 0; w < NT; ++w) b[w] = cut(x[2 * st][w], x[2 * st + 1][w]);
-#pragma unroll
-      for (int mt = 2 * st; mt < 4; ++mt) {
-        const half8_t hi = tied(0, mt, st, 0), lo = tied(0, mt, st, 1);
-#pragma unroll
-        for (int w = 0; w < NT; ++w) {
-          y[mt][w] = mfma(hi, b[w].hi, y[mt][w]);
-          y[mt][w] = mfma(hi, b[w].lo, y[mt][w]);
-          y[mt][w] = mfma(lo, b[w].hi, y[mt][w]);
-        }
-      }
-    }
+    b[1] = cut(x[2], x[3]);
 
-    // P V' onto Q S, and K^T V' onto the decayed state
+    // V' = T X; the state's decay among it
     const float whole = gates[kWhole * kC];
+    float4_t until[4], z[4] = {none, none, none, none};
+    half8_t turned[L::kTiles][L::kParts], inner[kTies][2];  // rows of K^T; P
+    auto read_turned = [&](int st) {
 #pragma unroll
-    for (int t = 0; t < L::kTiles; ++t)
-#pragma unroll
-      for (int w = 0; w < NT; ++w) s[t][w] *= whole;
-#pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      Parts b[NT], d[NT];
-      const float4_t until0 = gate(kUntil, 2 * st), until1 = gate(kUntil, 2 * st + 1);
-#pragma unroll
-      for (int w = 0; w < NT; ++w) {
-        const float4_t v0 = y[2 * st][w] * kDown, v1 = y[2 * st + 1][w] * kDown;
-        b[w] = cut(v0, v1);
-        d[w] = cut(v0 * until0, v1 * until1);
-      }
-#pragma unroll
-      for (int mt = 2 * st; mt < 4; ++mt) {
-        const half8_t hi = tied(kPAt, mt, st, 0), lo = tied(kPAt, mt, st, 1);
-#pragma unroll
-        for (int w = 0; w < NT; ++w) {
-          o[mt][w] = mfma(hi, b[w].hi, o[mt][w]);
-          o[mt][w] = mfma(hi, b[w].lo, o[mt][w]);
-          o[mt][w] = mfma(lo, b[w].hi, o[mt][w]);
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < L::kTiles; ++t) {
-        half8_t k[L::kParts];
+      for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
         for (int p = 0; p < L::kParts; ++p) {
           short4_t e[2];
@@ -663,73 +712,113 @@ __global__ __launch_bounds__(kThreads, 1) void gated_delta_chain_kernel(DeltaArg
           for (int j = 0; j < 2; ++j)  // tokens 32 st + 16 j + 4 g.., rows of this tile
             e[j] = read_columns(here + ((p * 4 + 2 * st + j) * L::kSteps + t / 2) * kBlock + ((n % 4) * 16 + 4 * g + n / 4) * 16 +
                                 8 * (t & 1));
-          k[p] = __builtin_bit_cast(half8_t, __builtin_shufflevector(e[0], e[1], 0, 1, 2, 3, 4, 5, 6, 7));
+          turned[t][p] = __builtin_bit_cast(half8_t, __builtin_shufflevector(e[0], e[1], 0, 1, 2, 3, 4, 5, 6, 7));
         }
+    };
+    read_ties(turn, 0, 1);
 #pragma unroll
-        for (int w = 0; w < NT; ++w) {
-          s[t][w] = mfma(k[0], d[w].hi, s[t][w]);
-          s[t][w] = mfma(k[0], d[w].lo, s[t][w]);
-          if constexpr (L::kParts == 2) s[t][w] = mfma(k[1], d[w].hi, s[t][w]);
-        }
+    for (int mt = 0; mt < 4; ++mt) {
+      until[mt] = gate(kUntil, mt);
+      gain_q[mt] = gate(kGainQ, mt);
+    }
+    read_turned(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int mt = 2 * half; mt < 2 * half + 2; ++mt) z[mt] = mfma(turn[tie(mt, 0)][i == 2], i == 1 ? b[0].lo : b[0].hi, z[mt]);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int mt = 2; mt < 4; ++mt) z[mt] = mfma(turn[tie(mt, 1)][i == 2], i == 1 ? b[1].lo : b[1].hi, z[mt]);
+#pragma unroll
+    for (int t = 0; t < L::kTiles; ++t) s[t] *= whole;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) o[mt] *= gain_q[mt];
+
+    // K^T V' onto the decayed state, P V' onto Q S
+    auto cut_values = [&](int st) {
+      const float4_t v0 = z[2 * st] * kDown, v1 = z[2 * st + 1] * kDown;
+      d[st] = cut(v0 * until[2 * st], v1 * until[2 * st + 1]);
+      b[st] = cut(v0, v1);
+    };
+    cut_values(0);
+    read_ties(inner, kPAt, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+#pragma unroll
+      for (int i = 0; i < 1 + L::kParts; ++i)
+#pragma unroll
+        for (int t = 0; t < L::kTiles; ++t) s[t] = mfma(turned[t][i == 2 ? L::kParts - 1 : 0], i == 1 ? d[st].lo : d[st].hi, s[t]);
+      if (st == 0) cut_values(1);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int mt = 2 * st; mt < 4; ++mt)
+          o[mt] = mfma(inner[tie(mt, st)][i == 2], i == 1 ? b[st].lo : b[st].hi, o[mt]);
+      if (st == 0) {
+        read_turned(1);
+        read_ties(inner, kPAt, 1);
       }
     }
 
-    // outputs
+    // outputs, to where this wave's values were
+    const float back = __builtin_amdgcn_ldexpf(a.scale, scaled - 14);
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int mt = 0; mt < 4; ++mt) {
+      uint8_t* row = mine + (16 * mt + 4 * g) * L::kRow + n * kSize;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t token = start + c * kC + 16 * mt + 4 * g + q;
-        if (token < end) {
-#pragma unroll
-          for (int w = 0; w < NT; ++w) {
-            Elements<DT, 1> e;
-            e.set({__builtin_amdgcn_ldexpf(o[mt][w][q] * a.scale, scaled[w] - 14)});
-            e.store(a.out.p, token * a.out.token + h * a.out.head + column + 16 * w + n);
-          }
+      for (int i = 0; i < 4; i += 2) {
+        const float z0 = o[mt][i] * back, z1 = o[mt][i + 1] * back;
+        if constexpr (DT == 0) {
+          *reinterpret_cast<float*>(row + i * L::kRow) = z0;
+          *reinterpret_cast<float*>(row + (i + 1) * L::kRow) = z1;
+        } else {
+          const uint32_t both = pack2<DT>(z0, z1);
+          *reinterpret_cast<uint16_t*>(row + i * L::kRow) = (uint16_t)both;
+          *reinterpret_cast<uint16_t*>(row + (i + 1) * L::kRow) = (uint16_t)(both >> 16);
         }
       }
-
-    arrived();
-    if (L::kStages == 1 && c + 1 < chunks) {
-      issue(c + 1, 0);
-      arrived();
     }
+    meet();
+    change(c);
   }
+  if (!LOADERS) put_out(chunks - 1, L::kStages == 2 ? (int)((chunks - 1) & 1) : 0);
 
 #pragma unroll
   for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-    for (int w = 0; w < NT; ++w)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        a.state_out[state + (int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * a.head_v + 16 * w] =
-            __builtin_amdgcn_ldexpf(s[t][w][q], scaled[w] - kLength);
+    for (int q = 0; q < 4; ++q)
+      a.state_out[state + (int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * a.head_v] =
+          __builtin_amdgcn_ldexpf(s[t][q], scaled - kLength);
 #endif
 }
 
-template <int DT, int DK>
-hipError_t launch_solve(const DeltaArgs& a, hipStream_t stream) {
-  const uint32_t blocks = (uint32_t)((a.v_heads + kWaves - 1) / kWaves);
-  const int64_t places = delta_chunk_places(a.tokens, a.n_seqs), most = std::max<int64_t>(kMostWorkgroups / blocks, 1);
-  const FastDiv by_group((uint32_t)(a.v_heads / a.k_heads)), by_blocks(blocks);
+// `launch(first place, places)` for all places of chunks, so many at a time
+template <typename F>
+hipError_t for_places(const DeltaArgs& a, int64_t workgroups_of_place, F launch) {
+  const int64_t places = delta_chunk_places(a.tokens, a.n_seqs), most = std::max<int64_t>(kMostWorkgroups / workgroups_of_place, 1);
   for (int64_t first = 0; first < places; first += most) {
-    const uint32_t grid = (uint32_t)std::min(most, places - first) * blocks;
-    gated_delta_solve_kernel<DT, DK><<<grid, kThreads, 0, stream>>>(a, by_group, by_blocks, first);
+    launch(first, (uint32_t)std::min(most, places - first));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <int DT, int DK, int NT>
+template <int DT, int DK, int WAVES, int LOADERS>
 hipError_t launch_chain(const DeltaArgs& a, hipStream_t stream) {
-  const uint32_t slices = (uint32_t)(a.head_v / Chain<DT, DK, NT>::kCols);
+  using L = Chain<DT, DK, WAVES, LOADERS>;
+  const uint32_t slices = (uint32_t)(a.head_v / L::kCols);
   const FastDiv by_seq((uint32_t)a.v_heads), by_key_heads((uint32_t)a.k_heads);
   const int64_t pairs = (int64_t)a.n_seqs * a.v_heads, all = (pairs + 7) / 8 * 8 * slices;
   for (int64_t first = 0; first < all; first += kMostWorkgroups) {
     const uint32_t grid = (uint32_t)std::min<int64_t>(kMostWorkgroups, all - first);
-    gated_delta_chain_kernel<DT, DK, NT><<<grid, kThreads, 0, stream>>>(a, by_seq, by_key_heads, slices, (uint32_t)first, (uint32_t)pairs);
+    gated_delta_chain_kernel<DT, DK, WAVES, LOADERS>
+        <<<grid, L::kThreads, 0, stream>>>(a, by_seq, by_key_heads, slices, (uint32_t)first, (uint32_t)pairs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -738,13 +827,22 @@ hipError_t launch_chain(const DeltaArgs& a, hipStream_t stream) {
 
 template <int DT, int DK>
 hipError_t launch_sized(const DeltaArgs& a, hipStream_t stream) {
-  const hipError_t e = launch_solve<DT, DK>(a, stream);
+  const uint32_t k_heads = (uint32_t)a.k_heads, blocks = (uint32_t)((a.v_heads + kWaves - 1) / kWaves);
+  const FastDiv by_heads(k_heads), by_group((uint32_t)(a.v_heads / a.k_heads)), by_blocks(blocks);
+  hipError_t e = for_places(a, k_heads, [&](int64_t first, uint32_t places) {
+    gated_delta_keys_kernel<DT, DK><<<places * k_heads, 512, 0, stream>>>(a, by_heads, first);
+  });
   if (e != hipSuccess) return e;
+  e = for_places(a, blocks, [&](int64_t first, uint32_t places) {
+    gated_delta_solve_kernel<DT, DK><<<places * blocks, kThreads, 0, stream>>>(a, by_group, by_blocks, first);
+  });
+  if (e != hipSuccess) return e;
+  const int64_t columns = (int64_t)a.n_seqs * a.v_heads * a.head_v;
+  if (columns <= 32 * device_cu_count()) return launch_chain<DT, DK, 2, 2>(a, stream);
   if constexpr (DT != 0) {
-    if (a.head_v % 128 == 0 && (int64_t)a.n_seqs * a.v_heads * (a.head_v / 64) > device_cu_count())
-      return launch_chain<DT, DK, 2>(a, stream);
+    if (a.head_v % 128 == 0) return launch_chain<DT, DK, 8, 0>(a, stream);
   }
-  return launch_chain<DT, DK, 1>(a, stream);
+  return launch_chain<DT, DK, 4, 0>(a, stream);
 }
 
 template <int DT>
