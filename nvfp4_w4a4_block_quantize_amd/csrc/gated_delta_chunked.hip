@@ -40,7 +40,7 @@ constexpr int kLength = 4;                                // rows of keys and qu
 constexpr float kLong = 1 << kLength;
 
 // per token of a chunk, after T and P
-enum { kBeta, kGainK, kUntil, kGainQ, kWhole, kGates };
+enum { kBeta, kGainK, kUntil, kGainQ, kDecay, kGates };
 static_assert(kGatesAt + kGates * kC * 4 <= kDeltaTieBytes, "the workspace's entry holds it");
 
 constexpr int tie(int mt, int s) { return mt < 2 ? mt : 2 * mt - 2 + s; }  // of rows 16 mt.., columns 32 s..
@@ -392,10 +392,32 @@ __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a
   gates[kGainK * kC + lane] = beta * since * k_norm * (1.0f / kLong);
   gates[kUntil * kC + lane] = __builtin_amdgcn_exp2f((float)(whole - log_decay)) * k_norm * kLong;
   gates[kGainQ * kC + lane] = since * q_norm * (kUp / kLong);
-  gates[kWhole * kC + lane] = __builtin_amdgcn_exp2f((float)whole);
+  gates[kDecay * kC + lane] = __builtin_amdgcn_exp2f((float)whole);
 }
 
 // -------------------------------------------------------------- the states' chain
+
+// What a launch does: whole sequences; the ends of their parts (of a part's state, started from zeros but for the first
+// part, and of the identity: a part takes any state S to `turn` S + `end`); or the parts themselves, from known states.
+enum { kWhole, kEnds, kPart };
+
+struct PartArgs {
+  int parts;           // of a sequence, at most
+  float *first, *turn;  // [sequence][v_heads][parts]: states that parts start from [head_k][head_v], what they do [head_k][head_k]
+};
+
+// the chunks of a part, equal in number but for the last part's
+struct Part {
+  int64_t low, high;  // of the sequence's chunks; none if not low < high
+  bool last;
+};
+__device__ __forceinline__ int64_t chunks_of_part(int64_t chunks, int parts) {
+  return std::max<int64_t>((chunks + parts - 1) / parts, kDeltaPartChunks);
+}
+__device__ __forceinline__ Part find_part(int64_t chunks, int parts, int part) {
+  const int64_t each = chunks_of_part(chunks, parts), high = (part + 1) * each;
+  return {part * each, std::min(high, chunks), high >= chunks};
+}
 
 typedef short short4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) short4_t lds_short4_t;
@@ -405,16 +427,18 @@ __device__ __forceinline__ short4_t read_columns(const uint8_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)p);
 }
 
-// WAVES of a workgroup hold columns, LOADERS more move data for them
-template <int DT, int DK, int WAVES, int LOADERS>
+// WAVES of a workgroup hold columns, LOADERS more move data for them.  A stage is keys, T, gates, values, queries, P: of the
+// ends of parts, all but the last two.
+template <int DT, int DK, int MODE, int WAVES, int LOADERS>
 struct Chain {
   static constexpr int kParts = DT == 0 ? 2 : 1, kSteps = DK / 32, kTiles = DK / 16;
   static constexpr int kCols = 16 * WAVES;                    // of a workgroup
   static constexpr int kThreads = 64 * (WAVES + LOADERS);
   static constexpr int kKeys = kParts * 4 * kSteps * kBlock;  // bytes of K; Q follows
   static constexpr int kRow = 16 * element_size(DT), kValues = kC * kRow;  // a wave's columns of V, then of the outputs
-  static constexpr int kTiesAt = 2 * kKeys, kValuesAt = kTiesAt + kDeltaTieBytes;
-  static constexpr int kStage = kValuesAt + WAVES * kValues;
+  static constexpr int kTurnAt = kKeys, kGatesIn = kTurnAt + kPAt, kValuesAt = kGatesIn + 2 * kBlock;
+  static constexpr int kQueriesAt = kValuesAt + WAVES * kValues, kInnerAt = kQueriesAt + kKeys;
+  static constexpr int kStage = MODE == kEnds ? kQueriesAt : kInnerAt + kPAt;
   static constexpr int kStages = 2 * kStage <= (160 << 10) ? 2 : 1;
   static_assert(kStages * kStage <= (160 << 10), "the stages fit LDS");
 };
@@ -441,11 +465,20 @@ __device__ __forceinline__ void to_lds(uint32_t lds, const void* p) {
 }
 #endif
 
-template <int DT, int DK, int WAVES, int LOADERS>
-__global__ __launch_bounds__(64 * (WAVES + LOADERS), (WAVES + LOADERS + 3) / 4) void gated_delta_chain_kernel(
-    DeltaArgs a, FastDiv by_seq, FastDiv by_key_heads, uint32_t slices, uint32_t first, uint32_t pairs) {
+// the largest of the four lanes that share a column
+__device__ __forceinline__ float of_column(float x) {
+  const auto rows = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
+  const auto pairs = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(pairs[0]), __uint_as_float(pairs[1]));
+}
+
+template <int DT, int DK, int MODE, int WAVES, int LOADERS>
+__global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves_per_eu(DT == 0 ? 1 : 2))) void gated_delta_chain_kernel(
+    DeltaArgs a, PartArgs parts, FastDiv by_seq, FastDiv by_key_heads, FastDiv by_parts, uint32_t slices, uint32_t first,
+    uint32_t pairs) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using L = Chain<DT, DK, WAVES, LOADERS>;
+  using L = Chain<DT, DK, MODE, WAVES, LOADERS>;
   constexpr int kSize = element_size(DT);
   __shared__ __attribute__((aligned(1024))) uint8_t stage[L::kStages * L::kStage];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -454,18 +487,29 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS), (WAVES + LOADERS + 3) / 4) 
   // Workgroups go to the XCDs in turn: those of one sequence and head, which read the same ties, and where there are 8 key
   // heads (or a multiple) those of one key head lie on one XCD, 8 apart.
   const uint32_t at = first + blockIdx.x, eight = at >> 3;
-  const uint32_t octet = eight / slices, pair = octet * 8 + (at & 7);
+  const uint32_t of_part = eight / slices, octet = MODE == kWhole ? of_part : by_parts.div(of_part);
+  const uint32_t pair = octet * 8 + (at & 7);
   if (pair >= pairs) return;
-  const int group_column = (int)(eight - octet * slices) * L::kCols;
   const uint32_t r = by_seq.div(pair), in_seq = pair - r * by_seq.d;
   const uint32_t of_group = by_key_heads.div(in_seq);
   const int kh = (int)(in_seq - of_group * by_key_heads.d), h = kh * (a.v_heads / a.k_heads) + (int)of_group;
   const int slot = a.slots[r];
-  const int64_t start = start_of(a.token_starts, (int)r, a.tokens), end = start_of(a.token_starts, (int)r + 1, a.tokens);
-  if (!slot_ok(slot, a.num_slots) || start >= end) return;
-  const int64_t chunks = (end - start + kC - 1) / kC;
+  const int64_t from_start = start_of(a.token_starts, (int)r, a.tokens), end = start_of(a.token_starts, (int)r + 1, a.tokens);
+  if (!slot_ok(slot, a.num_slots) || from_start >= end) return;
+  const int part = MODE == kWhole ? 0 : (int)(of_part - octet * by_parts.d);
+  Part of_chunks = {0, (end - from_start + kC - 1) / kC, true};
+  if (MODE != kWhole) of_chunks = find_part(of_chunks.high, parts.parts, part);
+  if (of_chunks.low >= of_chunks.high || (MODE == kEnds && of_chunks.last)) return;
+  // of the ends, slices behind the values' are columns of the identity
+  int group_column = (int)(eight - of_part * slices) * L::kCols;
+  const bool unit = MODE == kEnds && group_column >= a.head_v;
+  if (unit) {
+    if (part == 0) return;
+    group_column -= a.head_v;
+  }
+  const int64_t chunks = of_chunks.high - of_chunks.low, start = from_start + of_chunks.low * kC;
   const int64_t chunk_bytes = delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT);
-  const uint8_t* from = static_cast<const uint8_t*>(a.workspace) + (start / kC + r) * chunk_bytes;
+  const uint8_t* from = static_cast<const uint8_t*>(a.workspace) + (from_start / kC + r + of_chunks.low) * chunk_bytes;
   const int64_t keys_at = kh * delta_key_bytes(DK, DT),
                 ties_at = a.k_heads * delta_key_bytes(DK, DT) + (int64_t)h * kDeltaTieBytes;
   const char* values = static_cast<const char*>(a.v.p) + (h * a.v.head + group_column) * kSize;
@@ -476,32 +520,39 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS), (WAVES + LOADERS + 3) / 4) 
   constexpr int kOf = LOADERS ? LOADERS : WAVES;
   const int share = LOADERS ? wave - WAVES : wave;
   constexpr int kLanes = L::kRow / 16, kRows = 64 / kLanes, kMoves = kC / kRows;  // of a row, rows of a move
-  // a chunk on its way into a stage: turns of 4 blocks of keys and queries, then of T and P, the gates, and values
+  // a chunk on its way into a stage: values, turns of 4 blocks of keys, T, queries and P, and the gates
   auto issue = [&](int64_t c, int to) {
     const uint32_t lds = lds0 + to * L::kStage;
     const uint8_t* base = from + c * chunk_bytes;
-    constexpr int kTurns = 2 * L::kKeys / (4 * kBlock), kAll = kTurns + kGatesAt / (4 * kBlock);
+    if (!unit) {
 #pragma unroll
-    for (int w = 0; w < WAVES / kOf; ++w) {
-      const int of = share + w * kOf;
+      for (int w = 0; w < WAVES / kOf; ++w) {
+        const int of = share + w * kOf;
 #pragma unroll
-      for (int i = 0; i < kMoves; ++i) {
-        const int64_t token = std::min(start + c * kC + i * kRows + lane / kLanes, end - 1);
-        to_lds(lds + L::kValuesAt + of * L::kValues + i * kBlock,
-               values + token * a.v.token * kSize + of * L::kRow + lane % kLanes * 16);
+        for (int i = 0; i < kMoves; ++i) {
+          const int64_t token = std::min(start + c * kC + i * kRows + lane / kLanes, end - 1);
+          to_lds(lds + L::kValuesAt + of * L::kValues + i * kBlock,
+                 values + token * a.v.token * kSize + of * L::kRow + lane % kLanes * 16);
+        }
       }
     }
+    constexpr int kKeyTurns = L::kKeys / (4 * kBlock), kTieTurns = kPAt / (4 * kBlock);
+    constexpr int kAll = (MODE == kEnds ? 1 : 2) * (kKeyTurns + kTieTurns);
 #pragma unroll
     for (int i = 0; i < (kAll + kOf - 1) / kOf; ++i) {
-      const int turn = i * kOf + share;
+      int turn = i * kOf + share;
       if (turn >= kAll) break;
-      const bool tie = turn >= kTurns;
-      to_lds4(lds + turn * 4 * kBlock, base + (tie ? ties_at - L::kTiesAt : keys_at) + turn * 4 * kBlock, lane * 16);
+      const bool second = turn >= kKeyTurns + kTieTurns;  // queries and P
+      if (second) turn -= kKeyTurns + kTieTurns;
+      const bool tie = turn >= kKeyTurns;
+      const int64_t in = (tie ? ties_at + (second ? kPAt : 0) - L::kKeys : keys_at + (second ? L::kKeys : 0)) + turn * 4 * kBlock;
+      to_lds4(lds + (second ? L::kQueriesAt : 0) + turn * 4 * kBlock, base + in, lane * 16);
     }
-    if (share == kOf - 1) to_lds2(lds + L::kTiesAt + kGatesAt, base + ties_at + kGatesAt, lane * 16);
+    if (share == kOf - 1) to_lds2(lds + L::kGatesIn, base + ties_at + kGatesAt, lane * 16);
   };
   // outputs of a chunk from its stage
   auto put_out = [&](int64_t c, int from_stage) {
+    if (MODE == kEnds) return;
     const int64_t token = start + c * kC + lane / kLanes;
     char* to = static_cast<char*>(a.out.p) + (token * a.out.token + h * a.out.head + group_column) * kSize + lane % kLanes * 16;
     u32x4_t held[WAVES / kOf][kMoves];
@@ -556,26 +607,30 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS), (WAVES + LOADERS + 3) / 4) 
   // eight elements of an operand that meet elements 32 s + 8 g.. of a row of K or Q.
   float4_t s[L::kTiles];
   int scaled = kLength;  // the state is s 2^(scaled - 4), values are taken times 2^-scaled
-  const int64_t state = ((int64_t)slot * a.v_heads + h) * DK * a.head_v + group_column + 16 * wave + n;
-  const bool carried = !a.cached_lens || a.cached_lens[r] > 0;
+  const int col = group_column + 16 * wave + n;
+  const int64_t of_slot = ((int64_t)slot * a.v_heads + h) * DK * a.head_v;
+  const int64_t of_parts = ((int64_t)r * a.v_heads + h) * parts.parts + part;
+  const float* begin = MODE == kPart ? parts.first + of_parts * DK * a.head_v : a.state + of_slot;
+  const bool carried = MODE == kPart || (part == 0 && (!a.cached_lens || a.cached_lens[r] > 0));
 #pragma unroll
   for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      s[t][q] = carried ? a.state[state + (int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * a.head_v] : 0.0f;
+    for (int q = 0; q < 4; ++q) {
+      const int row = 32 * (t / 2) + 8 * g + 4 * (t & 1) + q;
+      s[t][q] = carried ? begin[(int64_t)row * a.head_v + col] : unit && row == col ? 1.0f : 0.0f;
+    }
   meet();
 
   for (int64_t c = 0; c < chunks; ++c) {
     const int now = L::kStages == 2 ? (int)(c & 1) : 0;
     uint8_t* here = stage + now * L::kStage;
-    const uint8_t* ties = here + L::kTiesAt;
-    const float* gates = reinterpret_cast<const float*>(ties + kGatesAt);
+    const float* gates = reinterpret_cast<const float*>(here + L::kGatesIn);
     uint8_t* mine = here + L::kValuesAt + wave * L::kValues;
     auto key = [&](int of_q, int part, int mt, int st) {
-      return *reinterpret_cast<const half8_t*>(here + of_q * L::kKeys + ((part * 4 + mt) * L::kSteps + st) * kBlock + lane * 16);
+      return *reinterpret_cast<const half8_t*>(here + (of_q ? L::kQueriesAt : 0) + ((part * 4 + mt) * L::kSteps + st) * kBlock + lane * 16);
     };
     auto tied = [&](int at, int mt, int st, int part) {
-      return *reinterpret_cast<const half8_t*>(ties + at + (2 * tie(mt, st) + part) * kBlock + lane * 16);
+      return *reinterpret_cast<const half8_t*>(here + at + (2 * tie(mt, st) + part) * kBlock + lane * 16);
     };
     auto gate = [&](int which, int mt) { return *reinterpret_cast<const float4_t*>(gates + which * kC + 16 * mt + 4 * g); };
 
@@ -583,7 +638,9 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS), (WAVES + LOADERS + 3) / 4) 
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
       beta[mt] = gate(kBeta, mt);
-      if constexpr (DT == 0) {
+      if (unit) {
+        x[mt] = float4_t{0, 0, 0, 0};
+      } else if constexpr (DT == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[mt][i] = *reinterpret_cast<const float*>(mine + (16 * mt + 4 * g + i) * L::kRow + 4 * n);
       } else {
@@ -597,80 +654,80 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS), (WAVES + LOADERS + 3) / 4) 
         }
       }
     }
-    // Operands are read a step before they are needed: at most two waves a SIMD hide little of what LDS takes.
-    half8_t keys[2][4][L::kParts];
-    auto read_keys = [&](int of_q, int st) {
+    // K S takes kSteps steps, Q S as many.  Operands are read kAhead steps before they are needed: with one wave a SIMD
+    // nothing else hides what LDS takes, with two the registers are fewer.
+    constexpr int kAhead = LOADERS && DK > 64 ? 3 : 2;
+    half8_t keys[kAhead][4][L::kParts];
+    auto read_step = [&](int i) {
+      if (i >= (MODE == kEnds ? 1 : 2) * L::kSteps) return;
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-        for (int p = 0; p < L::kParts; ++p) keys[st & 1][mt][p] = key(of_q, p, mt, st % L::kSteps);
+        for (int p = 0; p < L::kParts; ++p) keys[i % kAhead][mt][p] = key(i >= L::kSteps, p, mt, i % L::kSteps);
     };
-    read_keys(0, 0);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) read_step(i);
     if (!LOADERS) move(c, now);
     __builtin_amdgcn_sched_barrier(0);
 
+    // The state's parts, while those come, and its largest element.
+    Parts of_s[L::kSteps];
+    float top = 0.0f, high = 0.0f;
+#pragma unroll
+    for (int st = 0; st < L::kSteps; ++st) {
+      of_s[st] = cut(s[2 * st], s[2 * st + 1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(s[2 * st][i]), fabsf(s[2 * st + 1][i])));
+    }
+    __builtin_amdgcn_sched_barrier(0);
     // What a column's tokens bring, beta v, and its power of two, with M the largest of that and of the state's elements: M
     // goes to 2^7..2^8 when it has left 2^5..2^9.  The state's length is at most sqrt(128) M and grows by M a token, so that
     // X and V' stay below 75 M < 2^16; |S| 2^4 is below 2^13; a part's last bit lies 2^31 below M.
-    {
-      float top = 0.0f, high = 0.0f;
 #pragma unroll
-      for (int t = 0; t < L::kTiles; ++t)
+    for (int mt = 0; mt < 4; ++mt) {
+      x[mt] *= beta[mt];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(s[t][i]));
+      for (int i = 0; i < 4; ++i) high = fmaxf(high, fabsf(x[mt][i]));
+    }
+    const float both = of_column(fmaxf(top * (1.0f / kLong), __builtin_amdgcn_ldexpf(high, -scaled)));
+    if (__any(c == 0 || both > 512.0f || (both < 32.0f && both > 0.0f && scaled > -150))) {
+      top = of_column(top);
+      high = of_column(high);
+      constexpr int kNone = -100000;
+      const int of_state = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) + scaled - kLength : kNone;
+      const int of_values = high > 0.0f ? __builtin_amdgcn_frexp_expf(high) : kNone;
+      const int most = std::max(of_state, of_values), by_now = most - scaled;
+      if (most != kNone && (by_now > 9 || by_now < 6)) {
+        const int next = std::max(most - 8, -150), by = scaled - next;
+        scaled = next;
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        x[mt] *= beta[mt];
+        for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) high = fmaxf(high, fabsf(x[mt][i]));
+          for (int i = 0; i < 4; ++i) s[t][i] = __builtin_amdgcn_ldexpf(s[t][i], by);
       }
-      const float both = fmaxf(top * (1.0f / kLong), __builtin_amdgcn_ldexpf(high, -scaled));
-      if (__any(c == 0 || both > 512.0f || (both < 32.0f && both > 0.0f && scaled > -150))) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        high = fmaxf(high, __shfl_xor(high, 16));
-        high = fmaxf(high, __shfl_xor(high, 32));
-        constexpr int kNone = -100000;
-        const int of_state = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) + scaled - kLength : kNone;
-        const int of_values = high > 0.0f ? __builtin_amdgcn_frexp_expf(high) : kNone;
-        const int most = std::max(of_state, of_values), by_now = most - scaled;
-        if (most != kNone && (by_now > 9 || by_now < 6)) {
-          const int next = std::max(most - 8, -150), by = scaled - next;
-          scaled = next;
 #pragma unroll
-          for (int t = 0; t < L::kTiles; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[t][i] = __builtin_amdgcn_ldexpf(s[t][i], by);
-        }
-      }
+      for (int st = 0; st < L::kSteps; ++st) of_s[st] = cut(s[2 * st], s[2 * st + 1]);
     }
     __builtin_amdgcn_sched_barrier(0);
 
     // K S
     const float4_t none = {0, 0, 0, 0};
     float4_t y[4] = {none, none, none, none}, o[4] = {none, none, none, none};
-    Parts of_s[L::kSteps];
-    float4_t gain[4], gain_q[4];
-    of_s[0] = cut(s[0], s[1]);
 #pragma unroll
     for (int st = 0; st < L::kSteps; ++st) {
-      if (st + 1 < L::kSteps) {
-        read_keys(0, st + 1);
-      } else {
-        read_keys(1, L::kSteps);
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) gain[mt] = gate(kGainK, mt);
-      }
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < 1 + L::kParts; ++i)
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
-          y[mt] = mfma(keys[st & 1][mt][i == 2 ? L::kParts - 1 : 0], i == 1 ? of_s[st].lo : of_s[st].hi, y[mt]);
-      if (st + 1 < L::kSteps) of_s[st + 1] = cut(s[2 * st + 2], s[2 * st + 3]);
+          y[mt] = mfma(keys[st % kAhead][mt][i == 2 ? L::kParts - 1 : 0], i == 1 ? of_s[st].lo : of_s[st].hi, y[mt]);
+      read_step(st + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
     }
 
     // Q S, which nothing waits for, among the arithmetic of X
+    float4_t gain[4], gain_q[4];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) gain[mt] = gate(kGainK, mt);
     half8_t turn[kTies][2];
     auto read_ties = [&](half8_t (&to)[kTies][2], int at, int st) {
 #pragma unroll
@@ -681,25 +738,26 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS), (WAVES + LOADERS + 3) / 4) 
     Parts b[2], d[2];
 #pragma unroll
     for (int st = 0; st < L::kSteps; ++st) {
-      if (st + 1 < L::kSteps) read_keys(1, st + 1 + L::kSteps);
-      else read_ties(turn, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 1 + L::kParts; ++i)
+      for (int i = 0; i < (MODE == kEnds ? 0 : 1 + L::kParts); ++i)
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
-          o[mt] = mfma(keys[st & 1][mt][i == 2 ? L::kParts - 1 : 0], i == 1 ? of_s[st].lo : of_s[st].hi, o[mt]);
+          o[mt] = mfma(keys[(st + L::kSteps) % kAhead][mt][i == 2 ? L::kParts - 1 : 0], i == 1 ? of_s[st].lo : of_s[st].hi, o[mt]);
+      read_step(st + L::kSteps + kAhead);
+      if (st == L::kSteps / 2 - 1) read_ties(turn, L::kTurnAt, 0);
+      if (st == L::kSteps - 1) read_ties(turn, L::kTurnAt, 1);
       // a share of X in each step
 #pragma unroll
       for (int mt = 4 * st / L::kSteps; mt < 4 * (st + 1) / L::kSteps; ++mt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[mt][i] = __builtin_fmaf(-gain[mt][i], y[mt][i], __builtin_amdgcn_ldexpf(x[mt][i], -scaled));
-      if (st == L::kSteps / 2) b[0] = cut(x[0], x[1]);
+      if (st >= L::kSteps / 2 && st + 1 < L::kSteps + (L::kSteps == 2)) b[0] = cut(x[0], x[1]);
+      __builtin_amdgcn_sched_barrier(0);
     }
     b[1] = cut(x[2], x[3]);
 
     // V' = T X; the state's decay among it
-    const float whole = gates[kWhole * kC];
+    const float whole = gates[kDecay * kC];
     float4_t until[4], z[4] = {none, none, none, none};
     half8_t turned[L::kTiles][L::kParts], inner[kTies][2];  // rows of K^T; P
     auto read_turned = [&](int st) {
@@ -715,11 +773,10 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS), (WAVES + LOADERS + 3) / 4) 
           turned[t][p] = __builtin_bit_cast(half8_t, __builtin_shufflevector(e[0], e[1], 0, 1, 2, 3, 4, 5, 6, 7));
         }
     };
-    read_ties(turn, 0, 1);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
       until[mt] = gate(kUntil, mt);
-      gain_q[mt] = gate(kGainQ, mt);
+      if (MODE != kEnds) gain_q[mt] = gate(kGainQ, mt);
     }
     read_turned(0);
     __builtin_amdgcn_sched_barrier(0);
@@ -736,16 +793,17 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS), (WAVES + LOADERS + 3) / 4) 
 #pragma unroll
     for (int t = 0; t < L::kTiles; ++t) s[t] *= whole;
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) o[mt] *= gain_q[mt];
+    for (int mt = 0; mt < 4; ++mt)
+      if (MODE != kEnds) o[mt] *= gain_q[mt];
 
     // K^T V' onto the decayed state, P V' onto Q S
     auto cut_values = [&](int st) {
       const float4_t v0 = z[2 * st] * kDown, v1 = z[2 * st + 1] * kDown;
       d[st] = cut(v0 * until[2 * st], v1 * until[2 * st + 1]);
-      b[st] = cut(v0, v1);
+      if (MODE != kEnds) b[st] = cut(v0, v1);
     };
     cut_values(0);
-    read_ties(inner, kPAt, 0);
+    if (MODE != kEnds) read_ties(inner, L::kInnerAt, 0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
@@ -755,20 +813,20 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS), (WAVES + LOADERS + 3) / 4) 
         for (int t = 0; t < L::kTiles; ++t) s[t] = mfma(turned[t][i == 2 ? L::kParts - 1 : 0], i == 1 ? d[st].lo : d[st].hi, s[t]);
       if (st == 0) cut_values(1);
 #pragma unroll
-      for (int i = 0; i < 3; ++i)
+      for (int i = 0; i < (MODE == kEnds ? 0 : 3); ++i)
 #pragma unroll
         for (int mt = 2 * st; mt < 4; ++mt)
           o[mt] = mfma(inner[tie(mt, st)][i == 2], i == 1 ? b[st].lo : b[st].hi, o[mt]);
       if (st == 0) {
         read_turned(1);
-        read_ties(inner, kPAt, 1);
+        if (MODE != kEnds) read_ties(inner, L::kInnerAt, 1);
       }
     }
 
     // outputs, to where this wave's values were
     const float back = __builtin_amdgcn_ldexpf(a.scale, scaled - 14);
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
+    for (int mt = 0; mt < (MODE == kEnds ? 0 : 4); ++mt) {
       uint8_t* row = mine + (16 * mt + 4 * g) * L::kRow + n * kSize;
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
@@ -788,13 +846,63 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS), (WAVES + LOADERS + 3) / 4) 
   }
   if (!LOADERS) put_out(chunks - 1, L::kStages == 2 ? (int)((chunks - 1) & 1) : 0);
 
+  if (MODE == kPart && !of_chunks.last) return;
+  float* to = a.state_out + of_slot;  // of the ends: where the next part starts, or what this one does
+  if (MODE == kEnds) to = unit ? parts.turn + of_parts * DK * DK : parts.first + (of_parts + 1) * DK * a.head_v;
+  const int64_t pitch = unit ? DK : a.head_v;
 #pragma unroll
   for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      a.state_out[state + (int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * a.head_v] =
-          __builtin_amdgcn_ldexpf(s[t][q], scaled - kLength);
+      to[(int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * pitch + col] = __builtin_amdgcn_ldexpf(s[t][q], scaled - kLength);
 #endif
+}
+
+// The states that parts start from: S_0 as it is given, S_1 the first part's end, S_(p+1) = end_p + turn_p S_p.  A
+// workgroup has 16 columns of a sequence and head, each of its waves 16 rows; products in fp32, a state passes through LDS
+// in the order in which the matrix unit takes it (step r of four: elements 4 g + r of 16).
+template <int DK>
+__global__ __launch_bounds__(4 * DK) void gated_delta_join_kernel(DeltaArgs a, PartArgs parts, uint32_t slices) {
+  constexpr int kTiles = DK / 16;
+  __shared__ float4_t state[2][kTiles][64];
+  const int lane = threadIdx.x & 63, tile = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, n = lane & 15;
+  const int64_t item = blockIdx.x, pair = item / slices;
+  const int col = (int)(item - pair * slices) * 16 + n;
+  const int64_t r = pair / a.v_heads;
+  const int h = (int)(pair - r * a.v_heads);
+  const int slot = a.slots[r];
+  const int64_t start = start_of(a.token_starts, (int)r, a.tokens), end = start_of(a.token_starts, (int)r + 1, a.tokens);
+  if (!slot_ok(slot, a.num_slots) || start >= end) return;
+  const int64_t chunks = (end - start + kC - 1) / kC, each = chunks_of_part(chunks, parts.parts);
+  const int count = (int)((chunks + each - 1) / each);
+  const bool carried = !a.cached_lens || a.cached_lens[r] > 0;
+  const int64_t of_state = (int64_t)DK * a.head_v, own = (int64_t)(16 * tile + 4 * g) * a.head_v + col;
+  const float* given = a.state + ((int64_t)slot * a.v_heads + h) * of_state + own;
+  float* first = parts.first + pair * parts.parts * of_state + own;
+  const float* turn = parts.turn + pair * parts.parts * DK * DK + (16 * tile + n) * DK + 4 * g;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) first[q * a.head_v] = carried ? given[q * a.head_v] : 0.0f;
+  for (int p = 1; p < count; ++p) {
+    float4_t s;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s[q] = first[p * of_state + q * a.head_v];
+    if (p > 1) {
+      float4_t row[kTiles];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) row[t] = *reinterpret_cast<const float4_t*>(turn + (int64_t)(p - 1) * DK * DK + 16 * t);
+      __syncthreads();  // the last state is there
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        const float4_t b = state[p & 1][t][lane];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s = __builtin_amdgcn_mfma_f32_16x16x4f32(row[t][q], b[q], s, 0, 0, 0);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) first[p * of_state + q * a.head_v] = s[q];
+    }
+    state[(p + 1) & 1][tile][lane] = s;
+  }
 }
 
 // `launch(first place, places)` for all places of chunks, so many at a time
@@ -809,20 +917,42 @@ hipError_t for_places(const DeltaArgs& a, int64_t workgroups_of_place, F launch)
   return hipSuccess;
 }
 
-template <int DT, int DK, int WAVES, int LOADERS>
-hipError_t launch_chain(const DeltaArgs& a, hipStream_t stream) {
-  using L = Chain<DT, DK, WAVES, LOADERS>;
-  const uint32_t slices = (uint32_t)(a.head_v / L::kCols);
-  const FastDiv by_seq((uint32_t)a.v_heads), by_key_heads((uint32_t)a.k_heads);
-  const int64_t pairs = (int64_t)a.n_seqs * a.v_heads, all = (pairs + 7) / 8 * 8 * slices;
+template <int DT, int DK, int MODE, int WAVES, int LOADERS>
+hipError_t launch_chain(const DeltaArgs& a, const PartArgs& parts, hipStream_t stream) {
+  using L = Chain<DT, DK, MODE, WAVES, LOADERS>;
+  const uint32_t slices = (uint32_t)((a.head_v + (MODE == kEnds ? DK : 0)) / L::kCols);
+  const int of_parts = MODE == kWhole ? 1 : MODE == kEnds ? parts.parts - 1 : parts.parts;
+  const FastDiv by_seq((uint32_t)a.v_heads), by_key_heads((uint32_t)a.k_heads), by_parts((uint32_t)of_parts);
+  const int64_t pairs = (int64_t)a.n_seqs * a.v_heads, all = (pairs + 7) / 8 * 8 * slices * of_parts;
   for (int64_t first = 0; first < all; first += kMostWorkgroups) {
     const uint32_t grid = (uint32_t)std::min<int64_t>(kMostWorkgroups, all - first);
-    gated_delta_chain_kernel<DT, DK, WAVES, LOADERS>
-        <<<grid, L::kThreads, 0, stream>>>(a, by_seq, by_key_heads, slices, (uint32_t)first, (uint32_t)pairs);
+    gated_delta_chain_kernel<DT, DK, MODE, WAVES, LOADERS><<<grid, L::kThreads, 0, stream>>>(a, parts, by_seq, by_key_heads, by_parts, slices,
+                                                                                             (uint32_t)first, (uint32_t)pairs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+constexpr int kLeastParts = 4;
+
+template <int DT, int DK>
+hipError_t launch_parts(const DeltaArgs& a, int count, hipStream_t stream) {
+  PartArgs parts = {count, nullptr, nullptr};
+  const int64_t pairs = (int64_t)a.n_seqs * a.v_heads;
+  parts.first = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
+                                         delta_chunk_places(a.tokens, a.n_seqs) * delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT));
+  parts.turn = parts.first + pairs * count * DK * a.head_v;
+  hipError_t e = launch_chain<DT, DK, kEnds, 4, 0>(a, parts, stream);
+  if (e != hipSuccess) return e;
+  const uint32_t slices = (uint32_t)(a.head_v / 16);
+  gated_delta_join_kernel<DK><<<(uint32_t)(pairs * slices), 4 * DK, 0, stream>>>(a, parts, slices);  // few: a call in parts has few heads
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if constexpr (DT != 0) {
+    if (a.head_v % 128 == 0) return launch_chain<DT, DK, kPart, 8, 0>(a, parts, stream);
+  }
+  return launch_chain<DT, DK, kPart, 4, 0>(a, parts, stream);
 }
 
 template <int DT, int DK>
@@ -837,12 +967,14 @@ hipError_t launch_sized(const DeltaArgs& a, hipStream_t stream) {
     gated_delta_solve_kernel<DT, DK><<<places * blocks, kThreads, 0, stream>>>(a, by_group, by_blocks, first);
   });
   if (e != hipSuccess) return e;
+  const int64_t parts = delta_parts(a.tokens, a.n_seqs, a.v_heads, a.head_v);
+  if (parts >= kLeastParts) return launch_parts<DT, DK>(a, (int)parts, stream);
   const int64_t columns = (int64_t)a.n_seqs * a.v_heads * a.head_v;
-  if (columns <= 32 * device_cu_count()) return launch_chain<DT, DK, 2, 2>(a, stream);
+  if (columns <= 32 * device_cu_count()) return launch_chain<DT, DK, kWhole, 2, 2>(a, {}, stream);
   if constexpr (DT != 0) {
-    if (a.head_v % 128 == 0) return launch_chain<DT, DK, 8, 0>(a, stream);
+    if (a.head_v % 128 == 0) return launch_chain<DT, DK, kWhole, 8, 0>(a, {}, stream);
   }
-  return launch_chain<DT, DK, 4, 0>(a, stream);
+  return launch_chain<DT, DK, kWhole, 4, 0>(a, {}, stream);
 }
 
 template <int DT>

@@ -75,8 +75,23 @@ constexpr int64_t delta_chunk_bytes(int k_heads, int v_heads, int head_k, int dt
   return k_heads * delta_key_bytes(head_k, dtype) + (int64_t)v_heads * kDeltaTieBytes;
 }
 inline int64_t delta_chunk_places(int64_t tokens, int64_t n_seqs) { return tokens / kDeltaChunk + n_seqs; }
-inline int64_t gated_delta_workspace_bytes(int64_t tokens, int64_t n_seqs, int k_heads, int v_heads, int head_k, int dtype) {
-  return delta_chunk_places(tokens, n_seqs) * delta_chunk_bytes(k_heads, v_heads, head_k, dtype);
+
+// Behind the chunks: where heads are few, sequences are taken in parts, and each part of a sequence and head has the state
+// it starts from, and what it does to any.  At most kDeltaPartColumns columns of states in all parts, and at least
+// kDeltaPartChunks chunks to a part but the last.
+constexpr int kDeltaPartColumns = kMaxCus * 128, kDeltaPartChunks = 8, kDeltaMostParts = 32;
+inline int64_t delta_parts(int64_t tokens, int64_t n_seqs, int v_heads, int head_v) {
+  const int64_t by_columns = kDeltaPartColumns / (n_seqs * v_heads * head_v), by_chunks = tokens / (kDeltaChunk * kDeltaPartChunks);
+  const int64_t parts = by_columns < by_chunks ? by_columns : by_chunks;
+  return parts < kDeltaMostParts ? parts : kDeltaMostParts;
+}
+inline int64_t delta_part_bytes(int head_k, int head_v) { return (int64_t)4 * head_k * (head_v + head_k); }
+// enough for any number of sequences up to n_seqs
+inline int64_t gated_delta_workspace_bytes(int64_t tokens, int64_t n_seqs, int k_heads, int v_heads, int head_k, int head_v,
+                                           int dtype) {
+  const int64_t by_columns = kDeltaPartColumns / head_v, by_chunks = tokens / (kDeltaChunk * kDeltaPartChunks) * n_seqs * v_heads;
+  return delta_chunk_places(tokens, n_seqs) * delta_chunk_bytes(k_heads, v_heads, head_k, dtype) +
+         (by_columns < by_chunks ? by_columns : by_chunks) * delta_part_bytes(head_k, head_v);
 }
 
 }  // namespace nvfp4

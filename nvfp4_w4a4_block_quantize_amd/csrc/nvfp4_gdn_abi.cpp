@@ -128,7 +128,7 @@ nvfp4_status nvfp4_gated_delta_workspace(int64_t tokens, int64_t n_seqs, int64_t
   if (!size_ok(tokens) || n_seqs <= 0 || n_seqs >= kMaxDim - 1 || !delta_heads_ok(k_heads, v_heads, head_k, head_v) ||
       tokens * v_heads > kMaxTokenHeads || n_seqs * v_heads > kMaxSeqHeads)
     return NVFP4_ERR_SHAPE;
-  *bytes = gated_delta_workspace_bytes(tokens, n_seqs, (int)k_heads, (int)v_heads, (int)head_k, dtype);
+  *bytes = gated_delta_workspace_bytes(tokens, n_seqs, (int)k_heads, (int)v_heads, (int)head_k, (int)head_v, dtype);
   return NVFP4_OK;
 }
 
@@ -149,7 +149,7 @@ nvfp4_status nvfp4_gated_delta_chunked(int64_t tokens, int64_t k_heads, int64_t 
   const nvfp4_status s = delta_check(d, n);
   if (s != NVFP4_OK) return s;
   set_sizes(d, n);
-  if (workspace_bytes < gated_delta_workspace_bytes(tokens, n_seqs, d.k_heads, d.v_heads, d.head_k, dtype))
+  if (workspace_bytes < gated_delta_workspace_bytes(tokens, n_seqs, d.k_heads, d.v_heads, d.head_k, d.head_v, dtype))
     return NVFP4_ERR_SHAPE;
   if (!device_ok()) return NVFP4_ERR_DEVICE;
   return done(launch_gated_delta_chunked(d, static_cast<hipStream_t>(stream)));

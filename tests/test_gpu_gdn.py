@@ -324,6 +324,22 @@ def test_a_long_sequence_stays_exact(gpu_lib):
     d.check(gpu_lib, [0, 3000])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("heads,lens", [
+    ((1, 2, 128, 128), [2500, 513, 0, 700, 1]), ((1, 1, 64, 64), [4096]), ((2, 2, 64, 192), [2113]), ((1, 3, 128, 64), [600, 1600]),
+    ((1, 1, 128, 256), [2049, 64])])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_chunked_in_parts(gpu_lib, dtype, heads, lens, in_place):
+    """Few heads and long sequences, which are taken in parts that run at once."""
+    rng = np.random.default_rng([len(lens), *heads, 1])
+    log("parts", dtype, heads, lens, in_place)
+    starts = delta_starts(lens)
+    d = Delta(rng, dtype, int(starts[-1]) + 3, len(lens), *heads, decay=0.05)
+    if len(lens) == 5:
+        d.slots[3] = -1
+    d.check(gpu_lib, starts, cached=rng.integers(0, 2, len(lens)) * 5 if in_place else None, in_place=in_place)
+
+
 def test_the_result_is_the_same_in_every_call(gpu_lib):
     rng = np.random.default_rng(11)
     d = Delta(rng, "bf16", 1000, 3, 2, 4, 128, 128)
