@@ -4,7 +4,7 @@
 //   y_t[c] = act(bias[c] + sum_j w[c][j] x_{t-(W-1)+j}[c])
 //
 // Bandwidth kernel: each input read once and each output written once.  A thread
-// owns E neighbouring channels (16 bytes) and walks kRows tokens with the last
+// owns E neighbouring channels (16 bytes) and walks ROWS tokens with the last
 // W - 1 inputs and its weights in registers, so an input is loaded by one thread but
 // for the W - 1 rows before its first token.
 //
@@ -19,18 +19,32 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;
 
 template <int DT, int E, int W>
 struct Taps {
   float w[W][E], bias[E];
   __device__ __forceinline__ void load(const ConvArgs& a, int c) {
+    float flat[E * W];
+    if constexpr (E == 1) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
+      for (int i = 0; i < W; ++i) flat[i] = a.weight[(int64_t)c * W + i];
+      bias[0] = a.bias ? a.bias[c] : 0.0f;
+    } else {
+      Elements<0, E * W> all;
+      all.load(a.weight, (int64_t)c * W);
 #pragma unroll
-      for (int j = 0; j < W; ++j) w[j][e] = a.weight[(int64_t)(c + e) * W + j];
-      bias[e] = a.bias ? a.bias[c + e] : 0.0f;
+      for (int i = 0; i < E * W; ++i) flat[i] = all.get(i);
+      Elements<0, E> b;
+      b.zero();
+      if (a.bias) b.load(a.bias, c);
+#pragma unroll
+      for (int e = 0; e < E; ++e) bias[e] = b.get(e);
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][e] = flat[e * W + j];
   }
   // rows[0] is the oldest
   __device__ __forceinline__ Elements<DT, E> at(const Elements<DT, E> (&rows)[W], int activation) const {
@@ -58,7 +72,7 @@ __device__ __forceinline__ int sequence_at(const int32_t* starts, int n, int64_t
   return low;
 }
 
-template <int DT, int E, int W, int ROWS>
+template <int DT, int E, int W, int ROWS, bool PAST>
 __global__ __launch_bounds__(kThreads) void causal_conv_kernel(ConvArgs a, int64_t first_block) {
   const int c = (blockIdx.y * kThreads + threadIdx.x) * E;
   if (c >= a.channels) return;
@@ -112,18 +126,29 @@ __global__ __launch_bounds__(kThreads) void causal_conv_kernel(ConvArgs a, int64
     }
     const int64_t end = std::min(high, std::max(behind, mine ? std::min(low + W - 1, high) : behind));
     constexpr int kAhead = 8;  // rows under way at a time
-    while (t < end) {
+    for (; t + kAhead <= end; t += kAhead) {
+      Elements<DT, E> next[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) next[i].load(a.x, (t + i) * a.ldx + c);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        rows[W - 1] = next[i];
+        taps.at(rows, a.activation).template store<PAST>(a.out, (t + i) * a.ldo + c);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) rows[j] = rows[j + 1];
+      }
+    }
+    if (t < end) {
       Elements<DT, E> next[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) next[i].load(a.x, std::min(t + i, end - 1) * a.ldx + c);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         rows[W - 1] = next[i];
-        if (t + i < end) taps.at(rows, a.activation).store(a.out, (t + i) * a.ldo + c);
+        if (t + i < end) taps.at(rows, a.activation).template store<PAST>(a.out, (t + i) * a.ldo + c);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) rows[j] = rows[j + 1];
       }
-      t += kAhead;
     }
     t = end;
     if (t >= behind) return;
@@ -149,20 +174,38 @@ __global__ __launch_bounds__(kThreads) void causal_conv_step_kernel(ConvArgs a, 
   for (int j = 0; j < W - 1; ++j) rows[j + 1].store(a.state_out, state + (int64_t)j * a.channels);
 }
 
-template <int DT, int E, int W>
-hipError_t launch_width(const ConvArgs& a, bool step, hipStream_t stream) {
-  constexpr int kRows = 32;
-  const int64_t blocks = step ? a.tokens : (a.tokens + kRows - 1) / kRows;
-  const uint32_t columns = (uint32_t)((a.channels + (int64_t)kThreads * E - 1) / (kThreads * E));
+constexpr int64_t kManyBytes = 64 << 20;  // of outputs: a quarter of the Infinity Cache
+
+// `launch(blocks, columns, first block)`, so many blocks at a time
+template <typename F>
+hipError_t for_blocks(int64_t blocks, uint32_t columns, F launch) {
   const int64_t most = std::max<int64_t>(kMostWorkgroups / columns, 1);
   for (int64_t first = 0; first < blocks; first += most) {
-    const dim3 grid((uint32_t)std::min(most, blocks - first), columns);
-    if (step) causal_conv_step_kernel<DT, E, W><<<grid, kThreads, 0, stream>>>(a, first);
-    else causal_conv_kernel<DT, E, W, kRows><<<grid, kThreads, 0, stream>>>(a, first);
+    launch(dim3((uint32_t)std::min(most, blocks - first), columns), first);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+template <int DT, int E, int W, int ROWS, bool PAST>
+hipError_t launch_rows(const ConvArgs& a, uint32_t columns, hipStream_t stream) {
+  return for_blocks((a.tokens + ROWS - 1) / ROWS, columns, [&](dim3 grid, int64_t first) {
+    causal_conv_kernel<DT, E, W, ROWS, PAST><<<grid, kThreads, 0, stream>>>(a, first);
+  });
+}
+
+template <int DT, int E, int W>
+hipError_t launch_width(const ConvArgs& a, bool step, hipStream_t stream) {
+  const uint32_t columns = (uint32_t)((a.channels + (int64_t)kThreads * E - 1) / (kThreads * E));
+  if (step)
+    return for_blocks(a.tokens, columns, [&](dim3 grid, int64_t first) {
+      causal_conv_step_kernel<DT, E, W><<<grid, kThreads, 0, stream>>>(a, first);
+    });
+  if (E > 1 && a.tokens * a.channels * element_size(DT) >= kManyBytes) return launch_rows<DT, E, W, 32, true>(a, columns, stream);
+  const int64_t waves = a.tokens / 16 * columns;
+  if (waves >= 8 * device_cu_count()) return launch_rows<DT, E, W, 16, false>(a, columns, stream);
+  return launch_rows<DT, E, W, 8, false>(a, columns, stream);
 }
 
 template <int DT, int E>
@@ -179,7 +222,7 @@ hipError_t launch_typed(const ConvArgs& a, bool step, hipStream_t stream) {
   constexpr int kElements = 16 / element_size(DT);
   auto whole = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   if (a.channels % kElements == 0 && a.ldx % kElements == 0 && a.ldo % kElements == 0 && whole(a.x) && whole(a.out) &&
-      whole(a.state) && whole(a.state_out))
+      whole(a.state) && whole(a.state_out) && whole(a.weight) && whole(a.bias))
     return launch_elements<DT, kElements>(a, step, stream);
   return launch_elements<DT, 1>(a, step, stream);
 }

@@ -427,15 +427,15 @@ __device__ __forceinline__ short4_t read_columns(const uint8_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)p);
 }
 
-// WAVES of a workgroup hold columns, LOADERS more move data for them.  A stage is keys, T, gates, values, queries, P: of the
+// WAVES of a workgroup hold 16 NT columns each, LOADERS more move data for them.  A stage is keys, T, gates, values, queries, P: of the
 // ends of parts, all but the last two.
-template <int DT, int DK, int MODE, int WAVES, int LOADERS>
+template <int DT, int DK, int MODE, int NT, int WAVES, int LOADERS>
 struct Chain {
   static constexpr int kParts = DT == 0 ? 2 : 1, kSteps = DK / 32, kTiles = DK / 16;
-  static constexpr int kCols = 16 * WAVES;                    // of a workgroup
+  static constexpr int kCols = 16 * NT * WAVES;               // of a workgroup
   static constexpr int kThreads = 64 * (WAVES + LOADERS);
   static constexpr int kKeys = kParts * 4 * kSteps * kBlock;  // bytes of K; Q follows
-  static constexpr int kRow = 16 * element_size(DT), kValues = kC * kRow;  // a wave's columns of V, then of the outputs
+  static constexpr int kRow = 16 * NT * element_size(DT), kValues = kC * kRow;  // a wave's columns of V, then of the outputs
   static constexpr int kTurnAt = kKeys, kGatesIn = kTurnAt + kPAt, kValuesAt = kGatesIn + 2 * kBlock;
   static constexpr int kQueriesAt = kValuesAt + WAVES * kValues, kInnerAt = kQueriesAt + kKeys;
   static constexpr int kStage = MODE == kEnds ? kQueriesAt : kInnerAt + kPAt;
@@ -473,12 +473,12 @@ __device__ __forceinline__ float of_column(float x) {
   return fmaxf(__uint_as_float(pairs[0]), __uint_as_float(pairs[1]));
 }
 
-template <int DT, int DK, int MODE, int WAVES, int LOADERS>
-__global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves_per_eu(DT == 0 ? 1 : 2))) void gated_delta_chain_kernel(
+template <int DT, int DK, int MODE, int NT, int WAVES, int LOADERS>
+__global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves_per_eu(WAVES + LOADERS > 4 ? 2 : 1))) void gated_delta_chain_kernel(
     DeltaArgs a, PartArgs parts, FastDiv by_seq, FastDiv by_key_heads, FastDiv by_parts, uint32_t slices, uint32_t first,
     uint32_t pairs) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using L = Chain<DT, DK, MODE, WAVES, LOADERS>;
+  using L = Chain<DT, DK, MODE, NT, WAVES, LOADERS>;
   constexpr int kSize = element_size(DT);
   __shared__ __attribute__((aligned(1024))) uint8_t stage[L::kStages * L::kStage];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -605,20 +605,26 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
   if (!LOADERS) issue(0, 0);
   // The state: tile 2 s + t, register q of lane (g, n) is row 32 s + 8 g + 4 t + q, column n, so that two tiles are the
   // eight elements of an operand that meet elements 32 s + 8 g.. of a row of K or Q.
-  float4_t s[L::kTiles];
-  int scaled = kLength;  // the state is s 2^(scaled - 4), values are taken times 2^-scaled
-  const int col = group_column + 16 * wave + n;
+  float4_t s[L::kTiles][NT];
+  int scaled[NT];  // the state is s 2^(scaled - 4), values are taken times 2^-scaled
+  const int col = group_column + 16 * NT * wave + n;
   const int64_t of_slot = ((int64_t)slot * a.v_heads + h) * DK * a.head_v;
   const int64_t of_parts = ((int64_t)r * a.v_heads + h) * parts.parts + part;
-  const float* begin = MODE == kPart ? parts.first + of_parts * DK * a.head_v : a.state + of_slot;
-  const bool carried = MODE == kPart || (part == 0 && (!a.cached_lens || a.cached_lens[r] > 0));
+  {
+    const float* begin = MODE == kPart ? parts.first + of_parts * DK * a.head_v : a.state + of_slot;
+    const bool carried = MODE == kPart || (part == 0 && (!a.cached_lens || a.cached_lens[r] > 0));
 #pragma unroll
-  for (int t = 0; t < L::kTiles; ++t)
+    for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int row = 32 * (t / 2) + 8 * g + 4 * (t & 1) + q;
-      s[t][q] = carried ? begin[(int64_t)row * a.head_v + col] : unit && row == col ? 1.0f : 0.0f;
-    }
+      for (int w = 0; w < NT; ++w) {
+        scaled[w] = kLength;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = 32 * (t / 2) + 8 * g + 4 * (t & 1) + q;
+          s[t][w][q] = carried ? begin[(int64_t)row * a.head_v + col + 16 * w] : unit && row == col + 16 * w ? 1.0f : 0.0f;
+        }
+      }
+  }
   meet();
 
   for (int64_t c = 0; c < chunks; ++c) {
@@ -634,100 +640,96 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
     };
     auto gate = [&](int which, int mt) { return *reinterpret_cast<const float4_t*>(gates + which * kC + 16 * mt + 4 * g); };
 
-    float4_t x[4], beta[4];
+    // Operands are read a step before they are needed: few waves hide little of what LDS takes.
+    constexpr int kOfQ = MODE == kEnds ? 1 : 2;
+    half8_t keys[2][kOfQ][4][L::kParts];
+    auto read_keys = [&](int st) {
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      beta[mt] = gate(kBeta, mt);
-      if (unit) {
-        x[mt] = float4_t{0, 0, 0, 0};
-      } else if constexpr (DT == 0) {
+      for (int of_q = 0; of_q < kOfQ; ++of_q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[mt][i] = *reinterpret_cast<const float*>(mine + (16 * mt + 4 * g + i) * L::kRow + 4 * n);
-      } else {
-        const short4_t e = read_columns(mine + (16 * mt + 4 * g + n / 4) * L::kRow + (n % 4) * 8);
+        for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if constexpr (DT == 1)
-            x[mt][q] = __uint_as_float((uint32_t)(uint16_t)e[q] << 16);
-          else
-            x[mt][q] = (float)__builtin_bit_cast(_Float16, (short)e[q]);
+          for (int p = 0; p < L::kParts; ++p) keys[st & 1][of_q][mt][p] = key(of_q, p, mt, st);
+    };
+    float4_t beta[4];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) beta[mt] = gate(kBeta, mt);
+    float4_t x[4][NT];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int w = 0; w < NT; ++w) {
+        if (unit) {
+          x[mt][w] = float4_t{0, 0, 0, 0};
+        } else if constexpr (DT == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[mt][w][i] = *reinterpret_cast<const float*>(mine + (16 * mt + 4 * g + i) * L::kRow + 64 * w + 4 * n);
+        } else {
+          const short4_t e = read_columns(mine + (16 * mt + 4 * g + n / 4) * L::kRow + 32 * w + (n % 4) * 8);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (DT == 1)
+              x[mt][w][q] = __uint_as_float((uint32_t)(uint16_t)e[q] << 16);
+            else
+              x[mt][w][q] = (float)__builtin_bit_cast(_Float16, (short)e[q]);
+          }
         }
       }
-    }
-    // K S takes kSteps steps, Q S as many.  Operands are read kAhead steps before they are needed: with one wave a SIMD
-    // nothing else hides what LDS takes, with two the registers are fewer.
-    constexpr int kAhead = LOADERS && DK > 64 ? 3 : 2;
-    half8_t keys[kAhead][4][L::kParts];
-    auto read_step = [&](int i) {
-      if (i >= (MODE == kEnds ? 1 : 2) * L::kSteps) return;
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-        for (int p = 0; p < L::kParts; ++p) keys[i % kAhead][mt][p] = key(i >= L::kSteps, p, mt, i % L::kSteps);
-    };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) read_step(i);
+    read_keys(0);
     if (!LOADERS) move(c, now);
     __builtin_amdgcn_sched_barrier(0);
 
-    // The state's parts, while those come, and its largest element.
-    Parts of_s[L::kSteps];
-    float top = 0.0f, high = 0.0f;
-#pragma unroll
-    for (int st = 0; st < L::kSteps; ++st) {
-      of_s[st] = cut(s[2 * st], s[2 * st + 1]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(s[2 * st][i]), fabsf(s[2 * st + 1][i])));
-    }
-    __builtin_amdgcn_sched_barrier(0);
     // What a column's tokens bring, beta v, and its power of two, with M the largest of that and of the state's elements: M
     // goes to 2^7..2^8 when it has left 2^5..2^9.  The state's length is at most sqrt(128) M and grows by M a token, so that
     // X and V' stay below 75 M < 2^16; |S| 2^4 is below 2^13; a part's last bit lies 2^31 below M.
+    {
+      float top[NT], high[NT];
+      bool off = c == 0;
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      x[mt] *= beta[mt];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) high = fmaxf(high, fabsf(x[mt][i]));
-    }
-    const float both = of_column(fmaxf(top * (1.0f / kLong), __builtin_amdgcn_ldexpf(high, -scaled)));
-    if (__any(c == 0 || both > 512.0f || (both < 32.0f && both > 0.0f && scaled > -150))) {
-      top = of_column(top);
-      high = of_column(high);
-      constexpr int kNone = -100000;
-      const int of_state = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) + scaled - kLength : kNone;
-      const int of_values = high > 0.0f ? __builtin_amdgcn_frexp_expf(high) : kNone;
-      const int most = std::max(of_state, of_values), by_now = most - scaled;
-      if (most != kNone && (by_now > 9 || by_now < 6)) {
-        const int next = std::max(most - 8, -150), by = scaled - next;
-        scaled = next;
+      for (int w = 0; w < NT; ++w) {
+        top[w] = high[w] = 0.0f;
 #pragma unroll
         for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[t][i] = __builtin_amdgcn_ldexpf(s[t][i], by);
-      }
+          for (int i = 0; i < 4; ++i) top[w] = fmaxf(top[w], fabsf(s[t][w][i]));
 #pragma unroll
-      for (int st = 0; st < L::kSteps; ++st) of_s[st] = cut(s[2 * st], s[2 * st + 1]);
+        for (int mt = 0; mt < 4; ++mt) {
+          x[mt][w] *= beta[mt];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) high[w] = fmaxf(high[w], fabsf(x[mt][w][i]));
+        }
+        const float both = of_column(fmaxf(top[w] * (1.0f / kLong), __builtin_amdgcn_ldexpf(high[w], -scaled[w])));
+        off = off || both > 512.0f || (both < 32.0f && both > 0.0f && scaled[w] > -150);
+      }
+      if (__any(off)) {
+#pragma unroll
+        for (int w = 0; w < NT; ++w) {
+          const float of_s = of_column(top[w]), of_x = of_column(high[w]);
+          constexpr int kNone = -100000;
+          const int of_state = of_s > 0.0f ? __builtin_amdgcn_frexp_expf(of_s) + scaled[w] - kLength : kNone;
+          const int of_values = of_x > 0.0f ? __builtin_amdgcn_frexp_expf(of_x) : kNone;
+          const int most = std::max(of_state, of_values), by_now = most - scaled[w];
+          if (most != kNone && (by_now > 9 || by_now < 6)) {
+            const int next = std::max(most - 8, -150), by = scaled[w] - next;
+            scaled[w] = next;
+#pragma unroll
+            for (int t = 0; t < L::kTiles; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[t][w][i] = __builtin_amdgcn_ldexpf(s[t][w][i], by);
+          }
+        }
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
 
-    // K S
+    // K S and Q S
     const float4_t none = {0, 0, 0, 0};
-    float4_t y[4] = {none, none, none, none}, o[4] = {none, none, none, none};
+    float4_t y[4][NT], o[4][NT];
 #pragma unroll
-    for (int st = 0; st < L::kSteps; ++st) {
+    for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-      for (int i = 0; i < 1 + L::kParts; ++i)
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-          y[mt] = mfma(keys[st % kAhead][mt][i == 2 ? L::kParts - 1 : 0], i == 1 ? of_s[st].lo : of_s[st].hi, y[mt]);
-      read_step(st + kAhead);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-
-    // Q S, which nothing waits for, among the arithmetic of X
-    float4_t gain[4], gain_q[4];
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt) gain[mt] = gate(kGainK, mt);
+      for (int w = 0; w < NT; ++w) y[mt][w] = o[mt][w] = none;
     half8_t turn[kTies][2];
     auto read_ties = [&](half8_t (&to)[kTies][2], int at, int st) {
 #pragma unroll
@@ -735,30 +737,59 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
 #pragma unroll
         for (int p = 0; p < 2; ++p) to[tie(mt, st)][p] = tied(at, mt, st, p);
     };
-    Parts b[2], d[2];
+    float4_t gain[4];
+    Parts b[2][NT], d[NT];
+#pragma unroll
+    for (int w = 0; w < NT; ++w) b[0][w] = cut(s[0][w], s[1][w]);
 #pragma unroll
     for (int st = 0; st < L::kSteps; ++st) {
+      if (st + 1 < L::kSteps) {
+        read_keys(st + 1);
+      } else {
 #pragma unroll
-      for (int i = 0; i < (MODE == kEnds ? 0 : 1 + L::kParts); ++i)
+        for (int mt = 0; mt < 4; ++mt) gain[mt] = gate(kGainK, mt);
+        read_ties(turn, L::kTurnAt, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 1 + L::kParts; ++i)
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
-          o[mt] = mfma(keys[(st + L::kSteps) % kAhead][mt][i == 2 ? L::kParts - 1 : 0], i == 1 ? of_s[st].lo : of_s[st].hi, o[mt]);
-      read_step(st + L::kSteps + kAhead);
-      if (st == L::kSteps / 2 - 1) read_ties(turn, L::kTurnAt, 0);
-      if (st == L::kSteps - 1) read_ties(turn, L::kTurnAt, 1);
-      // a share of X in each step
 #pragma unroll
-      for (int mt = 4 * st / L::kSteps; mt < 4 * (st + 1) / L::kSteps; ++mt)
+          for (int w = 0; w < NT; ++w) {
+            const int part = i == 2 ? L::kParts - 1 : 0;
+            const half8_t of_s = i == 1 ? b[st & 1][w].lo : b[st & 1][w].hi;
+            y[mt][w] = mfma(keys[st & 1][0][mt][part], of_s, y[mt][w]);
+            if (MODE != kEnds) o[mt][w] = mfma(keys[st & 1][kOfQ - 1][mt][part], of_s, o[mt][w]);
+          }
+      if (st + 1 < L::kSteps) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[mt][i] = __builtin_fmaf(-gain[mt][i], y[mt][i], __builtin_amdgcn_ldexpf(x[mt][i], -scaled));
-      if (st >= L::kSteps / 2 && st + 1 < L::kSteps + (L::kSteps == 2)) b[0] = cut(x[0], x[1]);
-      __builtin_amdgcn_sched_barrier(0);
+        for (int w = 0; w < NT; ++w) b[(st + 1) & 1][w] = cut(s[2 * st + 2][w], s[2 * st + 3][w]);
+      }
     }
-    b[1] = cut(x[2], x[3]);
+    __builtin_amdgcn_sched_barrier(0);
 
-    // V' = T X; the state's decay among it
+    // X
     const float whole = gates[kDecay * kC];
-    float4_t until[4], z[4] = {none, none, none, none};
+    float4_t gain_q[4], until[4];
+    read_ties(turn, L::kTurnAt, 1);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      until[mt] = gate(kUntil, mt);
+      if (MODE != kEnds) gain_q[mt] = gate(kGainQ, mt);
+    }
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+#pragma unroll
+      for (int w = 0; w < NT; ++w) {
+#pragma unroll
+        for (int mt = 2 * st; mt < 2 * st + 2; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[mt][w][i] = __builtin_fmaf(-gain[mt][i], y[mt][w][i], __builtin_amdgcn_ldexpf(x[mt][w][i], -scaled[w]));
+        b[st][w] = cut(x[2 * st][w], x[2 * st + 1][w]);
+      }
+    }
     half8_t turned[L::kTiles][L::kParts], inner[kTies][2];  // rows of K^T; P
     auto read_turned = [&](int st) {
 #pragma unroll
@@ -773,34 +804,47 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
           turned[t][p] = __builtin_bit_cast(half8_t, __builtin_shufflevector(e[0], e[1], 0, 1, 2, 3, 4, 5, 6, 7));
         }
     };
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      until[mt] = gate(kUntil, mt);
-      if (MODE != kEnds) gain_q[mt] = gate(kGainQ, mt);
-    }
     read_turned(0);
     __builtin_amdgcn_sched_barrier(0);
+
+    // V' = T X; the state's decay among it
+    float4_t z[4][NT];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int w = 0; w < NT; ++w) z[mt][w] = none;
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
       for (int i = 0; i < 3; ++i)
 #pragma unroll
-        for (int mt = 2 * half; mt < 2 * half + 2; ++mt) z[mt] = mfma(turn[tie(mt, 0)][i == 2], i == 1 ? b[0].lo : b[0].hi, z[mt]);
+        for (int mt = 2 * half; mt < 2 * half + 2; ++mt)
+#pragma unroll
+          for (int w = 0; w < NT; ++w)
+            z[mt][w] = mfma(turn[tie(mt, 0)][i == 2], i == 1 ? b[0][w].lo : b[0][w].hi, z[mt][w]);
 #pragma unroll
     for (int i = 0; i < 3; ++i)
 #pragma unroll
-      for (int mt = 2; mt < 4; ++mt) z[mt] = mfma(turn[tie(mt, 1)][i == 2], i == 1 ? b[1].lo : b[1].hi, z[mt]);
+      for (int mt = 2; mt < 4; ++mt)
 #pragma unroll
-    for (int t = 0; t < L::kTiles; ++t) s[t] *= whole;
+        for (int w = 0; w < NT; ++w) z[mt][w] = mfma(turn[tie(mt, 1)][i == 2], i == 1 ? b[1][w].lo : b[1][w].hi, z[mt][w]);
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-      if (MODE != kEnds) o[mt] *= gain_q[mt];
+    for (int w = 0; w < NT; ++w) {
+#pragma unroll
+      for (int t = 0; t < L::kTiles; ++t) s[t][w] *= whole;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+        if (MODE != kEnds) o[mt][w] *= gain_q[mt];
+    }
 
     // K^T V' onto the decayed state, P V' onto Q S
     auto cut_values = [&](int st) {
-      const float4_t v0 = z[2 * st] * kDown, v1 = z[2 * st + 1] * kDown;
-      d[st] = cut(v0 * until[2 * st], v1 * until[2 * st + 1]);
-      if (MODE != kEnds) b[st] = cut(v0, v1);
+#pragma unroll
+      for (int w = 0; w < NT; ++w) {
+        const float4_t v0 = z[2 * st][w] * kDown, v1 = z[2 * st + 1][w] * kDown;
+        d[w] = cut(v0 * until[2 * st], v1 * until[2 * st + 1]);
+        if (MODE != kEnds) b[st][w] = cut(v0, v1);
+      }
     };
     cut_values(0);
     if (MODE != kEnds) read_ties(inner, L::kInnerAt, 0);
@@ -810,34 +854,41 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
 #pragma unroll
       for (int i = 0; i < 1 + L::kParts; ++i)
 #pragma unroll
-        for (int t = 0; t < L::kTiles; ++t) s[t] = mfma(turned[t][i == 2 ? L::kParts - 1 : 0], i == 1 ? d[st].lo : d[st].hi, s[t]);
-      if (st == 0) cut_values(1);
+        for (int t = 0; t < L::kTiles; ++t)
+#pragma unroll
+          for (int w = 0; w < NT; ++w) s[t][w] = mfma(turned[t][i == 2 ? L::kParts - 1 : 0], i == 1 ? d[w].lo : d[w].hi, s[t][w]);
+      if (st == 0) {
+        cut_values(1);
+        read_turned(1);
+      }
 #pragma unroll
       for (int i = 0; i < (MODE == kEnds ? 0 : 3); ++i)
 #pragma unroll
         for (int mt = 2 * st; mt < 4; ++mt)
-          o[mt] = mfma(inner[tie(mt, st)][i == 2], i == 1 ? b[st].lo : b[st].hi, o[mt]);
-      if (st == 0) {
-        read_turned(1);
-        if (MODE != kEnds) read_ties(inner, L::kInnerAt, 1);
-      }
+#pragma unroll
+          for (int w = 0; w < NT; ++w)
+            o[mt][w] = mfma(inner[tie(mt, st)][i == 2], i == 1 ? b[st][w].lo : b[st][w].hi, o[mt][w]);
+      if (MODE != kEnds && st == 0) read_ties(inner, L::kInnerAt, 1);
     }
 
     // outputs, to where this wave's values were
-    const float back = __builtin_amdgcn_ldexpf(a.scale, scaled - 14);
 #pragma unroll
-    for (int mt = 0; mt < (MODE == kEnds ? 0 : 4); ++mt) {
-      uint8_t* row = mine + (16 * mt + 4 * g) * L::kRow + n * kSize;
+    for (int w = 0; w < (MODE == kEnds ? 0 : NT); ++w) {
+      const float back = __builtin_amdgcn_ldexpf(a.scale, scaled[w] - 14);
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const float z0 = o[mt][i] * back, z1 = o[mt][i + 1] * back;
-        if constexpr (DT == 0) {
-          *reinterpret_cast<float*>(row + i * L::kRow) = z0;
-          *reinterpret_cast<float*>(row + (i + 1) * L::kRow) = z1;
-        } else {
-          const uint32_t both = pack2<DT>(z0, z1);
-          *reinterpret_cast<uint16_t*>(row + i * L::kRow) = (uint16_t)both;
-          *reinterpret_cast<uint16_t*>(row + (i + 1) * L::kRow) = (uint16_t)(both >> 16);
+      for (int mt = 0; mt < 4; ++mt) {
+        uint8_t* row = mine + (16 * mt + 4 * g) * L::kRow + (16 * w + n) * kSize;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float z0 = o[mt][w][i] * back, z1 = o[mt][w][i + 1] * back;
+          if constexpr (DT == 0) {
+            *reinterpret_cast<float*>(row + i * L::kRow) = z0;
+            *reinterpret_cast<float*>(row + (i + 1) * L::kRow) = z1;
+          } else {
+            const uint32_t both = pack2<DT>(z0, z1);
+            *reinterpret_cast<uint16_t*>(row + i * L::kRow) = (uint16_t)both;
+            *reinterpret_cast<uint16_t*>(row + (i + 1) * L::kRow) = (uint16_t)(both >> 16);
+          }
         }
       }
     }
@@ -853,8 +904,11 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
 #pragma unroll
   for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      to[(int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * pitch + col] = __builtin_amdgcn_ldexpf(s[t][q], scaled - kLength);
+    for (int w = 0; w < NT; ++w)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        to[(int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * pitch + col + 16 * w] =
+            __builtin_amdgcn_ldexpf(s[t][w][q], scaled[w] - kLength);
 #endif
 }
 
@@ -917,16 +971,16 @@ hipError_t for_places(const DeltaArgs& a, int64_t workgroups_of_place, F launch)
   return hipSuccess;
 }
 
-template <int DT, int DK, int MODE, int WAVES, int LOADERS>
+template <int DT, int DK, int MODE, int NT, int WAVES, int LOADERS>
 hipError_t launch_chain(const DeltaArgs& a, const PartArgs& parts, hipStream_t stream) {
-  using L = Chain<DT, DK, MODE, WAVES, LOADERS>;
+  using L = Chain<DT, DK, MODE, NT, WAVES, LOADERS>;
   const uint32_t slices = (uint32_t)((a.head_v + (MODE == kEnds ? DK : 0)) / L::kCols);
   const int of_parts = MODE == kWhole ? 1 : MODE == kEnds ? parts.parts - 1 : parts.parts;
   const FastDiv by_seq((uint32_t)a.v_heads), by_key_heads((uint32_t)a.k_heads), by_parts((uint32_t)of_parts);
   const int64_t pairs = (int64_t)a.n_seqs * a.v_heads, all = (pairs + 7) / 8 * 8 * slices * of_parts;
   for (int64_t first = 0; first < all; first += kMostWorkgroups) {
     const uint32_t grid = (uint32_t)std::min<int64_t>(kMostWorkgroups, all - first);
-    gated_delta_chain_kernel<DT, DK, MODE, WAVES, LOADERS><<<grid, L::kThreads, 0, stream>>>(a, parts, by_seq, by_key_heads, by_parts, slices,
+    gated_delta_chain_kernel<DT, DK, MODE, NT, WAVES, LOADERS><<<grid, L::kThreads, 0, stream>>>(a, parts, by_seq, by_key_heads, by_parts, slices,
                                                                                              (uint32_t)first, (uint32_t)pairs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -943,16 +997,16 @@ hipError_t launch_parts(const DeltaArgs& a, int count, hipStream_t stream) {
   parts.first = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
                                          delta_chunk_places(a.tokens, a.n_seqs) * delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT));
   parts.turn = parts.first + pairs * count * DK * a.head_v;
-  hipError_t e = launch_chain<DT, DK, kEnds, 4, 0>(a, parts, stream);
+  hipError_t e = launch_chain<DT, DK, kEnds, 1, 4, 0>(a, parts, stream);
   if (e != hipSuccess) return e;
   const uint32_t slices = (uint32_t)(a.head_v / 16);
   gated_delta_join_kernel<DK><<<(uint32_t)(pairs * slices), 4 * DK, 0, stream>>>(a, parts, slices);  // few: a call in parts has few heads
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   if constexpr (DT != 0) {
-    if (a.head_v % 128 == 0) return launch_chain<DT, DK, kPart, 8, 0>(a, parts, stream);
+    if (a.head_v % 128 == 0) return launch_chain<DT, DK, kPart, 1, 8, 0>(a, parts, stream);
   }
-  return launch_chain<DT, DK, kPart, 4, 0>(a, parts, stream);
+  return launch_chain<DT, DK, kPart, 1, 4, 0>(a, parts, stream);
 }
 
 template <int DT, int DK>
@@ -970,11 +1024,11 @@ hipError_t launch_sized(const DeltaArgs& a, hipStream_t stream) {
   const int64_t parts = delta_parts(a.tokens, a.n_seqs, a.v_heads, a.head_v);
   if (parts >= kLeastParts) return launch_parts<DT, DK>(a, (int)parts, stream);
   const int64_t columns = (int64_t)a.n_seqs * a.v_heads * a.head_v;
-  if (columns <= 32 * device_cu_count()) return launch_chain<DT, DK, kWhole, 2, 2>(a, {}, stream);
+  if (columns <= 32 * device_cu_count()) return launch_chain<DT, DK, kWhole, 1, 2, 2>(a, {}, stream);
   if constexpr (DT != 0) {
-    if (a.head_v % 128 == 0) return launch_chain<DT, DK, kWhole, 8, 0>(a, {}, stream);
+    if (a.head_v % 128 == 0) return launch_chain<DT, DK, kWhole, 1, 8, 0>(a, {}, stream);
   }
-  return launch_chain<DT, DK, kWhole, 4, 0>(a, {}, stream);
+  return launch_chain<DT, DK, kWhole, 1, 4, 0>(a, {}, stream);
 }
 
 template <int DT>

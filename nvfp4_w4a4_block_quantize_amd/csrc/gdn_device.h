@@ -42,6 +42,8 @@ struct Elements {
       }
     }
   }
+  // PAST: past the caches, where vectors are stored
+  template <bool PAST = false>
   __device__ __forceinline__ void store(void* base, int64_t elem) const {
     char* p = static_cast<char*>(base) + elem * element_size(DT);
     if constexpr (E == 1) {
@@ -51,8 +53,13 @@ struct Elements {
         *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
     } else {
 #pragma unroll
-      for (int i = 0; i < kWords / 4; ++i)
-        reinterpret_cast<u32x4_t*>(p)[i] = u32x4_t{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+      for (int i = 0; i < kWords / 4; ++i) {
+        const u32x4_t v = {w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+        if constexpr (PAST)
+          __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p) + i);
+        else
+          reinterpret_cast<u32x4_t*>(p)[i] = v;
+      }
     }
   }
   __device__ __forceinline__ float get(int i) const {

@@ -15,11 +15,27 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMany = 8;
+
+// `v` of the lane `by` places on, around each row of 16
+template <int BY>
+__device__ __forceinline__ float turned(float v) {
+  constexpr int kRowRor = 0x120;
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kRowRor + BY, 0xF, 0xF, false));
+}
 
 template <int LANES>
 __device__ __forceinline__ float sum_of(float v, float* lds) {
-#pragma unroll
-  for (int m = 1; m < std::min(LANES, 64); m *= 2) v += __shfl_xor(v, m);
+  v += turned<8>(v);
+  v += turned<4>(v);
+  v += turned<2>(v);
+  v += turned<1>(v);
+  if constexpr (LANES > 16) {
+    const auto rows = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(rows[0]) + __uint_as_float(rows[1]);
+    const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
+  }
   if constexpr (LANES > 64) {
     __syncthreads();  // what the last sum left in lds is read
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
@@ -29,84 +45,112 @@ __device__ __forceinline__ float sum_of(float v, float* lds) {
   return v;
 }
 
-// a group of up to LANES * N * E elements, E of them at a time
-template <int DT, int E, int LANES, int N>
-__global__ __launch_bounds__(kThreads) void group_norm_kernel(NormArgs a, int64_t first, int64_t items, float over_dim) {
+// Groups of up to LANES * N * E elements, E of them at a time, ITEMS groups one behind the other a thread.
+template <int DT, int E, int LANES, int N, int ITEMS>
+__global__ __launch_bounds__(kThreads) void group_norm_kernel(NormArgs a, FastDiv by_groups, uint32_t items, float over_dim) {
   __shared__ float lds[4];
   constexpr int kPer = kThreads / LANES;
-  const int64_t item = first + (int64_t)blockIdx.x * kPer + threadIdx.x / LANES;
-  const bool live = item < items;  // the others keep step with their wave
-  const int64_t token = live ? item / a.groups : 0;
-  const int group = live ? (int)(item - token * a.groups) : 0;
   const int lane = threadIdx.x % LANES;
-  const int64_t xo = token * a.x.token + group * a.x.head, zo = token * a.gate.token + group * a.gate.head;
-  Elements<DT, E> x[N], z[N];
   const bool gated = a.gate.p != nullptr;
+  Elements<DT, E> x[ITEMS][N], z[ITEMS][N];
+  int64_t token[ITEMS];
+  int group[ITEMS];
+  bool live[ITEMS];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int at = (i * LANES + lane) * E;
-    if (at < a.group_dim) {
-      x[i].load(a.x.p, xo + at);
-      if (gated) z[i].load(a.gate.p, zo + at);
-    } else {
-      x[i].zero();
+  for (int j = 0; j < ITEMS; ++j) {
+    const uint32_t item = (blockIdx.x * ITEMS + j) * kPer + threadIdx.x / LANES;
+    live[j] = item < items;  // the others keep step with their wave
+    const uint32_t t = by_groups.div(live[j] ? item : 0);
+    token[j] = t;
+    group[j] = live[j] ? (int)(item - t * by_groups.d) : 0;
+    const int64_t xo = token[j] * a.x.token + group[j] * a.x.head, zo = token[j] * a.gate.token + group[j] * a.gate.head;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = (i * LANES + lane) * E;
+      if (at < a.group_dim) {
+        x[j][i].load(a.x.p, xo + at);
+        if (gated) z[j][i].load(a.gate.p, zo + at);
+      } else {
+        x[j][i].zero();
+      }
     }
   }
-  float mean = 0.0f;
-  if (a.centred) {
+#pragma unroll
+  for (int j = 0; j < ITEMS; ++j) {
+    float mean = 0.0f;
+    if (a.centred) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += x[j][i].get(e);
+      mean = sum_of<LANES>(s, lds) * over_dim;
+    }
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < N; ++i) {
+      const bool inside = (i * LANES + lane) * E < a.group_dim;
 #pragma unroll
-      for (int e = 0; e < E; ++e) s += x[i].get(e);
-    mean = sum_of<LANES>(s, lds) * over_dim;
-  }
-  float s = 0.0f;
+      for (int e = 0; e < E; ++e) {
+        const float y = inside ? x[j][i].get(e) - mean : 0.0f;
+        s = __builtin_fmaf(y, y, s);
+      }
+    }
+    const float over = 1.0f / sqrtf(__builtin_fmaf(sum_of<LANES>(s, lds), over_dim, a.eps));
+    if (!live[j]) continue;
+    const float* weight = a.weight + (int64_t)group[j] * a.weight_group;
+    const float* bias = a.bias ? a.bias + (int64_t)group[j] * a.weight_group : nullptr;
+    const int64_t oo = token[j] * a.out.token + group[j] * a.out.head;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const bool inside = (i * LANES + lane) * E < a.group_dim;
+    for (int i = 0; i < N; ++i) {
+      const int at = (i * LANES + lane) * E;
+      if (at >= a.group_dim) continue;
+      float y[E];
+      Elements<0, E> w, b;
+      w.load(weight, at);
+      if (bias) b.load(bias, at);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float y = inside ? x[i].get(e) - mean : 0.0f;
-      s = __builtin_fmaf(y, y, s);
+      for (int e = 0; e < E; ++e) {
+        y[e] = (x[j][i].get(e) - mean) * over * w.get(e);
+        if (bias) y[e] += b.get(e);
+        const float g = gated ? z[j][i].get(e) : y[e];
+        const float act = a.activation ? g * sigmoid<DT == 0>(g) : g;
+        y[e] = gated ? y[e] * act : act;
+      }
+      Elements<DT, E> out;
+      out.set(y);
+      out.store(a.out.p, oo + at);
     }
   }
-  const float var = __builtin_fmaf(sum_of<LANES>(s, lds), over_dim, a.eps);
-  const float over = 1.0f / sqrtf(var);
-  if (!live) return;
-  const float* weight = a.weight + (int64_t)group * a.weight_group;
-  const float* bias = a.bias ? a.bias + (int64_t)group * a.weight_group : nullptr;
-  const int64_t oo = token * a.out.token + group * a.out.head;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int at = (i * LANES + lane) * E;
-    if (at >= a.group_dim) continue;
-    float y[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      y[e] = (x[i].get(e) - mean) * over * weight[at + e];
-      if (bias) y[e] += bias[at + e];
-      const float g = gated ? z[i].get(e) : y[e];
-      const float act = a.activation ? g * sigmoid<DT == 0>(g) : g;
-      y[e] = gated ? y[e] * act : act;
-    }
-    Elements<DT, E> out;
-    out.set(y);
-    out.store(a.out.p, oo + at);
+}
+
+template <int DT, int E, int LANES, int N, int ITEMS>
+hipError_t launch_items(NormArgs a, hipStream_t stream) {
+  constexpr int kPer = kThreads / LANES * ITEMS;
+  const FastDiv by_groups((uint32_t)a.groups);
+  // a launch takes whole tokens, of fewer than 2^31 groups in all
+  const int64_t most = std::max<int64_t>(kMostWorkgroups * kPer / a.groups, 1);
+  for (int64_t left = a.tokens;;) {
+    const int64_t tokens = std::min(left, most);
+    const uint32_t items = (uint32_t)(tokens * a.groups);
+    group_norm_kernel<DT, E, LANES, N, ITEMS>
+        <<<(items + kPer - 1) / kPer, kThreads, 0, stream>>>(a, by_groups, items, 1.0f / (float)a.group_dim);
+    const hipError_t e = hipGetLastError();
+    left -= tokens;
+    if (e != hipSuccess || left == 0) return e;
+    auto behind = [&](int64_t stride) { return tokens * stride * element_size(DT); };
+    a.x.p = static_cast<const char*>(a.x.p) + behind(a.x.token);
+    if (a.gate.p) a.gate.p = static_cast<const char*>(a.gate.p) + behind(a.gate.token);
+    a.out.p = static_cast<char*>(a.out.p) + behind(a.out.token);
   }
 }
 
 template <int DT, int E, int LANES, int N>
 hipError_t launch_lanes(const NormArgs& a, hipStream_t stream) {
-  const int64_t items = a.tokens * a.groups, per = kThreads / LANES, most = kMostWorkgroups * per;
-  for (int64_t first = 0; first < items; first += most) {
-    const int64_t left = std::min(items - first, most);
-    group_norm_kernel<DT, E, LANES, N>
-        <<<(uint32_t)((left + per - 1) / per), kThreads, 0, stream>>>(a, first, items, 1.0f / (float)a.group_dim);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  constexpr int kItems = 2;
+  if (N * kItems <= 16 && a.tokens * a.groups >= (int64_t)kMany * kItems * (kThreads / LANES) * device_cu_count())
+    return launch_items<DT, E, LANES, N, N * kItems <= 16 ? kItems : 1>(a, stream);
+  return launch_items<DT, E, LANES, N, 1>(a, stream);
 }
 
 template <int DT>
@@ -117,6 +161,7 @@ hipError_t launch_typed(const NormArgs& a, hipStream_t stream) {
   };
   const int n = a.group_dim;
   if (n % kE == 0 && whole(a.x.p, a.x.token, a.x.head) && whole(a.out.p, a.out.token, a.out.head) &&
+      whole(a.weight, 0, a.weight_group) && whole(a.bias, 0, 0) &&
       (!a.gate.p || whole(a.gate.p, a.gate.token, a.gate.head))) {
     if (n <= 16 * kE) return launch_lanes<DT, kE, 16, 1>(a, stream);
     if (n <= 32 * kE) return launch_lanes<DT, kE, 16, 2>(a, stream);
@@ -124,6 +169,7 @@ hipError_t launch_typed(const NormArgs& a, hipStream_t stream) {
     return launch_lanes<DT, kE, 256, 8192 / (256 * kE)>(a, stream);
   }
   if (n <= 64) return launch_lanes<DT, 1, 16, 4>(a, stream);
+  if (n <= 128) return launch_lanes<DT, 1, 16, 8>(a, stream);
   if (n <= 512) return launch_lanes<DT, 1, 64, 8>(a, stream);
   return launch_lanes<DT, 1, 256, 32>(a, stream);
 }
