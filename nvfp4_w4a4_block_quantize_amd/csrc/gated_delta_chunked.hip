@@ -236,14 +236,30 @@ __device__ __forceinline__ void store_ties(uint8_t* to, int mt, const float4_t (
 
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
 
+// Sequences in the order of their lengths, the longest first, so that the last workgroups of the chain have the least to do
+// (12 prompts up to 4096 tokens, 48 heads: LONGEST us).
+constexpr int kMostOrdered = 512;
+__device__ __forceinline__ void find_order(const DeltaArgs& a, int32_t* order) {
+  __shared__ int32_t lens[kMostOrdered];
+  const int r = threadIdx.x;
+  if (r < a.n_seqs) lens[r] = (int32_t)(start_of(a.token_starts, r + 1, a.tokens) - start_of(a.token_starts, r, a.tokens));
+  __syncthreads();
+  if (r >= a.n_seqs) return;
+  const int32_t own = lens[r];
+  int before = 0;
+  for (int i = 0; i < a.n_seqs; ++i) before += lens[i] > own || (lens[i] == own && i < r);
+  order[before] = r;
+}
+
 // Keys and queries of a chunk and key head: eight waves take 16 rows each.
 template <int DT, int DK>
-__global__ __launch_bounds__(512) void gated_delta_keys_kernel(DeltaArgs a, FastDiv by_heads, int64_t first_place) {
+__global__ __launch_bounds__(512) void gated_delta_keys_kernel(DeltaArgs a, FastDiv by_heads, int64_t first_place, int32_t* order) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, n = lane & 15;
   const uint32_t of_launch = by_heads.div(blockIdx.x);
   const int kh = (int)(blockIdx.x - of_launch * by_heads.d);
   const int64_t place = first_place + of_launch;
+  if (order && place == 0 && kh == 0) find_order(a, order);
   Place at;
   if (!find_place(a, place, at)) return;
   const int rows = (int)std::min<int64_t>(kC, at.end - at.begin);
@@ -475,7 +491,7 @@ __device__ __forceinline__ float of_column(float x) {
 
 template <int DT, int DK, int MODE, int NT, int WAVES, int LOADERS>
 __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves_per_eu(WAVES + LOADERS > 4 ? 2 : 1))) void gated_delta_chain_kernel(
-    DeltaArgs a, PartArgs parts, FastDiv by_seq, FastDiv by_key_heads, FastDiv by_parts, uint32_t slices, uint32_t first,
+    DeltaArgs a, PartArgs parts, const int32_t* order, FastDiv by_seq, FastDiv by_key_heads, FastDiv by_parts, uint32_t slices, uint32_t first,
     uint32_t pairs) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using L = Chain<DT, DK, MODE, NT, WAVES, LOADERS>;
@@ -490,7 +506,8 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
   const uint32_t of_part = eight / slices, octet = MODE == kWhole ? of_part : by_parts.div(of_part);
   const uint32_t pair = octet * 8 + (at & 7);
   if (pair >= pairs) return;
-  const uint32_t r = by_seq.div(pair), in_seq = pair - r * by_seq.d;
+  const uint32_t turn_of_seq = by_seq.div(pair), in_seq = pair - turn_of_seq * by_seq.d;
+  const uint32_t r = order ? (uint32_t)order[turn_of_seq] : turn_of_seq;
   const uint32_t of_group = by_key_heads.div(in_seq);
   const int kh = (int)(in_seq - of_group * by_key_heads.d), h = kh * (a.v_heads / a.k_heads) + (int)of_group;
   const int slot = a.slots[r];
@@ -921,9 +938,11 @@ __global__ __launch_bounds__(4 * DK) void gated_delta_join_kernel(DeltaArgs a, P
   __shared__ float4_t state[2][kTiles][64];
   const int lane = threadIdx.x & 63, tile = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, n = lane & 15;
-  const int64_t item = blockIdx.x, pair = item / slices;
-  const int col = (int)(item - pair * slices) * 16 + n;
-  const int64_t r = pair / a.v_heads;
+  // columns of one sequence and head lie on one XCD, 8 apart, whose L2 then fetches `turn` once for them
+  const uint32_t eight = blockIdx.x >> 3, octet = eight / slices;
+  const int64_t pair = octet * 8 + (blockIdx.x & 7), r = pair / a.v_heads;
+  if (r >= a.n_seqs) return;
+  const int col = (int)(eight - octet * slices) * 16 + n;
   const int h = (int)(pair - r * a.v_heads);
   const int slot = a.slots[r];
   const int64_t start = start_of(a.token_starts, (int)r, a.tokens), end = start_of(a.token_starts, (int)r + 1, a.tokens);
@@ -937,25 +956,43 @@ __global__ __launch_bounds__(4 * DK) void gated_delta_join_kernel(DeltaArgs a, P
   const float* turn = parts.turn + pair * parts.parts * DK * DK + (16 * tile + n) * DK + 4 * g;
 #pragma unroll
   for (int q = 0; q < 4; ++q) first[q * a.head_v] = carried ? given[q * a.head_v] : 0.0f;
-  for (int p = 1; p < count; ++p) {
-    float4_t s;
+  // ends and rows are asked for a part ahead
+  float4_t row[2][kTiles], end_of[2];
+  auto ask = [&](int p, int at) {
+    if (p >= count) return;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) s[q] = first[p * of_state + q * a.head_v];
-    if (p > 1) {
-      float4_t row[kTiles];
+    for (int t = 0; t < kTiles; ++t) row[at][t] = *reinterpret_cast<const float4_t*>(turn + (int64_t)(p - 1) * DK * DK + 16 * t);
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) row[t] = *reinterpret_cast<const float4_t*>(turn + (int64_t)(p - 1) * DK * DK + 16 * t);
-      __syncthreads();  // the last state is there
+    for (int q = 0; q < 4; ++q) end_of[at][q] = first[p * of_state + q * a.head_v];
+  };
+  if (count < 2) return;
+  float4_t one;
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        const float4_t b = state[p & 1][t][lane];
+  for (int q = 0; q < 4; ++q) one[q] = first[of_state + q * a.head_v];
+  ask(2, 0);
+  state[0][tile][lane] = one;
+  auto join = [&](int p, int at) {
+    ask(p + 1, at ^ 1);
+    // The last state is there.  Only LDS is waited for: what is asked for stays under way.
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    float4_t b[kTiles];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s = __builtin_amdgcn_mfma_f32_16x16x4f32(row[t][q], b[q], s, 0, 0, 0);
-      }
+    for (int t = 0; t < kTiles; ++t) b[t] = state[at][t][lane];
+    float4_t s = end_of[at];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) first[p * of_state + q * a.head_v] = s[q];
-    }
-    state[(p + 1) & 1][tile][lane] = s;
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s = __builtin_amdgcn_mfma_f32_16x16x4f32(row[at][t][q], b[t][q], s, 0, 0, 0);
+    state[at ^ 1][tile][lane] = s;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) first[p * of_state + q * a.head_v] = s[q];
+  };
+  for (int p = 2; p < count; p += 2) {
+    join(p, 0);
+    if (p + 1 < count) join(p + 1, 1);
   }
 }
 
@@ -972,7 +1009,7 @@ hipError_t for_places(const DeltaArgs& a, int64_t workgroups_of_place, F launch)
 }
 
 template <int DT, int DK, int MODE, int NT, int WAVES, int LOADERS>
-hipError_t launch_chain(const DeltaArgs& a, const PartArgs& parts, hipStream_t stream) {
+hipError_t launch_chain(const DeltaArgs& a, const PartArgs& parts, const int32_t* order, hipStream_t stream) {
   using L = Chain<DT, DK, MODE, NT, WAVES, LOADERS>;
   const uint32_t slices = (uint32_t)((a.head_v + (MODE == kEnds ? DK : 0)) / L::kCols);
   const int of_parts = MODE == kWhole ? 1 : MODE == kEnds ? parts.parts - 1 : parts.parts;
@@ -980,7 +1017,7 @@ hipError_t launch_chain(const DeltaArgs& a, const PartArgs& parts, hipStream_t s
   const int64_t pairs = (int64_t)a.n_seqs * a.v_heads, all = (pairs + 7) / 8 * 8 * slices * of_parts;
   for (int64_t first = 0; first < all; first += kMostWorkgroups) {
     const uint32_t grid = (uint32_t)std::min<int64_t>(kMostWorkgroups, all - first);
-    gated_delta_chain_kernel<DT, DK, MODE, NT, WAVES, LOADERS><<<grid, L::kThreads, 0, stream>>>(a, parts, by_seq, by_key_heads, by_parts, slices,
+    gated_delta_chain_kernel<DT, DK, MODE, NT, WAVES, LOADERS><<<grid, L::kThreads, 0, stream>>>(a, parts, order, by_seq, by_key_heads, by_parts, slices,
                                                                                              (uint32_t)first, (uint32_t)pairs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -988,7 +1025,7 @@ hipError_t launch_chain(const DeltaArgs& a, const PartArgs& parts, hipStream_t s
   return hipSuccess;
 }
 
-constexpr int kLeastParts = 4;
+constexpr int kLeastParts = 8;
 
 template <int DT, int DK>
 hipError_t launch_parts(const DeltaArgs& a, int count, hipStream_t stream) {
@@ -997,38 +1034,44 @@ hipError_t launch_parts(const DeltaArgs& a, int count, hipStream_t stream) {
   parts.first = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
                                          delta_chunk_places(a.tokens, a.n_seqs) * delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT));
   parts.turn = parts.first + pairs * count * DK * a.head_v;
-  hipError_t e = launch_chain<DT, DK, kEnds, 1, 4, 0>(a, parts, stream);
+  hipError_t e = launch_chain<DT, DK, kEnds, 1, 4, 0>(a, parts, nullptr, stream);
   if (e != hipSuccess) return e;
   const uint32_t slices = (uint32_t)(a.head_v / 16);
-  gated_delta_join_kernel<DK><<<(uint32_t)(pairs * slices), 4 * DK, 0, stream>>>(a, parts, slices);  // few: a call in parts has few heads
+  gated_delta_join_kernel<DK><<<(uint32_t)((pairs + 7) / 8 * 8 * slices), 4 * DK, 0, stream>>>(a, parts, slices);  // few: a call in parts has few heads
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   if constexpr (DT != 0) {
-    if (a.head_v % 128 == 0) return launch_chain<DT, DK, kPart, 1, 8, 0>(a, parts, stream);
+    if (a.head_v % 128 == 0) return launch_chain<DT, DK, kPart, 1, 8, 0>(a, parts, nullptr, stream);
   }
-  return launch_chain<DT, DK, kPart, 1, 4, 0>(a, parts, stream);
+  return launch_chain<DT, DK, kPart, 1, 4, 0>(a, parts, nullptr, stream);
 }
 
 template <int DT, int DK>
 hipError_t launch_sized(const DeltaArgs& a, hipStream_t stream) {
   const uint32_t k_heads = (uint32_t)a.k_heads, blocks = (uint32_t)((a.v_heads + kWaves - 1) / kWaves);
   const FastDiv by_heads(k_heads), by_group((uint32_t)(a.v_heads / a.k_heads)), by_blocks(blocks);
+  // behind the chunks; parts, which calls of few sequences have, would lie there too
+  int32_t* order = nullptr;
+  const int64_t parts = delta_parts(a.tokens, a.n_seqs, a.v_heads, a.head_v);
+  const bool in_parts = parts >= kLeastParts;
+  if (!in_parts && a.n_seqs > 1 && a.n_seqs <= kMostOrdered)
+    order = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(a.workspace) +
+                                       delta_chunk_places(a.tokens, a.n_seqs) * delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT));
   hipError_t e = for_places(a, k_heads, [&](int64_t first, uint32_t places) {
-    gated_delta_keys_kernel<DT, DK><<<places * k_heads, 512, 0, stream>>>(a, by_heads, first);
+    gated_delta_keys_kernel<DT, DK><<<places * k_heads, 512, 0, stream>>>(a, by_heads, first, order);
   });
   if (e != hipSuccess) return e;
   e = for_places(a, blocks, [&](int64_t first, uint32_t places) {
     gated_delta_solve_kernel<DT, DK><<<places * blocks, kThreads, 0, stream>>>(a, by_group, by_blocks, first);
   });
   if (e != hipSuccess) return e;
-  const int64_t parts = delta_parts(a.tokens, a.n_seqs, a.v_heads, a.head_v);
-  if (parts >= kLeastParts) return launch_parts<DT, DK>(a, (int)parts, stream);
-  const int64_t columns = (int64_t)a.n_seqs * a.v_heads * a.head_v;
-  if (columns <= 32 * device_cu_count()) return launch_chain<DT, DK, kWhole, 1, 2, 2>(a, {}, stream);
+  if (in_parts) return launch_parts<DT, DK>(a, (int)parts, stream);
+  const int64_t columns = (int64_t)a.n_seqs * a.v_heads * a.head_v, cus = device_cu_count();
+  if (columns <= 32 * cus) return launch_chain<DT, DK, kWhole, 1, 2, 2>(a, {}, order, stream);
   if constexpr (DT != 0) {
-    if (a.head_v % 128 == 0) return launch_chain<DT, DK, kWhole, 1, 8, 0>(a, {}, stream);
+    if (a.head_v % 128 == 0 && columns > 64 * cus) return launch_chain<DT, DK, kWhole, 1, 8, 0>(a, {}, order, stream);
   }
-  return launch_chain<DT, DK, kWhole, 1, 4, 0>(a, {}, stream);
+  return launch_chain<DT, DK, kWhole, 1, 4, 0>(a, {}, order, stream);
 }
 
 template <int DT>

@@ -90,8 +90,9 @@ inline int64_t delta_part_bytes(int head_k, int head_v) { return (int64_t)4 * he
 inline int64_t gated_delta_workspace_bytes(int64_t tokens, int64_t n_seqs, int k_heads, int v_heads, int head_k, int head_v,
                                            int dtype) {
   const int64_t by_columns = kDeltaPartColumns / head_v, by_chunks = tokens / (kDeltaChunk * kDeltaPartChunks) * n_seqs * v_heads;
+  const int64_t order = 4 * (n_seqs < 512 ? (n_seqs + 3) / 4 * 4 : 512);  // of sequences by their lengths, in calls without parts
   return delta_chunk_places(tokens, n_seqs) * delta_chunk_bytes(k_heads, v_heads, head_k, dtype) +
-         (by_columns < by_chunks ? by_columns : by_chunks) * delta_part_bytes(head_k, head_v);
+         (by_columns < by_chunks ? by_columns : by_chunks) * delta_part_bytes(head_k, head_v) + order;
 }
 
 }  // namespace nvfp4
