@@ -443,20 +443,22 @@ __device__ __forceinline__ short4_t read_columns(const uint8_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)p);
 }
 
-// WAVES of a workgroup hold 16 NT columns each, LOADERS more move data for them.  A stage is keys, T, gates, values, queries, P: of the
+// WAVES of a workgroup hold 16 columns each, LOADERS more move data for them.  A stage is keys, T, gates, values, queries, P: of the
 // ends of parts, all but the last two.
-template <int DT, int DK, int MODE, int NT, int WAVES, int LOADERS>
+template <int DT, int DK, int MODE, int WAVES, int LOADERS>
 struct Chain {
   static constexpr int kParts = DT == 0 ? 2 : 1, kSteps = DK / 32, kTiles = DK / 16;
-  static constexpr int kCols = 16 * NT * WAVES;               // of a workgroup
+  static constexpr int kCols = 16 * WAVES;                    // of a workgroup
   static constexpr int kThreads = 64 * (WAVES + LOADERS);
   static constexpr int kKeys = kParts * 4 * kSteps * kBlock;  // bytes of K; Q follows
-  static constexpr int kRow = 16 * NT * element_size(DT), kValues = kC * kRow;  // a wave's columns of V, then of the outputs
+  static constexpr int kRow = kCols * element_size(DT);       // of V, then of the outputs
   static constexpr int kTurnAt = kKeys, kGatesIn = kTurnAt + kPAt, kValuesAt = kGatesIn + 2 * kBlock;
-  static constexpr int kQueriesAt = kValuesAt + WAVES * kValues, kInnerAt = kQueriesAt + kKeys;
+  static constexpr int kQueriesAt = kValuesAt + kC * kRow, kInnerAt = kQueriesAt + kKeys;
   static constexpr int kStage = MODE == kEnds ? kQueriesAt : kInnerAt + kPAt;
   static constexpr int kStages = 2 * kStage <= (160 << 10) ? 2 : 1;
   static_assert(kStages * kStage <= (160 << 10), "the stages fit LDS");
+  // Where byte `x` of a row of V lies in it: rows of 128 bytes or more would meet in the same banks.
+  static __device__ __forceinline__ int turned(int row, int x) { return kRow >= 128 ? x ^ (((row ^ (row >> 2)) & 3) << 5) : x; }
 };
 
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -489,12 +491,12 @@ __device__ __forceinline__ float of_column(float x) {
   return fmaxf(__uint_as_float(pairs[0]), __uint_as_float(pairs[1]));
 }
 
-template <int DT, int DK, int MODE, int NT, int WAVES, int LOADERS>
+template <int DT, int DK, int MODE, int WAVES, int LOADERS>
 __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves_per_eu(WAVES + LOADERS > 4 ? 2 : 1))) void gated_delta_chain_kernel(
     DeltaArgs a, PartArgs parts, const int32_t* order, FastDiv by_seq, FastDiv by_key_heads, FastDiv by_parts, uint32_t slices, uint32_t first,
     uint32_t pairs) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using L = Chain<DT, DK, MODE, NT, WAVES, LOADERS>;
+  using L = Chain<DT, DK, MODE, WAVES, LOADERS>;
   constexpr int kSize = element_size(DT);
   __shared__ __attribute__((aligned(1024))) uint8_t stage[L::kStages * L::kStage];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -532,59 +534,58 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
   const char* values = static_cast<const char*>(a.v.p) + (h * a.v.head + group_column) * kSize;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)stage;
 
-  // Moving data is `of` waves' work, this one's share is `share`: the loaders' where there are any, else each wave's, and
-  // then its columns are its own, so that it may fill them again as soon as it has read them.
+  // Moving data is kOf waves' work, this one's share is `share`: the loaders' where there are any, else each wave's.  A
+  // wave's rows of values are its own here: it fills them again as soon as it has read the outputs in them.
   constexpr int kOf = LOADERS ? LOADERS : WAVES;
   const int share = LOADERS ? wave - WAVES : wave;
-  constexpr int kLanes = L::kRow / 16, kRows = 64 / kLanes, kMoves = kC / kRows;  // of a row, rows of a move
-  // a chunk on its way into a stage: values, turns of 4 blocks of keys, T, queries and P, and the gates
-  auto issue = [&](int64_t c, int to) {
+  constexpr int kLanes = L::kRow / 16, kRows = 64 / kLanes, kMoves = kC / kOf / kRows;  // of a row, rows of a move
+  auto moved_row = [&](int i) { return share * (kC / kOf) + i * kRows + lane / kLanes; };
+  // A chunk on its way into a stage: values,
+  auto issue_values = [&](int64_t c, int to) {
+    if (unit) return;
+#pragma unroll
+    for (int i = 0; i < kMoves; ++i) {
+      const int row = moved_row(i);
+      const int64_t token = std::min(start + c * kC + row, end - 1);
+      to_lds(lds0 + to * L::kStage + L::kValuesAt + (share * (kC / kOf) + i * kRows) * L::kRow,
+             values + token * a.v.token * kSize + L::turned(row, lane % kLanes * 16));
+    }
+  };
+  // and turns of 4 blocks of keys, T, queries and P, kOf of them at a time; the gates go with the first
+  constexpr int kKeyTurns = L::kKeys / (4 * kBlock), kTieTurns = kPAt / (4 * kBlock);
+  constexpr int kAll = (MODE == kEnds ? 1 : 2) * (kKeyTurns + kTieTurns), kTurns = (kAll + kOf - 1) / kOf;
+  auto issue_turn = [&](int64_t c, int to, int i) {
     const uint32_t lds = lds0 + to * L::kStage;
     const uint8_t* base = from + c * chunk_bytes;
-    if (!unit) {
+    if (i == 0 && share == kOf - 1) to_lds2(lds + L::kGatesIn, base + ties_at + kGatesAt, lane * 16);
+    int turn = i * kOf + share;
+    if (turn >= kAll) return;
+    const bool second = turn >= kKeyTurns + kTieTurns;  // queries and P
+    if (second) turn -= kKeyTurns + kTieTurns;
+    const bool tie = turn >= kKeyTurns;
+    const int64_t in = (tie ? ties_at + (second ? kPAt : 0) - L::kKeys : keys_at + (second ? L::kKeys : 0)) + turn * 4 * kBlock;
+    to_lds4(lds + (second ? L::kQueriesAt : 0) + turn * 4 * kBlock, base + in, lane * 16);
+  };
+  auto issue = [&](int64_t c, int to) {
+    issue_values(c, to);
 #pragma unroll
-      for (int w = 0; w < WAVES / kOf; ++w) {
-        const int of = share + w * kOf;
-#pragma unroll
-        for (int i = 0; i < kMoves; ++i) {
-          const int64_t token = std::min(start + c * kC + i * kRows + lane / kLanes, end - 1);
-          to_lds(lds + L::kValuesAt + of * L::kValues + i * kBlock,
-                 values + token * a.v.token * kSize + of * L::kRow + lane % kLanes * 16);
-        }
-      }
-    }
-    constexpr int kKeyTurns = L::kKeys / (4 * kBlock), kTieTurns = kPAt / (4 * kBlock);
-    constexpr int kAll = (MODE == kEnds ? 1 : 2) * (kKeyTurns + kTieTurns);
-#pragma unroll
-    for (int i = 0; i < (kAll + kOf - 1) / kOf; ++i) {
-      int turn = i * kOf + share;
-      if (turn >= kAll) break;
-      const bool second = turn >= kKeyTurns + kTieTurns;  // queries and P
-      if (second) turn -= kKeyTurns + kTieTurns;
-      const bool tie = turn >= kKeyTurns;
-      const int64_t in = (tie ? ties_at + (second ? kPAt : 0) - L::kKeys : keys_at + (second ? L::kKeys : 0)) + turn * 4 * kBlock;
-      to_lds4(lds + (second ? L::kQueriesAt : 0) + turn * 4 * kBlock, base + in, lane * 16);
-    }
-    if (share == kOf - 1) to_lds2(lds + L::kGatesIn, base + ties_at + kGatesAt, lane * 16);
+    for (int i = 0; i < kTurns; ++i) issue_turn(c, to, i);
   };
   // outputs of a chunk from its stage
   auto put_out = [&](int64_t c, int from_stage) {
     if (MODE == kEnds) return;
-    const int64_t token = start + c * kC + lane / kLanes;
-    char* to = static_cast<char*>(a.out.p) + (token * a.out.token + h * a.out.head + group_column) * kSize + lane % kLanes * 16;
-    u32x4_t held[WAVES / kOf][kMoves];
+    const uint8_t* outs = stage + from_stage * L::kStage + L::kValuesAt + share * (kC / kOf) * L::kRow;
+    char* to = static_cast<char*>(a.out.p) + (h * a.out.head + group_column) * kSize;
+    u32x4_t held[kMoves];
 #pragma unroll
-    for (int w = 0; w < WAVES / kOf; ++w)
+    for (int i = 0; i < kMoves; ++i) held[i] = *reinterpret_cast<const u32x4_t*>(outs + i * kBlock + lane * 16);
 #pragma unroll
-      for (int i = 0; i < kMoves; ++i)
-        held[w][i] = *reinterpret_cast<const u32x4_t*>(stage + from_stage * L::kStage + L::kValuesAt + (share + w * kOf) * L::kValues +
-                                                       i * kBlock + lane * 16);
-#pragma unroll
-    for (int w = 0; w < WAVES / kOf; ++w)
-#pragma unroll
-      for (int i = 0; i < kMoves; ++i)
-        if (token + i * kRows < end)
-          *reinterpret_cast<u32x4_t*>(to + i * kRows * a.out.token * kSize + (share + w * kOf) * L::kRow) = held[w][i];
+    for (int i = 0; i < kMoves; ++i) {
+      const int row = moved_row(i);
+      const int64_t token = start + c * kC + row;
+      if (token < end)
+        *reinterpret_cast<u32x4_t*>(to + token * a.out.token * kSize + L::turned(row, lane % kLanes * 16)) = held[i];
+    }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read, before it is filled again
   };
   auto meet = [&] {  // everyone's loads are there and LDS accesses done
@@ -596,7 +597,9 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
   auto move = [&](int64_t c, int now) {
     if (L::kStages == 1) return;
     if (c > 0) put_out(c - 1, now ^ 1);
-    if (c + 1 < chunks) issue(c + 1, now ^ 1);
+    if (c + 1 >= chunks) return;
+    if (LOADERS) issue(c + 1, now ^ 1);
+    else issue_values(c + 1, now ^ 1);
   };
   // with one stage: between the chunks, which all wait for
   auto change = [&](int64_t c) {
@@ -622,9 +625,9 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
   if (!LOADERS) issue(0, 0);
   // The state: tile 2 s + t, register q of lane (g, n) is row 32 s + 8 g + 4 t + q, column n, so that two tiles are the
   // eight elements of an operand that meet elements 32 s + 8 g.. of a row of K or Q.
-  float4_t s[L::kTiles][NT];
-  int scaled[NT];  // the state is s 2^(scaled - 4), values are taken times 2^-scaled
-  const int col = group_column + 16 * NT * wave + n;
+  float4_t s[L::kTiles];
+  int scaled = kLength;  // the state is s 2^(scaled - 4), values are taken times 2^-scaled
+  const int col = group_column + 16 * wave + n;
   const int64_t of_slot = ((int64_t)slot * a.v_heads + h) * DK * a.head_v;
   const int64_t of_parts = ((int64_t)r * a.v_heads + h) * parts.parts + part;
   {
@@ -633,13 +636,9 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
 #pragma unroll
     for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-      for (int w = 0; w < NT; ++w) {
-        scaled[w] = kLength;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int row = 32 * (t / 2) + 8 * g + 4 * (t & 1) + q;
-          s[t][w][q] = carried ? begin[(int64_t)row * a.head_v + col + 16 * w] : unit && row == col + 16 * w ? 1.0f : 0.0f;
-        }
+      for (int q = 0; q < 4; ++q) {
+        const int row = 32 * (t / 2) + 8 * g + 4 * (t & 1) + q;
+        s[t][q] = carried ? begin[(int64_t)row * a.head_v + col] : unit && row == col ? 1.0f : 0.0f;
       }
   }
   meet();
@@ -648,7 +647,11 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
     const int now = L::kStages == 2 ? (int)(c & 1) : 0;
     uint8_t* here = stage + now * L::kStage;
     const float* gates = reinterpret_cast<const float*>(here + L::kGatesIn);
-    uint8_t* mine = here + L::kValuesAt + wave * L::kValues;
+    uint8_t* rows = here + L::kValuesAt;  // of values, then of outputs
+    // byte x of this wave's columns in row 16 mt + 4 g + i
+    auto place = [&](int mt, int i, int x) {
+      return rows + (4 * g + i) * L::kRow + L::turned(4 * g + i, 16 * wave * kSize + x) + 16 * mt * L::kRow;
+    };
     auto key = [&](int of_q, int part, int mt, int st) {
       return *reinterpret_cast<const half8_t*>(here + (of_q ? L::kQueriesAt : 0) + ((part * 4 + mt) * L::kSteps + st) * kBlock + lane * 16);
     };
@@ -671,25 +674,24 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
     float4_t beta[4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) beta[mt] = gate(kBeta, mt);
-    float4_t x[4][NT];
+    float4_t x[4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int w = 0; w < NT; ++w) {
+      {
         if (unit) {
-          x[mt][w] = float4_t{0, 0, 0, 0};
+          x[mt] = float4_t{0, 0, 0, 0};
         } else if constexpr (DT == 0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            x[mt][w][i] = *reinterpret_cast<const float*>(mine + (16 * mt + 4 * g + i) * L::kRow + 64 * w + 4 * n);
+            x[mt][i] = *reinterpret_cast<const float*>(place(mt, i, 4 * n));
         } else {
-          const short4_t e = read_columns(mine + (16 * mt + 4 * g + n / 4) * L::kRow + 32 * w + (n % 4) * 8);
+          const short4_t e = read_columns(place(mt, n / 4, (n % 4) * 8));
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             if constexpr (DT == 1)
-              x[mt][w][q] = __uint_as_float((uint32_t)(uint16_t)e[q] << 16);
+              x[mt][q] = __uint_as_float((uint32_t)(uint16_t)e[q] << 16);
             else
-              x[mt][w][q] = (float)__builtin_bit_cast(_Float16, (short)e[q]);
+              x[mt][q] = (float)__builtin_bit_cast(_Float16, (short)e[q]);
           }
         }
       }
@@ -701,39 +703,37 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
     // goes to 2^7..2^8 when it has left 2^5..2^9.  The state's length is at most sqrt(128) M and grows by M a token, so that
     // X and V' stay below 75 M < 2^16; |S| 2^4 is below 2^13; a part's last bit lies 2^31 below M.
     {
-      float top[NT], high[NT];
+      float top, high;
       bool off = c == 0;
-#pragma unroll
-      for (int w = 0; w < NT; ++w) {
-        top[w] = high[w] = 0.0f;
+      {
+        top = high = 0.0f;
 #pragma unroll
         for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top[w] = fmaxf(top[w], fabsf(s[t][w][i]));
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(s[t][i]));
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-          x[mt][w] *= beta[mt];
+          x[mt] *= beta[mt];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) high[w] = fmaxf(high[w], fabsf(x[mt][w][i]));
+          for (int i = 0; i < 4; ++i) high = fmaxf(high, fabsf(x[mt][i]));
         }
-        const float both = of_column(fmaxf(top[w] * (1.0f / kLong), __builtin_amdgcn_ldexpf(high[w], -scaled[w])));
-        off = off || both > 512.0f || (both < 32.0f && both > 0.0f && scaled[w] > -150);
+        const float both = of_column(fmaxf(top * (1.0f / kLong), __builtin_amdgcn_ldexpf(high, -scaled)));
+        off = off || both > 512.0f || (both < 32.0f && both > 0.0f && scaled > -150);
       }
       if (__any(off)) {
-#pragma unroll
-        for (int w = 0; w < NT; ++w) {
-          const float of_s = of_column(top[w]), of_x = of_column(high[w]);
+        {
+          const float of_s = of_column(top), of_x = of_column(high);
           constexpr int kNone = -100000;
-          const int of_state = of_s > 0.0f ? __builtin_amdgcn_frexp_expf(of_s) + scaled[w] - kLength : kNone;
+          const int of_state = of_s > 0.0f ? __builtin_amdgcn_frexp_expf(of_s) + scaled - kLength : kNone;
           const int of_values = of_x > 0.0f ? __builtin_amdgcn_frexp_expf(of_x) : kNone;
-          const int most = std::max(of_state, of_values), by_now = most - scaled[w];
+          const int most = std::max(of_state, of_values), by_now = most - scaled;
           if (most != kNone && (by_now > 9 || by_now < 6)) {
-            const int next = std::max(most - 8, -150), by = scaled[w] - next;
-            scaled[w] = next;
+            const int next = std::max(most - 8, -150), by = scaled - next;
+            scaled = next;
 #pragma unroll
             for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) s[t][w][i] = __builtin_amdgcn_ldexpf(s[t][w][i], by);
+              for (int i = 0; i < 4; ++i) s[t][i] = __builtin_amdgcn_ldexpf(s[t][i], by);
           }
         }
       }
@@ -742,11 +742,10 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
 
     // K S and Q S
     const float4_t none = {0, 0, 0, 0};
-    float4_t y[4][NT], o[4][NT];
+    float4_t y[4], o[4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int w = 0; w < NT; ++w) y[mt][w] = o[mt][w] = none;
+      y[mt] = o[mt] = none;
     half8_t turn[kTies][2];
     auto read_ties = [&](half8_t (&to)[kTies][2], int at, int st) {
 #pragma unroll
@@ -755,14 +754,12 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
         for (int p = 0; p < 2; ++p) to[tie(mt, st)][p] = tied(at, mt, st, p);
     };
     float4_t gain[4];
-    Parts b[2][NT], d[NT];
-#pragma unroll
-    for (int w = 0; w < NT; ++w) b[0][w] = cut(s[0][w], s[1][w]);
+    Parts b[2], d;
+    b[0] = cut(s[0], s[1]);
 #pragma unroll
     for (int st = 0; st < L::kSteps; ++st) {
-      if (st + 1 < L::kSteps) {
-        read_keys(st + 1);
-      } else {
+      if (st + 1 < L::kSteps) read_keys(st + 1);
+      if (st + 1 == L::kSteps) {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) gain[mt] = gate(kGainK, mt);
         read_ties(turn, L::kTurnAt, 0);
@@ -772,16 +769,18 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
       for (int i = 0; i < 1 + L::kParts; ++i)
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int w = 0; w < NT; ++w) {
+          {
             const int part = i == 2 ? L::kParts - 1 : 0;
-            const half8_t of_s = i == 1 ? b[st & 1][w].lo : b[st & 1][w].hi;
-            y[mt][w] = mfma(keys[st & 1][0][mt][part], of_s, y[mt][w]);
-            if (MODE != kEnds) o[mt][w] = mfma(keys[st & 1][kOfQ - 1][mt][part], of_s, o[mt][w]);
+            const half8_t of_s = i == 1 ? b[st & 1].lo : b[st & 1].hi;
+            y[mt] = mfma(keys[st & 1][0][mt][part], of_s, y[mt]);
+            if (MODE != kEnds) o[mt] = mfma(keys[st & 1][kOfQ - 1][mt][part], of_s, o[mt]);
           }
-      if (st + 1 < L::kSteps) {
+      if (st + 1 < L::kSteps) b[(st + 1) & 1] = cut(s[2 * st + 2], s[2 * st + 3]);
+      // The next chunk's loads in between: LDS takes some 30 bytes a cycle from memory, and a wave that has more to issue
+      // than the queue holds waits (all of them at once, at the chunk's begin: NEXTLOADS).
+      if (!LOADERS && L::kStages == 2 && c + 1 < chunks) {
 #pragma unroll
-        for (int w = 0; w < NT; ++w) b[(st + 1) & 1][w] = cut(s[2 * st + 2][w], s[2 * st + 3][w]);
+        for (int i = st; i < kTurns; i += L::kSteps) issue_turn(c + 1, now ^ 1, i);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -797,14 +796,13 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
     }
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
-#pragma unroll
-      for (int w = 0; w < NT; ++w) {
+      {
 #pragma unroll
         for (int mt = 2 * st; mt < 2 * st + 2; ++mt)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            x[mt][w][i] = __builtin_fmaf(-gain[mt][i], y[mt][w][i], __builtin_amdgcn_ldexpf(x[mt][w][i], -scaled[w]));
-        b[st][w] = cut(x[2 * st][w], x[2 * st + 1][w]);
+            x[mt][i] = __builtin_fmaf(-gain[mt][i], y[mt][i], __builtin_amdgcn_ldexpf(x[mt][i], -scaled));
+        b[st] = cut(x[2 * st], x[2 * st + 1]);
       }
     }
     half8_t turned[L::kTiles][L::kParts], inner[kTies][2];  // rows of K^T; P
@@ -825,42 +823,36 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
     __builtin_amdgcn_sched_barrier(0);
 
     // V' = T X; the state's decay among it
-    float4_t z[4][NT];
+    float4_t z[4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int w = 0; w < NT; ++w) z[mt][w] = none;
+      z[mt] = none;
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
       for (int i = 0; i < 3; ++i)
 #pragma unroll
         for (int mt = 2 * half; mt < 2 * half + 2; ++mt)
-#pragma unroll
-          for (int w = 0; w < NT; ++w)
-            z[mt][w] = mfma(turn[tie(mt, 0)][i == 2], i == 1 ? b[0][w].lo : b[0][w].hi, z[mt][w]);
+            z[mt] = mfma(turn[tie(mt, 0)][i == 2], i == 1 ? b[0].lo : b[0].hi, z[mt]);
 #pragma unroll
     for (int i = 0; i < 3; ++i)
 #pragma unroll
       for (int mt = 2; mt < 4; ++mt)
+        z[mt] = mfma(turn[tie(mt, 1)][i == 2], i == 1 ? b[1].lo : b[1].hi, z[mt]);
+    {
 #pragma unroll
-        for (int w = 0; w < NT; ++w) z[mt][w] = mfma(turn[tie(mt, 1)][i == 2], i == 1 ? b[1][w].lo : b[1][w].hi, z[mt][w]);
-#pragma unroll
-    for (int w = 0; w < NT; ++w) {
-#pragma unroll
-      for (int t = 0; t < L::kTiles; ++t) s[t][w] *= whole;
+      for (int t = 0; t < L::kTiles; ++t) s[t] *= whole;
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
-        if (MODE != kEnds) o[mt][w] *= gain_q[mt];
+        if (MODE != kEnds) o[mt] *= gain_q[mt];
     }
 
     // K^T V' onto the decayed state, P V' onto Q S
     auto cut_values = [&](int st) {
-#pragma unroll
-      for (int w = 0; w < NT; ++w) {
-        const float4_t v0 = z[2 * st][w] * kDown, v1 = z[2 * st + 1][w] * kDown;
-        d[w] = cut(v0 * until[2 * st], v1 * until[2 * st + 1]);
-        if (MODE != kEnds) b[st][w] = cut(v0, v1);
+      {
+        const float4_t v0 = z[2 * st] * kDown, v1 = z[2 * st + 1] * kDown;
+        d = cut(v0 * until[2 * st], v1 * until[2 * st + 1]);
+        if (MODE != kEnds) b[st] = cut(v0, v1);
       }
     };
     cut_values(0);
@@ -872,8 +864,7 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
       for (int i = 0; i < 1 + L::kParts; ++i)
 #pragma unroll
         for (int t = 0; t < L::kTiles; ++t)
-#pragma unroll
-          for (int w = 0; w < NT; ++w) s[t][w] = mfma(turned[t][i == 2 ? L::kParts - 1 : 0], i == 1 ? d[w].lo : d[w].hi, s[t][w]);
+          s[t] = mfma(turned[t][i == 2 ? L::kParts - 1 : 0], i == 1 ? d.lo : d.hi, s[t]);
       if (st == 0) {
         cut_values(1);
         read_turned(1);
@@ -882,29 +873,25 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
       for (int i = 0; i < (MODE == kEnds ? 0 : 3); ++i)
 #pragma unroll
         for (int mt = 2 * st; mt < 4; ++mt)
-#pragma unroll
-          for (int w = 0; w < NT; ++w)
-            o[mt][w] = mfma(inner[tie(mt, st)][i == 2], i == 1 ? b[st][w].lo : b[st][w].hi, o[mt][w]);
+            o[mt] = mfma(inner[tie(mt, st)][i == 2], i == 1 ? b[st].lo : b[st].hi, o[mt]);
       if (MODE != kEnds && st == 0) read_ties(inner, L::kInnerAt, 1);
     }
 
     // outputs, to where this wave's values were
-#pragma unroll
-    for (int w = 0; w < (MODE == kEnds ? 0 : NT); ++w) {
-      const float back = __builtin_amdgcn_ldexpf(a.scale, scaled[w] - 14);
+    if (MODE != kEnds) {
+      const float back = __builtin_amdgcn_ldexpf(a.scale, scaled - 14);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
-        uint8_t* row = mine + (16 * mt + 4 * g) * L::kRow + (16 * w + n) * kSize;
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          const float z0 = o[mt][w][i] * back, z1 = o[mt][w][i + 1] * back;
+          const float z0 = o[mt][i] * back, z1 = o[mt][i + 1] * back;
           if constexpr (DT == 0) {
-            *reinterpret_cast<float*>(row + i * L::kRow) = z0;
-            *reinterpret_cast<float*>(row + (i + 1) * L::kRow) = z1;
+            *reinterpret_cast<float*>(place(mt, i, 4 * n)) = z0;
+            *reinterpret_cast<float*>(place(mt, i + 1, 4 * n)) = z1;
           } else {
             const uint32_t both = pack2<DT>(z0, z1);
-            *reinterpret_cast<uint16_t*>(row + i * L::kRow) = (uint16_t)both;
-            *reinterpret_cast<uint16_t*>(row + (i + 1) * L::kRow) = (uint16_t)(both >> 16);
+            *reinterpret_cast<uint16_t*>(place(mt, i, 2 * n)) = (uint16_t)both;
+            *reinterpret_cast<uint16_t*>(place(mt, i + 1, 2 * n)) = (uint16_t)(both >> 16);
           }
         }
       }
@@ -921,11 +908,9 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
 #pragma unroll
   for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-    for (int w = 0; w < NT; ++w)
-#pragma unroll
       for (int q = 0; q < 4; ++q)
-        to[(int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * pitch + col + 16 * w] =
-            __builtin_amdgcn_ldexpf(s[t][w][q], scaled[w] - kLength);
+        to[(int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + q) * pitch + col] =
+            __builtin_amdgcn_ldexpf(s[t][q], scaled - kLength);
 #endif
 }
 
@@ -1008,16 +993,16 @@ hipError_t for_places(const DeltaArgs& a, int64_t workgroups_of_place, F launch)
   return hipSuccess;
 }
 
-template <int DT, int DK, int MODE, int NT, int WAVES, int LOADERS>
+template <int DT, int DK, int MODE, int WAVES, int LOADERS>
 hipError_t launch_chain(const DeltaArgs& a, const PartArgs& parts, const int32_t* order, hipStream_t stream) {
-  using L = Chain<DT, DK, MODE, NT, WAVES, LOADERS>;
+  using L = Chain<DT, DK, MODE, WAVES, LOADERS>;
   const uint32_t slices = (uint32_t)((a.head_v + (MODE == kEnds ? DK : 0)) / L::kCols);
   const int of_parts = MODE == kWhole ? 1 : MODE == kEnds ? parts.parts - 1 : parts.parts;
   const FastDiv by_seq((uint32_t)a.v_heads), by_key_heads((uint32_t)a.k_heads), by_parts((uint32_t)of_parts);
   const int64_t pairs = (int64_t)a.n_seqs * a.v_heads, all = (pairs + 7) / 8 * 8 * slices * of_parts;
   for (int64_t first = 0; first < all; first += kMostWorkgroups) {
     const uint32_t grid = (uint32_t)std::min<int64_t>(kMostWorkgroups, all - first);
-    gated_delta_chain_kernel<DT, DK, MODE, NT, WAVES, LOADERS><<<grid, L::kThreads, 0, stream>>>(a, parts, order, by_seq, by_key_heads, by_parts, slices,
+    gated_delta_chain_kernel<DT, DK, MODE, WAVES, LOADERS><<<grid, L::kThreads, 0, stream>>>(a, parts, order, by_seq, by_key_heads, by_parts, slices,
                                                                                              (uint32_t)first, (uint32_t)pairs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -1034,16 +1019,16 @@ hipError_t launch_parts(const DeltaArgs& a, int count, hipStream_t stream) {
   parts.first = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
                                          delta_chunk_places(a.tokens, a.n_seqs) * delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT));
   parts.turn = parts.first + pairs * count * DK * a.head_v;
-  hipError_t e = launch_chain<DT, DK, kEnds, 1, 4, 0>(a, parts, nullptr, stream);
+  hipError_t e = launch_chain<DT, DK, kEnds, 4, 0>(a, parts, nullptr, stream);
   if (e != hipSuccess) return e;
   const uint32_t slices = (uint32_t)(a.head_v / 16);
   gated_delta_join_kernel<DK><<<(uint32_t)((pairs + 7) / 8 * 8 * slices), 4 * DK, 0, stream>>>(a, parts, slices);  // few: a call in parts has few heads
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   if constexpr (DT != 0) {
-    if (a.head_v % 128 == 0) return launch_chain<DT, DK, kPart, 1, 8, 0>(a, parts, nullptr, stream);
+    if (a.head_v % 128 == 0) return launch_chain<DT, DK, kPart, 8, 0>(a, parts, nullptr, stream);
   }
-  return launch_chain<DT, DK, kPart, 1, 4, 0>(a, parts, nullptr, stream);
+  return launch_chain<DT, DK, kPart, 4, 0>(a, parts, nullptr, stream);
 }
 
 template <int DT, int DK>
@@ -1067,11 +1052,11 @@ hipError_t launch_sized(const DeltaArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   if (in_parts) return launch_parts<DT, DK>(a, (int)parts, stream);
   const int64_t columns = (int64_t)a.n_seqs * a.v_heads * a.head_v, cus = device_cu_count();
-  if (columns <= 32 * cus) return launch_chain<DT, DK, kWhole, 1, 2, 2>(a, {}, order, stream);
+  if (columns <= 32 * cus) return launch_chain<DT, DK, kWhole, 2, 2>(a, {}, order, stream);
   if constexpr (DT != 0) {
-    if (a.head_v % 128 == 0 && columns > 64 * cus) return launch_chain<DT, DK, kWhole, 1, 8, 0>(a, {}, order, stream);
+    if (a.head_v % 128 == 0 && columns > 64 * cus) return launch_chain<DT, DK, kWhole, 8, 0>(a, {}, order, stream);
   }
-  return launch_chain<DT, DK, kWhole, 1, 4, 0>(a, {}, order, stream);
+  return launch_chain<DT, DK, kWhole, 4, 0>(a, {}, order, stream);
 }
 
 template <int DT>
