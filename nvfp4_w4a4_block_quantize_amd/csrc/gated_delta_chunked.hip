@@ -88,14 +88,18 @@ __device__ __forceinline__ Parts cut(float4_t a, float4_t b) {
 
 // ---------------------------------------------------------------- a chunk's ties
 
-constexpr int kPitch = 20;  // floats of a row of 16 in LDS: rows that lanes read side by side meet distinct banks
-constexpr int kSquare = 16 * kPitch;
+// A block of 16 x 16 floats in LDS: where four of a row lie.  Lanes that take one column of rows 4 g + r, or four elements of
+// every row, meet distinct banks; 16 floats between blocks part those that the diagonals' lanes read together (against rows
+// 20 floats apart, with which two workgroups fit a CU and not three: 8192 tokens of 48 heads 42.0 -> 37.4 us, 12 ragged
+// prompts 147 -> 134).
+constexpr int kSquare = 16 * 16 + 16;
+__device__ __forceinline__ int cell(int row, int quad) { return ((row & 3) * 4 + (row >> 2)) * 16 + 4 * (quad ^ (row & 3)); }
 constexpr int square(int j, int i) { return i * (i + 1) / 2 + j; }  // of block column j, block row i
 
 struct SolveLds {
   float a[10 * kSquare];  // A^T by blocks: row j, column i; then the inverse's
   double log_decay[kC];
-  float beta[kC], k_norm[kC];
+  float beta[kC];
 };
 
 // Rows of q or k as operands: lane (g, m) holds elements 32 s + 8 g.. of row m, a power of two times the input; what that
@@ -206,7 +210,7 @@ __device__ __forceinline__ bool find_place(const DeltaArgs& a, int64_t c, Place&
 // c - a b, of 16 x 16 blocks in fp32: a from LDS by rows, b and c as the matrix unit leaves results.  Step r of four takes
 // the products' elements 4 g + r, which are register r of b.
 __device__ __forceinline__ float4_t less_product(const float* a, float4_t b, float4_t c, int g, int n) {
-  const float4_t row = *reinterpret_cast<const float4_t*>(a + n * kPitch + 4 * g);
+  const float4_t row = *reinterpret_cast<const float4_t*>(a + cell(n, g));
 #pragma unroll
   for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(-row[r], b[r], c, 0, 0, 0);
   return c;
@@ -214,12 +218,12 @@ __device__ __forceinline__ float4_t less_product(const float* a, float4_t b, flo
 
 __device__ __forceinline__ void store_block(float* to, float4_t x, int g, int n) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) to[(4 * g + r) * kPitch + n] = x[r];
+  for (int r = 0; r < 4; ++r) to[cell(4 * g + r, n >> 2) + (n & 3)] = x[r];
 }
 __device__ __forceinline__ float4_t load_block(const float* from, int g, int n) {
   float4_t x;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) x[r] = from[(4 * g + r) * kPitch + n];
+  for (int r = 0; r < 4; ++r) x[r] = from[cell(4 * g + r, n >> 2) + (n & 3)];
   return x;
 }
 
@@ -251,9 +255,21 @@ __device__ __forceinline__ void find_order(const DeltaArgs& a, int32_t* order) {
   order[before] = r;
 }
 
-// Keys and queries of a chunk and key head: eight waves take 16 rows each.
+// An entry of a chunk and key head: operands of keys and of queries, the rows' norms, and the products k~_i . k~_j and
+// q~_i . k~_j that its value heads share, by blocks j <= i as the matrix unit leaves them (lane (g, n): j = 4 g.., i = n).
+template <int DT, int DK>
+struct KeyEntry {
+  static constexpr int64_t kBytes = delta_key_bytes(DK, DT), kImage = 2 * kC * DK * (DT == 0 ? 2 : 1), kNorms = 2 * kImage;
+  static constexpr int64_t kDots = kNorms + 2 * kC * 4;
+  static_assert(kDots + 20 * kBlock <= kBytes, "the workspace's entry holds it");
+};
+
+// Keys and queries of a chunk and key head: eight waves take 16 rows each, then every eighth of the products' 20 blocks.
 template <int DT, int DK>
 __global__ __launch_bounds__(512) void gated_delta_keys_kernel(DeltaArgs a, FastDiv by_heads, int64_t first_place, int32_t* order) {
+  using E = KeyEntry<DT, DK>;
+  __shared__ __attribute__((aligned(16))) uint8_t images[2 * E::kImage];
+  __shared__ float norms[2 * kC];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, n = lane & 15;
   const uint32_t of_launch = by_heads.div(blockIdx.x);
@@ -265,17 +281,30 @@ __global__ __launch_bounds__(512) void gated_delta_keys_kernel(DeltaArgs a, Fast
   const int rows = (int)std::min<int64_t>(kC, at.end - at.begin);
   const bool of_q = wave >= 4;
   const int mt = wave & 3, row = 16 * mt + n;
-  constexpr int64_t kBytes = delta_key_bytes(DK, DT), kImage = (kBytes - 1024) / 2;
-  uint8_t* keys = static_cast<uint8_t*>(a.workspace) + place * delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT) + kh * kBytes;
+  uint8_t* entry = static_cast<uint8_t*>(a.workspace) + place * delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT) + kh * E::kBytes;
   Row<DT, DK> x;
   x.load(of_q ? a.q : a.k, at.begin + std::min(row, rows - 1), kh, g, row < rows, a.eps);
-  x.store(keys + (of_q ? kImage : 0), mt, lane);
-  if (g == 0) reinterpret_cast<float*>(keys + 2 * kImage)[(of_q ? kC : 0) + row] = x.norm;
+  x.store(entry + (of_q ? E::kImage : 0), mt, lane);
+  x.store(images + (of_q ? E::kImage : 0), mt, lane);
+  if (g == 0) {
+    norms[(of_q ? kC : 0) + row] = x.norm;
+    reinterpret_cast<float*>(entry + E::kNorms)[(of_q ? kC : 0) + row] = x.norm;
+  }
+  __syncthreads();
+  for (int t = wave; t < 20; t += 8) {
+    const int q = t >= 10, of = t - 10 * q, bi = (of >= 1) + (of >= 3) + (of >= 6), bj = of - square(0, bi);
+    Row<DT, DK> y;
+    x.read(images, bj, lane);
+    y.read(images + q * E::kImage, bi, lane);
+    const float4_t of_rows = *reinterpret_cast<const float4_t*>(norms + 16 * bj + 4 * g);
+    *reinterpret_cast<float4_t*>(entry + E::kDots + t * kBlock + lane * 16) = dots(x, y) * (of_rows * norms[q * kC + 16 * bi + n]);
+  }
 }
 
 template <int DT, int DK>
 __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a, FastDiv by_group, FastDiv by_blocks,
                                                                      int64_t first_place) {
+  using E = KeyEntry<DT, DK>;
   __shared__ SolveLds all[kWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, n = lane & 15;
@@ -287,15 +316,14 @@ __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a
   const int kh = (int)by_group.div((uint32_t)h);
   const int rows = (int)std::min<int64_t>(kC, at.end - at.begin);
   SolveLds& lds = all[wave];
-  constexpr int64_t kBytes = delta_key_bytes(DK, DT), kImage = (kBytes - 1024) / 2;
   uint8_t* base = static_cast<uint8_t*>(a.workspace) + place * delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT);
-  const uint8_t* keys = base + kh * kBytes;
-  const float* norms = reinterpret_cast<const float*>(keys + 2 * kImage);
-  uint8_t* ties = base + a.k_heads * kBytes + (int64_t)h * kDeltaTieBytes;
+  const uint8_t* entry = base + kh * E::kBytes;
+  const float* norms = reinterpret_cast<const float*>(entry + E::kNorms);
+  uint8_t* ties = base + a.k_heads * E::kBytes + (int64_t)h * kDeltaTieBytes;
 
-  Row<DT, DK> k[4];
+  float4_t dot[20];
 #pragma unroll
-  for (int mt = 0; mt < 4; ++mt) k[mt].read(keys, mt, lane);
+  for (int t = 0; t < 20; ++t) dot[t] = *reinterpret_cast<const float4_t*>(entry + E::kDots + t * kBlock + lane * 16);
   const float k_norm = norms[lane], q_norm = norms[kC + lane];
 
   // gates of token `lane`: the sum of log2 decays in 64 bits, since only differences count
@@ -310,8 +338,7 @@ __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a
   }
   const double whole = __shfl(log_decay, 63);
   lds.log_decay[lane] = log_decay;
-  lds.beta[lane] = beta * k_norm;
-  lds.k_norm[lane] = k_norm;
+  lds.beta[lane] = beta;
   wave_sync();
 
   // e^(G_i - G_j) of this lane's elements of block (j, i): column i = 16 bi + n, rows j = 16 bj + 4 g + r
@@ -325,20 +352,17 @@ __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a
     }
     return x;
   };
-  auto of_rows = [&](const float* x, int bj) { return *reinterpret_cast<const float4_t*>(x + 16 * bj + 4 * g); };
 
   // P by rows of blocks, and A^T
 #pragma unroll
   for (int bi = 0; bi < 4; ++bi) {
-    Row<DT, DK> q;
-    q.read(keys + kImage, bi, lane);
-    const float strength = lds.beta[16 * bi + n], of_q = __shfl(q_norm, 16 * bi + n);
+    const float strength = lds.beta[16 * bi + n];
     float4_t p[4];
 #pragma unroll
     for (int bj = 0; bj <= bi; ++bj) {
-      const float4_t e = ratio(bj, bi) * of_rows(lds.k_norm, bj);
-      p[bj] = e * of_q * dots(k[bj], q);
-      float4_t x = e * strength * dots(k[bj], k[bi]);
+      const float4_t e = ratio(bj, bi);
+      p[bj] = e * dot[10 + square(bj, bi)];
+      float4_t x = e * strength * dot[square(bj, bi)];
       if (bj == bi) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[r] = 4 * g + r < n ? x[r] : 0.0f;
@@ -359,7 +383,7 @@ __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a
     for (int j = 0; j < 15; ++j) {
 #pragma unroll
       for (int i4 = (j + 1) / 4; i4 < 4; ++i4) {
-        const float4_t col = *reinterpret_cast<const float4_t*>(block + j * kPitch + 4 * i4);
+        const float4_t col = *reinterpret_cast<const float4_t*>(block + cell(j, i4));
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (4 * i4 + i > j) x[4 * i4 + i] = __builtin_fmaf(-col[i], x[j], x[4 * i4 + i]);
@@ -368,7 +392,7 @@ __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a
     wave_sync();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<float4_t*>(block + n * kPitch + 4 * i) = float4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+      *reinterpret_cast<float4_t*>(block + cell(n, i)) = float4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
     wave_sync();
   }
   // U = T^T by blocks: [U0 U01; 0 U1] has U01 = -U0 A01^T U1, first of 16 x 16, then of 32 x 32

@@ -68,8 +68,8 @@ hipError_t launch_group_norm(const NormArgs& a, hipStream_t stream);
 // floor(start_r / 64) + r + i, which no other chunk has.
 constexpr int kDeltaChunk = 64;
 constexpr int kDeltaTieBytes = 26 << 10;
-constexpr int64_t delta_key_bytes(int head_k, int dtype) {  // float32: two fp16 parts; then a norm for each row
-  return (int64_t)2 * kDeltaChunk * head_k * (dtype == 0 ? 4 : 2) + 1024;
+constexpr int64_t delta_key_bytes(int head_k, int dtype) {  // float32: two fp16 parts; then norms (padded) and products
+  return (int64_t)2 * kDeltaChunk * head_k * (dtype == 0 ? 4 : 2) + (21 << 10);
 }
 constexpr int64_t delta_chunk_bytes(int k_heads, int v_heads, int head_k, int dtype) {
   return k_heads * delta_key_bytes(head_k, dtype) + (int64_t)v_heads * kDeltaTieBytes;
