@@ -529,8 +529,8 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
   // Workgroups go to the XCDs in turn: those of one sequence and head, which read the same ties, and where there are 8 key
   // heads (or a multiple) those of one key head lie on one XCD, 8 apart.
   const uint32_t at = first + blockIdx.x, eight = at >> 3;
-  const uint32_t of_part = eight / slices, octet = MODE == kWhole ? of_part : by_parts.div(of_part);
-  const uint32_t pair = octet * 8 + (at & 7);
+  const uint32_t octet = eight / slices, unit_of_work = octet * 8 + (at & 7);
+  const uint32_t pair = MODE == kWhole ? unit_of_work : by_parts.div(unit_of_work);
   if (pair >= pairs) return;
   const uint32_t turn_of_seq = by_seq.div(pair), in_seq = pair - turn_of_seq * by_seq.d;
   const uint32_t r = order ? (uint32_t)order[turn_of_seq] : turn_of_seq;
@@ -539,12 +539,12 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
   const int slot = a.slots[r];
   const int64_t from_start = start_of(a.token_starts, (int)r, a.tokens), end = start_of(a.token_starts, (int)r + 1, a.tokens);
   if (!slot_ok(slot, a.num_slots) || from_start >= end) return;
-  const int part = MODE == kWhole ? 0 : (int)(of_part - octet * by_parts.d);
+  const int part = MODE == kWhole ? 0 : (int)(unit_of_work - pair * by_parts.d);
   Part of_chunks = {0, (end - from_start + kC - 1) / kC, true};
   if (MODE != kWhole) of_chunks = find_part(of_chunks.high, parts.parts, part);
   if (of_chunks.low >= of_chunks.high || (MODE == kEnds && of_chunks.last)) return;
   // of the ends, slices behind the values' are columns of the identity
-  int group_column = (int)(eight - of_part * slices) * L::kCols;
+  int group_column = (int)(eight - octet * slices) * L::kCols;
   const bool unit = MODE == kEnds && group_column >= a.head_v;
   if (unit) {
     if (part == 0) return;
@@ -1023,7 +1023,7 @@ hipError_t launch_chain(const DeltaArgs& a, const PartArgs& parts, const int32_t
   const uint32_t slices = (uint32_t)((a.head_v + (MODE == kEnds ? DK : 0)) / L::kCols);
   const int of_parts = MODE == kWhole ? 1 : MODE == kEnds ? parts.parts - 1 : parts.parts;
   const FastDiv by_seq((uint32_t)a.v_heads), by_key_heads((uint32_t)a.k_heads), by_parts((uint32_t)of_parts);
-  const int64_t pairs = (int64_t)a.n_seqs * a.v_heads, all = (pairs + 7) / 8 * 8 * slices * of_parts;
+  const int64_t pairs = (int64_t)a.n_seqs * a.v_heads, all = (pairs * of_parts + 7) / 8 * 8 * slices;
   for (int64_t first = 0; first < all; first += kMostWorkgroups) {
     const uint32_t grid = (uint32_t)std::min<int64_t>(kMostWorkgroups, all - first);
     gated_delta_chain_kernel<DT, DK, MODE, WAVES, LOADERS><<<grid, L::kThreads, 0, stream>>>(a, parts, order, by_seq, by_key_heads, by_parts, slices,
@@ -1033,8 +1033,6 @@ hipError_t launch_chain(const DeltaArgs& a, const PartArgs& parts, const int32_t
   }
   return hipSuccess;
 }
-
-constexpr int kLeastParts = 8;
 
 template <int DT, int DK>
 hipError_t launch_parts(const DeltaArgs& a, int count, hipStream_t stream) {
@@ -1050,7 +1048,7 @@ hipError_t launch_parts(const DeltaArgs& a, int count, hipStream_t stream) {
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   if constexpr (DT != 0) {
-    if (a.head_v % 128 == 0) return launch_chain<DT, DK, kPart, 8, 0>(a, parts, nullptr, stream);
+    if (a.head_v % 128 == 0 && pairs * count * a.head_v > 64 * device_cu_count()) return launch_chain<DT, DK, kPart, 8, 0>(a, parts, nullptr, stream);
   }
   return launch_chain<DT, DK, kPart, 4, 0>(a, parts, nullptr, stream);
 }
@@ -1062,8 +1060,7 @@ hipError_t launch_sized(const DeltaArgs& a, hipStream_t stream) {
   // behind the chunks; parts, which calls of few sequences have, would lie there too
   int32_t* order = nullptr;
   const int64_t parts = delta_parts(a.tokens, a.n_seqs, a.v_heads, a.head_v);
-  const bool in_parts = parts >= kLeastParts;
-  if (!in_parts && a.n_seqs > 1 && a.n_seqs <= kMostOrdered)
+  if (parts == 0 && a.n_seqs > 1 && a.n_seqs <= kMostOrdered)
     order = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(a.workspace) +
                                        delta_chunk_places(a.tokens, a.n_seqs) * delta_chunk_bytes(a.k_heads, a.v_heads, DK, DT));
   hipError_t e = for_places(a, k_heads, [&](int64_t first, uint32_t places) {
@@ -1074,7 +1071,7 @@ hipError_t launch_sized(const DeltaArgs& a, hipStream_t stream) {
     gated_delta_solve_kernel<DT, DK><<<places * blocks, kThreads, 0, stream>>>(a, by_group, by_blocks, first);
   });
   if (e != hipSuccess) return e;
-  if (in_parts) return launch_parts<DT, DK>(a, (int)parts, stream);
+  if (parts) return launch_parts<DT, DK>(a, (int)parts, stream);
   const int64_t columns = (int64_t)a.n_seqs * a.v_heads * a.head_v, cus = device_cu_count();
   if (columns <= 32 * cus) return launch_chain<DT, DK, kWhole, 2, 2>(a, {}, order, stream);
   if constexpr (DT != 0) {

@@ -77,13 +77,20 @@ constexpr int64_t delta_chunk_bytes(int k_heads, int v_heads, int head_k, int dt
 inline int64_t delta_chunk_places(int64_t tokens, int64_t n_seqs) { return tokens / kDeltaChunk + n_seqs; }
 
 // Behind the chunks: where heads are few, sequences are taken in parts, and each part of a sequence and head has the state
-// it starts from, and what it does to any.  At most kDeltaPartColumns columns of states in all parts, and at least
-// kDeltaPartChunks chunks to a part but the last.
-constexpr int kDeltaPartColumns = kMaxCus * 128, kDeltaPartChunks = 8, kDeltaMostParts = 32;
+// it starts from, and what it does to any.  Of 64 columns of states a CU in all parts (as many as run at once, with as
+// many again for what parts do) if those are 8 parts or more, else of twice that; a part has 8 chunks or more but for the
+// last.  Fewer than 5 parts are none: they cost three times the work.  In us, bf16 and fp16, heads of 128:
+//   6 heads, 16411 tokens: 619 whole, 158 in 21 parts, 184 in 32     16 heads: 634, 259 in 8, 270 in 16
+//   24 heads: 645, 368 in 5, 350 in 10     48 heads, 8192 tokens: 357, 389 in 2, 330 in 5
+//   64 heads, 16411 tokens: 706, 775 in 4     8 heads, 2048 tokens: 94, 87 in 4     40 heads, 3000 tokens: 140, 152 in 5
+constexpr int kDeltaPartColumns = kMaxCus * 128, kDeltaPartChunks = 8, kDeltaMostParts = 32, kDeltaLeastParts = 5;
 inline int64_t delta_parts(int64_t tokens, int64_t n_seqs, int v_heads, int head_v) {
-  const int64_t by_columns = kDeltaPartColumns / (n_seqs * v_heads * head_v), by_chunks = tokens / (kDeltaChunk * kDeltaPartChunks);
-  const int64_t parts = by_columns < by_chunks ? by_columns : by_chunks;
-  return parts < kDeltaMostParts ? parts : kDeltaMostParts;
+  const int64_t columns = n_seqs * v_heads * head_v, by_chunks = tokens / (kDeltaChunk * kDeltaPartChunks);
+  int64_t parts = kDeltaPartColumns / 2 / columns;
+  if (parts < 8) parts = kDeltaPartColumns / columns;
+  if (parts > by_chunks) parts = by_chunks;
+  if (parts > kDeltaMostParts) parts = kDeltaMostParts;
+  return parts < kDeltaLeastParts ? 0 : parts;
 }
 inline int64_t delta_part_bytes(int head_k, int head_v) { return (int64_t)4 * head_k * (head_v + head_k); }
 // enough for any number of sequences up to n_seqs
