@@ -130,16 +130,18 @@ nvfp4_status nvfp4_causal_conv_step(int64_t n_seqs, int64_t channels, int64_t wi
  * Tokens are taken in chunks of 64: what a chunk's tokens write into each other
  * is solved for at once (a unit lower triangular system), and only the chunks
  * follow one another.  Products run on the matrix units with operands cut into
- * fp16 parts: q, k, scaled by a power of two a row (exact but for what lies 2^-25
- * below its largest element; float32 in two parts), states, decays, solutions and
- * values in two (2^-22 of each element's value).  Sums, states and gates are fp32,
- * sums of log decays 64 bits.  The result is the same in every call.
+ * fp16 parts: q, k, scaled by a power of two a row (exact but for what lies 2^-30
+ * below the row's length; float32 in two parts), states, decays, solutions and
+ * values in two (2^-22 of an element's value, or 2^-31 of the largest of its
+ * column).  Sums, states and gates are fp32, sums of log decays 64 bits.  Where
+ * heads are few, parts of a sequence are taken at once and joined in fp32.  The
+ * result is the same in every call on cards with as many CUs.
  *
  * Errors: NULL pointers -> ERR_NULL; sizes <= 0 or >= 2^31, head counts and
  * sizes other than above, heads * head_dim > 2^26, tokens * v_heads > 2^37,
- * n_seqs * v_heads > 2^28, overlapping strides, out = v, workspace_bytes too small -> ERR_SHAPE; alignment
- * -> ERR_ALIGN; dtype -> ERR_DTYPE; scale not finite or <= 0, eps not finite or
- * < 0 -> ERR_RANGE.
+ * n_seqs * v_heads > 2^28, overlapping strides, out = v, workspace_bytes too
+ * small -> ERR_SHAPE; alignment -> ERR_ALIGN; dtype -> ERR_DTYPE; scale not finite
+ * or <= 0, eps not finite or < 0 -> ERR_RANGE.
  */
 nvfp4_status nvfp4_gated_delta_chunked(int64_t tokens, int64_t k_heads, int64_t v_heads, int64_t head_k,
                                        int64_t head_v, int32_t dtype, const void* q, int64_t q_token, int64_t q_head,

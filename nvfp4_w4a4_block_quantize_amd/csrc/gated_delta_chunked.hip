@@ -11,11 +11,21 @@
 //   out  = scale (e^G Q~ S + P V'),  P_ij = e^(G_i - G_j) q~_i . k~_j  (j <= i)
 //   S   <- e^(G_C) S + (e^(G_C - G) K~)^T V'
 //
-// Three kernels.  The first normalises keys and queries.  The second has a wave for each
-// chunk and value head, all independent, and leaves T, P and the gates in the workspace.
-// The third walks the chunks of a sequence with 16 columns of the state in a wave's registers:
-// columns never meet, and the matrix unit's results lie as its next operands want them,
-// so S, X and V' pass through neither LDS nor other lanes.
+// Three kernels.  The first normalises keys and queries and leaves their products, which a
+// key head's value heads share.  The second has a wave for each chunk and value head, all
+// independent, and leaves T, P and the gates in the workspace.  The third, the chain, walks
+// the chunks of a sequence with 16 columns of the state in a wave's registers: columns never
+// meet, and the matrix unit's results lie as its next operands want them, so S, X and V' pass
+// through neither LDS nor other lanes.  Where columns are too few to fill the card, sequences
+// are taken in parts at once, as a part does one linear map to the state it is given.
+//
+// In us (bf16 and fp16, heads of 128; keys, solve, chain; the whole call as a graph):
+//   8192 tokens of 48 heads     23, 38, ends 151 + join 22 + parts 137; 335
+//   12 prompts, 27264 tokens    58, 134, 440; 607
+//   16411 tokens of 6 heads     8, 16, ends 51 + join 45 + parts 49; 159
+// The solve's stores bound it (26 KB a chunk and head: 4 TB/s).  The chain's chunk takes a
+// wave some 2100 cycles of the matrix unit; with 8 waves LDS (6300) and issue (5800) bound it,
+// 10400 cycles a chunk, with one wave a SIMD what a product waits for the one before, 6000.
 //
 // Precision.  Operands are fp16 parts, sums fp32.  A row of keys or queries is scaled by a
 // power of two to a length in [16, 32): 16-bit inputs fit one part but for what lies 2^-30
@@ -241,7 +251,7 @@ __device__ __forceinline__ void store_ties(uint8_t* to, int mt, const float4_t (
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
 
 // Sequences in the order of their lengths, the longest first, so that the last workgroups of the chain have the least to do
-// (12 prompts up to 4096 tokens, 48 heads: LONGEST us).
+// (12 prompts up to 4096 tokens of 48 heads, in the order they are given: 682 us and not 608).
 constexpr int kMostOrdered = 512;
 __device__ __forceinline__ void find_order(const DeltaArgs& a, int32_t* order) {
   __shared__ int32_t lens[kMostOrdered];
@@ -467,8 +477,8 @@ __device__ __forceinline__ short4_t read_columns(const uint8_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)p);
 }
 
-// WAVES of a workgroup hold 16 columns each, LOADERS more move data for them.  A stage is keys, T, gates, values, queries, P: of the
-// ends of parts, all but the last two.
+// WAVES of a workgroup hold 16 columns each, LOADERS more move data for them.  A stage is keys, T, gates, values, queries, P:
+// of the ends of parts, all but the last two.
 template <int DT, int DK, int MODE, int WAVES, int LOADERS>
 struct Chain {
   static constexpr int kParts = DT == 0 ? 2 : 1, kSteps = DK / 32, kTiles = DK / 16;
@@ -516,9 +526,10 @@ __device__ __forceinline__ float of_column(float x) {
 }
 
 template <int DT, int DK, int MODE, int WAVES, int LOADERS>
-__global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves_per_eu(WAVES + LOADERS > 4 ? 2 : 1))) void gated_delta_chain_kernel(
-    DeltaArgs a, PartArgs parts, const int32_t* order, FastDiv by_seq, FastDiv by_key_heads, FastDiv by_parts, uint32_t slices, uint32_t first,
-    uint32_t pairs) {
+__global__ __launch_bounds__(64 * (WAVES + LOADERS))
+    __attribute__((amdgpu_waves_per_eu(WAVES + LOADERS > 4 ? 2 : 1))) void gated_delta_chain_kernel(
+        DeltaArgs a, PartArgs parts, const int32_t* order, FastDiv by_seq, FastDiv by_key_heads, FastDiv by_parts, uint32_t slices,
+        uint32_t first, uint32_t pairs) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using L = Chain<DT, DK, MODE, WAVES, LOADERS>;
   constexpr int kSize = element_size(DT);
@@ -526,8 +537,9 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, n = lane & 15;
 
-  // Workgroups go to the XCDs in turn: those of one sequence and head, which read the same ties, and where there are 8 key
-  // heads (or a multiple) those of one key head lie on one XCD, 8 apart.
+  // Workgroups go to the XCDs in turn: those of one sequence and head (and part), which read the same ties, and where there
+  // are 8 key heads (or a multiple) those of one key head lie on one XCD, 8 apart.  Parts are dealt one by one, so that few
+  // heads reach every XCD (6 heads in 32 parts: 184 us, and 200 with a head on one XCD).
   const uint32_t at = first + blockIdx.x, eight = at >> 3;
   const uint32_t octet = eight / slices, unit_of_work = octet * 8 + (at & 7);
   const uint32_t pair = MODE == kWhole ? unit_of_work : by_parts.div(unit_of_work);
@@ -700,25 +712,23 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
     for (int mt = 0; mt < 4; ++mt) beta[mt] = gate(kBeta, mt);
     float4_t x[4];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-      {
-        if (unit) {
-          x[mt] = float4_t{0, 0, 0, 0};
-        } else if constexpr (DT == 0) {
+    for (int mt = 0; mt < 4; ++mt) {
+      if (unit) {
+        x[mt] = float4_t{0, 0, 0, 0};
+      } else if constexpr (DT == 0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[mt][i] = *reinterpret_cast<const float*>(place(mt, i, 4 * n));
-        } else {
-          const short4_t e = read_columns(place(mt, n / 4, (n % 4) * 8));
+        for (int i = 0; i < 4; ++i) x[mt][i] = *reinterpret_cast<const float*>(place(mt, i, 4 * n));
+      } else {
+        const short4_t e = read_columns(place(mt, n / 4, (n % 4) * 8));
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if constexpr (DT == 1)
-              x[mt][q] = __uint_as_float((uint32_t)(uint16_t)e[q] << 16);
-            else
-              x[mt][q] = (float)__builtin_bit_cast(_Float16, (short)e[q]);
-          }
+        for (int q = 0; q < 4; ++q) {
+          if constexpr (DT == 1)
+            x[mt][q] = __uint_as_float((uint32_t)(uint16_t)e[q] << 16);
+          else
+            x[mt][q] = (float)__builtin_bit_cast(_Float16, (short)e[q]);
         }
       }
+    }
     read_keys(0);
     if (!LOADERS) move(c, now);
     __builtin_amdgcn_sched_barrier(0);
@@ -727,38 +737,31 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
     // goes to 2^7..2^8 when it has left 2^5..2^9.  The state's length is at most sqrt(128) M and grows by M a token, so that
     // X and V' stay below 75 M < 2^16; |S| 2^4 is below 2^13; a part's last bit lies 2^31 below M.
     {
-      float top, high;
-      bool off = c == 0;
-      {
-        top = high = 0.0f;
+      float top = 0.0f, high = 0.0f;
 #pragma unroll
-        for (int t = 0; t < L::kTiles; ++t)
+      for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(s[t][i]));
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(s[t][i]));
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-          x[mt] *= beta[mt];
+      for (int mt = 0; mt < 4; ++mt) {
+        x[mt] *= beta[mt];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) high = fmaxf(high, fabsf(x[mt][i]));
-        }
-        const float both = of_column(fmaxf(top * (1.0f / kLong), __builtin_amdgcn_ldexpf(high, -scaled)));
-        off = off || both > 512.0f || (both < 32.0f && both > 0.0f && scaled > -150);
+        for (int i = 0; i < 4; ++i) high = fmaxf(high, fabsf(x[mt][i]));
       }
-      if (__any(off)) {
-        {
-          const float of_s = of_column(top), of_x = of_column(high);
-          constexpr int kNone = -100000;
-          const int of_state = of_s > 0.0f ? __builtin_amdgcn_frexp_expf(of_s) + scaled - kLength : kNone;
-          const int of_values = of_x > 0.0f ? __builtin_amdgcn_frexp_expf(of_x) : kNone;
-          const int most = std::max(of_state, of_values), by_now = most - scaled;
-          if (most != kNone && (by_now > 9 || by_now < 6)) {
-            const int next = std::max(most - 8, -150), by = scaled - next;
-            scaled = next;
+      const float both = of_column(fmaxf(top * (1.0f / kLong), __builtin_amdgcn_ldexpf(high, -scaled)));
+      if (__any(c == 0 || both > 512.0f || (both < 32.0f && both > 0.0f && scaled > -150))) {
+        const float of_s = of_column(top), of_x = of_column(high);
+        constexpr int kNone = -100000;
+        const int of_state = of_s > 0.0f ? __builtin_amdgcn_frexp_expf(of_s) + scaled - kLength : kNone;
+        const int of_values = of_x > 0.0f ? __builtin_amdgcn_frexp_expf(of_x) : kNone;
+        const int most = std::max(of_state, of_values), by_now = most - scaled;
+        if (most != kNone && (by_now > 9 || by_now < 6)) {
+          const int next = std::max(most - 8, -150), by = scaled - next;
+          scaled = next;
 #pragma unroll
-            for (int t = 0; t < L::kTiles; ++t)
+          for (int t = 0; t < L::kTiles; ++t)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) s[t][i] = __builtin_amdgcn_ldexpf(s[t][i], by);
-          }
+            for (int i = 0; i < 4; ++i) s[t][i] = __builtin_amdgcn_ldexpf(s[t][i], by);
         }
       }
     }
@@ -768,8 +771,7 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
     const float4_t none = {0, 0, 0, 0};
     float4_t y[4], o[4];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-      y[mt] = o[mt] = none;
+    for (int mt = 0; mt < 4; ++mt) y[mt] = o[mt] = none;
     half8_t turn[kTies][2];
     auto read_ties = [&](half8_t (&to)[kTies][2], int at, int st) {
 #pragma unroll
@@ -792,16 +794,15 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
 #pragma unroll
       for (int i = 0; i < 1 + L::kParts; ++i)
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-          {
-            const int part = i == 2 ? L::kParts - 1 : 0;
-            const half8_t of_s = i == 1 ? b[st & 1].lo : b[st & 1].hi;
-            y[mt] = mfma(keys[st & 1][0][mt][part], of_s, y[mt]);
-            if (MODE != kEnds) o[mt] = mfma(keys[st & 1][kOfQ - 1][mt][part], of_s, o[mt]);
-          }
+        for (int mt = 0; mt < 4; ++mt) {
+          const int part = i == 2 ? L::kParts - 1 : 0;
+          const half8_t of_s = i == 1 ? b[st & 1].lo : b[st & 1].hi;
+          y[mt] = mfma(keys[st & 1][0][mt][part], of_s, y[mt]);
+          if (MODE != kEnds) o[mt] = mfma(keys[st & 1][kOfQ - 1][mt][part], of_s, o[mt]);
+        }
       if (st + 1 < L::kSteps) b[(st + 1) & 1] = cut(s[2 * st + 2], s[2 * st + 3]);
-      // The next chunk's loads in between: LDS takes some 30 bytes a cycle from memory, and a wave that has more to issue
-      // than the queue holds waits (all of them at once, at the chunk's begin: NEXTLOADS).
+      // The next chunk's loads in between: all at once, at the chunk's begin, a wave waits until its queue takes them (the
+      // chain of 12 prompts 466 us and not 449, the ends of 31 parts of 6 heads 74 and not 70).
       if (!LOADERS && L::kStages == 2 && c + 1 < chunks) {
 #pragma unroll
         for (int i = st; i < kTurns; i += L::kSteps) issue_turn(c + 1, now ^ 1, i);
@@ -820,14 +821,12 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
     }
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
-      {
 #pragma unroll
-        for (int mt = 2 * st; mt < 2 * st + 2; ++mt)
+      for (int mt = 2 * st; mt < 2 * st + 2; ++mt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[mt][i] = __builtin_fmaf(-gain[mt][i], y[mt][i], __builtin_amdgcn_ldexpf(x[mt][i], -scaled));
-        b[st] = cut(x[2 * st], x[2 * st + 1]);
-      }
+        for (int i = 0; i < 4; ++i)
+          x[mt][i] = __builtin_fmaf(-gain[mt][i], y[mt][i], __builtin_amdgcn_ldexpf(x[mt][i], -scaled));
+      b[st] = cut(x[2 * st], x[2 * st + 1]);
     }
     half8_t turned[L::kTiles][L::kParts], inner[kTies][2];  // rows of K^T; P
     auto read_turned = [&](int st) {
@@ -838,8 +837,8 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
           short4_t e[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j)  // tokens 32 st + 16 j + 4 g.., rows of this tile
-            e[j] = read_columns(here + ((p * 4 + 2 * st + j) * L::kSteps + t / 2) * kBlock + ((n % 4) * 16 + 4 * g + n / 4) * 16 +
-                                8 * (t & 1));
+            e[j] = read_columns(here + ((p * 4 + 2 * st + j) * L::kSteps + t / 2) * kBlock +
+                                ((n % 4) * 16 + 4 * g + n / 4) * 16 + 8 * (t & 1));
           turned[t][p] = __builtin_bit_cast(half8_t, __builtin_shufflevector(e[0], e[1], 0, 1, 2, 3, 4, 5, 6, 7));
         }
     };
@@ -849,35 +848,29 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
     // V' = T X; the state's decay among it
     float4_t z[4];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-      z[mt] = none;
+    for (int mt = 0; mt < 4; ++mt) z[mt] = none;
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
       for (int i = 0; i < 3; ++i)
 #pragma unroll
         for (int mt = 2 * half; mt < 2 * half + 2; ++mt)
-            z[mt] = mfma(turn[tie(mt, 0)][i == 2], i == 1 ? b[0].lo : b[0].hi, z[mt]);
+          z[mt] = mfma(turn[tie(mt, 0)][i == 2], i == 1 ? b[0].lo : b[0].hi, z[mt]);
 #pragma unroll
     for (int i = 0; i < 3; ++i)
 #pragma unroll
-      for (int mt = 2; mt < 4; ++mt)
-        z[mt] = mfma(turn[tie(mt, 1)][i == 2], i == 1 ? b[1].lo : b[1].hi, z[mt]);
-    {
+      for (int mt = 2; mt < 4; ++mt) z[mt] = mfma(turn[tie(mt, 1)][i == 2], i == 1 ? b[1].lo : b[1].hi, z[mt]);
 #pragma unroll
-      for (int t = 0; t < L::kTiles; ++t) s[t] *= whole;
+    for (int t = 0; t < L::kTiles; ++t) s[t] *= whole;
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
-        if (MODE != kEnds) o[mt] *= gain_q[mt];
-    }
+    for (int mt = 0; mt < 4; ++mt)
+      if (MODE != kEnds) o[mt] *= gain_q[mt];
 
     // K^T V' onto the decayed state, P V' onto Q S
     auto cut_values = [&](int st) {
-      {
-        const float4_t v0 = z[2 * st] * kDown, v1 = z[2 * st + 1] * kDown;
-        d = cut(v0 * until[2 * st], v1 * until[2 * st + 1]);
-        if (MODE != kEnds) b[st] = cut(v0, v1);
-      }
+      const float4_t v0 = z[2 * st] * kDown, v1 = z[2 * st + 1] * kDown;
+      d = cut(v0 * until[2 * st], v1 * until[2 * st + 1]);
+      if (MODE != kEnds) b[st] = cut(v0, v1);
     };
     cut_values(0);
     if (MODE != kEnds) read_ties(inner, L::kInnerAt, 0);
@@ -897,7 +890,7 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS)) __attribute__((amdgpu_waves
       for (int i = 0; i < (MODE == kEnds ? 0 : 3); ++i)
 #pragma unroll
         for (int mt = 2 * st; mt < 4; ++mt)
-            o[mt] = mfma(inner[tie(mt, st)][i == 2], i == 1 ? b[st].lo : b[st].hi, o[mt]);
+          o[mt] = mfma(inner[tie(mt, st)][i == 2], i == 1 ? b[st].lo : b[st].hi, o[mt]);
       if (MODE != kEnds && st == 0) read_ties(inner, L::kInnerAt, 1);
     }
 
@@ -1026,13 +1019,19 @@ hipError_t launch_chain(const DeltaArgs& a, const PartArgs& parts, const int32_t
   const int64_t pairs = (int64_t)a.n_seqs * a.v_heads, all = (pairs * of_parts + 7) / 8 * 8 * slices;
   for (int64_t first = 0; first < all; first += kMostWorkgroups) {
     const uint32_t grid = (uint32_t)std::min<int64_t>(kMostWorkgroups, all - first);
-    gated_delta_chain_kernel<DT, DK, MODE, WAVES, LOADERS><<<grid, L::kThreads, 0, stream>>>(a, parts, order, by_seq, by_key_heads, by_parts, slices,
-                                                                                             (uint32_t)first, (uint32_t)pairs);
+    gated_delta_chain_kernel<DT, DK, MODE, WAVES, LOADERS><<<grid, L::kThreads, 0, stream>>>(
+        a, parts, order, by_seq, by_key_heads, by_parts, slices, (uint32_t)first, (uint32_t)pairs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
+
+// Columns of a workgroup of the chain: 32, with two waves besides that move its data, while a CU then has one workgroup at
+// most; 64 while that still holds, 128 above it (float32's stage holds 64).  8192 tokens, heads of 128, in us for 32, 64 and
+// 128:  32 heads 344, 405, 583   64 heads 369, 435, 609   72 heads 668, 442, 617   128 heads 715, 508, 664
+// 192 heads 1059, 895, 733   12 prompts of 48 heads 974, 690, 618.  float32: 64 heads 772, 863   96 heads 1439, 903
+bool wide(const DeltaArgs& a, int64_t states) { return a.head_v % 128 == 0 && states * a.head_v > 64 * device_cu_count(); }
 
 template <int DT, int DK>
 hipError_t launch_parts(const DeltaArgs& a, int count, hipStream_t stream) {
@@ -1044,11 +1043,12 @@ hipError_t launch_parts(const DeltaArgs& a, int count, hipStream_t stream) {
   hipError_t e = launch_chain<DT, DK, kEnds, 4, 0>(a, parts, nullptr, stream);
   if (e != hipSuccess) return e;
   const uint32_t slices = (uint32_t)(a.head_v / 16);
-  gated_delta_join_kernel<DK><<<(uint32_t)((pairs + 7) / 8 * 8 * slices), 4 * DK, 0, stream>>>(a, parts, slices);  // few: a call in parts has few heads
+  // a call in parts has at most 2^15 columns
+  gated_delta_join_kernel<DK><<<(uint32_t)((pairs + 7) / 8 * 8 * slices), 4 * DK, 0, stream>>>(a, parts, slices);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   if constexpr (DT != 0) {
-    if (a.head_v % 128 == 0 && pairs * count * a.head_v > 64 * device_cu_count()) return launch_chain<DT, DK, kPart, 8, 0>(a, parts, nullptr, stream);
+    if (wide(a, pairs * count)) return launch_chain<DT, DK, kPart, 8, 0>(a, parts, nullptr, stream);
   }
   return launch_chain<DT, DK, kPart, 4, 0>(a, parts, nullptr, stream);
 }
@@ -1072,10 +1072,10 @@ hipError_t launch_sized(const DeltaArgs& a, hipStream_t stream) {
   });
   if (e != hipSuccess) return e;
   if (parts) return launch_parts<DT, DK>(a, (int)parts, stream);
-  const int64_t columns = (int64_t)a.n_seqs * a.v_heads * a.head_v, cus = device_cu_count();
-  if (columns <= 32 * cus) return launch_chain<DT, DK, kWhole, 2, 2>(a, {}, order, stream);
+  const int64_t pairs = (int64_t)a.n_seqs * a.v_heads;
+  if (pairs * a.head_v <= 32 * device_cu_count()) return launch_chain<DT, DK, kWhole, 2, 2>(a, {}, order, stream);
   if constexpr (DT != 0) {
-    if (a.head_v % 128 == 0 && columns > 64 * cus) return launch_chain<DT, DK, kWhole, 8, 0>(a, {}, order, stream);
+    if (wide(a, pairs)) return launch_chain<DT, DK, kWhole, 8, 0>(a, {}, order, stream);
   }
   return launch_chain<DT, DK, kWhole, 4, 0>(a, {}, order, stream);
 }

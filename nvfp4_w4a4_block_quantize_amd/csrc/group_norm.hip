@@ -6,7 +6,11 @@
 // Bandwidth kernel: x and gate are read once and stay in registers, so the mean can be
 // taken off before squares are summed, and out may be either of them.  LANES lanes
 // share a group: 16 of them (a group of 128 in 16-bit types is one 16-byte load each),
-// a wave, or a workgroup, whatever holds it.
+// a wave, or a workgroup, whatever holds it.  Rows that are not whole 16-byte pieces are
+// taken element by element, 16 lanes of up to 8.  Sums go round rows of 16 lanes without
+// LDS.  8192 tokens of 48 groups of 128, bf16, with a gate: 59 us, 5.1 TB/s (weights
+// loaded one by one 122; two groups a thread 59, at 1024 tokens 11.0 and not 9.5); 4099 of
+// 20 of 121 in float32: 21.6 (two groups a thread 23.1; through LDS and 64 lanes 36).
 #include <algorithm>
 
 #include "gdn_device.h"
@@ -15,7 +19,6 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMany = 8;
 
 // `v` of the lane `by` places on, around each row of 16
 template <int BY>
@@ -45,95 +48,85 @@ __device__ __forceinline__ float sum_of(float v, float* lds) {
   return v;
 }
 
-// Groups of up to LANES * N * E elements, E of them at a time, ITEMS groups one behind the other a thread.
-template <int DT, int E, int LANES, int N, int ITEMS>
+// Groups of up to LANES * N * E elements, E of them at a time.
+template <int DT, int E, int LANES, int N>
 __global__ __launch_bounds__(kThreads) void group_norm_kernel(NormArgs a, FastDiv by_groups, uint32_t items, float over_dim) {
   __shared__ float lds[4];
-  constexpr int kPer = kThreads / LANES;
   const int lane = threadIdx.x % LANES;
   const bool gated = a.gate.p != nullptr;
-  Elements<DT, E> x[ITEMS][N], z[ITEMS][N];
-  int64_t token[ITEMS];
-  int group[ITEMS];
-  bool live[ITEMS];
+  const uint32_t item = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+  const bool live = item < items;  // the others keep step with their wave
+  const uint32_t t = by_groups.div(live ? item : 0);
+  const int64_t token = t;
+  const int group = live ? (int)(item - t * by_groups.d) : 0;
+  const int64_t xo = token * a.x.token + group * a.x.head, zo = token * a.gate.token + group * a.gate.head;
+  Elements<DT, E> x[N], z[N];
 #pragma unroll
-  for (int j = 0; j < ITEMS; ++j) {
-    const uint32_t item = (blockIdx.x * ITEMS + j) * kPer + threadIdx.x / LANES;
-    live[j] = item < items;  // the others keep step with their wave
-    const uint32_t t = by_groups.div(live[j] ? item : 0);
-    token[j] = t;
-    group[j] = live[j] ? (int)(item - t * by_groups.d) : 0;
-    const int64_t xo = token[j] * a.x.token + group[j] * a.x.head, zo = token[j] * a.gate.token + group[j] * a.gate.head;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = (i * LANES + lane) * E;
-      if (at < a.group_dim) {
-        x[j][i].load(a.x.p, xo + at);
-        if (gated) z[j][i].load(a.gate.p, zo + at);
-      } else {
-        x[j][i].zero();
-      }
+  for (int i = 0; i < N; ++i) {
+    const int at = (i * LANES + lane) * E;
+    if (at < a.group_dim) {
+      x[i].load(a.x.p, xo + at);
+      if (gated) z[i].load(a.gate.p, zo + at);
+    } else {
+      x[i].zero();
     }
   }
-#pragma unroll
-  for (int j = 0; j < ITEMS; ++j) {
-    float mean = 0.0f;
-    if (a.centred) {
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int e = 0; e < E; ++e) s += x[j][i].get(e);
-      mean = sum_of<LANES>(s, lds) * over_dim;
-    }
+  float mean = 0.0f;
+  if (a.centred) {
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const bool inside = (i * LANES + lane) * E < a.group_dim;
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float y = inside ? x[j][i].get(e) - mean : 0.0f;
-        s = __builtin_fmaf(y, y, s);
-      }
+      for (int e = 0; e < E; ++e) s += x[i].get(e);
+    mean = sum_of<LANES>(s, lds) * over_dim;
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool inside = (i * LANES + lane) * E < a.group_dim;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float y = inside ? x[i].get(e) - mean : 0.0f;
+      s = __builtin_fmaf(y, y, s);
     }
-    const float over = 1.0f / sqrtf(__builtin_fmaf(sum_of<LANES>(s, lds), over_dim, a.eps));
-    if (!live[j]) continue;
-    const float* weight = a.weight + (int64_t)group[j] * a.weight_group;
-    const float* bias = a.bias ? a.bias + (int64_t)group[j] * a.weight_group : nullptr;
-    const int64_t oo = token[j] * a.out.token + group[j] * a.out.head;
+  }
+  const float over = 1.0f / sqrtf(__builtin_fmaf(sum_of<LANES>(s, lds), over_dim, a.eps));
+  if (!live) return;
+  const float* weight = a.weight + (int64_t)group * a.weight_group;
+  const float* bias = a.bias ? a.bias + (int64_t)group * a.weight_group : nullptr;
+  const int64_t oo = token * a.out.token + group * a.out.head;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = (i * LANES + lane) * E;
-      if (at >= a.group_dim) continue;
-      float y[E];
-      Elements<0, E> w, b;
-      w.load(weight, at);
-      if (bias) b.load(bias, at);
+  for (int i = 0; i < N; ++i) {
+    const int at = (i * LANES + lane) * E;
+    if (at >= a.group_dim) continue;
+    float y[E];
+    Elements<0, E> w, b;
+    w.load(weight, at);
+    if (bias) b.load(bias, at);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        y[e] = (x[j][i].get(e) - mean) * over * w.get(e);
-        if (bias) y[e] += b.get(e);
-        const float g = gated ? z[j][i].get(e) : y[e];
-        const float act = a.activation ? g * sigmoid<DT == 0>(g) : g;
-        y[e] = gated ? y[e] * act : act;
-      }
-      Elements<DT, E> out;
-      out.set(y);
-      out.store(a.out.p, oo + at);
+    for (int e = 0; e < E; ++e) {
+      y[e] = (x[i].get(e) - mean) * over * w.get(e);
+      if (bias) y[e] += b.get(e);
+      const float g = gated ? z[i].get(e) : y[e];
+      const float act = a.activation ? g * sigmoid<DT == 0>(g) : g;
+      y[e] = gated ? y[e] * act : act;
     }
+    Elements<DT, E> out;
+    out.set(y);
+    out.store(a.out.p, oo + at);
   }
 }
 
-template <int DT, int E, int LANES, int N, int ITEMS>
-hipError_t launch_items(NormArgs a, hipStream_t stream) {
-  constexpr int kPer = kThreads / LANES * ITEMS;
+template <int DT, int E, int LANES, int N>
+hipError_t launch_lanes(NormArgs a, hipStream_t stream) {
+  constexpr int kPer = kThreads / LANES;
   const FastDiv by_groups((uint32_t)a.groups);
   // a launch takes whole tokens, of fewer than 2^31 groups in all
   const int64_t most = std::max<int64_t>(kMostWorkgroups * kPer / a.groups, 1);
   for (int64_t left = a.tokens;;) {
     const int64_t tokens = std::min(left, most);
     const uint32_t items = (uint32_t)(tokens * a.groups);
-    group_norm_kernel<DT, E, LANES, N, ITEMS>
+    group_norm_kernel<DT, E, LANES, N>
         <<<(items + kPer - 1) / kPer, kThreads, 0, stream>>>(a, by_groups, items, 1.0f / (float)a.group_dim);
     const hipError_t e = hipGetLastError();
     left -= tokens;
@@ -143,14 +136,6 @@ hipError_t launch_items(NormArgs a, hipStream_t stream) {
     if (a.gate.p) a.gate.p = static_cast<const char*>(a.gate.p) + behind(a.gate.token);
     a.out.p = static_cast<char*>(a.out.p) + behind(a.out.token);
   }
-}
-
-template <int DT, int E, int LANES, int N>
-hipError_t launch_lanes(const NormArgs& a, hipStream_t stream) {
-  constexpr int kItems = 2;
-  if (N * kItems <= 16 && a.tokens * a.groups >= (int64_t)kMany * kItems * (kThreads / LANES) * device_cu_count())
-    return launch_items<DT, E, LANES, N, N * kItems <= 16 ? kItems : 1>(a, stream);
-  return launch_items<DT, E, LANES, N, 1>(a, stream);
 }
 
 template <int DT>

@@ -1,0 +1,58 @@
+"""The gated delta layer's kernels that only larger calls reach: many columns of states, parts of long
+sequences of every head size, more sequences than are put in order, and convolutions of many rows.
+Checks, bounds and their reasons are those of test_gpu_gdn."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_gdn import Delta, check_conv, conv_inputs, delta_starts, log
+
+pytestmark = pytest.mark.gpu
+
+LENS = [70, 1, 64, 0, 130, 63, 2, 65, 5, 128, 31, 64, 97]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("heads,n", [((2, 6, 128, 128), 13), ((2, 6, 128, 128), 25), ((1, 5, 64, 192), 20), ((1, 9, 64, 256), 9), ((3, 12, 64, 64), 14)])
+def test_chunked_of_many_columns(gpu_lib, dtype, heads, n):
+    """9984, 19200, 19200, 20736 and 10752 columns: workgroups of 64 and of 128 of them."""
+    rng = np.random.default_rng([n, *heads, 2])
+    starts = delta_starts([LENS[i % len(LENS)] for i in range(n)])
+    log("many columns", dtype, heads, n)
+    d = Delta(rng, dtype, int(starts[-1]) + 3, n, *heads, extra=8 * (n % 2))
+    d.slots[5] = -1
+    d.check(gpu_lib, starts, cached=rng.integers(0, 2, n) * 5, in_place=n % 2 == 1, out_extra=8 * (n % 2))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("heads,lens", [
+    ((2, 2, 64, 192), [2700]), ((1, 3, 128, 64), [1100, 1700]), ((1, 1, 128, 256), [2600, 64]), ((1, 2, 64, 128), [513, 4000, 0, 3]),
+    ((8, 24, 64, 128), [3100]), ((2, 12, 128, 128), [1700, 1500])])
+def test_chunked_in_parts_of_every_size(gpu_lib, dtype, heads, lens):
+    """Parts of sequences, the last two cases' in workgroups of 128 columns."""
+    rng = np.random.default_rng([len(lens), *heads, 3])
+    log("parts", dtype, heads, lens)
+    starts = delta_starts(lens) + 2
+    d = Delta(rng, dtype, int(starts[-1]) + 3, len(lens), *heads, decay=0.05)
+    d.check(gpu_lib, starts, cached=np.arange(len(lens)) % 2 == 0, in_place=len(lens) == 1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [511, 512, 513, 700])
+def test_chunked_of_many_sequences(gpu_lib, dtype, n):
+    rng = np.random.default_rng([n, 4])
+    starts = delta_starts([(0, 1, 2, 65)[i * 7 % 11 % 4] for i in range(n)])
+    log("many sequences", dtype, n)
+    Delta(rng, dtype, int(starts[-1]), n, 1, 1, 64, 64).check(gpu_lib, starts, cached=rng.integers(0, 2, n))
+
+
+@pytest.mark.parametrize("dtype,channels", [("f32", 2056), ("f16", 2056), ("bf16", 4104)])
+@pytest.mark.parametrize("width", [2, 4])
+def test_conv_of_many_rows(gpu_lib, dtype, channels, width):
+    """16 rows a thread, and 32 with outputs stored past the caches."""
+    rng = np.random.default_rng([channels, width])
+    lens = [1000, 1, 31, 32, 33, 0, 2, 1999, 3, 999]
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    x, weight, bias, state, slots = conv_inputs(rng, int(starts[-1]) + 2, channels, width, dtype, len(lens))
+    slots[3] = -1
+    log("conv of many rows", dtype, channels, width)
+    check_conv(gpu_lib, dtype, x, weight, bias, "silu", state, slots, starts, rng.integers(0, 2, len(lens)), in_place=width == 4)
