@@ -20,9 +20,9 @@
 // are taken in parts at once, as a part does one linear map to the state it is given.
 //
 // In us (bf16 and fp16, heads of 128; keys, solve, chain; the whole call as a graph):
-//   8192 tokens of 48 heads     23, 38, ends 151 + join 22 + parts 137; 335
-//   12 prompts, 27264 tokens    58, 134, 440; 607
-//   16411 tokens of 6 heads     8, 16, ends 51 + join 45 + parts 49; 159
+//   8192 tokens of 48 heads     22, 39, ends 156 + join 20 + parts 140; 336
+//   12 prompts, 27264 tokens    56, 127, 446; 604
+//   16411 tokens of 6 heads     9, 16, ends 51 + join 43 + parts 49; 159
 // The solve's stores bound it (26 KB a chunk and head: 4 TB/s).  The chain's chunk takes a
 // wave some 2100 cycles of the matrix unit; with 8 waves LDS (6300) and issue (5800) bound it,
 // 10400 cycles a chunk, with one wave a SIMD what a product waits for the one before, 6000.
@@ -340,7 +340,8 @@ __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a
   const int64_t token = at.begin + std::min(lane, rows - 1);
   const float decay = -expf(a.a_log[h]) * softplus(element<DT>(a.a, token * a.a_token + h) + a.dt_bias[h]);
   const float beta = lane < rows ? sigmoid<true>(element<DT>(a.b, token * a.b_token + h)) : 0.0f;
-  double log_decay = lane < rows ? (double)decay * 1.4426950408889634 : 0.0;
+  // at 2^-256 nothing is left in fp32; less would cost the sums of later tokens their last bits
+  double log_decay = lane < rows ? fmax((double)decay * 1.4426950408889634, -256.0) : 0.0;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
     const double before = __shfl_up(log_decay, d);

@@ -7,6 +7,7 @@ import pytest
 from tests.test_gpu_gdn import Delta, check_conv, conv_inputs, delta_starts, log
 
 pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
 
 LENS = [70, 1, 64, 0, 130, 63, 2, 65, 5, 128, 31, 64, 97]
 
@@ -56,3 +57,22 @@ def test_conv_of_many_rows(gpu_lib, dtype, channels, width):
     slots[3] = -1
     log("conv of many rows", dtype, channels, width)
     check_conv(gpu_lib, dtype, x, weight, bias, "silu", state, slots, starts, rng.integers(0, 2, len(lens)), in_place=width == 4)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("huge", [300.0, 1e9, 1e30, 3e38])
+def test_tokens_after_one_that_forgets_all(gpu_lib, dtype, huge):
+    """A token's decay of any size, also one that overflows, leaves the later tokens' decays exact."""
+    rng = np.random.default_rng(21)
+    starts = delta_starts([130, 200])
+    log("forgets", dtype, huge)
+    d = Delta(rng, dtype, int(starts[-1]), 2, 1, 2, 64, 64)
+    d.a_log[:] = torch.tensor([0.0, 3.0], device="cuda")
+    d.dt_bias.zero_()
+    d.a[:] = torch.as_tensor(rng.uniform(-5, -2, d.a.shape), device="cuda").to(d.a.dtype)
+    for token in (0, 5, 70, 71, 127, 140, 250):
+        d.a[token] = huge
+    for step in (False, True):
+        if step:
+            d.slots = np.concatenate([d.slots, [-1] * (len(d.q) - len(d.slots))])
+        d.check(gpu_lib, np.arange(len(d.q) + 1) if step else starts, step=step)
