@@ -21,7 +21,7 @@
 //
 // In us (bf16 and fp16, heads of 128; keys, solve, chain; the whole call as a graph):
 //   8192 tokens of 48 heads     22, 39, ends 156 + join 20 + parts 140; 336
-//   12 prompts, 27264 tokens    56, 127, 446; 604
+//   12 prompts, 26518 tokens    56, 127, 446; 604
 //   16411 tokens of 6 heads     9, 16, ends 51 + join 43 + parts 49; 159
 // The solve's stores bound it (26 KB a chunk and head: 4 TB/s).  The chain's chunk takes a
 // wave some 2100 cycles of the matrix unit; with 8 waves LDS (6300) and issue (5800) bound it,
@@ -505,7 +505,7 @@ __device__ __forceinline__ void to_lds4(uint32_t lds, const void* base, uint32_t
       "global_load_lds_dwordx4 %1, %2\n\t"
       "global_load_lds_dwordx4 %1, %2 offset:1024\n\t"
       "global_load_lds_dwordx4 %1, %2 offset:2048\n\t"
-      "global_load_lds_dwordx4 %1, %2 offset:3072" ::"s"(lds), "v"(offset), "s"(base) : "memory");
+      "global_load_lds_dwordx4 %1, %2 offset:3*1024" ::"s"(lds), "v"(offset), "s"(base) : "memory");
 }
 __device__ __forceinline__ void to_lds2(uint32_t lds, const void* base, uint32_t offset) {
   asm volatile(
