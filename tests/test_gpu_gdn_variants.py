@@ -76,3 +76,21 @@ def test_tokens_after_one_that_forgets_all(gpu_lib, dtype, huge):
         if step:
             d.slots = np.concatenate([d.slots, [-1] * (len(d.q) - len(d.slots))])
         d.check(gpu_lib, np.arange(len(d.q) + 1) if step else starts, step=step)
+
+
+@pytest.mark.parametrize("channels", [2 ** 26, 2 ** 26 - 3])
+@pytest.mark.parametrize("step", [False, True])
+def test_conv_of_the_widest_rows(gpu_lib, channels, step):
+    """Two tokens of two sequences; three products of 2^-24 and their sum's roundings: 2^-22 of the sizes."""
+    log("widest", channels, step)
+    gen = torch.Generator("cuda").manual_seed(3)
+    make = lambda *shape: torch.randn(*shape, generator=gen, device="cuda")
+    x, weight, state = make(2, channels), make(channels, 2), make(2, 1, channels)
+    slots, starts = torch.tensor([1, 0], dtype=torch.int32, device="cuda"), torch.arange(3, dtype=torch.int32, device="cuda")
+    was, after = state.flip(0)[:, 0], torch.zeros_like(state)
+    args = (x, weight, state, slots) if step else (x, weight, state, slots, starts)
+    out = (gpu_lib.nvfp4_causal_conv_step if step else gpu_lib.nvfp4_causal_conv)(*args, activation="none", state_out=after)
+    assert torch.equal(after[:, 0].flip(0), x)
+    for r in range(2):
+        old, new = was[r].double() * weight[:, 0].double(), x[r].double() * weight[:, 1].double()
+        assert ((out[r].double() - old - new).abs() <= 2.0 ** -22 * (old.abs() + new.abs()) + 1e-37).all()
