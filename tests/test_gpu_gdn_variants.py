@@ -94,3 +94,56 @@ def test_conv_of_the_widest_rows(gpu_lib, channels, step):
     for r in range(2):
         old, new = was[r].double() * weight[:, 0].double(), x[r].double() * weight[:, 1].double()
         assert ((out[r].double() - old - new).abs() <= 2.0 ** -22 * (old.abs() + new.abs()) + 1e-37).all()
+
+
+def test_conv_in_two_launches(gpu_lib):
+    """More tokens than one launch takes."""
+    tokens, channels = 2 ** 24 + 50, 3
+    log("conv in two launches")
+    gen = torch.Generator("cuda").manual_seed(4)
+    make = lambda *shape: torch.randn(*shape, generator=gen, device="cuda")
+    x, weight, state = make(tokens, channels), make(channels, 2), make(1, 1, channels)
+    starts, slots = torch.tensor([0, tokens], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    after = torch.zeros_like(state)
+    out = gpu_lib.nvfp4_causal_conv(x, weight, state, slots, starts, activation="none", state_out=after)
+    assert torch.equal(after[0], x[-1:])
+    old = torch.cat([state[0], x[:-1]]).double() * weight[:, 0].double()
+    new = x.double() * weight[:, 1].double()
+    assert ((out.double() - old - new).abs() <= 2.0 ** -22 * (old.abs() + new.abs()) + 1e-37).all()
+
+
+def test_norm_in_two_launches(gpu_lib):
+    """More groups than one launch takes; eight squares, their mean and its root, a product: 2^-19 of the value, and bf16's rounding."""
+    tokens = 2 ** 24 + 100
+    log("norm in two launches")
+    x = torch.randn(tokens, 1, 8, generator=torch.Generator("cuda").manual_seed(5), device="cuda", dtype=torch.bfloat16)
+    out = gpu_lib.nvfp4_group_norm(x, torch.ones(8, device="cuda"), activation="none", eps=1e-6)
+    for rows in (slice(0, 1000), slice(2 ** 24 - 1000, tokens)):
+        y = x[rows].double()
+        want = y / (y.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+        assert ((out[rows].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -19) * want.abs() + 1e-37).all()
+
+
+def test_chunked_in_two_launches(gpu_lib):
+    """More sequences than one launch takes, of a token each: out = scale (q~ . k~) beta v, S = k~ (beta v)^T."""
+    n = 2 ** 20 + 100
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("needs 120 GiB")
+    log("chunked in two launches")
+    gen = torch.Generator("cuda").manual_seed(6)
+    q, k, v = (torch.randn(n, 1, 64, generator=gen, device="cuda").half() for _ in range(3))
+    a, b = torch.zeros(n, 1, device="cuda").half(), torch.randn(n, 1, generator=gen, device="cuda").half()
+    zero = torch.zeros(1, device="cuda")
+    state = torch.empty(n, 1, 64, 64, device="cuda")
+    slots = torch.arange(n - 1, -1, -1, dtype=torch.int32, device="cuda")
+    starts, cached = torch.arange(n + 1, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    out = gpu_lib.nvfp4_gated_delta_chunked(q, k, v, a, b, zero, zero, state, slots, starts, cached_lens=cached, scale=0.125, eps=1e-6)
+    torch.cuda.synchronize()
+    qn, kn = (x[:, 0].double() / (x[:, 0].double().square().sum(-1, keepdim=True) + 1e-6).sqrt() for x in (q, k))
+    d = torch.sigmoid(b.double()) * v[:, 0].double()
+    want = 0.125 * (qn * kn).sum(-1, keepdim=True) * d
+    assert ((out[:, 0].double() - want).abs() <= 2.0 ** -11 * want.abs() + 2.0 ** -19 * 0.125 * d.abs() + 2.0 ** -25).all()
+    for r in (*range(0, n, 65536), *range(n - 101, n)):
+        got = state[n - 1 - r, 0].double()
+        exact = kn[r][:, None] * d[r]
+        assert ((got - exact).abs() <= 2.0 ** -19 * d[r].abs()).all(), r
