@@ -31,10 +31,10 @@ inline bool row_ok(int64_t heads, int64_t head_dim) {
   return heads > 0 && head_dim > 0 && heads < kMaxRow && head_dim < kMaxRow && heads * head_dim <= kMaxRow;
 }
 
-// no two elements of a [tokens][heads][head_dim] tensor share a place
+// a token's heads lie one behind another and end before the next token; (heads - 1) * head may pass 2^63
 inline bool strides_ok(int64_t heads, int64_t head_dim, int64_t token, int64_t head) {
   if (token >= kMaxStride || head >= kMaxStride || head < head_dim || token < head_dim) return false;
-  return (heads - 1) * head + head_dim <= token;
+  return heads == 1 || head <= (token - head_dim) / (heads - 1);
 }
 
 inline bool by16(int64_t stride, int es) { return (stride * es) % 16 == 0; }

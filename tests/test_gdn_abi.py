@@ -125,6 +125,21 @@ def test_products_of_sizes_past_32_bits(lib):
     assert c["step"](hk=1 << 25, hv=1 << 25) == SHAPE
 
 
+def test_strides_whose_products_pass_64_bits(lib):
+    """Heads by a head's stride, up to 2^26 by 2^40: what wraps to a small or negative number overlaps all the same."""
+    c = calls(lib)
+    many = (1 << 25) + 1
+    for token, group in ((1, 1 << 39), (1, (1 << 40) - 1), (many, 1 << 39), ((1 << 40) - 1, (1 << 40) - 1), ((1 << 40) - 1, 1 << 38)):
+        for row in ("x", "o", "g"):
+            rows = dict(xt=many, xg=1, ot=many, og=1, gt=many, gg=1)
+            rows[row + "t"], rows[row + "g"] = token, group
+            assert c["norm"](groups=many, dim=1, wg=0, **rows) == SHAPE, (row, token, group)
+    for heads in (2, 3, 1 << 19):  # of 128
+        far = (1 << 40) - 8
+        assert c["step"](hk=heads, hv=heads, dk=128, dv=128, vt=heads * 128, vh=128, ot=heads * 128, oh=128, qt=heads * 128, qh=128, kt=far, kh=far,
+                         at=heads, bt=heads) == SHAPE
+
+
 def test_valid_calls_without_a_gpu_return_device_error(lib):
     if not no_gpu():
         pytest.skip("a GPU is visible: valid calls would launch kernels on these placeholder addresses")

@@ -117,6 +117,16 @@ def test_in_place_rope_wants_the_same_strides(lib):
     assert call(ko=P, koh=64, kot=256) == SHAPE
 
 
+def test_strides_whose_products_pass_64_bits(lib):
+    """Heads by a head's stride, up to 2^25 by 2^40: what wraps to a small or negative number overlaps all the same."""
+    call = calls(lib)["rope"]
+    for heads, stride in (((1 << 24) + 1, (1 << 40) - 1), (1 << 25, 1 << 39), (1 << 25, (1 << 40) - 2)):
+        for row in ("q", "qo", "k", "ko"):
+            rows = {r + s: n for r in ("q", "qo", "k", "ko") for s, n in (("t", 2 * heads), ("h", 2))}
+            rows[row + "h"], rows[row + "t"] = stride, 2
+            assert call(dim=2, rot=2, hq=heads, hk=heads, **rows) == SHAPE, (row, heads, stride)
+
+
 def test_pages_of_a_long_table_and_cache(lib):
     """Products of sizes that pass 32 bits are seen as what they are."""
     c = calls(lib)
