@@ -112,6 +112,9 @@ nvfp4_status nvfp4_causal_conv_step(int64_t n_seqs, int64_t channels, int64_t wi
  *   g = -e^a_log[h] ln(1 + e^(a[h] + dt_bias[h])),  beta = 1 / (1 + e^-b[h])
  *   S <- e^g S;  S <- S + k~ (beta (v - S^T k~))^T;  out = scale S^T q~
  *
+ * Finite rows of q and k of any size are normalised; a row of zeros is one of
+ * zeros, also where eps is 0.
+ *
  *   q, k       [tokens][k_heads][head_k], v and out [tokens][v_heads][head_v],
  *              elements of dtype; pointers 16-byte aligned, strides multiples of
  *              16 bytes; the rows of a tensor may not overlap.  v_heads is a

@@ -161,10 +161,7 @@ struct Row {
         part[0][s] = halves(y);
       }
     }
-    // 1 / sqrt(|x|^2 + eps), of x scaled: where eps is then infinite, x is nothing beside it
-    const float more = __builtin_amdgcn_ldexpf(eps, 2 * up), all = squares + more;
-    norm = more > 3e38f ? __builtin_amdgcn_ldexpf(1.0f / sqrtf(eps), -up) : 1.0f / sqrtf(all);
-    if (squares == 0.0f) norm = 0.0f;  // at most 2^-4 then, whatever eps is
+    norm = norm_of(squares, up, eps);
   }
   __device__ __forceinline__ void store(uint8_t* image, int mt, int lane) const {
 #pragma unroll

@@ -121,6 +121,15 @@ __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(d);
 }
 
+// What a row x 2^up whose squares sum to `squares` is multiplied by to be x / sqrt(|x|^2 + eps).  A row of zeros stays one,
+// also where eps is 0.
+__device__ __forceinline__ float norm_of(float squares, int up, float eps) {
+  if (squares == 0.0f) return 0.0f;
+  const float more = __builtin_amdgcn_ldexpf(eps, 2 * up);
+  // where that is infinite, x is nothing beside eps
+  return more > 3e38f ? __builtin_amdgcn_ldexpf(1.0f / sqrtf(eps), -up) : 1.0f / sqrtf(squares + more);
+}
+
 // first row and end of sequence r, inside the buffers whatever the starts hold
 __device__ __forceinline__ int64_t start_of(const int32_t* starts, int r, int64_t tokens) {
   const int64_t s = starts[r];
