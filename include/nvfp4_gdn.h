@@ -113,7 +113,8 @@ nvfp4_status nvfp4_causal_conv_step(int64_t n_seqs, int64_t channels, int64_t wi
  *   S <- e^g S;  S <- S + k~ (beta (v - S^T k~))^T;  out = scale S^T q~
  *
  * Finite rows of q and k of any size are normalised; a row of zeros is one of
- * zeros, also where eps is 0.
+ * zeros, also where eps is 0.  A NaN in a, b, k or v is never lost: the state
+ * behind it has NaNs (which outputs have them is unspecified).
  *
  *   q, k       [tokens][k_heads][head_k], v and out [tokens][v_heads][head_v],
  *              elements of dtype; pointers 16-byte aligned, strides multiples of

@@ -337,8 +337,10 @@ __global__ __launch_bounds__(kThreads) void gated_delta_solve_kernel(DeltaArgs a
   const int64_t token = at.begin + std::min(lane, rows - 1);
   const float decay = -expf(a.a_log[h]) * softplus(element<DT>(a.a, token * a.a_token + h) + a.dt_bias[h]);
   const float beta = lane < rows ? sigmoid<true>(element<DT>(a.b, token * a.b_token + h)) : 0.0f;
-  // at 2^-256 nothing is left in fp32; less would cost the sums of later tokens their last bits
-  double log_decay = lane < rows ? fmax((double)decay * 1.4426950408889634, -256.0) : 0.0;
+  // at 2^-256 nothing is left in fp32; less would cost the sums of later tokens their last bits.  A NaN stays one, for the
+  // chunk's outputs and the state behind it to show.
+  double log_decay = lane < rows ? (double)decay * 1.4426950408889634 : 0.0;
+  if (log_decay < -256.0) log_decay = -256.0;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
     const double before = __shfl_up(log_decay, d);

@@ -45,3 +45,35 @@ def test_keys_of_any_size(gpu_lib, step, eps, dtype, low, high, head_k):
         d.check(gpu_lib, np.arange(tokens + 1) if step else starts, step=step)
         d.k[:, :, 5] *= 100.0  # one element far above the rest
         d.q[:, :, 6] *= 100.0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,step", [([200, 130], False), ([2700, 65], False), ([1] * 7, True)])  # the second in parts
+@pytest.mark.parametrize("which", ["a", "b", "k", "v"])
+def test_a_nan_reaches_the_state(gpu_lib, dtype, lens, step, which):
+    """And no other sequence, head or column of it."""
+    rng = np.random.default_rng(len(lens))
+    log("nan", dtype, lens, step, which)
+    starts = delta_starts(lens)
+    d = Delta(rng, dtype, int(starts[-1]), len(lens), 1, 2, 64, 64, decay=0.05)
+
+    def call():
+        after = torch.zeros_like(d.state)
+        out = d.run(gpu_lib, starts, step=step, state=d.state, after=after, out=torch.zeros_like(d.v))
+        torch.cuda.synchronize()
+        return out, after
+
+    clean = call()
+    tensor = getattr(d, which)
+    for token in {0, min(70, lens[0] - 1), lens[0] - 1}:
+        where = {"a": (token, 1), "b": (token, 1), "k": (token, 0, 9), "v": (token, 1, 21)}[which]
+        was = tensor[where].clone()
+        tensor[where] = float("nan")
+        out, after = call()
+        tensor[where] = was
+        at = (d.slots[0], slice(None) if which == "k" else 1) + ((slice(None), 21) if which == "v" else ())
+        assert after[at].isnan().all(), token
+        want = clean[1].clone()
+        want[at] = after[at]
+        assert torch.equal(after.nan_to_num(7.0), want.nan_to_num(7.0)), token
+        assert torch.equal(out[lens[0]:], clean[0][lens[0]:]), token
