@@ -198,7 +198,8 @@ nvfp4_status nvfp4_gated_delta_step(int64_t n_seqs, int64_t k_heads, int64_t v_h
  *   group_dim  up to 8192
  *
  * Everything in fp32, the mean taken off before squares are summed; one rounding
- * to dtype.
+ * to dtype.  Finite groups of any size are normalised; where the squares are all 0
+ * and eps is too, (x - m) / 0 counts as 0.
  *
  * Errors: NULL pointers -> ERR_NULL; sizes <= 0 or >= 2^31, group_dim > 8192,
  * groups * group_dim > 2^26, weight_group, overlapping strides, out = x or gate

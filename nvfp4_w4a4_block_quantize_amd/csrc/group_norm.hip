@@ -27,25 +27,85 @@ __device__ __forceinline__ float turned(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kRowRor + BY, 0xF, 0xF, false));
 }
 
-template <int LANES>
-__device__ __forceinline__ float sum_of(float v, float* lds) {
-  v += turned<8>(v);
-  v += turned<4>(v);
-  v += turned<2>(v);
-  v += turned<1>(v);
+// of a group's lanes, the same in all of them
+template <int LANES, typename F>
+__device__ __forceinline__ float joined(float v, float* lds, F join) {
+  v = join(v, turned<8>(v));
+  v = join(v, turned<4>(v));
+  v = join(v, turned<2>(v));
+  v = join(v, turned<1>(v));
   if constexpr (LANES > 16) {
     const auto rows = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(rows[0]) + __uint_as_float(rows[1]);
+    v = join(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
     const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
+    v = join(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
   }
   if constexpr (LANES > 64) {
-    __syncthreads();  // what the last sum left in lds is read
+    __syncthreads();  // what the last one left in lds is read
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = lds[0] + lds[1] + lds[2] + lds[3];
+    v = join(join(join(lds[0], lds[1]), lds[2]), lds[3]);
   }
   return v;
+}
+template <int LANES>
+__device__ __forceinline__ float sum_of(float v, float* lds) {
+  return joined<LANES>(v, lds, [](float a, float b) { return a + b; });
+}
+
+// A group's sum of squares is taken as it is below 2^126, and from 2^-80 on or beside an eps of 2^-100 and more: what
+// squares lose below the normal range is nothing then.
+constexpr float kMostSquares = 0x1p126f, kLeastSquares = 0x1p-80f, kLeastEps = 0x1p-100f;
+
+// A group: where its elements are, and its weights.
+struct Group {
+  int64_t x, gate, out, weight;
+};
+
+// elements `at` of a group, normalised, on to the output
+template <int DT, int E>
+__device__ __forceinline__ void put(const NormArgs& a, const Group& group, int at, float (&y)[E], const Elements<DT, E>& gate) {
+  const bool gated = a.gate.p != nullptr;
+  Elements<0, E> w, b;
+  w.load(a.weight, group.weight + at);
+  if (a.bias) b.load(a.bias, group.weight + at);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    y[e] *= w.get(e);
+    if (a.bias) y[e] += b.get(e);
+    const float g = gated ? gate.get(e) : y[e];
+    const float act = a.activation ? g * sigmoid<DT == 0>(g) : g;
+    y[e] = gated ? y[e] * act : act;
+  }
+  Elements<DT, E> out;
+  out.set(y);
+  out.store(a.out.p, group.out + at);
+}
+
+// A group whose squares leave the range: times a power of two that takes the largest element into [1/4, 1/2), an element at a
+// time and from memory each time, so that the common case's registers are its own.
+template <int DT, int LANES>
+__device__ __forceinline__ void norm_scaled(const NormArgs& a, const Group& group, int lane, float over_dim, float* lds) {
+  int up = 0;
+  auto each = [&](auto f) {
+#pragma unroll 1
+    for (int at = lane; at < a.group_dim; at += LANES) f(at, __builtin_amdgcn_ldexpf(element<DT>(a.x.p, group.x + at), up));
+  };
+  float top = 0.0f, mean = 0.0f, s = 0.0f;
+  each([&](int, float x) { top = fmaxf(top, fabsf(x)); });
+  up = -1 - __builtin_amdgcn_frexp_expf(joined<LANES>(top, lds, [](float a, float b) { return fmaxf(a, b); }));
+  if (a.centred) {
+    each([&](int, float x) { mean += x; });
+    mean = sum_of<LANES>(mean, lds) * over_dim;
+  }
+  each([&](int, float x) { s = __builtin_fmaf(x - mean, x - mean, s); });
+  const float over = norm_of(sum_of<LANES>(s, lds) * over_dim, up, a.eps);
+  each([&](int at, float x) {
+    Elements<DT, 1> z;
+    if (a.gate.p) z.load(a.gate.p, group.gate + at);
+    float y[1] = {(x - mean) * over};
+    put<DT, 1>(a, group, at, y, z);
+  });
 }
 
 // Groups of up to LANES * N * E elements, E of them at a time.
@@ -58,15 +118,16 @@ __global__ __launch_bounds__(kThreads) void group_norm_kernel(NormArgs a, FastDi
   const bool live = item < items;  // the others keep step with their wave
   const uint32_t t = by_groups.div(live ? item : 0);
   const int64_t token = t;
-  const int group = live ? (int)(item - t * by_groups.d) : 0;
-  const int64_t xo = token * a.x.token + group * a.x.head, zo = token * a.gate.token + group * a.gate.head;
+  const int of_token = live ? (int)(item - t * by_groups.d) : 0;
+  const Group group = {token * a.x.token + of_token * a.x.head, token * a.gate.token + of_token * a.gate.head,
+                       token * a.out.token + of_token * a.out.head, (int64_t)of_token * a.weight_group};
   Elements<DT, E> x[N], z[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int at = (i * LANES + lane) * E;
     if (at < a.group_dim) {
-      x[i].load(a.x.p, xo + at);
-      if (gated) z[i].load(a.gate.p, zo + at);
+      x[i].load(a.x.p, group.x + at);
+      if (gated) z[i].load(a.gate.p, group.gate + at);
     } else {
       x[i].zero();
     }
@@ -90,30 +151,23 @@ __global__ __launch_bounds__(kThreads) void group_norm_kernel(NormArgs a, FastDi
       s = __builtin_fmaf(y, y, s);
     }
   }
-  const float over = 1.0f / sqrtf(__builtin_fmaf(sum_of<LANES>(s, lds), over_dim, a.eps));
+  s = sum_of<LANES>(s, lds);
+  float over = 1.0f / sqrtf(__builtin_fmaf(s, over_dim, a.eps));
+  if constexpr (DT == 2) {  // squares of fp16 are in range, or all zeros
+    if (s == 0.0f) over = fminf(over, 1.0f);
+  } else if (!(s < kMostSquares && (s >= kLeastSquares || a.eps >= kLeastEps))) {  // a group's lanes agree
+    if (live) norm_scaled<DT, LANES>(a, group, lane, over_dim, lds);
+    return;
+  }
   if (!live) return;
-  const float* weight = a.weight + (int64_t)group * a.weight_group;
-  const float* bias = a.bias ? a.bias + (int64_t)group * a.weight_group : nullptr;
-  const int64_t oo = token * a.out.token + group * a.out.head;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int at = (i * LANES + lane) * E;
     if (at >= a.group_dim) continue;
     float y[E];
-    Elements<0, E> w, b;
-    w.load(weight, at);
-    if (bias) b.load(bias, at);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      y[e] = (x[i].get(e) - mean) * over * w.get(e);
-      if (bias) y[e] += b.get(e);
-      const float g = gated ? z[i].get(e) : y[e];
-      const float act = a.activation ? g * sigmoid<DT == 0>(g) : g;
-      y[e] = gated ? y[e] * act : act;
-    }
-    Elements<DT, E> out;
-    out.set(y);
-    out.store(a.out.p, oo + at);
+    for (int e = 0; e < E; ++e) y[e] = (x[i].get(e) - mean) * over;
+    put<DT, E>(a, group, at, y, z[i]);
   }
 }
 

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from tests import gdn_reference as R
-from tests.test_gpu_gdn import Delta, delta_starts, host, ints, log
+from tests.test_gpu_gdn import DTYPES, NORM_SLACK, Delta, delta_starts, dev, host, ints, log, within
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -77,3 +77,29 @@ def test_a_nan_reaches_the_state(gpu_lib, dtype, lens, step, which):
         want[at] = after[at]
         assert torch.equal(after.nan_to_num(7.0), want.nan_to_num(7.0)), token
         assert torch.equal(out[lens[0]:], clean[0][lens[0]:]), token
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-36, 1e-6, 1e30])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [1, 16, 121, 128, 200, 256, 300, 512, 1024, 4096, 4100, 8191, 8192])
+@pytest.mark.parametrize("centred", [False, True])
+def test_norm_of_groups_of_any_size(gpu_lib, eps, dtype, dim, centred):
+    """From 10^-36 to 10^37, each group of a token another one, and a group of zeros: squares that overflow or vanish."""
+    rng = np.random.default_rng([dim, 5])
+    log("norm of any size", eps, dtype, dim, centred)
+    tokens, groups = 5, 7
+    sizes = 10.0 ** rng.uniform(-36, 37, (tokens, groups, 1))
+    sizes[0, 0], sizes[1, 1], sizes[2, 2] = 0.0, 1e-36, 1e37
+    x = rng.standard_normal((tokens, groups, dim)) * sizes
+    x[3, 3], x[4, 4] = 3.3e38, -3.3e38  # sums overflow too
+    x[3, 4, ::2], x[3, 4, 1::2] = 3.3e38, -3.3e38
+    x = dev(x, DTYPES[dtype])
+    weight, bias = dev(1 + 0.3 * rng.standard_normal((groups, dim))), dev(rng.standard_normal((groups, dim)))
+    if centred:  # without differences beyond roundings, and eps nothing beside them, nothing is defined
+        x[3, 3], x[4, 4] = x[3, 4], -x[3, 4]
+        if dim == 1:
+            x[:] = 0.0
+    want, sizes = R.norm(host(x), host(weight), host(bias), None, False, centred, max(eps, 1e-200))
+    got = gpu_lib.nvfp4_group_norm(x, weight, bias=bias, activation="none", centred=centred, eps=eps)
+    torch.cuda.synchronize()
+    within(got, want, NORM_SLACK * sizes, dtype, "norm")
