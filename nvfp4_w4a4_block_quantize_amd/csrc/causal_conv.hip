@@ -62,9 +62,9 @@ struct Taps {
   }
 };
 
-// the last sequence that starts at or before row t; 0 if none does
-__device__ __forceinline__ int sequence_at(const int32_t* starts, int n, int64_t t) {
-  int low = 0, high = n;  // the answer is in [low, high)
+// the last sequence from `low` on that starts at or before row t; `low` if none does
+__device__ __forceinline__ int sequence_at(const int32_t* starts, int low, int n, int64_t t) {
+  int high = n;  // the answer is in [low, high)
   while (high - low > 1) {
     const int mid = low + (high - low) / 2;
     if (starts[mid] <= t) low = mid; else high = mid;
@@ -79,15 +79,20 @@ __global__ __launch_bounds__(kThreads) void causal_conv_kernel(ConvArgs a, int64
   const int64_t begin = (first_block + blockIdx.x) * ROWS, behind = std::min(begin + ROWS, a.tokens);
   Taps<DT, E, W> taps;
   taps.load(a, c);
-  int r = sequence_at(a.token_starts, a.n_seqs, begin);
+  int r = sequence_at(a.token_starts, 0, a.n_seqs, begin);
   int64_t low = start_of(a.token_starts, r, a.tokens), high = start_of(a.token_starts, r + 1, a.tokens);
   // tokens that see a sequence's state belong to the workgroup of its first one
   int64_t t = low >= begin ? low : std::max(begin, std::min(low + W - 1, high));
   for (;;) {
     while (t >= high) {  // on to the next sequence with rows
-      if (++r >= a.n_seqs) return;
+      if (high >= behind || ++r >= a.n_seqs) return;
       low = std::max(high, start_of(a.token_starts, r, a.tokens));
       high = start_of(a.token_starts, r + 1, a.tokens);
+      if (high <= low && r + 1 < a.n_seqs) {  // none, nor maybe have many behind it: the last one that starts here
+        r = sequence_at(a.token_starts, r + 1, a.n_seqs, low);
+        low = std::max(low, start_of(a.token_starts, r, a.tokens));
+        high = start_of(a.token_starts, r + 1, a.tokens);
+      }
       t = low;
     }
     const bool mine = t == low;  // its first token
