@@ -179,15 +179,6 @@ __global__ __launch_bounds__(kThreads) void causal_conv_step_kernel(ConvArgs a, 
   for (int j = 0; j < W - 1; ++j) rows[j + 1].store(a.state_out, state + (int64_t)j * a.channels);
 }
 
-// Tokens a thread: with more of them fewer rows are loaded twice, with fewer the card is filled.  32 from 48 MiB of outputs on,
-// which then go past the caches, else 16 or, while that is less than 4 waves a CU, 8.  8192 channels in bf16, width 4, us:
-//   tokens   256    512   1024   2048   4096   8192
-//   8        5.4    7.2   10.9   17.6   35.7   70.9
-//   16       6.8    8.5   10.3   16.0   32.0   65.1
-//   32      10.0   11.1   12.1   14.5   28.2   58.2
-// (32, but through the caches, 65.6 at 8192; 13 ragged prompts of 2568 channels in fp16: 19.1, 18.2, 20.0)
-constexpr int64_t kManyBytes = 48 << 20;
-
 // `launch(blocks, columns, first block)`, so many blocks at a time
 template <typename F>
 hipError_t for_blocks(int64_t blocks, uint32_t columns, F launch) {
@@ -214,10 +205,11 @@ hipError_t launch_width(const ConvArgs& a, bool step, hipStream_t stream) {
     return for_blocks(a.tokens, columns, [&](dim3 grid, int64_t first) {
       causal_conv_step_kernel<DT, E, W><<<grid, kThreads, 0, stream>>>(a, first);
     });
-  if (E > 1 && a.tokens * a.channels * element_size(DT) >= kManyBytes) return launch_rows<DT, E, W, 32, true>(a, columns, stream);
-  const int64_t waves = a.tokens / 16 * columns;
-  if (waves >= 4 * device_cu_count()) return launch_rows<DT, E, W, 16, false>(a, columns, stream);
-  return launch_rows<DT, E, W, 8, false>(a, columns, stream);
+  const int rows = conv_rows(a.tokens, columns, E > 1, device_cu_count());
+  if constexpr (E > 1) {
+    if (rows == 32) return launch_rows<DT, E, W, 32, true>(a, columns, stream);
+  }
+  return rows == 16 ? launch_rows<DT, E, W, 16, false>(a, columns, stream) : launch_rows<DT, E, W, 8, false>(a, columns, stream);
 }
 
 template <int DT, int E>

@@ -25,6 +25,25 @@ struct ConvArgs {
   void* out;
   int64_t ldo;
 };
+// Tokens a thread of the convolution of prompts takes; `columns` workgroups of a wave hold a row.  With more of them fewer
+// rows are loaded twice, with fewer the card is filled: 32, in vectors of 16 bytes and past the caches, from 5 1/2
+// waves a CU on, else 16 from 4 waves a CU on, else 8.  us:
+//   tokens, channels     waves a CU of 32    8      16     32
+//   1024 x 8192, bf16    2                   10.7   10.2   12.1
+//   2048 x 8192, bf16    4                   17.6   15.9   14.7
+//   1024 x 8192, f32     4                   15.8   15.3   16.4
+//   7069 x 2568, f16     5.2                 18.9   16.7   18.4
+//   13 prompts, 7069     5.2                 19.2   18.3   20.1
+//   3000 x 8192, bf16    5.9                 26.2   22.9   20.7
+//   1500 x 8192, f32     5.9                 22.9   22.9   20.3
+//   10000 x 2568, f16    7.3                 28.7   25.6   21.6
+//   13 prompts, 10400    7.6                 30.0   27.8   25.0
+//   8192 x 8192, bf16    16                  69.8   64.9   59.0 (through the caches 63.2)
+// (2568 channels: width 3, else 4)
+inline int conv_rows(int64_t tokens, int64_t columns, bool vectors, int cus) {
+  if (vectors && tokens / 32 * columns * 2 >= 11 * cus) return 32;
+  return tokens / 16 * columns >= 4 * cus ? 16 : 8;
+}
 hipError_t launch_causal_conv(const ConvArgs& a, hipStream_t stream);
 hipError_t launch_causal_conv_step(const ConvArgs& a, hipStream_t stream);
 

@@ -25,3 +25,6 @@ extern "C" int64_t gdn_test_used(int64_t tokens, int64_t n_seqs, int k_heads, in
 extern "C" int64_t gdn_test_parts(int64_t tokens, int64_t n_seqs, int v_heads, int head_v) {
   return nvfp4::delta_parts(tokens, n_seqs, v_heads, head_v);
 }
+extern "C" int gdn_test_conv_rows(int64_t tokens, int64_t columns, int vectors, int cus) {
+  return nvfp4::conv_rows(tokens, columns, vectors != 0, cus);
+}

@@ -69,6 +69,19 @@ def test_workspace_holds_what_a_call_and_smaller_calls_use(tmp_path):
     assert in_parts > 1000
 
 
+def test_convolutions_of_the_gpu_tests_reach_every_number_of_rows(tmp_path):
+    """What tests/test_gpu_gdn_batches.py means to run, on a card of 256 CUs."""
+    from tests.test_gpu_gdn_batches import CONV_ROWS, conv_columns
+
+    path = str(tmp_path / "libnvfp4_gdn_rows.so")
+    build(path)
+    rows = ctypes.CDLL(path).gdn_test_conv_rows
+    rows.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int]
+    for dtype, channels, tokens, want in CONV_ROWS:
+        assert rows(tokens, conv_columns(dtype, channels), channels % 8 == 0, 256) == want, (dtype, channels, tokens)
+    assert {(dtype, want) for dtype, _, _, want in CONV_ROWS} == {(d, n) for d in ("f32", "bf16", "f16") for n in (8, 16, 32)}
+
+
 def test_chunks_of_ragged_sequences_have_places_of_their_own():
     rng = random.Random(3)
     for _ in range(300):

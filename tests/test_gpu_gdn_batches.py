@@ -1,4 +1,5 @@
-"""The gated delta layer's calls over batches of unusual make: many sequences without rows.  Checks, bounds and their
+"""The gated delta layer's calls over batches of unusual make, and of the sizes at which variants
+begin and end: many sequences without rows, convolutions of 8, 16 and 32 rows a thread.  Checks, bounds and their
 reasons are those of test_gpu_gdn."""
 import numpy as np
 import pytest
@@ -28,3 +29,28 @@ def test_conv_among_many_sequences_without_rows(gpu_lib, dtype, channels):
     torch.cuda.synchronize()
     # a step over a sequence is a load that waits, 0.1 us at least: 40000 of them, 4 ms; a bisection has 17
     assert begin.elapsed_time(end) / 10 < 1.0
+
+
+# (type, channels, tokens, rows a thread): just below and from what takes more of them on, a card of 256 CUs supposed
+CONV_ROWS = [("f32", 1032, 3279, 8), ("f32", 1032, 3280, 16), ("f32", 1032, 9023, 16), ("f32", 1032, 9024, 32),
+             ("bf16", 1032, 5455, 8), ("bf16", 1032, 15039, 16), ("bf16", 1032, 15040, 32), ("f16", 1032, 5456, 8), ("f16", 1032, 15039, 16),
+             ("f16", 1032, 16500, 32), ("bf16", 135, 40000, 16)]
+
+
+def conv_columns(dtype, channels):
+    """Waves of a row: vectors of 16 bytes where rows are made of them, 64 a wave."""
+    each = (4 if dtype == "f32" else 8) if channels % 8 == 0 else 1
+    return -(-channels // (64 * each))
+
+
+@pytest.mark.parametrize("dtype,channels,tokens,rows", CONV_ROWS)
+@pytest.mark.parametrize("width", [2, 3, 4])
+def test_conv_of_every_number_of_rows(gpu_lib, dtype, channels, tokens, rows, width):
+    """Sequences that begin and end around a thread's rows, one left out, rows behind the last."""
+    rng = np.random.default_rng([channels, tokens, width])
+    lens = [1000, 1, 31, 32, 33, 0, 2, 999, 3, 8, 16]
+    lens.append(tokens - 5 - sum(lens))
+    log("conv rows", dtype, channels, tokens, rows, width)
+    x, weight, bias, state, slots = conv_inputs(rng, tokens, channels, width, dtype, len(lens))
+    slots[3] = -1
+    check_conv(gpu_lib, dtype, x, weight, bias, "silu", state, slots, delta_starts(lens), rng.integers(0, 2, len(lens)), in_place=width == 4)
