@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "kv_internal.h"
 
 namespace nvfp4 {
@@ -98,18 +100,38 @@ inline int64_t delta_chunk_places(int64_t tokens, int64_t n_seqs) { return token
 // Behind the chunks: where heads are few, sequences are taken in parts, and each part of a sequence and head has the state
 // it starts from, and what it does to any.  Of 64 columns of states a CU in all parts (as many as run at once, with as
 // many again for what parts do) if those are 8 parts or more, else of twice that; a part has 8 chunks or more but for the
-// last.  Fewer than 5 parts are none: they cost three times the work.  In us, bf16 and fp16, heads of 128:
-//   6 heads, 16411 tokens: 619 whole, 158 in 21 parts, 184 in 32     16 heads: 634, 259 in 8, 270 in 16
-//   24 heads: 645, 368 in 5, 350 in 10     48 heads, 8192 tokens: 357, 389 in 2, 330 in 5
-//   64 heads, 16411 tokens: 706, 775 in 4     8 heads, 2048 tokens: 94, 87 in 4     40 heads, 3000 tokens: 140, 152 in 5
-constexpr int kDeltaPartColumns = kMaxCus * 128, kDeltaPartChunks = 8, kDeltaMostParts = 32, kDeltaLeastParts = 5;
+// last.
+//
+// And only where that is not slower: both passes over a part take 2.4 times as long a chunk as the whole chain takes, 4.3
+// times where a CU has more than 64 columns meanwhile, and each part adds a join, all together two launches.  Lengths are
+// not known here: the longest of n sequences is between 1 / n of the tokens and all of them, 1 / sqrt(n) is taken, and all
+// are cut alike.  In us, whole and in parts, bf16 and heads of 128 if not said:
+//   6 heads, 1024 tokens: 55, 65 in 2           1536: 75, 70 in 3              2048: 95, 75 in 4
+//   6 heads, 16411: 615, 158 in 21, 181 in 32   8 heads, 2048: 97, 81 in 4     16 heads, 4096: 172, 102 in 8
+//   24 heads, 16411: 664, 384 in 10             32 heads, 2048: 97, 92 in 4    32 heads, 8192: 340, 256 in 8
+//   40 heads, 3000: 136, 149 in 5               40 heads, 8192: 351, 319 in 5  48 heads, 3000: 139, 154 in 5
+//   48 heads, 4096: 178, 186 in 5               48 heads, 6000: 266, 262 in 5  48 heads, 8192: 355, 332 in 5
+//   56 heads, 8192: 360, 385 in 4               64 heads, 16411: 726, 779 in 4
+//   float32: 6 heads, 1536: 120, 95 in 3        40 heads, 3000: 226, 258 in 5  48 heads, 8192: 740, 671 in 5
+//   heads of 64: 48 heads, 2048: 82, 74 in 4    96 heads, 4096: 156, 172 in 5  96 heads, 8192: 317, 334 in 5
+//   8 sequences of 6 heads, the longest 1024: 63, 95    2048: 101, 121    4096: 175, 162    3 of them, 4096: 170, 106
+//   16 of one head of 64, 1024: 45, 57          2048: 76, 63
+// It misses 6 heads of 1536 tokens, 96 heads of 64, the 8 sequences up to 2048 and the 16 up to 1024.
+constexpr int kDeltaPartColumns = kMaxCus * 128, kDeltaPartChunks = 8, kDeltaMostParts = 32;
 inline int64_t delta_parts(int64_t tokens, int64_t n_seqs, int v_heads, int head_v) {
-  const int64_t columns = n_seqs * v_heads * head_v, by_chunks = tokens / (kDeltaChunk * kDeltaPartChunks);
+  const int64_t of_seq = (int64_t)v_heads * head_v, columns = n_seqs * of_seq;
   int64_t parts = kDeltaPartColumns / 2 / columns;
   if (parts < 8) parts = kDeltaPartColumns / columns;
-  if (parts > by_chunks) parts = by_chunks;
+  if (parts > tokens / (kDeltaChunk * kDeltaPartChunks)) parts = tokens / (kDeltaChunk * kDeltaPartChunks);
   if (parts > kDeltaMostParts) parts = kDeltaMostParts;
-  return parts < kDeltaLeastParts ? 0 : parts;
+  if (parts < 2) return 0;
+  const int64_t all = (tokens + kDeltaChunk - 1) / kDeltaChunk, longest = (int64_t)((double)all / std::sqrt((double)n_seqs));
+  int64_t each = (longest + parts - 1) / parts;
+  if (each < kDeltaPartChunks) each = kDeltaPartChunks;
+  auto cut = [&](int64_t chunks) { return (chunks + each - 1) / each; };
+  // in tenths of a chunk of the whole chain
+  const int64_t pass = (cut(all) + n_seqs - 1) * of_seq > 64 * kMaxCus ? 43 : 24, join = 15, launches = 15;
+  return each * pass + cut(longest) * join + launches < longest * 10 ? parts : 0;
 }
 inline int64_t delta_part_bytes(int head_k, int head_v) { return (int64_t)4 * head_k * (head_v + head_k); }
 // enough for any number of sequences up to n_seqs

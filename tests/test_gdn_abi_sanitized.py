@@ -82,6 +82,21 @@ def test_convolutions_of_the_gpu_tests_reach_every_number_of_rows(tmp_path):
     assert {(dtype, want) for dtype, _, _, want in CONV_ROWS} == {(d, n) for d in ("f32", "bf16", "f16") for n in (8, 16, 32)}
 
 
+def test_prompts_of_the_gpu_tests_are_whole_and_in_parts_as_they_mean(tmp_path):
+    from tests.test_gpu_gdn_batches import BEHIND, PARTS
+
+    path = str(tmp_path / "libnvfp4_gdn_parts.so")
+    build(path)
+    parts = ctypes.CDLL(path).gdn_test_parts
+    parts.argtypes, parts.restype = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32], ctypes.c_int64
+    for heads, lens, want in PARTS:
+        assert parts(sum(lens) + BEHIND, len(lens), heads[1], heads[3]) == want, (heads, lens)
+    # calls of one sequence, with what is slower: whole and in parts, both measured
+    for tokens, heads, want in ((1024, 6, 0), (2048, 6, 4), (16411, 6, 21), (2048, 8, 4), (4096, 16, 8), (3000, 40, 0), (8192, 40, 6), (3000, 48, 0),
+                                (4096, 48, 0), (8192, 48, 5), (8192, 56, 0), (16411, 64, 0)):
+        assert parts(tokens, 1, heads, 128) == want, (tokens, heads)
+
+
 def test_chunks_of_ragged_sequences_have_places_of_their_own():
     rng = random.Random(3)
     for _ in range(300):

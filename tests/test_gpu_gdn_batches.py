@@ -1,10 +1,11 @@
 """The gated delta layer's calls over batches of unusual make, and of the sizes at which variants
-begin and end: many sequences without rows, convolutions of 8, 16 and 32 rows a thread.  Checks, bounds and their
+begin and end: many sequences without rows, convolutions of 8, 16 and 32 rows a thread,
+sequences whole and in parts.  Checks, bounds and their
 reasons are those of test_gpu_gdn."""
 import numpy as np
 import pytest
 
-from tests.test_gpu_gdn import check_conv, conv_inputs, delta_starts, ints, log
+from tests.test_gpu_gdn import Delta, check_conv, conv_inputs, delta_starts, ints, log
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -54,3 +55,22 @@ def test_conv_of_every_number_of_rows(gpu_lib, dtype, channels, tokens, rows, wi
     x, weight, bias, state, slots = conv_inputs(rng, tokens, channels, width, dtype, len(lens))
     slots[3] = -1
     check_conv(gpu_lib, dtype, x, weight, bias, "silu", state, slots, delta_starts(lens), rng.integers(0, 2, len(lens)), in_place=width == 4)
+
+
+# (heads, lengths, parts that a sequence may have): 0 where whole ones are faster
+PARTS = [((1, 2, 128, 128), [2044], 0), ((1, 2, 128, 128), [2045], 4), ((2, 2, 64, 64), [2100], 4), ((1, 6, 128, 128), [300, 4000, 0, 700], 9),
+         ((1, 3, 128, 64), [5, 513, 2600], 6), ((1, 1, 128, 256), [2500, 64], 5), ((2, 4, 64, 192), [2300], 4), ((20, 20, 64, 128), [3600], 7),
+         ((1, 6, 64, 64), [150] * 8, 0), ((1, 6, 64, 64), [400] * 8, 0), ((1, 1, 64, 64), [260] * 16, 0), ((8, 24, 64, 128), [1536], 0)]
+BEHIND = 3  # rows behind the last sequence
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("heads,lens,parts", PARTS)
+def test_chunked_whole_and_in_parts(gpu_lib, dtype, heads, lens, parts):
+    rng = np.random.default_rng([len(lens), *heads, 6])
+    log("whole and in parts", dtype, heads, lens, parts)
+    starts = delta_starts(lens)
+    d = Delta(rng, dtype, int(starts[-1]) + BEHIND, len(lens), *heads, decay=0.05)
+    if len(lens) > 3:
+        d.slots[3] = -1
+    d.check(gpu_lib, starts, cached=np.arange(len(lens)) % 2, in_place=len(lens) == 1)
