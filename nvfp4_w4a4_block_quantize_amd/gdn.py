@@ -113,6 +113,8 @@ def nvfp4_gated_delta_chunked(q, k, v, a, b, a_log, dt_bias, state, slots, token
     """
     if kv._bind is None:
         kv._load()
+    if q.dim() != 3 or v.dim() != 3 or slots.dim() != 1:  # sizes are read from them here
+        raise ValueError(f"q and v must be [tokens, heads, head_dim] and slots [n], got {tuple(q.shape)}, {tuple(v.shape)}, {tuple(slots.shape)}")
     if out is None:
         out = kv._new(v.shape, v.dtype, v, stream)
     if scale is None:
@@ -136,6 +138,8 @@ def nvfp4_gated_delta_step(q, k, v, a, b, a_log, dt_bias, state, slots, scale=No
     its row out.  Returns out, shaped like v."""
     if kv._bind is None:
         kv._load()
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q.shape)}")
     if out is None:
         out = kv._new(v.shape, v.dtype, v, stream)
     status = kv._bind.gated_delta_step(q, k, v, a, b, a_log, dt_bias, state, state if state_out is None else state_out,

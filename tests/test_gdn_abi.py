@@ -223,3 +223,20 @@ def test_binding_refuses_bad_tensors():
         nv.nvfp4_group_norm(**good)
     with pytest.raises(TypeError, match="unsupported dtype"):
         nv.nvfp4_group_norm(x.double(), torch.zeros(24))
+
+
+def test_binding_refuses_tensors_of_other_dimensions():
+    """Before any size of them is read, with a workspace given or not."""
+    torch = pytest.importorskip("torch")
+    q, v, a, per = torch.zeros((9, 2, 64)), torch.zeros((9, 4, 128)), torch.zeros((9, 4)), torch.zeros(4)
+    good = dict(q=q, k=q.clone(), v=v, a=a, b=a, a_log=per, dt_bias=per, state=torch.zeros((5, 4, 64, 128)),
+                slots=torch.zeros(3, dtype=torch.int32), token_starts=torch.zeros(4, dtype=torch.int32))
+    for change in ({"q": q[0]}, {"q": q[0, 0, 0]}, {"v": v[0]}, {"v": v.view(9, 4, 2, 64)}, {"slots": good["slots"][0]},
+                   {"slots": good["slots"].view(1, 3)}):
+        for workspace in (None, torch.zeros(64, dtype=torch.uint8)):
+            with pytest.raises(ValueError, match="must be"):
+                nv.nvfp4_gated_delta_chunked(**{**good, **change}, workspace=workspace)
+    step = {k: t for k, t in good.items() if k != "token_starts"}
+    for change in ({"q": q[0, 0, 0]}, {"q": q[0]}, {"v": v[0]}):
+        with pytest.raises(ValueError, match="must be"):
+            nv.nvfp4_gated_delta_step(**{**step, **change, "slots": torch.zeros(9, dtype=torch.int32)})
