@@ -20,7 +20,10 @@
  *   - The stream's device is the current device of the calling thread.
  *   - An output may not overlap another argument unless its comment says so.
  *   - Strides are in elements, below 2^40.  Tensors of heads are addressed by
- *     (token, head) strides with head_dim consecutive elements.
+ *     (token, head) strides with head_dim consecutive elements.  A token's heads
+ *     lie one behind another and end before the next token (token >= (heads - 1) *
+ *     head + head_dim), as in nvfp4_kv.h: other strides, those of tensors laid out
+ *     by heads first among them, are refused.
  *   - Values that live on the device (slots, starts) cannot be refused by the
  *     call.  What a wrong one does is part of the description; none leads to an
  *     access outside the buffers.
@@ -143,8 +146,8 @@ nvfp4_status nvfp4_causal_conv_step(int64_t n_seqs, int64_t channels, int64_t wi
  *
  * Errors: NULL pointers -> ERR_NULL; sizes <= 0 or >= 2^31, head counts and
  * sizes other than above, heads * head_dim > 2^26, tokens * v_heads > 2^37,
- * n_seqs * v_heads > 2^28, overlapping strides, out = v, workspace_bytes too
- * small -> ERR_SHAPE; alignment -> ERR_ALIGN; dtype -> ERR_DTYPE; scale not finite
+ * n_seqs * v_heads > 2^28, other strides than above, out = v, workspace_bytes
+ * too small -> ERR_SHAPE; alignment -> ERR_ALIGN; dtype -> ERR_DTYPE; scale not finite
  * or <= 0, eps not finite or < 0 -> ERR_RANGE.
  */
 nvfp4_status nvfp4_gated_delta_chunked(int64_t tokens, int64_t k_heads, int64_t v_heads, int64_t head_k,
@@ -202,8 +205,8 @@ nvfp4_status nvfp4_gated_delta_step(int64_t n_seqs, int64_t k_heads, int64_t v_h
  * and eps is too, (x - m) / 0 counts as 0.
  *
  * Errors: NULL pointers -> ERR_NULL; sizes <= 0 or >= 2^31, group_dim > 8192,
- * groups * group_dim > 2^26, weight_group, overlapping strides, out = x or gate
- * with other strides -> ERR_SHAPE; pointers not aligned to their elements ->
+ * groups * group_dim > 2^26, weight_group, other strides than above, out = x or
+ * gate with other strides -> ERR_SHAPE; pointers not aligned to their elements ->
  * ERR_ALIGN; dtype, activation, centred not 0 or 1 -> ERR_DTYPE; eps not finite
  * or < 0 -> ERR_RANGE.
  */

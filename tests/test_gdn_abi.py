@@ -125,6 +125,16 @@ def test_products_of_sizes_past_32_bits(lib):
     assert c["step"](hk=1 << 25, hv=1 << 25) == SHAPE
 
 
+def test_heads_lie_within_their_token(lib):
+    """Tensors laid out by heads first, which do not overlap either, are refused, as the header says."""
+    c = calls(lib)
+    assert c["norm"](xt=24, xg=9 * 24) == SHAPE and c["norm"](ot=24, og=9 * 24) == SHAPE and c["norm"](gt=24, gg=9 * 24) == SHAPE
+    for name in ("step", "chunked"):
+        assert c[name](qt=128, qh=9 * 128) == SHAPE and c[name](kt=128, kh=9 * 128) == SHAPE
+        assert c[name](vt=64, vh=9 * 64) == SHAPE and c[name](ot=64, oh=9 * 64) == SHAPE
+    assert "token >= (heads - 1) *" in open(HEADER).read()
+
+
 def test_strides_whose_products_pass_64_bits(lib):
     """Heads by a head's stride, up to 2^26 by 2^40: what wraps to a small or negative number overlaps all the same."""
     c = calls(lib)
