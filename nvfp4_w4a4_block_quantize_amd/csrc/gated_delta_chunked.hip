@@ -23,16 +23,20 @@
 //   8192 tokens of 48 heads     22, 39, ends 156 + join 20 + parts 140; 336
 //   12 prompts, 26518 tokens    56, 127, 446; 604
 //   16411 tokens of 6 heads     9, 16, ends 51 + join 43 + parts 49; 159
-// The solve's stores bound it (26 KB a chunk and head: 4 TB/s).  The chain's chunk takes a
+// The solve's stores bound it (25 KB a chunk and head: 4 TB/s).  The chain's chunk takes a
 // wave some 2100 cycles of the matrix unit; with 8 waves LDS (6300) and issue (5800) bound it,
 // 10400 cycles a chunk, with one wave a SIMD what a product waits for the one before, 6000.
 //
 // Precision.  Operands are fp16 parts, sums fp32.  A row of keys or queries is scaled by a
-// power of two to a length in [16, 32): 16-bit inputs fit one part but for what lies 2^-30
-// below that length; float32 takes two.  |T| and |P| are at most 1 and scaled by 2^14;
-// a column of S, and with it X and V', is scaled by a power of two that follows it and the
-// values: each is cut into two parts, 2^-22 of the element or 2^-31 of the column's largest.
-// Of products of two cut operands the low parts' is dropped (2^-22 again).
+// power of two to a length in [16, 32): 16-bit inputs fit one part but for 2^-29 of that
+// length (half of fp16's last step, 2^-25, of 2^4); float32 takes two.  |T| and |P| are at
+// most 1 and scaled by 2^14; a column of S, and with it X and V', is scaled by a power of two
+// that follows it and the values, so that their largest M is from 2^5 to 2^9: each is cut into
+// two parts, off by 2^-22 of the element or 2^-25, which is 2^-30 of M, and 2^-29 where V'
+// has been taken by a key's norm.  Of products of two cut operands the low parts' is dropped
+// (2^-22 again).  Against 64 bits, relative lengths, beside products in fp32: outputs 0.95 to
+// 1.11 times as far off (float32, 2.1e-7 to 3.4e-7); states of 16-bit inputs 0.94 to 1.13
+// times, of float32 inputs 1.1 to 2.1 times (2.3e-7 and 1.1e-7 under strong decay).
 #include <algorithm>
 
 #include "gdn_device.h"
@@ -244,8 +248,6 @@ __device__ __forceinline__ void store_ties(uint8_t* to, int mt, const float4_t (
     *reinterpret_cast<half8_t*>(to + (2 * tie(mt, s) + 1) * kBlock + lane * 16) = p.lo;
   }
 }
-
-__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
 
 // Sequences in the order of their lengths, the longest first, so that the last workgroups of the chain have the least to do
 // (12 prompts up to 4096 tokens of 48 heads, in the order they are given: 682 us and not 608).
@@ -497,7 +499,8 @@ struct Chain {
 
 #if defined(__HIP_DEVICE_COMPILE__)
 // From memory to LDS past the registers, 16 bytes a lane to byte lds + 16 lane.  M0 is set in the same block, one wait
-// state before the loads read it; an instruction's offset counts on both sides.
+// state before the loads read it; an instruction's offset counts on both sides.  M0 is a reserved register, which a block
+// cannot name as changed: nothing else in these kernels uses it.
 __device__ __forceinline__ void to_lds4(uint32_t lds, const void* base, uint32_t offset) {
   asm volatile(
       "s_mov_b32 m0, %0\n\ts_nop 0\n\t"
@@ -735,7 +738,7 @@ __global__ __launch_bounds__(64 * (WAVES + LOADERS))
 
     // What a column's tokens bring, beta v, and its power of two, with M the largest of that and of the state's elements: M
     // goes to 2^7..2^8 when it has left 2^5..2^9.  The state's length is at most sqrt(128) M and grows by M a token, so that
-    // X and V' stay below 75 M < 2^16; |S| 2^4 is below 2^13; a part's last bit lies 2^31 below M.
+    // X and V' stay below 75 M < 2^16; |S| 2^4 is below 2^13; half of a part's last step is 2^-30 of M at most.
     {
       float top = 0.0f, high = 0.0f;
 #pragma unroll

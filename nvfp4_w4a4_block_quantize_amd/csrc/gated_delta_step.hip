@@ -23,9 +23,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// ln(1 + e^x)
-__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
-
 __device__ __forceinline__ float sum_of_wave(float x) {
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) x += __shfl_xor(x, m);

@@ -121,6 +121,9 @@ __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(d);
 }
 
+// ln(1 + e^x)
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
+
 // What a row x 2^up whose squares sum to `squares` is multiplied by to be x / sqrt(|x|^2 + eps).  A row of zeros stays one,
 // also where eps is 0.
 __device__ __forceinline__ float norm_of(float squares, int up, float eps) {
