@@ -155,7 +155,7 @@ __global__ __launch_bounds__(kThreads) void group_norm_kernel(NormArgs a, FastDi
   float over = 1.0f / sqrtf(__builtin_fmaf(s, over_dim, a.eps));
   if constexpr (DT == 2) {  // squares of fp16 are in range, or all zeros
     if (s == 0.0f) over = fminf(over, 1.0f);
-  } else if (!(s < kMostSquares && (s >= kLeastSquares || a.eps >= kLeastEps))) {  // a group's lanes agree
+  } else if (__builtin_expect(!(s < kMostSquares && (s >= kLeastSquares || a.eps >= kLeastEps)), 0)) {  // a group's lanes agree
     if (live) norm_scaled<DT, LANES>(a, group, lane, over_dim, lds);
     return;
   }
