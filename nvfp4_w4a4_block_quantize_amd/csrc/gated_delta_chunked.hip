@@ -20,9 +20,9 @@
 // are taken in parts at once, as a part does one linear map to the state it is given.
 //
 // In us (bf16 and fp16, heads of 128; keys, solve, chain; the whole call as a graph):
-//   8192 tokens of 48 heads     22, 39, ends 156 + join 20 + parts 140; 336
-//   12 prompts, 26518 tokens    56, 127, 446; 604
-//   16411 tokens of 6 heads     9, 16, ends 51 + join 43 + parts 49; 159
+//   8192 tokens of 48 heads     21, 39, ends 154 + join 20 + parts 141; 336
+//   12 prompts, 26518 tokens    57, 128, 463; 616
+//   16411 tokens of 6 heads     9, 16, ends 51 + join 44 + parts 48; 158
 // The solve's stores bound it (25 KB a chunk and head: 4 TB/s).  The chain's chunk takes a
 // wave some 2100 cycles of the matrix unit; with 8 waves LDS (6300) and issue (5800) bound it,
 // 10400 cycles a chunk, with one wave a SIMD what a product waits for the one before, 6000.
