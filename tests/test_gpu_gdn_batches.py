@@ -74,3 +74,38 @@ def test_chunked_whole_and_in_parts(gpu_lib, dtype, heads, lens, parts):
     if len(lens) > 3:
         d.slots[3] = -1
     d.check(gpu_lib, starts, cached=np.arange(len(lens)) % 2, in_place=len(lens) == 1)
+
+
+def test_prompts_in_parts_in_graphs_of_one_workspace(gpu_lib):
+    """Replays follow the starts, lengths of 0 and 1 among them, and share a workspace with eager calls between them."""
+    rng = np.random.default_rng(31)
+    tokens = 2600
+    d = Delta(rng, "bf16", tokens, 2, 1, 2, 128, 64, decay=0.05)
+    ws = torch.empty(gpu_lib.nvfp4_gated_delta_workspace(tokens, 2, 1, 2, 128, 64, torch.bfloat16), dtype=torch.uint8, device="cuda")
+    slots, starts, cached = ints(d.slots), ints([0, 0, 0]), ints([0, 0])
+    after, out = torch.zeros_like(d.state), torch.zeros_like(d.v)
+
+    def call():
+        gpu_lib.nvfp4_gated_delta_chunked(d.q, d.k, d.v, d.a, d.b, d.a_log, d.dt_bias, d.state, slots, starts, cached_lens=cached,
+                                          state_out=after, out=out, workspace=ws)
+
+    graphs = []
+    call()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    log("graphs in parts")
+    for i, (at, have) in enumerate((([0, 2100, 2600], [0, 3]), ([0, 1, 2600], [1, 1]), ([30, 30, 2590], [0, 0]), ([0, 1300, 1300], [2, 0]))):
+        starts.copy_(ints(at))
+        cached.copy_(ints(have))
+        out.zero_(), after.zero_()
+        call()
+        want = out.clone(), after.clone()
+        out.zero_(), after.zero_()
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(after, want[1]), i
+    checked = d.check(gpu_lib, [0, 1300, 1300], cached=[2, 0])
+    assert torch.equal(checked[1][d.slots[0]], after[d.slots[0]])

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from tests import gdn_reference as R
-from tests.test_gpu_gdn import DTYPES, NORM_SLACK, Delta, delta_starts, dev, host, ints, log, within
+from tests.test_gpu_gdn import DELTA_LEAST, DELTA_SLACK, DTYPES, NORM_SLACK, Delta, delta_starts, dev, host, ints, log, within
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -103,3 +103,80 @@ def test_norm_of_groups_of_any_size(gpu_lib, eps, dtype, dim, centred):
     got = gpu_lib.nvfp4_group_norm(x, weight, bias=bias, activation="none", centred=centred, eps=eps)
     torch.cuda.synchronize()
     within(got, want, NORM_SLACK * sizes, dtype, "norm")
+
+
+IN_PARTS = 2113  # tokens of one sequence of few heads that are taken in parts
+
+
+def check_without_shortening(d, nv, starts):
+    """Delta.check for keys along one line that nothing decays.  Its bound on a state's length, 2^-20 of it, is that of a
+    chunk's roundings, which the rule shortens from chunk to chunk.  Across such keys it shortens nothing: each of n chunks
+    leaves its own rounding, at most 2^-20 and independent of the others', and their sum has a length of 2^-20 sqrt(n)."""
+    out, after = torch.zeros_like(d.v), torch.full_like(d.state, 3.0)
+    was = host(after)
+    want, slack, left, left_slack, floors = d.want(np.asarray(starts), None, host(out), DELTA_LEAST)
+    slot = d.slots[0]
+    was[slot] = left[slot]
+    d.run(nv, starts, None, False, d.state, after, out)
+    torch.cuda.synchronize()
+    within(out, want, DELTA_SLACK * slack, d.dtype, "out")
+    within(after, was, DELTA_SLACK * left_slack, "f32", "state")
+    off, length = (np.sqrt((x ** 2).sum((1, 2))) for x in (host(after)[slot] - left[slot], left[slot]))
+    chunks = -(-(starts[1] - starts[0]) // 64)
+    assert (off <= 2.0 ** -20 * chunks ** 0.5 * length + DELTA_SLACK * np.sqrt((floors[slot] ** 2).sum(1))).all(), (off / length)
+
+
+@pytest.mark.parametrize("case", ["no decay", "full decay", "mixed", "beta 0", "beta 1", "same key", "opposed keys", "zero keys", "zero all"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gates_and_keys_at_their_ends_in_parts(gpu_lib, case, dtype):
+    rng = np.random.default_rng(40)
+    log("ends in parts", case, dtype)
+    d = Delta(rng, dtype, IN_PARTS + 2, 1, 1, 2, 64, 64, extra=8)
+    if case == "no decay":
+        d.a.fill_(-100.0)
+        d.dt_bias.fill_(-50.0)
+    elif case == "full decay":
+        d.a.fill_(100.0)
+        d.a_log.fill_(4.0)
+    elif case == "mixed":
+        d.a_log.fill_(2.5)
+        d.a.copy_(torch.where(torch.rand(d.a.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(1)) < 0.3, 60.0, -12.0))
+    elif case in ("beta 0", "beta 1"):
+        d.b.fill_(-200.0 if case == "beta 0" else 200.0)
+    elif case in ("same key", "opposed keys"):
+        d.k.copy_(d.k[:1].clone().expand_as(d.k))
+        d.b.fill_(200.0)
+        d.a.fill_(-100.0)
+        if case == "opposed keys":
+            d.k[::2] *= -1.0
+    elif case == "zero keys":
+        d.k[::3] = 0.0
+        d.q[1::3] = 0.0
+    else:
+        for t in (d.q, d.k, d.v, d.state):
+            t.zero_()
+    if case in ("same key", "opposed keys"):
+        check_without_shortening(d, gpu_lib, [1, IN_PARTS + 1])
+    else:
+        d.check(gpu_lib, [1, IN_PARTS + 1], out_extra=8)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [1e-20, 300.0, 1e15])
+def test_values_of_any_size_in_parts(gpu_lib, dtype, size):
+    rng = np.random.default_rng(41)
+    log("size in parts", dtype, size)
+    Delta(rng, dtype, IN_PARTS, 1, 1, 2, 64, 64, size=size, decay=0.05).check(gpu_lib, [0, IN_PARTS])
+
+
+@pytest.mark.parametrize("down", [False, True])
+@pytest.mark.parametrize("strong", [False, True])
+def test_values_that_grow_and_shrink_in_parts(gpu_lib, down, strong):
+    """Values pass 36 powers of ten, states with them, so that parts start from states far from what they add."""
+    rng = np.random.default_rng(42)
+    log("growing in parts", down, strong)
+    d = Delta(rng, "f32", IN_PARTS, 1, 1, 2, 64, 64)
+    climb = np.linspace(18, -18, IN_PARTS) if down else np.linspace(-18, 18, IN_PARTS)
+    d.v *= dev(10.0 ** climb)[:, None, None]
+    d.a += 4.0 if strong else -2.0
+    d.check(gpu_lib, [0, IN_PARTS])
