@@ -53,7 +53,8 @@ __device__ __forceinline__ float unit_norm(float (&x)[N], float eps) {
 // Four waves a SIMD where a state's head has 128 rows: with the five that its registers allow, 128 sequences take 145.9 us
 // and not 144.3.  Heads of 64 rows take as many as fit (21.5 us at 32 sequences in float32, with four 21.9).
 template <int DT, int DK, int COLS>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4, DK == 128 ? 4 : 8))) void gated_delta_step_kernel(DeltaArgs a, FastDiv by_group, int64_t first) {
+__global__ __launch_bounds__(kThreads)
+    __attribute__((amdgpu_waves_per_eu(4, DK == 128 ? 4 : 8))) void gated_delta_step_kernel(DeltaArgs a, FastDiv by_group, int64_t first) {
   constexpr int kLanes = COLS / 4;            // of a row
   constexpr int kGroups = kThreads / kLanes;  // rows at a time
   constexpr int kRows = DK / kGroups;
